@@ -69,6 +69,7 @@ typedef int pa_status;
 #define PA_DEV_BAD_SEQLEN 4  /* cu_seqlens_q / seqused_k inconsistent with the stated bounds */
 #define PA_DEV_TIMEOUT 8     /* a bounded wait on a pipeline barrier gave up */
 #define PA_DEV_CASCADE 16    /* cascade precondition violated (see pa_cascade_fwd) */
+#define PA_DEV_BAD_POSITION 32 /* a token position past the cos/sin table: token skipped */
 
 #define PA_BF16 0 /* bfloat16 */
 #define PA_F16 1  /* IEEE half (float16) */
@@ -471,6 +472,89 @@ pa_status pa_cascade_fwd_ex(const pa_kv_update* update, const void* q, int64_t q
                             int num_kv_heads, int head_size, int block_size, int num_blocks,
                             float softmax_scale, int common_prefix_len, const pa_attn_opts* opts,
                             void* out, float* lse, void* workspace, size_t workspace_bytes,
+                            int dtype, int32_t* dev_status, void* stream);
+
+/*
+ * pa_rope_table -- the rotary cos/sin table of positions 0 .. table_len - 1.
+ * Pair i of rot_dim / 2 turns by f_i = base^(-2i / rot_dim) radians per
+ * position; row p holds mscale * cos(p f_i) for every i, then mscale *
+ * sin(p f_i). Angles are exact to about 1e-9 radian at a million positions.
+ *   cos_sin  : float32 [table_len, rot_dim], 16-byte aligned.
+ *   rot_dim  : even, 2 .. 256 (pa_rope_and_cache takes multiples of 16).
+ *   base     : finite, > 0.
+ *   scaling  : NULL for none, else how the rates change for contexts longer
+ *              than the model was trained on (orig_len positions):
+ *     PA_ROPE_LINEAR      f_i / factor
+ *     PA_ROPE_NTK         base * factor^(rot_dim / (rot_dim - 2)) as the base
+ *                         (rot_dim > 2)
+ *     PA_ROPE_WAVELENGTH  with n = orig_len f_i / 2 pi turns in the original
+ *                         length: f_i / factor where n <= low, f_i where n >=
+ *                         high, a mix linear in n in between
+ *     PA_ROPE_YARN        with d(n) = rot_dim ln(orig_len / (2 pi n)) / (2 ln
+ *                         base), the pair that makes n turns: f_i below pair
+ *                         floor(d(high)), f_i / factor from pair ceil(d(low))
+ *                         on, a mix linear in i in between (base > 1)
+ *              factor, orig_len > 0 and high > low > 0 where used; mscale
+ *              finite, multiplies every entry (PA_ROPE_YARN commonly 0.1 ln
+ *              factor + 1).
+ * The scaling struct is read on the host during the call.
+ */
+#define PA_ROPE_NONE 0
+#define PA_ROPE_LINEAR 1
+#define PA_ROPE_NTK 2
+#define PA_ROPE_WAVELENGTH 3
+#define PA_ROPE_YARN 4
+typedef struct pa_rope_scaling {
+  int kind; /* PA_ROPE_* */
+  double factor;
+  double orig_len;
+  double low;
+  double high;
+  double mscale;
+} pa_rope_scaling;
+pa_status pa_rope_table(float* cos_sin, int table_len, int rot_dim, double base,
+                        const pa_rope_scaling* scaling, void* stream);
+
+/*
+ * pa_rope_and_cache -- what a decoder layer does to a step's new q, k and v
+ * before attention, in one pass: per-head RMS norm of q and k (optional),
+ * rotation of q and k, and the write of k and v into their pages
+ * (pa_reshape_and_cache, or with fp8 pa_reshape_and_cache_fp8). The attention
+ * call that follows takes q_out and no update.
+ *   positions : int64 [num_tokens]; token t turns by row positions[t] of the
+ *               table. A negative position marks a padding token: nothing of
+ *               it is written. A position >= table_len sets
+ *               PA_DEV_BAD_POSITION and its token is skipped likewise.
+ *   q         : [num_tokens, num_heads, head_size] in dtype, token t at
+ *               q + t*q_token_stride; q_out likewise. q_out may be q (same
+ *               pointer and stride); it must not overlap q otherwise
+ *               (PA_ERR_INVALID_ARG), nor the update's keys and values.
+ *   update    : the new tokens' k and v, their slots and num_tokens, as in
+ *               pa_varlen_fwd_with_update. slot < 0: the token's k and v are
+ *               not written (its q is).
+ *   key_cache, value_cache, ... : as in pa_reshape_and_cache.
+ *   fp8       : NULL for pools in dtype, else e4m3 pools with these scales
+ *               (head_size 128).
+ * With x a head of q or k: if the norm weight w is given, x_j becomes
+ * x_j w_j / sqrt(mean(x^2) + norm_eps); then each pair (a, b) of the first
+ * rot_dim elements becomes (a cos - b sin, b cos + a sin) and the rest stays.
+ * All in float32 with one rounding, to dtype or to e4m3 (after the division
+ * by the head's scale). v is copied (or quantized) as it is.
+ */
+typedef struct pa_rope {
+  const float* cos_sin; /* device float32 [table_len, rot_dim], 16-byte aligned */
+  int table_len;
+  int rot_dim;          /* multiple of 16, <= head_size */
+  int interleaved;      /* 1: pair i is elements (2i, 2i + 1); 0: (i, i + rot_dim / 2) */
+  const float* q_norm;  /* device float32 [head_size], 16-byte aligned, or NULL: no norm */
+  const float* k_norm;
+  float norm_eps;       /* finite, >= 0 */
+} pa_rope;
+pa_status pa_rope_and_cache(const pa_rope* rope, const int64_t* positions, const void* q,
+                            int64_t q_token_stride, void* q_out, int64_t q_out_token_stride,
+                            const pa_kv_update* update, void* key_cache, void* value_cache,
+                            int64_t cache_block_stride, int num_heads, int num_kv_heads,
+                            int head_size, int block_size, int num_blocks, const pa_kv_fp8* fp8,
                             int dtype, int32_t* dev_status, void* stream);
 
 #ifdef __cplusplus

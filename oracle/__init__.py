@@ -21,3 +21,4 @@ from .paged_attention import (  # noqa: F401
     reshape_and_cache_e4m3,
     varlen_attention_e4m3,
 )
+from . import cache_ops  # noqa: F401

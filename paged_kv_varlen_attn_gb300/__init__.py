@@ -9,6 +9,7 @@ functions raise if the library or a GPU is missing.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -29,8 +30,10 @@ PA_DEV_BAD_SLOT = 2
 PA_DEV_BAD_SEQLEN = 4
 PA_DEV_TIMEOUT = 8
 PA_DEV_CASCADE = 16
+PA_DEV_BAD_POSITION = 32
 PA_BF16 = 0
 PA_F16 = 1
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "wavelength": 3, "yarn": 4}
 
 EXPORTS = (
     "pa_status_string",
@@ -53,12 +56,15 @@ EXPORTS = (
     "pa_merge_attn_states_n",
     "pa_varlen_fwd_ex",
     "pa_cascade_fwd_ex",
+    "pa_rope_table",
+    "pa_rope_and_cache",
 )
 
 _lib = None
 
 _c = ctypes
 _vp, _i64, _i32, _f32, _sz = _c.c_void_p, _c.c_int64, _c.c_int, _c.c_float, _c.c_size_t
+_f64 = _c.c_double
 
 
 class KvUpdate(ctypes.Structure):
@@ -75,6 +81,18 @@ class KvFp8(ctypes.Structure):
 class AttnOpts(ctypes.Structure):
     """struct pa_attn_opts of include/pa.h."""
     _fields_ = [("sinks", _vp), ("fp8", ctypes.POINTER(KvFp8))]
+
+
+class RopeScaling(ctypes.Structure):
+    """struct pa_rope_scaling of include/pa.h."""
+    _fields_ = [("kind", _i32), ("factor", _f64), ("orig_len", _f64), ("low", _f64),
+                ("high", _f64), ("mscale", _f64)]
+
+
+class Rope(ctypes.Structure):
+    """struct pa_rope of include/pa.h."""
+    _fields_ = [("cos_sin", _vp), ("table_len", _i32), ("rot_dim", _i32), ("interleaved", _i32),
+                ("q_norm", _vp), ("k_norm", _vp), ("norm_eps", _f32)]
 
 
 _ATTN_ARGS = [_vp, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i32,
@@ -109,6 +127,10 @@ _SIGS = {
                          [ctypes.POINTER(AttnOpts)] + _ATTN_ARGS[20:], _i32),
     "pa_cascade_fwd_ex": ([ctypes.POINTER(KvUpdate)] + _ATTN_ARGS[:20] +
                           [ctypes.POINTER(AttnOpts)] + _ATTN_ARGS[20:], _i32),
+    "pa_rope_table": ([_vp, _i32, _i32, _f64, ctypes.POINTER(RopeScaling), _vp], _i32),
+    "pa_rope_and_cache": ([ctypes.POINTER(Rope), _vp, _vp, _i64, _vp, _i64,
+                           ctypes.POINTER(KvUpdate), _vp, _vp, _i64, _i32, _i32, _i32, _i32, _i32,
+                           ctypes.POINTER(KvFp8), _i32, _vp, _vp], _i32),
     "pa_cascade_fwd_fp8kv_workspace_size": ([_i32] * 9, _sz),
     "pa_varlen_fwd_fp8kv": ([ctypes.POINTER(KvUpdate)] + _ATTN_ARGS[:20] +
                             [ctypes.POINTER(KvFp8)] + _ATTN_ARGS[20:], _i32),
@@ -507,3 +529,85 @@ def cascade_fwd_fp8kv(q, key_cache, value_cache, cu_seqlens_q, seqused_k, block_
                   update_tensors=(key, value))
     del keep
     return res
+
+
+# ---------------------------------------------------------------------------
+# Rotary positions
+def rope_table(table_len, rot_dim, base=10000.0, scaling="none", factor=1.0, orig_len=0.0,
+               low=None, high=None, mscale=None, out=None, device="cuda"):
+    """Rotary cos/sin table float32 [table_len, rot_dim] (row: rot_dim / 2
+    cosines, then sines). scaling: "none", "linear", "ntk", "wavelength" (low,
+    high turns within orig_len, default 1 and 4) or "yarn" (default 1 and 32;
+    mscale default 0.1 ln factor + 1 for factor > 1)."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}, got {scaling!r}")
+    if out is None:
+        out = torch.empty((table_len, rot_dim), dtype=torch.float32, device=device)
+    _need_cuda(out)
+    if out.dtype != torch.float32 or out.shape != (table_len, rot_dim) or not out.is_contiguous():
+        raise ValueError("out must be a contiguous float32 [table_len, rot_dim] tensor")
+    if mscale is None:
+        mscale = 0.1 * math.log(factor) + 1.0 if scaling == "yarn" and factor > 1 else 1.0
+    desc = RopeScaling(ROPE_SCALINGS[scaling], factor, orig_len, 1.0 if low is None else low,
+                       (32.0 if scaling == "yarn" else 4.0) if high is None else high, mscale)
+    with torch.cuda.device(out.device):
+        code = load_library().pa_rope_table(_ptr(out), int(table_len), int(rot_dim), float(base),
+                                            ctypes.byref(desc), _stream(out.device))
+    _check(code, "pa_rope_table")
+    return out
+
+
+def _f32_vector(t, n, name):
+    if t is not None and (t.dtype != torch.float32 or t.shape != (n,) or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous float32 tensor of {n} values")
+
+
+def rope_and_cache(q, key, value, positions, cos_sin, key_cache, value_cache, slot_mapping,
+                   interleaved=False, q_norm=None, k_norm=None, eps=1e-6, k_scale=None,
+                   v_scale=None, out=None, dev_status=None):
+    """Norm (optional weights q_norm, k_norm) and rotate the new queries and
+    keys by the table rows of their positions, and write keys and values into
+    their pages (in place on the caches; with k_scale and v_scale the caches
+    hold e4m3 bytes). Returns the rotated queries; out may be q itself."""
+    lib = load_library()
+    _need_cuda(q, key, value, positions, cos_sin, key_cache, value_cache, slot_mapping, q_norm,
+               k_norm, out, dev_status)
+    if key_cache.stride(0) != value_cache.stride(0) or key_cache.shape != value_cache.shape:
+        raise ValueError("key and value caches must have the same shape and page stride")
+    nb, bs, hk, d = key_cache.shape
+    T, H = q.shape[0], q.shape[1]
+    if q.shape != (T, H, d) or key.shape != (T, hk, d) or value.shape != (T, hk, d):
+        raise ValueError("q, key and value must be [tokens, heads, head_size] of the caches' "
+                         "heads and head size")
+    for t, name in ((positions, "positions"), (slot_mapping, "slot_mapping")):
+        if t.dtype != torch.int64 or t.shape != (T,) or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous int64 tensor of one value per token")
+    if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+        raise ValueError("cos_sin must be a contiguous float32 [positions, rot_dim] tensor")
+    _f32_vector(q_norm, d, "q_norm")
+    _f32_vector(k_norm, d, "k_norm")
+    if (k_scale is None) != (v_scale is None):
+        raise ValueError("k_scale and v_scale go together")
+    if out is None:
+        out = torch.empty((T, H, d), dtype=q.dtype, device=q.device)
+    elif out.shape != q.shape:
+        raise ValueError("out must have the shape of q")
+    if k_scale is None:
+        dtype, desc, keep = _dtype_code(q, key, value, out, key_cache, value_cache), None, None
+    else:
+        _fp8_pool(key_cache), _fp8_pool(value_cache)
+        dtype = _dtype_code(q, key, value, out)
+        desc, keep = _fp8_desc(k_scale, v_scale, hk, q.device)
+    rope = Rope(cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], int(bool(interleaved)),
+                None if q_norm is None else q_norm.data_ptr(),
+                None if k_norm is None else k_norm.data_ptr(), float(eps))
+    with torch.cuda.device(q.device):
+        code = lib.pa_rope_and_cache(
+            ctypes.byref(rope), _ptr(positions), _ptr(q), _row_stride(q), _ptr(out),
+            _row_stride(out), ctypes.byref(_kv_update(key, value, slot_mapping)), _ptr(key_cache),
+            _ptr(value_cache), _cache_stride(key_cache), H, hk, d, bs, nb,
+            None if desc is None else ctypes.byref(desc), dtype, _ptr(dev_status),
+            _stream(q.device))
+    _check(code, "pa_rope_and_cache")
+    del keep
+    return out

@@ -1001,4 +1001,130 @@ pa_status pa_cascade_fwd_ex(const pa_kv_update* update, const void* q, int64_t q
                       opts ? opts->sinks : nullptr);
 }
 
+// ---------------------------------------------------------------- rotary positions
+pa_status pa_rope_table(float* cos_sin, int table_len, int rot_dim, double base,
+                        const pa_rope_scaling* scaling, void* stream) {
+  constexpr double kTwoPi = 6.283185307179586;
+  if (table_len < 0 || rot_dim < 2 || rot_dim > 256 || rot_dim % 2 != 0) return PA_ERR_INVALID_ARG;
+  if (!std::isfinite(base) || !(base > 0.0)) return PA_ERR_INVALID_ARG;
+  RopeTableArgs a{};
+  a.table_len = table_len;
+  a.rot = rot_dim;
+  a.base = base;
+  a.mscale = 1.f;
+  if (scaling) {
+    const pa_rope_scaling& s = *scaling;
+    a.kind = s.kind;
+    a.factor = s.factor;
+    a.orig_len = s.orig_len;
+    a.low = s.low;
+    a.high = s.high;
+    a.mscale = static_cast<float>(s.mscale);
+    if (!std::isfinite(s.mscale)) return PA_ERR_INVALID_ARG;
+    if (s.kind < PA_ROPE_NONE || s.kind > PA_ROPE_YARN) return PA_ERR_INVALID_ARG;
+    if (s.kind != PA_ROPE_NONE && (!std::isfinite(s.factor) || !(s.factor > 0.0)))
+      return PA_ERR_INVALID_ARG;
+    if (s.kind == PA_ROPE_WAVELENGTH || s.kind == PA_ROPE_YARN) {
+      if (!std::isfinite(s.orig_len) || !(s.orig_len > 0.0) || !std::isfinite(s.high) ||
+          !(s.low > 0.0) || !(s.high > s.low))
+        return PA_ERR_INVALID_ARG;
+    }
+    if (s.kind == PA_ROPE_NTK) {
+      if (rot_dim == 2) return PA_ERR_INVALID_ARG;
+      a.base = base * std::pow(s.factor, rot_dim / (rot_dim - 2.0));
+      if (!std::isfinite(a.base) || !(a.base > 0.0)) return PA_ERR_INVALID_ARG;
+    }
+    if (s.kind == PA_ROPE_YARN) {
+      if (!(base > 1.0)) return PA_ERR_INVALID_ARG;
+      auto pair_of = [&](double turns) {
+        return rot_dim * std::log(s.orig_len / (turns * kTwoPi)) / (2.0 * std::log(base));
+      };
+      const double lo = std::fmax(std::floor(pair_of(s.high)), 0.0);
+      const double hi = std::fmin(std::ceil(pair_of(s.low)), rot_dim - 1.0);
+      a.ramp_lo = lo;
+      a.ramp_len = std::fmax(hi - lo, 0.001);
+    }
+  }
+  if (table_len == 0) return PA_OK;
+  if (!cos_sin || !aligned16(cos_sin)) return PA_ERR_INVALID_ARG;
+  const int sms = query_sms(0);
+  if (sms <= 0) return PA_ERR_CUDA;
+  return launch_rope_table(cos_sin, a, static_cast<cudaStream_t>(stream), sms) == cudaSuccess
+             ? PA_OK
+             : PA_ERR_CUDA;
+}
+
+pa_status pa_rope_and_cache(const pa_rope* rope, const int64_t* positions, const void* q,
+                            int64_t q_token_stride, void* q_out, int64_t q_out_token_stride,
+                            const pa_kv_update* update, void* key_cache, void* value_cache,
+                            int64_t cache_block_stride, int num_heads, int num_kv_heads,
+                            int head_size, int block_size, int num_blocks, const pa_kv_fp8* fp8,
+                            int dtype, int32_t* dev_status, void* stream) {
+  if (!rope || !update || num_heads <= 0) return PA_ERR_INVALID_ARG;
+  const KvFormat kv = fp8 ? fp8_format(fp8) : kKvBf16;
+  pa_status st = check_update(update->key, update->value, update->key_token_stride,
+                              update->value_token_stride, key_cache, value_cache,
+                              cache_block_stride, update->slot_mapping, update->num_tokens,
+                              num_kv_heads, head_size, block_size, num_blocks, dtype, kv);
+  if (st != PA_OK) return st;
+  if (rope->table_len < 0 || rope->rot_dim < 16 || rope->rot_dim % 16 != 0 ||
+      rope->rot_dim > head_size || (rope->interleaved != 0 && rope->interleaved != 1))
+    return PA_ERR_INVALID_ARG;
+  if (!std::isfinite(rope->norm_eps) || rope->norm_eps < 0.f) return PA_ERR_INVALID_ARG;
+  const int T = update->num_tokens;
+  if (T == 0) return PA_OK;
+  if (!positions || (reinterpret_cast<uintptr_t>(positions) & 7u) != 0) return PA_ERR_INVALID_ARG;
+  if (!rope->cos_sin || !aligned16(rope->cos_sin) || !aligned16(rope->q_norm) ||
+      !aligned16(rope->k_norm))
+    return PA_ERR_INVALID_ARG;
+  if (!q || !q_out || !aligned16(q) || !aligned16(q_out)) return PA_ERR_INVALID_ARG;
+  const int64_t row = static_cast<int64_t>(num_heads) * head_size;
+  if (q_token_stride < row || q_out_token_stride < row || q_token_stride % 8 != 0 ||
+      q_out_token_stride % 8 != 0)
+    return PA_ERR_INVALID_ARG;
+  if (q_out != q || q_out_token_stride != q_token_stride) {
+    // Rows are read and written by different warps: in place or apart.
+    const char* lo = static_cast<const char*>(q);
+    const char* out = static_cast<const char*>(q_out);
+    if (out < lo + 2 * ((T - 1) * q_token_stride + row) &&
+        lo < out + 2 * ((T - 1) * q_out_token_stride + row))
+      return PA_ERR_INVALID_ARG;
+  }
+  const int sms = query_sms(0);
+  if (sms <= 0) return PA_ERR_CUDA;
+  RopeArgs a{};
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = static_cast<const uint16_t*>(update->key);
+  a.v = static_cast<const uint16_t*>(update->value);
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.q_stride = q_token_stride;
+  a.k_stride = update->key_token_stride;
+  a.v_stride = update->value_token_stride;
+  a.q_out_stride = q_out_token_stride;
+  a.kc = static_cast<uint8_t*>(key_cache);
+  a.vc = static_cast<uint8_t*>(value_cache);
+  a.block_stride_bytes = cache_block_stride * (kv.fp8 ? 1 : 2);
+  a.slots = update->slot_mapping;
+  a.positions = positions;
+  a.cos_sin = rope->cos_sin;
+  a.table_len = rope->table_len;
+  a.rot = rope->rot_dim;
+  a.interleaved = rope->interleaved;
+  a.q_norm = rope->q_norm;
+  a.k_norm = rope->k_norm;
+  a.eps = rope->norm_eps;
+  a.k_scale = kv.k_scale;
+  a.v_scale = kv.v_scale;
+  a.num_tokens = T;
+  a.H = num_heads;
+  a.H_kv = num_kv_heads;
+  a.bs = block_size;
+  a.num_slots = static_cast<int64_t>(num_blocks) * block_size;
+  a.status = dev_status;
+  return launch_rope_and_cache(a, head_size, dtype == PA_F16, kv.fp8,
+                               static_cast<cudaStream_t>(stream), sms) == cudaSuccess
+             ? PA_OK
+             : PA_ERR_CUDA;
+}
+
 }  // extern "C"

@@ -191,4 +191,43 @@ cudaError_t launch_cascade_combine(const AttnArgs& a0, const AttnArgs& a1, int g
 cudaError_t launch_attn_tc(const CUtensorMap& tmK, const CUtensorMap& tmV, const CUtensorMap& tmQ,
                            const AttnArgs& a, int items_bound, cudaStream_t st);
 
+// Rotary cos/sin table (rope.cu).
+struct RopeTableArgs {
+  int table_len, rot, kind;       // kind: PA_ROPE_*
+  double base;                    // of pair i's rate base^(-2i / rot) (PA_ROPE_NTK: scaled)
+  double factor, orig_len, low, high;
+  double ramp_lo, ramp_len;       // PA_ROPE_YARN: the ramp over the pairs
+  float mscale;
+  int per_block;                  // positions per block (set by the launcher)
+};
+cudaError_t launch_rope_table(float* table, RopeTableArgs a, cudaStream_t st, int sms);
+
+// Norm, rotation and cache write of new tokens (rope.cu). Strides in
+// elements, the pools' page stride in bytes.
+struct RopeArgs {
+  const uint16_t* q;
+  const uint16_t* k;
+  const uint16_t* v;
+  uint16_t* q_out;
+  int64_t q_stride, k_stride, v_stride, q_out_stride;
+  uint8_t* kc;
+  uint8_t* vc;
+  int64_t block_stride_bytes;
+  const int64_t* slots;
+  const int64_t* positions;
+  const float* cos_sin;           // [table_len, rot]
+  int table_len, rot, interleaved;
+  const float* q_norm;            // [D] or NULL
+  const float* k_norm;
+  float eps;
+  const float* k_scale;           // [H_kv], e4m3 pools only
+  const float* v_scale;
+  int num_tokens, H, H_kv, bs;
+  int64_t num_slots;
+  int32_t* status;
+  int items_per_warp, chunks;     // warps a token's heads are shared among (set by the launcher)
+};
+cudaError_t launch_rope_and_cache(RopeArgs a, int D, bool f16, bool fp8, cudaStream_t st,
+                                  int sms);
+
 }  // namespace pa
