@@ -557,6 +557,70 @@ pa_status pa_rope_and_cache(const pa_rope* rope, const int64_t* positions, const
                             int head_size, int block_size, int num_blocks, const pa_kv_fp8* fp8,
                             int dtype, int32_t* dev_status, void* stream);
 
+/*
+ * pa_attn_weights -- adds up, for every cached key, the attention weight that
+ * a call's queries gave it: the running sums that pa_evict keeps keys by.
+ *   q, key_cache, cu_seqlens_q, seqused_k, block_table, max_seqlen_q,
+ *   max_seqlen_k, softmax_scale, causal : as in the attention call.
+ *   lse       : float32 [num_heads, total_q], that call's log-sum-exp (with
+ *               its sinks, if any; a row of -inf saw nothing and adds nothing).
+ *   weights   : float32, one value per cache slot and KV head: key row r of
+ *               page b, head h at b * weights_block_stride + h * block_size +
+ *               r. weights_block_stride a multiple of 4.
+ *   fp8       : NULL for a pool in dtype, else an e4m3 pool with these scales
+ *               (head_size 128; only k_scale is read).
+ * For every key j of a sequence of kv_len keys and q_len queries:
+ *   weights[h][j] = (j >= kv_len - q_len ? 0 : weights[h][j])
+ *                   + sum over queries i that see j, over heads g of KV head h,
+ *                     of e^(softmax_scale q_ig.k_j - lse_ig)
+ * so a key starts from 0 in the call that brings it. Rows past a sequence's
+ * keys are left as they were. Sums are float32 in a fixed order: the same
+ * call gives the same bits. A sequence's pages must be its own (a page shared
+ * with another sequence of the call gets the sum of one of them).
+ * A key in a page outside the pool sets PA_DEV_BAD_PAGE and is skipped; a
+ * sequence whose lengths break the stated bounds sets PA_DEV_BAD_SEQLEN, and
+ * with inconsistent cu_seqlens_q it is skipped.
+ */
+pa_status pa_attn_weights(const void* q, int64_t q_token_stride, const void* key_cache,
+                          int64_t cache_block_stride, const float* lse,
+                          const int32_t* cu_seqlens_q, const int32_t* seqused_k,
+                          const int32_t* block_table, int bt_stride, int num_seqs, int total_q,
+                          int max_seqlen_q, int max_seqlen_k, int num_heads, int num_kv_heads,
+                          int head_size, int block_size, int num_blocks, float softmax_scale,
+                          int causal, float* weights, int64_t weights_block_stride,
+                          const pa_kv_fp8* fp8, int dtype, int32_t* dev_status, void* stream);
+
+/*
+ * pa_evict -- eviction by accumulated attention weight: every sequence of
+ * more than `budget` keys is cut down to `budget`, per KV head, in place.
+ * Each KV head keeps the first num_first keys, the last num_recent keys and
+ * of the others those of the largest weight (ties: the lowest index; a NaN
+ * counts as -inf). Kept keys keep their order and move to rows 0 .. budget - 1
+ * of the sequence's pages, K, V and weights alike; rows from budget on are
+ * left as they were, so the pages past the first ceil(budget / block_size)
+ * may be freed. Sequences of at most budget keys stay untouched.
+ * Keys are cached after their rotation, so moving them does not change what
+ * later queries compute with them; the heads of a row then belong to
+ * different tokens.
+ *   elem_size    : bytes of a cache element: 2, or 1 (e4m3, head_size 128).
+ *   weights      : as in pa_attn_weights.
+ *   budget       : >= 1, num_first, num_recent >= 0, num_first + num_recent
+ *                  <= budget.
+ *   kept         : int32 [num_seqs, num_kv_heads, budget], out: the former
+ *                  index of each row, ascending; rows past a shorter
+ *                  sequence's keys get -1.
+ *   new_lens     : int32 [num_seqs], out: min(keys, budget). May be seqused_k.
+ * A sequence's pages must be its own (rows are rewritten in place). A page
+ * outside the pool sets PA_DEV_BAD_PAGE: its keys count as the lightest and
+ * no row moves out of it or into it.
+ */
+pa_status pa_evict(void* key_cache, void* value_cache, int64_t cache_block_stride, float* weights,
+                   int64_t weights_block_stride, const int32_t* seqused_k,
+                   const int32_t* block_table, int bt_stride, int num_seqs, int max_seqlen_k,
+                   int num_kv_heads, int head_size, int block_size, int num_blocks, int elem_size,
+                   int budget, int num_first, int num_recent, int32_t* kept, int32_t* new_lens,
+                   int32_t* dev_status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -58,6 +58,8 @@ EXPORTS = (
     "pa_cascade_fwd_ex",
     "pa_rope_table",
     "pa_rope_and_cache",
+    "pa_attn_weights",
+    "pa_evict",
 )
 
 _lib = None
@@ -131,6 +133,10 @@ _SIGS = {
     "pa_rope_and_cache": ([ctypes.POINTER(Rope), _vp, _vp, _i64, _vp, _i64,
                            ctypes.POINTER(KvUpdate), _vp, _vp, _i64, _i32, _i32, _i32, _i32, _i32,
                            ctypes.POINTER(KvFp8), _i32, _vp, _vp], _i32),
+    "pa_attn_weights": ([_vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp] + [_i32] * 10 + [
+        _f32, _i32, _vp, _i64, ctypes.POINTER(KvFp8), _i32, _vp, _vp], _i32),
+    "pa_evict": ([_vp, _vp, _i64, _vp, _i64, _vp, _vp] + [_i32] * 11 + [_vp, _vp, _vp, _vp],
+                 _i32),
     "pa_cascade_fwd_fp8kv_workspace_size": ([_i32] * 9, _sz),
     "pa_varlen_fwd_fp8kv": ([ctypes.POINTER(KvUpdate)] + _ATTN_ARGS[:20] +
                             [ctypes.POINTER(KvFp8)] + _ATTN_ARGS[20:], _i32),
@@ -611,3 +617,88 @@ def rope_and_cache(q, key, value, positions, cos_sin, key_cache, value_cache, sl
     _check(code, "pa_rope_and_cache")
     del keep
     return out
+
+
+# ---------------------------------------------------------------------------
+# Accumulated attention weight of the cached keys, and eviction by it
+def _weights_stride(weights, nb, bs, hk):
+    """Page stride of a weights tensor [num_blocks, num_kv_heads, block_size]."""
+    if weights.dtype != torch.float32 or weights.shape != (nb, hk, bs) or \
+            weights.stride(2) != 1 or weights.stride(1) != bs:
+        raise ValueError("weights must be float32 [num_blocks, num_kv_heads, block_size] with "
+                         "contiguous pages")
+    return weights.stride(0)
+
+
+def attn_weights(q, key_cache, lse, weights, cu_seqlens_q, seqused_k, block_table, max_seqlen_q,
+                 max_seqlen_k, softmax_scale, causal, k_scale=None, dev_status=None):
+    """Add the attention weight that this call's queries gave every cached key
+    (recomputed from K and the attention call's lse) to weights, float32
+    [num_blocks, num_kv_heads, block_size], in place; the keys of the call's
+    own queries start from zero. With k_scale the key cache holds e4m3 bytes.
+    Returns weights."""
+    lib = load_library()
+    _need_cuda(lse, weights, dev_status)
+    _attn_common(q, key_cache, key_cache, cu_seqlens_q, seqused_k, block_table)
+    T, H, D = q.shape
+    nb, bs, hk, d = key_cache.shape
+    if d != D:
+        raise ValueError("q and the key cache must share the head size")
+    if lse.dtype != torch.float32 or lse.shape != (H, T) or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous float32 [num_heads, total_q] tensor")
+    desc = keep = None
+    if k_scale is not None:
+        _fp8_pool(key_cache)
+        desc, keep = _fp8_desc(k_scale, k_scale, hk, q.device)
+    dtype = _dtype_code(q) if desc is not None else _dtype_code(q, key_cache)
+    with torch.cuda.device(q.device):
+        code = lib.pa_attn_weights(
+            _ptr(q), _row_stride(q), _ptr(key_cache), _cache_stride(key_cache), _ptr(lse),
+            _ptr(cu_seqlens_q), _ptr(seqused_k), _ptr(block_table), block_table.stride(0),
+            cu_seqlens_q.numel() - 1, T, int(max_seqlen_q), int(max_seqlen_k), H, hk, D, bs, nb,
+            float(softmax_scale), int(bool(causal)), _ptr(weights),
+            _weights_stride(weights, nb, bs, hk), None if desc is None else ctypes.byref(desc),
+            dtype, _ptr(dev_status), _stream(q.device))
+    _check(code, "pa_attn_weights")
+    del keep
+    return weights
+
+
+def evict(key_cache, value_cache, weights, seqused_k, block_table, max_seqlen_k, budget,
+          num_first=0, num_recent=0, kept=None, new_lens=None, dev_status=None):
+    """Cut every sequence of more than budget keys down to budget, per KV head:
+    its first num_first keys, its last num_recent and the heaviest of the rest
+    by weights; kept rows of the caches (2-byte or e4m3 elements) and of
+    weights move to the front of the sequence's pages. Returns (kept int32
+    [num_seqs, num_kv_heads, budget], new_lens int32 [num_seqs]); new_lens may
+    be seqused_k itself."""
+    lib = load_library()
+    _need_cuda(key_cache, value_cache, weights, seqused_k, block_table, kept, new_lens,
+               dev_status)
+    if key_cache.stride(0) != value_cache.stride(0) or key_cache.shape != value_cache.shape or \
+            key_cache.dtype != value_cache.dtype:
+        raise ValueError("key and value caches must have the same shape, type and page stride")
+    nb, bs, hk, d = key_cache.shape
+    S = seqused_k.numel()
+    for t, name in ((seqused_k, "seqused_k"), (block_table, "block_table")):
+        if t.dtype != torch.int32:
+            raise ValueError(f"{name} must be int32")
+    if block_table.dim() != 2 or block_table.stride(1) != 1 or block_table.shape[0] != S:
+        raise ValueError("block_table must be [num_seqs, max_blocks] with unit column stride")
+    if kept is None:
+        kept = torch.empty((S, hk, max(int(budget), 0)), dtype=torch.int32,
+                           device=key_cache.device)
+    if new_lens is None:
+        new_lens = torch.empty(S, dtype=torch.int32, device=key_cache.device)
+    for t, shape, name in ((kept, (S, hk, budget), "kept"), (new_lens, (S,), "new_lens")):
+        if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape}")
+    with torch.cuda.device(key_cache.device):
+        code = lib.pa_evict(
+            _ptr(key_cache), _ptr(value_cache), _cache_stride(key_cache), _ptr(weights),
+            _weights_stride(weights, nb, bs, hk), _ptr(seqused_k), _ptr(block_table),
+            block_table.stride(0), S, int(max_seqlen_k), hk, d, bs, nb,
+            key_cache.element_size(), int(budget), int(num_first), int(num_recent), _ptr(kept),
+            _ptr(new_lens), _ptr(dev_status), _stream(key_cache.device))
+    _check(code, "pa_evict")
+    return kept, new_lens

@@ -1127,4 +1127,128 @@ pa_status pa_rope_and_cache(const pa_rope* rope, const int64_t* positions, const
              : PA_ERR_CUDA;
 }
 
+// ---------------------------------------------------------------- weights, eviction
+pa_status pa_attn_weights(const void* q, int64_t q_token_stride, const void* key_cache,
+                          int64_t cache_block_stride, const float* lse,
+                          const int32_t* cu_seqlens_q, const int32_t* seqused_k,
+                          const int32_t* block_table, int bt_stride, int num_seqs, int total_q,
+                          int max_seqlen_q, int max_seqlen_k, int num_heads, int num_kv_heads,
+                          int head_size, int block_size, int num_blocks, float softmax_scale,
+                          int causal, float* weights, int64_t weights_block_stride,
+                          const pa_kv_fp8* fp8, int dtype, int32_t* dev_status, void* stream) {
+  pa_status st = check_shape(num_seqs, total_q, max_seqlen_q, max_seqlen_k, num_heads,
+                             num_kv_heads, head_size, block_size, dtype);
+  if (st != PA_OK) return st;
+  if (fp8 && head_size != 128) return PA_ERR_UNSUPPORTED;
+  if (fp8 && (!fp8->k_scale || (reinterpret_cast<uintptr_t>(fp8->k_scale) & 3u) != 0))
+    return PA_ERR_INVALID_ARG;
+  if (num_seqs > 0 && (!cu_seqlens_q || !seqused_k || !block_table)) return PA_ERR_INVALID_ARG;
+  if (total_q > 0 && (!q || !lse)) return PA_ERR_INVALID_ARG;
+  if (!key_cache || !weights) return PA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(key_cache) || !aligned16(weights)) return PA_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(lse) & 3u) != 0) return PA_ERR_INVALID_ARG;
+  if (q_token_stride < static_cast<int64_t>(num_heads) * head_size || q_token_stride % 8 != 0)
+    return PA_ERR_INVALID_ARG;
+  if (cache_block_stride < static_cast<int64_t>(block_size) * num_kv_heads * head_size ||
+      cache_block_stride % (fp8 ? 16 : 8) != 0)
+    return PA_ERR_INVALID_ARG;
+  if (weights_block_stride < static_cast<int64_t>(block_size) * num_kv_heads ||
+      weights_block_stride % 4 != 0)
+    return PA_ERR_INVALID_ARG;
+  if (bt_stride < 0 || num_blocks < 0 || !std::isfinite(softmax_scale) ||
+      (causal != 0 && causal != 1))
+    return PA_ERR_INVALID_ARG;
+  // Blocks of one launch: 64 keys of a sequence and a KV head each.
+  if (num_kv_heads > 65535 ||
+      static_cast<long long>(num_seqs) * cdiv(max_seqlen_k, 64) > 0x7fffffffLL)
+    return PA_ERR_INVALID_ARG;
+  if (num_seqs == 0 || total_q == 0) return PA_OK;
+  WeightArgs a{};
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_stride = q_token_stride;
+  a.kc = static_cast<const uint8_t*>(key_cache);
+  a.block_stride_bytes = cache_block_stride * (fp8 ? 1 : 2);
+  a.lse = lse;
+  a.weights = weights;
+  a.weights_stride = weights_block_stride;
+  a.cu = cu_seqlens_q;
+  a.seqused_k = seqused_k;
+  a.bt = block_table;
+  a.bt_stride = bt_stride;
+  a.H = num_heads;
+  a.H_kv = num_kv_heads;
+  a.G = num_heads / num_kv_heads;
+  a.bs = block_size;
+  a.num_blocks = num_blocks;
+  a.total_q = total_q;
+  a.max_q = max_seqlen_q;
+  a.max_k = max_seqlen_k;
+  const long long cap = static_cast<long long>(bt_stride) * block_size;
+  a.kv_len_cap = cap > 0x7fffffff ? 0x7fffffff : static_cast<int>(cap);
+  a.scale_log2 = softmax_scale * 1.4426950408889634f;
+  a.causal = causal;
+  a.k_scale = fp8 ? fp8->k_scale : nullptr;
+  a.status = dev_status;
+  return launch_attn_weights(a, num_seqs, head_size, dtype == PA_F16, fp8 != nullptr,
+                             static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? PA_OK
+             : PA_ERR_CUDA;
+}
+
+pa_status pa_evict(void* key_cache, void* value_cache, int64_t cache_block_stride, float* weights,
+                   int64_t weights_block_stride, const int32_t* seqused_k,
+                   const int32_t* block_table, int bt_stride, int num_seqs, int max_seqlen_k,
+                   int num_kv_heads, int head_size, int block_size, int num_blocks, int elem_size,
+                   int budget, int num_first, int num_recent, int32_t* kept, int32_t* new_lens,
+                   int32_t* dev_status, void* stream) {
+  if (num_seqs < 0 || max_seqlen_k < 0 || num_kv_heads <= 0 || num_kv_heads > 65535 ||
+      num_blocks < 0 || bt_stride < 0)
+    return PA_ERR_INVALID_ARG;
+  if (budget < 1 || num_first < 0 || num_recent < 0 || num_first > budget ||
+      num_recent > budget - num_first)
+    return PA_ERR_INVALID_ARG;
+  if (elem_size != 1 && elem_size != 2) return PA_ERR_UNSUPPORTED;
+  if (head_size != 64 && head_size != 128 && head_size != 256) return PA_ERR_UNSUPPORTED;
+  if (elem_size == 1 && head_size != 128) return PA_ERR_UNSUPPORTED;
+  if (block_size <= 0 || block_size % 16 != 0 || block_size > 1024) return PA_ERR_BLOCK_SIZE;
+  if (num_seqs == 0) return PA_OK;
+  if (num_seqs > 0x7fffffff / 64) return PA_ERR_INVALID_ARG;   // blocks of one launch
+  if (!key_cache || !value_cache || !weights || !seqused_k || !block_table || !kept || !new_lens)
+    return PA_ERR_INVALID_ARG;
+  if (!aligned16(key_cache) || !aligned16(value_cache) || !aligned16(weights))
+    return PA_ERR_INVALID_ARG;
+  if (((reinterpret_cast<uintptr_t>(kept) | reinterpret_cast<uintptr_t>(new_lens)) & 3u) != 0)
+    return PA_ERR_INVALID_ARG;
+  if (cache_block_stride < static_cast<int64_t>(block_size) * num_kv_heads * head_size ||
+      cache_block_stride % (elem_size == 1 ? 16 : 8) != 0)
+    return PA_ERR_INVALID_ARG;
+  if (weights_block_stride < static_cast<int64_t>(block_size) * num_kv_heads ||
+      weights_block_stride % 4 != 0)
+    return PA_ERR_INVALID_ARG;
+  EvictArgs a{};
+  a.kc = static_cast<uint8_t*>(key_cache);
+  a.vc = static_cast<uint8_t*>(value_cache);
+  a.block_stride_bytes = cache_block_stride * elem_size;
+  a.weights = weights;
+  a.weights_stride = weights_block_stride;
+  a.seqused_k = seqused_k;
+  a.bt = block_table;
+  a.bt_stride = bt_stride;
+  a.H_kv = num_kv_heads;
+  a.bs = block_size;
+  a.num_blocks = num_blocks;
+  a.row_bytes = head_size * elem_size;
+  a.max_k = max_seqlen_k;
+  const long long cap = static_cast<long long>(bt_stride) * block_size;
+  a.kv_len_cap = cap > 0x7fffffff ? 0x7fffffff : static_cast<int>(cap);
+  a.budget = budget;
+  a.recent = num_recent;
+  a.kept = kept;
+  a.new_lens = new_lens;
+  a.status = dev_status;
+  return launch_evict(a, num_seqs, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? PA_OK
+             : PA_ERR_CUDA;
+}
+
 }  // extern "C"

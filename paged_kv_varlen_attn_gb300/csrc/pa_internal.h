@@ -230,4 +230,46 @@ struct RopeArgs {
 cudaError_t launch_rope_and_cache(RopeArgs a, int D, bool f16, bool fp8, cudaStream_t st,
                                   int sms);
 
+// Eviction (evict.cu). Rows of head_size elements are row_bytes long.
+struct EvictArgs {
+  uint8_t* kc;
+  uint8_t* vc;
+  int64_t block_stride_bytes;
+  float* weights;                 // page b, head h, row r at b * weights_stride + h * bs + r
+  int64_t weights_stride;
+  const int32_t* seqused_k;
+  const int32_t* bt;
+  int bt_stride;
+  int H_kv, bs, num_blocks, row_bytes;
+  int max_k, kv_len_cap;          // host bound; keys addressable through a block_table row
+  int budget, first, recent;
+  int32_t* kept;                  // [num_seqs, H_kv, budget]
+  int32_t* new_lens;              // [num_seqs]
+  int32_t* status;
+};
+cudaError_t launch_evict(const EvictArgs& a, int num_seqs, cudaStream_t st);
+
+// Accumulated attention weight of every cached key (weights.cu).
+struct WeightArgs {
+  const uint16_t* q;
+  int64_t q_stride;
+  const uint8_t* kc;
+  int64_t block_stride_bytes;
+  const float* lse;               // [H, total_q]
+  float* weights;
+  int64_t weights_stride;
+  const int32_t* cu;
+  const int32_t* seqused_k;
+  const int32_t* bt;
+  int bt_stride;
+  int H, H_kv, G, bs, num_blocks, total_q;
+  int max_q, max_k, kv_len_cap;
+  float scale_log2;               // softmax_scale * log2(e)
+  int causal;
+  const float* k_scale;           // e4m3 pools
+  int32_t* status;
+};
+cudaError_t launch_attn_weights(const WeightArgs& a, int num_seqs, int D, bool f16, bool fp8,
+                                cudaStream_t st);
+
 }  // namespace pa
