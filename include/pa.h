@@ -475,6 +475,28 @@ pa_status pa_cascade_fwd_ex(const pa_kv_update* update, const void* q, int64_t q
                             int dtype, int32_t* dev_status, void* stream);
 
 /*
+ * pa_window_fwd -- pa_varlen_fwd_ex (causal) with a sliding window and a few
+ * first tokens that stay visible: the query at position p (p = kv_len - q_len
+ * + i) sees key j <= p if j > p - window (the last `window` keys, its own
+ * among them) or j < num_first. window >= 1, num_first >= 0
+ * (PA_ERR_INVALID_ARG); a window of at least max_seqlen_k is plain causal
+ * attention. opts->sinks and opts->fp8 as there; workspace as for
+ * pa_varlen_fwd (pa_varlen_fwd_fp8kv with opts->fp8).
+ * Keys that no query of the call sees are not read in whole pages: their
+ * block_table entries may be stale (the pages freed), and what the pages hold
+ * does not matter, in partly visible pages either.
+ */
+pa_status pa_window_fwd(const pa_kv_update* update, const void* q, int64_t q_token_stride,
+                        void* key_cache, void* value_cache, int64_t cache_block_stride,
+                        const int32_t* cu_seqlens_q, const int32_t* seqused_k,
+                        const int32_t* block_table, int bt_stride, int num_seqs, int total_q,
+                        int max_seqlen_q, int max_seqlen_k, int num_heads, int num_kv_heads,
+                        int head_size, int block_size, int num_blocks, float softmax_scale,
+                        int window, int num_first, const pa_attn_opts* opts, void* out,
+                        float* lse, void* workspace, size_t workspace_bytes, int dtype,
+                        int32_t* dev_status, void* stream);
+
+/*
  * pa_rope_table -- the rotary cos/sin table of positions 0 .. table_len - 1.
  * Pair i of rot_dim / 2 turns by f_i = base^(-2i / rot_dim) radians per
  * position; row p holds mscale * cos(p f_i) for every i, then mscale *

@@ -56,6 +56,7 @@ EXPORTS = (
     "pa_merge_attn_states_n",
     "pa_varlen_fwd_ex",
     "pa_cascade_fwd_ex",
+    "pa_window_fwd",
     "pa_rope_table",
     "pa_rope_and_cache",
     "pa_attn_weights",
@@ -129,6 +130,8 @@ _SIGS = {
                          [ctypes.POINTER(AttnOpts)] + _ATTN_ARGS[20:], _i32),
     "pa_cascade_fwd_ex": ([ctypes.POINTER(KvUpdate)] + _ATTN_ARGS[:20] +
                           [ctypes.POINTER(AttnOpts)] + _ATTN_ARGS[20:], _i32),
+    "pa_window_fwd": ([ctypes.POINTER(KvUpdate)] + _ATTN_ARGS[:20] +
+                      [_i32, ctypes.POINTER(AttnOpts)] + _ATTN_ARGS[20:], _i32),
     "pa_rope_table": ([_vp, _i32, _i32, _f64, ctypes.POINTER(RopeScaling), _vp], _i32),
     "pa_rope_and_cache": ([ctypes.POINTER(Rope), _vp, _vp, _i64, _vp, _i64,
                            ctypes.POINTER(KvUpdate), _vp, _vp, _i64, _i32, _i32, _i32, _i32, _i32,
@@ -535,6 +538,66 @@ def cascade_fwd_fp8kv(q, key_cache, value_cache, cu_seqlens_q, seqused_k, block_
                   update_tensors=(key, value))
     del keep
     return res
+
+
+# ---------------------------------------------------------------------------
+# Sliding window with first tokens
+def window_fwd(q, key_cache, value_cache, cu_seqlens_q, seqused_k, block_table, max_seqlen_q,
+               max_seqlen_k, softmax_scale, window, num_first=0, sinks=None, k_scale=None,
+               v_scale=None, key=None, value=None, slot_mapping=None, out=None, lse=None,
+               return_lse=True, workspace=None, dev_status=None):
+    """Causal varlen attention in which a query sees its last window keys (its
+    own among them) and the first num_first keys of its sequence; optionally
+    the new tokens' K/V are first scattered into the caches (key, value,
+    slot_mapping). With k_scale and v_scale the caches hold e4m3 bytes.
+    Returns (out, lse or None)."""
+    lib = load_library()
+    _attn_common(q, key_cache, value_cache, cu_seqlens_q, seqused_k, block_table)
+    _need_cuda(sinks, out, lse, workspace, dev_status)
+    T, H, D = q.shape
+    nb, bs, hk, d = key_cache.shape
+    S = cu_seqlens_q.numel() - 1
+    if d != D or seqused_k.numel() != S or block_table.shape[0] != S:
+        raise ValueError("q and the caches must share the head size; seqused_k and block_table "
+                         "have one row per sequence of cu_seqlens_q")
+    if (k_scale is None) != (v_scale is None):
+        raise ValueError("k_scale and v_scale go together")
+    if out is None:
+        out = torch.empty((T, H, D), dtype=q.dtype, device=q.device)
+    if lse is None and return_lse:
+        lse = torch.empty((H, T), dtype=torch.float32, device=q.device)
+    if out.shape != (T, H, D) or not out.is_contiguous():
+        raise ValueError("out must be a contiguous [total_q, num_heads, head_size] tensor")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (H, T) or
+                            not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous float32 [num_heads, total_q] tensor")
+    _f32_vector(sinks, H, "sinks")
+    new = (key, value) if key is not None else ()
+    update = _kv_update(key, value, slot_mapping)
+    desc = keep = None
+    if k_scale is None:
+        dtype = _dtype_code(q, out, key_cache, value_cache, *new)
+    else:
+        _fp8_pool(key_cache), _fp8_pool(value_cache)
+        dtype = _dtype_code(q, out, *new)
+        desc, keep = _fp8_desc(k_scale, v_scale, hk, q.device)
+    if workspace is None:
+        size = varlen_fwd_workspace_size if desc is None else varlen_fwd_fp8kv_workspace_size
+        workspace = alloc_workspace(size(S, T, max_seqlen_q, max_seqlen_k, H, hk, D, bs,
+                                         _sm_count(q.device)), q.device)
+    opts = AttnOpts(None if sinks is None else sinks.data_ptr(),
+                    None if desc is None else ctypes.pointer(desc))
+    with torch.cuda.device(q.device):
+        code = lib.pa_window_fwd(
+            None if update is None else ctypes.byref(update), _ptr(q), _row_stride(q),
+            _ptr(key_cache), _ptr(value_cache), _cache_stride(key_cache), _ptr(cu_seqlens_q),
+            _ptr(seqused_k), _ptr(block_table), block_table.stride(0), S, T, int(max_seqlen_q),
+            int(max_seqlen_k), H, hk, D, bs, nb, float(softmax_scale), int(window),
+            int(num_first), ctypes.byref(opts), _ptr(out), _ptr(lse), _ptr(workspace),
+            workspace.numel(), dtype, _ptr(dev_status), _stream(q.device))
+    _check(code, "pa_window_fwd")
+    del keep
+    return out, lse
 
 
 # ---------------------------------------------------------------------------

@@ -129,15 +129,33 @@ __device__ __forceinline__ void zero_v_tail(uint8_t* vtile, int tile_key0, int s
   __syncwarp();
 }
 
+// Sliding window: the same for the V rows of the slice whose keys no query of
+// the item sees (keys [first, lo)).
+template <int KW, int HALVES, int HALF_BYTES>
+__device__ __forceinline__ void zero_v_hidden(uint8_t* vtile, int tile_key0, int slice0, int first,
+                                              int lo, int lane) {
+  const int from = max(first - tile_key0, slice0), to = min(lo - tile_key0, slice0 + KW);
+  if (from >= to) return;
+  for (int idx = lane; idx < (to - from) * HALVES * 8; idx += 32) {
+    const int rr = from + idx / (HALVES * 8);
+    const int rem = idx % (HALVES * 8);
+    *reinterpret_cast<uint4*>(vtile + (rem >> 3) * HALF_BYTES + rr * 128 + (rem & 7) * 16) =
+        make_uint4(0, 0, 0, 0);
+  }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncwarp();
+}
+
 // ---------------------------------------------------------------------------
 // Consumers. RGN = number of 16-row groups (1, 2 or 4); 4 / RGN warps share
 // each group and split every key tile between them.
 // ---------------------------------------------------------------------------
-template <int D, int RGN, bool FP8, bool F16>
+// WIN: kb and the tiles are numbered as in geo; ke is the last visible key + 1.
+template <int D, int RGN, bool FP8, bool F16, bool WIN>
 __device__ __forceinline__ void split_consumer(const AttnArgs& a, uint8_t* ring, SplitShared sh,
                                                int hk, int seg, int rt, int j, int q_start,
                                                int q_len, int kv_len, int kb, int ke, int ntiles,
-                                               int nsplit, int slot_base) {
+                                               int nsplit, int slot_base, const WinGeo& geo) {
   using C = SplitCfg<D, FP8>;
   using E = Elem<F16>;
   static_assert(!FP8 || D == 128, "FP8 pools: head size 128");
@@ -224,10 +242,12 @@ __device__ __forceinline__ void split_consumer(const AttnArgs& a, uint8_t* ring,
     consumed = t + 1;
     uint8_t* ktile = ring + s * C::STAGE_BYTES;
     uint8_t* vtile = ktile + C::TILE_BYTES;
-    const int tile_key0 = kb + t * C::BN;
+    const int tile_key0 = WIN ? geo.key(kb + t * C::BN) : kb + t * C::BN;
     const int key_base = tile_key0 + slice0;
     if (key_base < ke && key_base <= lim_max) {
       zero_v_tail<KW, C::HALVES, C::HALF_BYTES>(vtile, tile_key0, slice0, kv_len, lane);
+      if constexpr (WIN)
+        zero_v_hidden<KW, C::HALVES, C::HALF_BYTES>(vtile, tile_key0, slice0, a.first, geo.lo, lane);
 #pragma unroll
       for (int ch = 0; ch < NCH; ++ch) {
       const int cs = slice0 + ch * KWC;        // first key of the chunk in the tile
@@ -272,7 +292,8 @@ __device__ __forceinline__ void split_consumer(const AttnArgs& a, uint8_t* ring,
       // Mask, scale into the log2 domain, running max. A chunk inside every
       // valid row's visible range needs no mask.
       float mx[2] = {-INFINITY, -INFINITY};
-      if (ckey + KWC <= ke && ckey + KWC - 1 <= lim_min) {
+      if (ckey + KWC <= ke && ckey + KWC - 1 <= lim_min &&
+          (!WIN || ckey + KWC <= a.first || ckey > lim_max - a.window)) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -289,7 +310,8 @@ __device__ __forceinline__ void split_consumer(const AttnArgs& a, uint8_t* ring,
         for (int e = 0; e < 4; ++e) {
           const int key = ckey + n * 8 + 2 * cq + (e & 1);
           const int r = e >> 1;
-          const bool ok = key < ke && key <= lim[r];
+          bool ok = key < ke && key <= lim[r];
+          if constexpr (WIN) ok = ok && (key > lim[r] - a.window || key < a.first);
           const float v = ok ? sacc[n][e] * sl2 : -INFINITY;
           sacc[n][e] = v;
           mx[r] = fmaxf(mx[r], v);
@@ -549,12 +571,12 @@ __device__ __forceinline__ void split_consumer(const AttnArgs& a, uint8_t* ring,
 // The four warps take 16 keys each of every 64-key tile; their states are
 // merged through shared memory as in the other consumer.
 // ---------------------------------------------------------------------------
-template <bool F16>
+template <bool F16, bool WIN>
 __device__ __forceinline__ void split_consumer_fp8_dec(const AttnArgs& a, uint8_t* ring,
                                                        SplitShared sh, int hk, int rt, int j,
                                                        int q_start, int q_len, int kv_len, int kb,
                                                        int ke, int ntiles, int nsplit,
-                                                       int slot_base) {
+                                                       int slot_base, const WinGeo& geo) {
   using C = SplitCfg<128, true>;
   constexpr int D = 128;
   constexpr int KW = C::BN / 4;     // keys per warp per tile
@@ -670,10 +692,12 @@ __device__ __forceinline__ void split_consumer_fp8_dec(const AttnArgs& a, uint8_
     consumed = t + 1;
     const uint8_t* ktile = ring + s * C::STAGE_BYTES;
     uint8_t* vtile = ring + s * C::STAGE_BYTES + C::TILE_BYTES;
-    const int tile_key0 = kb + t * C::BN;
+    const int tile_key0 = WIN ? geo.key(kb + t * C::BN) : kb + t * C::BN;
     const int ckey = tile_key0 + slice0;
     if (ckey < ke && ckey <= lim_max) {
       zero_v_tail<KW, C::HALVES, C::HALF_BYTES>(vtile, tile_key0, slice0, kv_len, lane);
+      if constexpr (WIN)
+        zero_v_hidden<KW, C::HALVES, C::HALF_BYTES>(vtile, tile_key0, slice0, a.first, geo.lo, lane);
       // S^T for keys slice0 + g (rows of a0, a2) and slice0 + g + 8 (a1, a3).
       float st[4] = {0.f, 0.f, 0.f, 0.f};
       {
@@ -695,14 +719,16 @@ __device__ __forceinline__ void split_consumer_fp8_dec(const AttnArgs& a, uint8_
         }
       }
       // Mask (keys ckey + g and ckey + g + 8; rows 2c + (e & 1)), scale, max.
-      if (ckey + KW <= ke && ckey + KW - 1 <= lim_min) {
+      if (ckey + KW <= ke && ckey + KW - 1 <= lim_min &&
+          (!WIN || ckey + KW <= a.first || ckey > lim_max - a.window)) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) st[e] *= sl2r[e & 1];
       } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int key = ckey + g + (e >> 1) * 8;
-          const bool ok = key < ke && key <= lim[e & 1];
+          bool ok = key < ke && key <= lim[e & 1];
+          if constexpr (WIN) ok = ok && (key > lim[e & 1] - a.window || key < a.first);
           st[e] = ok ? st[e] * sl2r[e & 1] : -INFINITY;
         }
       }
@@ -893,7 +919,7 @@ __device__ __forceinline__ void split_consumer_fp8_dec(const AttnArgs& a, uint8_
   finish_group<D, F16>(a, sh, slot_base, rt, nsplit, hk, R, row0, q_start);
 }
 
-template <int D, bool FP8, bool F16>
+template <int D, bool FP8, bool F16, bool WIN>
 __global__ void __launch_bounds__(SplitCfg<D, FP8>::THREADS, SplitCfg<D, FP8>::CTAS_PER_SM)
 attn_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                   const __grid_constant__ AttnArgs a) {
@@ -923,11 +949,21 @@ attn_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
   const int R = min(kRowsSplit, q_len * G - row0);
   const int kb = j * chunk;
   int ke = min(kv_len, kb + chunk);
-  if (a.causal) {
+  int ntiles;
+  WinGeo geo{};
+  if constexpr (WIN) {
     const int i_last = (row0 + R - 1) / G;
-    ke = min(ke, kv_len - q_len + i_last + 1);
+    geo = win_geo(kv_len, q_len, row0 / G, i_last, a.window, a.first, C::BN);
+    ke = min(kv_len, kv_len - q_len + i_last + 1);
+    const int vke = min(geo.vend, kb + chunk);
+    ntiles = vke > kb ? (vke - kb + C::BN - 1) / C::BN : 0;
+  } else {
+    if (a.causal) {
+      const int i_last = (row0 + R - 1) / G;
+      ke = min(ke, kv_len - q_len + i_last + 1);
+    }
+    ntiles = ke > kb ? (ke - kb + C::BN - 1) / C::BN : 0;
   }
-  const int ntiles = ke > kb ? (ke - kb + C::BN - 1) / C::BN : 0;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
@@ -943,32 +979,32 @@ attn_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
   if (warp == 4) {
     if (ntiles > 0) {
       const int32_t* bt_row = a.bt + static_cast<int64_t>(seg) * a.bt_row_stride + a.bt_col_offset;
-      produce_kv<C::BN, C::HALVES, C::STAGES>(&tmK, &tmV, a, ring, sh.full, sh.empty,
-                                              &sh.flags[0], &sh.flags[2], bt_row, hk, kb, kv_len,
-                                              ntiles, threadIdx.x & 31);
+      produce_kv<C::BN, C::HALVES, C::STAGES, false, WIN>(
+          &tmK, &tmV, a, ring, sh.full, sh.empty, &sh.flags[0], &sh.flags[2], bt_row, hk, kb,
+          kv_len, ntiles, threadIdx.x & 31, 0, geo);
     }
     return;
   }
   if constexpr (FP8) {
     if (R <= 8) {
-      split_consumer_fp8_dec<F16>(a, ring, sh, hk, rt, j, q_start, q_len, kv_len, kb, ke, ntiles,
-                             nsplit, slot_base);
+      split_consumer_fp8_dec<F16, WIN>(a, ring, sh, hk, rt, j, q_start, q_len, kv_len, kb, ke,
+                                       ntiles, nsplit, slot_base, geo);
       return;
     }
   }
   if (R <= 16)
-    split_consumer<D, 1, FP8, F16>(a, ring, sh, hk, seg, rt, j, q_start, q_len, kv_len, kb, ke,
-                              ntiles, nsplit, slot_base);
+    split_consumer<D, 1, FP8, F16, WIN>(a, ring, sh, hk, seg, rt, j, q_start, q_len, kv_len, kb,
+                                          ke, ntiles, nsplit, slot_base, geo);
   else if (R <= 32)
-    split_consumer<D, 2, FP8, F16>(a, ring, sh, hk, seg, rt, j, q_start, q_len, kv_len, kb, ke,
-                              ntiles, nsplit, slot_base);
+    split_consumer<D, 2, FP8, F16, WIN>(a, ring, sh, hk, seg, rt, j, q_start, q_len, kv_len, kb,
+                                          ke, ntiles, nsplit, slot_base, geo);
   else
-    split_consumer<D, 4, FP8, F16>(a, ring, sh, hk, seg, rt, j, q_start, q_len, kv_len, kb, ke,
-                              ntiles, nsplit, slot_base);
+    split_consumer<D, 4, FP8, F16, WIN>(a, ring, sh, hk, seg, rt, j, q_start, q_len, kv_len, kb,
+                                          ke, ntiles, nsplit, slot_base, geo);
 }
 
-template <int D, bool FP8, bool F16>
-static cudaError_t launch_split_d(const CUtensorMap& tmK, const CUtensorMap& tmV,
+template <int D, bool FP8, bool F16, bool WIN>
+static cudaError_t launch_split_w(const CUtensorMap& tmK, const CUtensorMap& tmV,
                                   const AttnArgs& a, int items_bound, cudaStream_t st) {
   using C = SplitCfg<D, FP8>;
   // The shared-memory opt-in is a per-device function attribute: set it on
@@ -981,7 +1017,7 @@ static cudaError_t launch_split_d(const CUtensorMap& tmK, const CUtensorMap& tmV
   if (e != cudaSuccess) return e;
   const bool known = dev >= 0 && dev < kMaxDevices;
   if (!known || !configured[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(attn_split_kernel<D, FP8, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(attn_split_kernel<D, FP8, F16, WIN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              C::SMEM_BYTES);
     if (e != cudaSuccess) return e;
     if (known) configured[dev].store(true, std::memory_order_release);
@@ -998,9 +1034,16 @@ static cudaError_t launch_split_d(const CUtensorMap& tmK, const CUtensorMap& tmV
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, attn_split_kernel<D, FP8, F16>, tmK, tmV, a);
+  e = cudaLaunchKernelEx(&cfg, attn_split_kernel<D, FP8, F16, WIN>, tmK, tmV, a);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
+}
+
+template <int D, bool FP8, bool F16>
+static cudaError_t launch_split_d(const CUtensorMap& tmK, const CUtensorMap& tmV,
+                                  const AttnArgs& a, int items_bound, cudaStream_t st) {
+  return a.window > 0 ? launch_split_w<D, FP8, F16, true>(tmK, tmV, a, items_bound, st)
+                      : launch_split_w<D, FP8, F16, false>(tmK, tmV, a, items_bound, st);
 }
 
 cudaError_t launch_attn_split(const CUtensorMap& tmK, const CUtensorMap& tmV, const AttnArgs& a,

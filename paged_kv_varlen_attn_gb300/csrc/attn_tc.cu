@@ -138,9 +138,11 @@ struct TcBars {
 // they all see the zeros. V(t) has its own barrier and may land after S(t):
 // wait for it first, so the copy cannot overwrite the zeros. False on
 // timeout.
-template <int D>
+// Sliding window (WIN): likewise the rows of keys [first, lo), which no query
+// of the item sees.
+template <int D, bool WIN>
 __device__ __forceinline__ bool zero_v_tail(TcBars* bars, uint8_t* smem, int t, int key0,
-                                            int kv_len, int tid) {
+                                            int kv_len, int tid, int first_key, int lo) {
   using C = TcCfg<D>;
   if (!mbar_wait(&bars->kv_full[C::STAGES + t % C::STAGES], (t / C::STAGES) & 1)) return false;
   const int first = max(0, kv_len - key0);
@@ -152,6 +154,15 @@ __device__ __forceinline__ bool zero_v_tail(TcBars* bars, uint8_t* smem, int t, 
     *reinterpret_cast<uint4*>(vt + (rem >> 3) * C::KV_HALF + rr * 128 + (rem & 7) * 16) =
         make_uint4(0, 0, 0, 0);
   }
+  if constexpr (WIN) {
+    const int from = max(0, first_key - key0), to = min(C::BN, lo - key0);
+    for (int idx = tid; idx < (to - from) * C::HALVES * 8; idx += 128) {
+      const int rr = from + idx / (C::HALVES * 8);
+      const int rem = idx % (C::HALVES * 8);
+      *reinterpret_cast<uint4*>(vt + (rem >> 3) * C::KV_HALF + rr * 128 + (rem & 7) * 16) =
+          make_uint4(0, 0, 0, 0);
+    }
+  }
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   return true;
 }
@@ -162,8 +173,10 @@ __device__ __forceinline__ bool zero_v_tail(TcBars* bars, uint8_t* smem, int t, 
 // of row r at r*128 + ((c ^ r%8) << 4)). Every e4m3 value is exact in f16.
 // Rows from zero_from on are written as zeros (keys past the sequence end:
 // their bytes are arbitrary and P = 0 there must not meet a NaN).
+// WIN: rows [hide_from, hide_to) -- keys that no query of the item sees -- too.
+template <bool WIN>
 __device__ __forceinline__ void widen_e4m3_tile(const uint8_t* src, uint8_t* dst, int ct,
-                                                int zero_from) {
+                                                int zero_from, int hide_from, int hide_to) {
   using C = TcCfg<128>;
   static_assert(TcFp8::CONV_THREADS % 8 == 0, "a thread keeps one chunk column");
   // Thread ct takes chunk column jj = ct % 8 of rows ct / 8, ct / 8 + 8, ...;
@@ -179,7 +192,7 @@ __device__ __forceinline__ void widen_e4m3_tile(const uint8_t* src, uint8_t* dst
 #pragma unroll 4
   for (int r = r0; r < C::BN; r += kStep, sp += kStep * 128, dp += kStep * 128) {
     uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-    if (r < zero_from) {
+    if (r < zero_from && (!WIN || r < hide_from || r >= hide_to)) {
       const uint4 w = *reinterpret_cast<const uint4*>(sp);
       lo = make_uint4(e4m3x2_to_f16x2(w.x), e4m3x2_to_f16x2(w.x >> 16), e4m3x2_to_f16x2(w.y),
                       e4m3x2_to_f16x2(w.y >> 16));
@@ -264,12 +277,12 @@ __device__ __forceinline__ void q_split_e4m3(uint8_t* q, float* rs, int tiles, i
   }
 }
 
-template <int D, bool F16, bool FP8>
+template <int D, bool F16, bool FP8, bool WIN>
 __device__ __forceinline__ void tc_softmax_tile(const AttnArgs& a, TcBars* bars, uint8_t* smem,
                                                 uint32_t tmem, int X, int q_start, int q_len,
                                                 int kv_len, int kb, int ke, int ntiles, int row0,
                                                 int R, int hk, int nsplit, int slot_base, int rt,
-                                                int j) {
+                                                int j, const WinGeo& geo) {
   using C = TcCfg<D>;
   using E = Elem<F16>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -304,7 +317,7 @@ __device__ __forceinline__ void tc_softmax_tile(const AttnArgs& a, TcBars* bars,
   for (int t = 0; ok && t < ntiles; ++t) {
     if (!mbar_wait(&bars->s_full[X], t & 1)) { ok = false; break; }
     tc_fence_after();
-    const int key0 = kb + t * C::BN;
+    const int key0 = WIN ? geo.key(kb + t * C::BN) : kb + t * C::BN;
     const int vis_end = min(ke, lim + 1);   // keys [key0, vis_end) are visible
     const bool edge = key0 + C::BN > vis_end;
     uint32_t xs_u[C::BN];
@@ -317,6 +330,15 @@ __device__ __forceinline__ void tc_softmax_tile(const AttnArgs& a, TcBars* bars,
 #pragma unroll
       for (int e = 0; e < C::BN; ++e)
         if (key0 + e >= vis_end) xs[e] = -INFINITY;
+    }
+    if constexpr (WIN) {
+      // Keys [first, lim - window] are behind this row's window.
+      const int hide_from = a.first - key0, hide_to = lim - a.window - key0;
+      if (hide_from < C::BN && hide_to >= 0) {
+#pragma unroll
+        for (int e = 0; e < C::BN; ++e)
+          if (e >= hide_from && e <= hide_to) xs[e] = -INFINITY;
+      }
     }
     // Row max: eight independent chains of three-input maxima over the
     // values j, j+8, j+16, ... of the tile.
@@ -380,8 +402,11 @@ __device__ __forceinline__ void tc_softmax_tile(const AttnArgs& a, TcBars* bars,
       tmem_st16(tm_row + s_col + c * 16, pk);
       if (c == C::BN / 64 - 1) {   // the first half of the tile's keys
         tmem_wait_st();
-        if (!FP8 && X == 0 && key0 + C::BN > kv_len)   // warp-uniform condition and result
-          ok = __all_sync(0xffffffffu, zero_v_tail<D>(bars, smem, t, key0, kv_len, tid));
+        // warp-uniform condition and result
+        if (!FP8 && X == 0 &&
+            (key0 + C::BN > kv_len || (WIN && key0 < geo.lo && key0 + C::BN > a.first)))
+          ok = __all_sync(0xffffffffu, zero_v_tail<D, WIN>(bars, smem, t, key0, kv_len, tid,
+                                                           a.first, geo.lo));
         if (!ok) break;
         tc_fence_before();
         mbar_arrive(&bars->p_full[0][X]);
@@ -486,7 +511,7 @@ __device__ __forceinline__ void tc_softmax_tile(const AttnArgs& a, TcBars* bars,
   }
 }
 
-template <int D, bool F16, bool FP8>
+template <int D, bool F16, bool FP8, bool WIN>
 __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
 attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ AttnArgs a) {
@@ -513,8 +538,18 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
   const bool two = R > TR;   // tile B has rows
   const int kb = j * chunk;
   int ke = min(kv_len, kb + chunk);
-  if (a.causal) ke = min(ke, kv_len - q_len + (row0 + R - 1) / G + 1);
-  const int ntiles = ke > kb ? (ke - kb + C::BN - 1) / C::BN : 0;
+  int ntiles;
+  WinGeo geo{};
+  if constexpr (WIN) {
+    const int i_last = (row0 + R - 1) / G;
+    geo = win_geo(kv_len, q_len, row0 / G, i_last, a.window, a.first, C::BN);
+    ke = min(kv_len, kv_len - q_len + i_last + 1);
+    const int vke = min(geo.vend, kb + chunk);
+    ntiles = vke > kb ? (vke - kb + C::BN - 1) / C::BN : 0;
+  } else {
+    if (a.causal) ke = min(ke, kv_len - q_len + (row0 + R - 1) / G + 1);
+    ntiles = ke > kb ? (ke - kb + C::BN - 1) / C::BN : 0;
+  }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -586,15 +621,13 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
           a.bt + static_cast<int64_t>(seg) * a.bt_row_stride + a.bt_col_offset;
       if constexpr (FP8) {
         static_assert(2 * TcFp8::STAGES8 <= 8, "the ring barrier arrays hold 8");
-        produce_kv<C::BN, 1, TcFp8::STAGES8, true>(&tmK, &tmV, a, smem + TcFp8::OFF_R8,
-                                                   bars->kv_full, bars->kv_empty, &bars->abort,
-                                                   bars->issued, bt_row, hk, kb, kv_len, ntiles,
-                                                   lane);
+        produce_kv<C::BN, 1, TcFp8::STAGES8, true, WIN>(
+            &tmK, &tmV, a, smem + TcFp8::OFF_R8, bars->kv_full, bars->kv_empty, &bars->abort,
+            bars->issued, bt_row, hk, kb, kv_len, ntiles, lane, 0, geo);
       } else {
-        produce_kv<C::BN, C::HALVES, C::STAGES, true>(&tmK, &tmV, a, smem + C::OFF_KV,
-                                                      bars->kv_full, bars->kv_empty, &bars->abort,
-                                                      bars->issued, bt_row, hk, kb, kv_len,
-                                                      ntiles, lane);
+        produce_kv<C::BN, C::HALVES, C::STAGES, true, WIN>(
+            &tmK, &tmV, a, smem + C::OFF_KV, bars->kv_full, bars->kv_empty, &bars->abort,
+            bars->issued, bt_row, hk, kb, kv_len, ntiles, lane, 0, geo);
       }
     }
   } else if (warp == 1) {
@@ -795,8 +828,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
       if (!(ok = mbar_wait(&bars->kv_full[S8 + t % S8], (t / S8) & 1))) break;
       if (ct == 0) bars->consumed[1] = t + 1;
       if (t >= VB && !(ok = mbar_wait(&bars->vw_free[t % VB], ((t / VB) - 1) & 1))) break;
-      widen_e4m3_tile(v8, smem + TcFp8::OFF_VW + (t % VB) * C::KV_TILE, ct,
-                      kv_len - (kb + t * C::BN));
+      const int key0 = WIN ? geo.key(kb + t * C::BN) : kb + t * C::BN;
+      widen_e4m3_tile<WIN>(v8, smem + TcFp8::OFF_VW + (t % VB) * C::KV_TILE, ct, kv_len - key0,
+                           a.first - key0, geo.lo - key0);
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       mbar_arrive(&bars->vw_full[t % VB]);
       mbar_arrive(&bars->kv_empty[S8 + t % S8]);
@@ -811,8 +845,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     // ------------------------------------------------------------ softmax
     const int X = (warp - 4) >> 2;   // warps 4-7: tile A, 8-11: tile B
     if (X == 0 || two)
-      tc_softmax_tile<D, F16, FP8>(a, bars, smem, tmem, X, q_start, q_len, kv_len, kb, ke, ntiles, row0,
-                         R, hk, nsplit, slot_base, rt, j);
+      tc_softmax_tile<D, F16, FP8, WIN>(a, bars, smem, tmem, X, q_start, q_len, kv_len, kb, ke,
+                                        ntiles, row0, R, hk, nsplit, slot_base, rt, j, geo);
     if (nsplit > 1 && !a.partials_only) {
       // Both warpgroups (256 threads) take part, active tile or not.
       __threadfence();
@@ -849,8 +883,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
   }
 }
 
-template <int D, bool F16, bool FP8 = false>
-static cudaError_t launch_tc_d(const CUtensorMap& tmK, const CUtensorMap& tmV,
+template <int D, bool F16, bool FP8, bool WIN>
+static cudaError_t launch_tc_w(const CUtensorMap& tmK, const CUtensorMap& tmV,
                                const CUtensorMap& tmQ, const AttnArgs& a, int items_bound,
                                cudaStream_t st) {
   using C = TcCfg<D>;
@@ -864,7 +898,7 @@ static cudaError_t launch_tc_d(const CUtensorMap& tmK, const CUtensorMap& tmV,
   if (e != cudaSuccess) return e;
   const bool known = dev >= 0 && dev < kMaxDevices;
   if (!known || !configured[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(attn_tc_kernel<D, F16, FP8>,
+    e = cudaFuncSetAttribute(attn_tc_kernel<D, F16, FP8, WIN>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                              FP8 ? TcFp8::SMEM_BYTES : C::SMEM_BYTES);
     if (e != cudaSuccess) return e;
@@ -882,9 +916,17 @@ static cudaError_t launch_tc_d(const CUtensorMap& tmK, const CUtensorMap& tmV,
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, attn_tc_kernel<D, F16, FP8>, tmK, tmV, tmQ, a);
+  e = cudaLaunchKernelEx(&cfg, attn_tc_kernel<D, F16, FP8, WIN>, tmK, tmV, tmQ, a);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
+}
+
+template <int D, bool F16, bool FP8 = false>
+static cudaError_t launch_tc_d(const CUtensorMap& tmK, const CUtensorMap& tmV,
+                               const CUtensorMap& tmQ, const AttnArgs& a, int items_bound,
+                               cudaStream_t st) {
+  return a.window > 0 ? launch_tc_w<D, F16, FP8, true>(tmK, tmV, tmQ, a, items_bound, st)
+                      : launch_tc_w<D, F16, FP8, false>(tmK, tmV, tmQ, a, items_bound, st);
 }
 
 cudaError_t launch_attn_tc(const CUtensorMap& tmK, const CUtensorMap& tmV, const CUtensorMap& tmQ,

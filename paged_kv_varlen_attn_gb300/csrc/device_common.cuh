@@ -239,6 +239,33 @@ __device__ __forceinline__ void fadd2(float& d0, float& d1, float a0, float a1, 
       : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
 }
 
+// The keys a row tile reads under a sliding window with first tokens. Queries
+// i0 .. i1 of a sequence (positions kv_len - q_len + i) see keys [0, first) and,
+// each, the last `window` keys up to its own; no query of the tile sees a key
+// of [first, lo). The tile's key tiles (align keys each) are numbered without
+// the ones between the two parts: virtual key v is key v below fe (`first`
+// rounded up to whole tiles) and key v + gap from there on, up to vend. Where
+// the parts meet or overlap, gap = 0 and the numbering is the plain one.
+struct WinGeo {
+  int fe, gap, vend, lo;
+  __device__ __forceinline__ int key(int v) const { return v < fe ? v : v + gap; }
+  // Whether some query of the tile may see a key of [k, k + n).
+  __device__ __forceinline__ bool wanted(int k, int n, int first) const {
+    return k < first || k + n > lo;
+  }
+};
+__device__ __forceinline__ WinGeo win_geo(int kv_len, int q_len, int i0, int i1, int window,
+                                          int first, int align) {
+  WinGeo w;
+  const int ke = max(0, min(kv_len, kv_len - q_len + i1 + 1));
+  const long long lo = static_cast<long long>(kv_len) - q_len + i0 - window + 1;
+  w.lo = lo > 0 ? static_cast<int>(lo) : 0;
+  w.fe = (min(first, ke) + align - 1) / align * align;
+  w.gap = max(0, w.lo / align * align - w.fe);
+  w.vend = max(0, ke - w.gap);
+  return w;
+}
+
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kLog2e = 1.442695040888963407f;
 
@@ -453,13 +480,15 @@ __device__ __forceinline__ void abort_call(const AttnArgs& a) {
 // barriers -- full/empty[s] for K, full/empty[STAGES + s] for V -- so a
 // consumer that is done with K(t) before V(t) can release it early, and
 // issued[0] / issued[1] count the issued K / V tiles.
+// WIN = true: kb and the tiles are in the virtual numbering of geo, and a box
+// that no query of the row tile sees reads as zeros, its page id unread.
 // Returns false on timeout/abort.
-template <int BN, int HALVES, int STAGES, bool SEP = false>
+template <int BN, int HALVES, int STAGES, bool SEP = false, bool WIN = false>
 __device__ bool produce_kv(const CUtensorMap* tmK, const CUtensorMap* tmV, const AttnArgs& a,
                            uint8_t* ring, uint64_t* full, uint64_t* empty,
                            volatile int* cta_abort, volatile int* issued,
                            const int32_t* bt_row, int hk, int kb, int kv_len, int ntiles,
-                           int lane, int t0 = 0) {
+                           int lane, int t0 = 0, WinGeo geo = WinGeo{}) {
   constexpr int HALF = BN * 128;
   constexpr int TILE = HALVES * HALF;
   constexpr int STAGE = 2 * TILE;
@@ -469,10 +498,15 @@ __device__ bool produce_kv(const CUtensorMap* tmK, const CUtensorMap* tmV, const
   const int ngroups = (ntiles + tpg - 1) / tpg;
   // Lane i holds the page id and page row of box i of a group.
   auto load_page = [&](int g, int& prow) -> int {
-    const int k = kb + g * tpg * BN + lane * box_rows;
+    int k = kb + g * tpg * BN + lane * box_rows;
+    bool read = true;
+    if constexpr (WIN) {
+      k = geo.key(k);
+      read = geo.wanted(k, box_rows, a.first);
+    }
     int page = a.num_blocks;
     prow = 0;
-    if (k < kv_len) {
+    if (k < kv_len && read) {
       const int lp = k / a.bs;
       prow = k - lp * a.bs;
       const int pg = __ldg(bt_row + lp);

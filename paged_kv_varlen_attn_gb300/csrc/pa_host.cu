@@ -554,7 +554,8 @@ static pa_status varlen_impl(const pa_kv_update* upd, const void* q, int64_t q_t
                              int head_size, int block_size, int num_blocks, float softmax_scale,
                              int causal, void* out, float* lse, void* workspace,
                              size_t workspace_bytes, int dtype, int32_t* dev_status,
-                             void* stream, const KvFormat& kv, const float* sinks = nullptr) {
+                             void* stream, const KvFormat& kv, const float* sinks = nullptr,
+                             int window = 0, int num_first = 0) {
   pa_status st = check_shape(num_seqs, total_q, max_seqlen_q, max_seqlen_k, num_heads,
                              num_kv_heads, head_size, block_size, dtype);
   if (st != PA_OK) return st;
@@ -587,6 +588,15 @@ static pa_status varlen_impl(const pa_kv_update* upd, const void* q, int64_t q_t
   d.max_kv = max_seqlen_k;
   d.kv_fp8 = kv.fp8;
   d.tc_allowed = softmax_scale > 0.f;
+  if (window > 0) {
+    // A window of at least every sequence is no window; else a row tile reads
+    // at most the first tokens, the window and its own tokens, in whole tiles.
+    if (window >= max_seqlen_k) window = num_first = 0;
+    if (num_first > max_seqlen_k) num_first = max_seqlen_k;
+    const long long reach = static_cast<long long>(cdiv(num_first, 128)) * 128 + window +
+                            2 * kTcTileRows + 2 + 128;
+    if (window > 0 && reach < d.max_kv) d.max_kv = static_cast<int>(reach);
+  }
   const PassLayout L = layout_pass(d, 0);
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) % kAlign) != 0 ||
       workspace_bytes < L.end)
@@ -608,10 +618,14 @@ static pa_status varlen_impl(const pa_kv_update* upd, const void* q, int64_t q_t
   PlanPasses pp{};
   pp.p[0] = make_plan(c, ws, L, 0, 0, 0, cap > 0x7fffffff ? 0x7fffffff : static_cast<int>(cap),
                       causal, 0);
+  pp.p[0].window = window;
+  pp.p[0].first = num_first;
   if (launch_plan(pp, 1, c.st) != cudaSuccess) return PA_ERR_CUDA;
   st = launch_kv_update(upd, c, key_cache, value_cache, sms);
   if (st != PA_OK) return st;
   AttnArgs a = make_attn(c, ws, L, bt_stride, 0, causal, out, lse);
+  a.window = window;
+  a.first = num_first;
   bool first = true;
   return launch_pass(c, tmK, tmV, tmQ, a, ws, L, &first);
 }
@@ -1001,6 +1015,25 @@ pa_status pa_cascade_fwd_ex(const pa_kv_update* update, const void* q, int64_t q
                       opts ? opts->sinks : nullptr);
 }
 
+// ---------------------------------------------------------------- sliding window
+pa_status pa_window_fwd(const pa_kv_update* update, const void* q, int64_t q_token_stride,
+                        void* key_cache, void* value_cache, int64_t cache_block_stride,
+                        const int32_t* cu_seqlens_q, const int32_t* seqused_k,
+                        const int32_t* block_table, int bt_stride, int num_seqs, int total_q,
+                        int max_seqlen_q, int max_seqlen_k, int num_heads, int num_kv_heads,
+                        int head_size, int block_size, int num_blocks, float softmax_scale,
+                        int window, int num_first, const pa_attn_opts* opts, void* out,
+                        float* lse, void* workspace, size_t workspace_bytes, int dtype,
+                        int32_t* dev_status, void* stream) {
+  if (window < 1 || num_first < 0) return PA_ERR_INVALID_ARG;
+  const KvFormat kv = opts && opts->fp8 ? fp8_format(opts->fp8) : kKvBf16;
+  return varlen_impl(update, q, q_token_stride, key_cache, value_cache, cache_block_stride,
+                     cu_seqlens_q, seqused_k, block_table, bt_stride, num_seqs, total_q,
+                     max_seqlen_q, max_seqlen_k, num_heads, num_kv_heads, head_size, block_size,
+                     num_blocks, softmax_scale, 1, out, lse, workspace, workspace_bytes, dtype,
+                     dev_status, stream, kv, opts ? opts->sinks : nullptr, window, num_first);
+}
+
 // ---------------------------------------------------------------- rotary positions
 pa_status pa_rope_table(float* cos_sin, int table_len, int rot_dim, double base,
                         const pa_rope_scaling* scaling, void* stream) {
@@ -1242,6 +1275,7 @@ pa_status pa_evict(void* key_cache, void* value_cache, int64_t cache_block_strid
   const long long cap = static_cast<long long>(bt_stride) * block_size;
   a.kv_len_cap = cap > 0x7fffffff ? 0x7fffffff : static_cast<int>(cap);
   a.budget = budget;
+  a.first = num_first;
   a.recent = num_recent;
   a.kept = kept;
   a.new_lens = new_lens;

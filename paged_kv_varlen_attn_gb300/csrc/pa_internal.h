@@ -90,6 +90,7 @@ struct PlanArgs {
   int check_cascade;     // flag q_len > kv_len (suffix pass of cascade)
   int partials_only;     // every item gets a partial-state slot and a zeroed counter (cascade)
   int make_groups;       // list the (segment, row tile) groups of each class (cascade suffix)
+  int window, first;     // sliding window (0: none) and first tokens (see WinGeo)
 };
 
 struct PlanPasses {
@@ -144,6 +145,9 @@ struct AttnArgs {
   // softmax_scale * q.k), an extra key with value zero; NULL for none. Added
   // once per row, where the final output is written.
   const float* sinks;
+  // Sliding window: a query at position p sees key j <= p if j > p - window or
+  // j < first. window = 0: none (the kernels' plain instantiations).
+  int window, first;
   // Launch order inside one call. The kernels after the planner are launched
   // as programmatic dependents of the kernel before them, so a grid can start
   // while its predecessor drains. pdl_first = 1 for the first kernel after the
@@ -179,6 +183,7 @@ cudaError_t launch_merge(void* out, float* out_lse, const void* a, const float* 
 cudaError_t launch_merge_n(void* out, float* out_lse, const void* parts, int64_t part_stride,
                            const float* parts_lse, int64_t lse_stride, int n, int T, int H, int D,
                            cudaStream_t st, int sms, int f16);
+// Every pass of a call has a window, or none has.
 cudaError_t launch_plan(const PlanPasses& passes, int npasses, cudaStream_t st);
 cudaError_t launch_attn_split(const CUtensorMap& tmK, const CUtensorMap& tmV, const AttnArgs& a,
                               int items_bound, cudaStream_t st);

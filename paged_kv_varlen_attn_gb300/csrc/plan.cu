@@ -70,17 +70,34 @@ constexpr int kPlanThreads = 256;
 constexpr int kSizeBuckets = 1024;
 constexpr int kPlanSmemSegs = 1024;   // segment tables kept in shared memory up to this many
 
+// Sliding window: the keys of one tile of the kernel a class runs on, and a
+// bound on the (virtual, see WinGeo) keys of any row tile of a segment: the
+// first tokens and the window of the tile's first query rounded out to whole
+// tiles, and one key more per further query of the tile.
+__device__ __forceinline__ int win_align(int cls, int D) { return cls && D <= 128 ? 128 : kKeyTile; }
+__device__ __forceinline__ int win_keys(int4 g, int rows_per_item, const PlanArgs& P) {
+  const int align = win_align(g.w, P.D);
+  const long long tokens = min(g.y, rows_per_item / P.G + 2);
+  const long long n = static_cast<long long>((min(P.first, g.z) + align - 1) / align) * align +
+                      P.window + tokens + align;
+  return n < g.z ? static_cast<int>(n) : g.z;
+}
+
 // Size bucket of work item (segment s, row tile rt, split j): the number of
 // 64-key tiles the attention kernel will process for it (capped).
+template <bool WIN>
 __device__ __forceinline__ int item_bucket(int s, int rt, int j, int4 g, int chunk, int G, int D,
-                                           int causal) {
+                                           int causal, const PlanArgs& P) {
   const int cls = g.w, q_len = g.y, kv = g.z;
   const int R = cls ? tc_item_rows(G, D) : kRowsSplit;
   const int rows = q_len * G;
   const int last_row = min(rows, (rt + 1) * R) - 1;
   const int kb = j * chunk;
   int ke = min(kv, kb + chunk);
-  if (causal) ke = min(ke, kv - q_len + last_row / G + 1);
+  if constexpr (WIN)
+    ke = min(win_geo(kv, q_len, rt * R / G, last_row / G, P.window, P.first, win_align(cls, D)).vend,
+             kb + chunk);
+  else if (causal) ke = min(ke, kv - q_len + last_row / G + 1);
   const int tiles = ke > kb ? (ke - kb + kKeyTile - 1) / kKeyTile : 0;
   return min(tiles, kSizeBuckets - 1);
 }
@@ -96,6 +113,7 @@ __device__ __forceinline__ int find_segment(const int4* spl, int nseg, int idx) 
   return lo;
 }
 
+template <bool WIN>
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ PlanPasses pp) {
   // The first attention kernel may be scheduled now; its blocks wait for
   // this grid to complete before they read the plan.
@@ -181,9 +199,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     const int cls = (P.tc_enabled && rows > P.tc_min_rows) ? 1 : 0;
     const int rpi = cls ? tc_item_rows(G, P.D) : kRowsSplit;
     const int nrt = (rows + rpi - 1) / rpi;
-    const unsigned long long w = static_cast<unsigned long long>(nrt) * static_cast<unsigned>(kv);
-    if (cls) w1 += w; else w0 += w;
     const int4 g = make_int4(q_start, q_len, kv, cls);
+    const int work_keys = WIN ? win_keys(g, rpi, P) : kv;
+    const unsigned long long w =
+        static_cast<unsigned long long>(nrt) * static_cast<unsigned>(work_keys);
+    if (cls) w1 += w; else w0 += w;
     seg[s] = g;
     if (in_smem) tab_geo[s] = g;
   }
@@ -211,7 +231,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     else L = (W + tg - 1) / tg;
     const int min_chunk = c ? P.min_chunk_tc : kMinChunkSplit;
     if (L < static_cast<unsigned long long>(min_chunk)) L = min_chunk;
-    L = (L + kKeyTile - 1) / kKeyTile * kKeyTile;
+    const int round_to = WIN ? win_align(c, P.D) : kKeyTile;   // whole key tiles
+    L = (L + round_to - 1) / round_to * round_to;
     if (L > 0x40000000ull) L = 0x40000000ull;
     chunk_max[c] = static_cast<int>(L);
   }
@@ -229,16 +250,17 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
       cls = g.w;
       const int R = cls ? tc_item_rows(G, P.D) : kRowsSplit;
       const int nrt = (g.y * G + R - 1) / R;
-      const int kv = g.z;
+      const int kv = WIN ? win_keys(g, R, P) : g.z;
       const int L = cls ? chunk_max[1] : chunk_max[0];
+      const int round_to = WIN ? win_align(cls, P.D) : kKeyTile;
       if (kv > 0) {
         nsplit = (kv + L - 1) / L;
         chunk = (kv + nsplit - 1) / nsplit;
-        chunk = (chunk + kKeyTile - 1) / kKeyTile * kKeyTile;
+        chunk = (chunk + round_to - 1) / round_to * round_to;
         nsplit = (kv + chunk - 1) / chunk;
       } else {
         nsplit = 1;
-        chunk = kKeyTile;
+        chunk = round_to;
       }
       const int n_items = nrt * nsplit;
       const int n_slots = (nsplit > 1 || P.partials_only) ? n_items : 0;
@@ -270,7 +292,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     const int4 g = geo_tab[s];
     const int local = idx - sp.w;
     const int rt = local / sp.x, j = local - rt * sp.x;
-    atomicAdd(&hist[g.w][item_bucket(s, rt, j, g, sp.z, G, P.D, P.causal)], 1);
+    atomicAdd(&hist[g.w][item_bucket<WIN>(s, rt, j, g, sp.z, G, P.D, P.causal, P)], 1);
     if (j == 0 && (sp.x > 1 || P.partials_only)) {
       const int grp = sp.y + rt * sp.x;
       const int sbound = g.w ? P.slots_bound1 : P.slots_bound0;
@@ -321,7 +343,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     const int local = idx - sp.w;
     const int rt = local / sp.x, j = local - rt * sp.x;
     const int cls = g.w;
-    const int pos = atomicAdd(&hist[cls][item_bucket(s, rt, j, g, sp.z, G, P.D, P.causal)], 1);
+    const int pos = atomicAdd(&hist[cls][item_bucket<WIN>(s, rt, j, g, sp.z, G, P.D, P.causal, P)], 1);
     if (pos < (cls ? P.items_bound1 : P.items_bound0))
       (cls ? items1 : items0)[pos] = make_int4(s, rt, j, 0);
   }
@@ -346,7 +368,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
 }
 
 cudaError_t launch_plan(const PlanPasses& pp, int npasses, cudaStream_t st) {
-  plan_kernel<<<npasses, kPlanThreads, 0, st>>>(pp);
+  if (pp.p[0].window > 0)
+    plan_kernel<true><<<npasses, kPlanThreads, 0, st>>>(pp);
+  else
+    plan_kernel<false><<<npasses, kPlanThreads, 0, st>>>(pp);
   return cudaGetLastError();
 }
 

@@ -1,0 +1,253 @@
+"""GPU parity of sliding-window attention with first tokens against the fp64
+definition, on every kernel path: the split-KV kernel (one split and several,
+2-byte pools and both FP8 consumers), the tensor-core prefill kernel at every
+head size (one split and several), with sinks and with an in-call update.
+
+Tolerance of an output element, from arithmetic: with p_j the softmax weights,
+each P entry is rounded to the MMA's operand type (half a step of it, relative
+to the entry) and the result to the output type, so the element is off by at
+most half a step times (|out| + sum_j p_j |v_j|), the float32 steps adding a
+few 2^-24 of the same sums and the scores' own error (1e-4 is far above it).
+The definition computes sum_j p_j |v_j| as the attention over |V|. Over
+e4m3 pools an f16 query enters Q.K^T as two e4m3 terms of four significant
+bits each: the first leaves a remainder of at most 2^-4 of the element's power
+of two, the second rounds it by at most 2^-9 of that, so a score is off by at
+most ds = 2^-9 scale sum_d |q_d k_d|, a weight by a factor e^(2 ds) at most and
+the LSE by ds (bf16 has eight significant bits: exact). (A fixed
+1e-2, as for batches whose rows average many keys, does not hold here: a row
+that sees two keys has outputs of 4 and more, and 2^-8 * 4 > 1e-2.)"""
+import math
+
+import pytest
+import torch
+
+import paged_kv_varlen_attn_gb300 as pa
+import workloads as W
+from helpers import LSE_TOL, oracle_pools
+from oracle import cache_ops as ref
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from paged_kv_varlen_attn_gb300 import _build
+    _build.build()
+    pa.load_library()
+
+
+def define(wl, kc, vc, window, first, scale=None, sinks=None):
+    """(out, lse, sum_j p_j |v_j|) of the definition."""
+    args = (wl.cu_seqlens_q, wl.seqused_k, wl.block_table,
+            wl.softmax_scale if scale is None else scale, window, first)
+    sinks = None if sinks is None else sinks.double()
+    o, l = ref.window_attention(wl.q, kc, vc, *args, sinks=sinks)
+    return o, l, ref.window_attention(wl.q, kc, vc.abs(), *args, sinks=sinks)[0]
+
+
+def check(got, want, ds=0.0):
+    (out, lse), (ref_o, ref_l, ref_a) = got, want
+    o, l = out.cpu().double(), lse.cpu().double()
+    fin = torch.isfinite(ref_l)
+    assert torch.equal(fin, torch.isfinite(l))
+    half = torch.finfo(out.dtype).eps / 2
+    assert ((o - ref_o).abs() <= half * (ref_o.abs() + ref_a) +
+            math.expm1(2 * ds) * ref_a + 1e-4).all()
+    if fin.any():
+        assert (l[fin] - ref_l[fin]).abs().max().item() <= LSE_TOL + ds
+
+
+def dev(wl):
+    return tuple(t.to(DEV) for t in (wl.cu_seqlens_q, wl.seqused_k, wl.block_table))
+
+
+def hide(wl, kc, vc, window, first, seqs=None):
+    """The pools and table as a user that frees what nobody sees may leave
+    them: NaN in every unseen row, a stale entry for every unseen page."""
+    kc, vc, bt = kc.clone(), vc.clone(), wl.block_table.clone()
+    bs = wl.block_size
+    seen = torch.zeros(wl.num_blocks * bs, dtype=torch.bool)
+    for s, (ql, kv) in enumerate(zip(wl.q_lens, wl.kv_lens)):
+        lo = max(0, kv - ql - window + 1)
+        for p in range((kv + bs - 1) // bs):
+            keys = [j for j in range(p * bs, min(kv, (p + 1) * bs)) if j < first or j >= lo]
+            if not keys:
+                bt[s, p] = -1 if p % 2 else W.INT32_MAX
+            for j in keys:
+                seen[int(wl.block_table[s, p]) * bs + j % bs] = True
+    kc.view(-1, *kc.shape[2:])[~seen] = float("nan")
+    vc.view(-1, *vc.shape[2:])[~seen] = float("nan")
+    return kc, vc, bt
+
+
+CASES = [
+    # seed, S, H, hk, D, bs, max_q, max_kv, decode_frac, empty_ok, window, first, dtype
+    (701, 5, 8, 2, 64, 16, 1, 200, 1.0, False, 1, 0, torch.bfloat16),     # only its own key
+    (702, 6, 32, 8, 128, 16, 1, 3000, 1.0, False, 700, 4, torch.bfloat16),
+    (703, 6, 32, 8, 128, 16, 1, 3000, 1.0, False, 64, 0, torch.float16),
+    (704, 4, 8, 8, 64, 32, 1, 900, 1.0, False, 130, 300, torch.bfloat16),
+    (705, 4, 16, 2, 128, 64, 3, 1500, 0.2, False, 100, 7, torch.bfloat16),  # short queries
+    (706, 5, 8, 2, 64, 16, 12, 60, 0.3, True, 5, 2, torch.bfloat16),     # empty rows, D 64
+    (707, 3, 16, 2, 128, 32, 300, 700, 0.0, False, 50, 3, torch.bfloat16),
+    (708, 2, 32, 8, 128, 128, 200, 4000, 0.0, False, 900, 16, torch.bfloat16),
+    (709, 2, 14, 2, 128, 16, 400, 1200, 0.0, False, 257, 129, torch.float16),   # GQA 7
+    (710, 2, 8, 2, 64, 16, 500, 1500, 0.0, False, 128, 64, torch.bfloat16),
+    (711, 3, 8, 4, 256, 16, 200, 900, 0.3, False, 100, 5, torch.bfloat16),
+    (712, 3, 4, 2, 256, 64, 1, 2500, 1.0, False, 1000, 1, torch.float16),
+    (713, 3, 12, 4, 128, 16, 80, 500, 0.4, True, 33, 1, torch.bfloat16),
+    (714, 1, 200, 1, 128, 16, 3, 300, 0.0, False, 40, 2, torch.bfloat16),   # a wide group
+    (715, 2, 32, 8, 128, 16, 700, 700, 0.0, False, 1, 1, torch.bfloat16),
+    (716, 2, 8, 1, 128, 16, 260, 6000, 0.0, False, 3000, 4, torch.bfloat16),   # KV splits
+]
+
+
+@pytest.mark.parametrize("seed,S,H,hk,D,bs,mq,mk,dfrac,empty,window,first,dtype", CASES)
+def test_window(seed, S, H, hk, D, bs, mq, mk, dfrac, empty, window, first, dtype):
+    wl = W.random_case(seed, num_seqs=S, num_heads=H, num_kv_heads=hk, head_size=D,
+                       block_size=bs, max_q=mq, max_kv=mk, decode_frac=dfrac, empty_ok=empty,
+                       dtype=dtype)
+    kc, vc = oracle_pools(wl)
+    want = define(wl, kc, vc, window, first)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    tail = (wl.max_seqlen_q, wl.max_seqlen_k, wl.softmax_scale, window, first)
+    out, lse = pa.window_fwd(wl.q.to(DEV), kc.to(DEV), vc.to(DEV), *dev(wl), *tail,
+                             dev_status=status)
+    check((out, lse), want)
+    assert int(status) == 0
+    # what nobody sees may be anything: the same bits
+    hk_, hv_, hbt = hide(wl, kc, vc, window, first)
+    o2, l2 = pa.window_fwd(wl.q.to(DEV), hk_.to(DEV), hv_.to(DEV), *dev(wl)[:2], hbt.to(DEV),
+                           *tail, dev_status=status)
+    assert int(status) == 0
+    assert torch.equal(o2, out) and torch.equal(l2, lse)
+    # looser bounds: the same values (the split of the keys may differ)
+    check(pa.window_fwd(wl.q.to(DEV), kc.to(DEV), vc.to(DEV), *dev(wl),
+                        2 * wl.max_seqlen_q + 40, 3 * wl.max_seqlen_k + 500, *tail[2:]), want)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("H,hk,bs,mq,mk,dfrac,window,first", [
+    (32, 8, 16, 1, 2500, 1.0, 600, 4),      # the FP8 decode consumer
+    (16, 2, 32, 2, 900, 0.3, 77, 3),        # wider items
+    (16, 2, 128, 300, 800, 0.0, 120, 5),    # the prefill kernel
+    (8, 1, 16, 260, 3000, 0.0, 1500, 130),
+])
+def test_window_fp8(H, hk, bs, mq, mk, dfrac, window, first, dtype):
+    wl = W.random_case(730 + mq, num_seqs=3, num_heads=H, num_kv_heads=hk, head_size=128,
+                       block_size=bs, max_q=mq, max_kv=mk, decode_frac=dfrac, dtype=dtype)
+    kc, vc = oracle_pools(wl)
+    ks, vs = torch.linspace(0.02, 0.05, hk), torch.linspace(0.03, 0.02, hk)
+
+    def quant(x, s):
+        return (x.float() / s[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn)
+    qk, qv = quant(kc, ks), quant(vc, vs)
+    want = define(wl, qk.float() * ks[:, None], qv.float() * vs[:, None], window, first)
+    ds = 0.0
+    if dtype == torch.float16:
+        aq, ak = wl.q.double().abs(), (qk.float() * ks[:, None]).flatten(0, 1).double().abs()
+        ds = 2.0 ** -9 * wl.softmax_scale * max(
+            (aq[:, h] @ ak[:, h * hk // H].T).max().item() for h in range(H))
+    tail = (wl.max_seqlen_q, wl.max_seqlen_k, wl.softmax_scale, window, first)
+    kw = dict(k_scale=ks.to(DEV), v_scale=vs.to(DEV))
+    out, lse = pa.window_fwd(wl.q.to(DEV), qk.view(torch.uint8).to(DEV),
+                             qv.view(torch.uint8).to(DEV), *dev(wl), *tail, **kw)
+    check((out, lse), want, ds)
+    kn, vn, hbt = hide(wl, kc, vc, window, first)
+    kn, vn = quant(kn, ks), quant(vn, vs)      # NaN codes where nobody looks
+    o2, l2 = pa.window_fwd(wl.q.to(DEV), kn.view(torch.uint8).to(DEV),
+                           vn.view(torch.uint8).to(DEV), *dev(wl)[:2], hbt.to(DEV), *tail, **kw)
+    assert torch.equal(o2, out) and torch.equal(l2, lse)
+
+
+@pytest.mark.parametrize("mq,mk,dfrac", [(1, 1500, 1.0), (250, 700, 0.0)])
+def test_window_with_sinks_update_and_strided_q(mq, mk, dfrac):
+    wl = W.random_case(760 + mq, num_seqs=4, num_heads=16, num_kv_heads=4, head_size=128,
+                       block_size=16, max_q=mq, max_kv=mk, decode_frac=dfrac)
+    kc, vc = oracle_pools(wl)
+    sinks = torch.linspace(-1.0, 3.0, 16)
+    window, first = 200, 4
+    want = define(wl, kc, vc, window, first, sinks=sinks)
+    wide = torch.zeros((wl.total_q, 24, 128), dtype=wl.dtype, device=DEV)
+    wide[:, :16] = wl.q.to(DEV)
+    dk, dv = wl.pool(0).to(DEV), wl.pool(1).to(DEV)
+    out, lse = pa.window_fwd(wide[:, :16], dk, dv, *dev(wl), wl.max_seqlen_q, wl.max_seqlen_k,
+                             wl.softmax_scale, window, first, sinks=sinks.to(DEV),
+                             key=wl.k_new.to(DEV), value=wl.v_new.to(DEV),
+                             slot_mapping=wl.slot_mapping.to(DEV))
+    check((out, lse), want)
+    assert torch.equal(dk.cpu(), kc) and torch.equal(dv.cpu(), vc)
+
+
+@pytest.mark.parametrize("D,mq,mk,dfrac", [(128, 1, 900, 1.0), (128, 200, 600, 0.0),
+                                           (64, 9, 300, 0.3), (256, 100, 300, 0.2)])
+def test_window_that_covers_everything(D, mq, mk, dfrac):
+    """A window of at least max_seqlen_k is plain causal attention, bit by
+    bit; one key short of it leaves out one key of the longest sequence."""
+    wl = W.random_case(770 + D, num_seqs=3, num_heads=8, num_kv_heads=2, head_size=D,
+                       block_size=16, max_q=mq, max_kv=mk, decode_frac=dfrac)
+    kc, vc = oracle_pools(wl)
+    args = (wl.q.to(DEV), kc.to(DEV), vc.to(DEV), *dev(wl), wl.max_seqlen_q, wl.max_seqlen_k,
+            wl.softmax_scale)
+    plain = pa.varlen_fwd(*args, True)
+    for window, first in ((wl.max_seqlen_k, 0), (2 ** 31 - 1, 2 ** 31 - 1)):
+        out, lse = pa.window_fwd(*args, window, first)
+        assert torch.equal(out, plain[0]) and torch.equal(lse, plain[1])
+    for window, first in ((wl.max_seqlen_k - 1, 0), (3, 2 ** 31 - 1), (3, wl.max_seqlen_k)):
+        check(pa.window_fwd(*args, window, first), define(wl, kc, vc, window, first))
+
+
+def test_window_nonpositive_scale_and_more_queries_than_keys():
+    wl = W.random_case(780, num_seqs=3, num_heads=8, num_kv_heads=2, head_size=64, block_size=16,
+                       max_q=90, max_kv=200, decode_frac=0.0)
+    kc, vc = oracle_pools(wl)
+    for scale in (0.0, -0.2):
+        check(pa.window_fwd(wl.q.to(DEV), kc.to(DEV), vc.to(DEV), *dev(wl), wl.max_seqlen_q,
+                            wl.max_seqlen_k, scale, 30, 2),
+              define(wl, kc, vc, 30, 2, scale=scale))
+    # fewer keys than queries: the first queries see nothing
+    lens = torch.tensor([max(0, q - 5) for q in wl.q_lens], dtype=torch.int32)
+    kvs = lens.tolist()
+    T = wl.total_q
+    ref_o = torch.zeros((T, 8, 64), dtype=torch.float64)
+    ref_a = ref_o.clone()
+    ref_l = torch.full((8, T), float("-inf"), dtype=torch.float64)
+    cu = wl.cu_seqlens_q.tolist()
+    sub = [(a + min(5, b - a), b) for a, b in zip(cu, cu[1:])]
+    idx = torch.cat([torch.arange(a, b) for a, b in sub])
+    cu2 = torch.tensor([0] + torch.tensor(kvs).cumsum(0).tolist(), dtype=torch.int32)
+    tail = (cu2, lens, wl.block_table, wl.softmax_scale, 30, 2)
+    ref_o[idx], ref_l[:, idx] = ref.window_attention(wl.q[idx], kc, vc, *tail)
+    ref_a[idx] = ref.window_attention(wl.q[idx], kc, vc.abs(), *tail)[0]
+    got = pa.window_fwd(wl.q.to(DEV), kc.to(DEV), vc.to(DEV), dev(wl)[0], lens.to(DEV),
+                        dev(wl)[2], wl.max_seqlen_q, wl.max_seqlen_k, wl.softmax_scale, 30, 2)
+    check(got, (ref_o, ref_l, ref_a))
+
+
+def test_window_captured_and_repeatable():
+    wl = W.random_case(790, num_seqs=8, num_heads=32, num_kv_heads=8, head_size=128,
+                       block_size=16, max_q=150, max_kv=2500, decode_frac=0.6)
+    kc, vc = oracle_pools(wl)
+    d = (wl.q.to(DEV), kc.to(DEV), vc.to(DEV), *dev(wl))
+    tail = (wl.max_seqlen_q, wl.max_seqlen_k, wl.softmax_scale, 300, 4)
+    ws = pa.alloc_workspace(pa.varlen_fwd_workspace_size(8, wl.total_q, *tail[:2], 32, 8, 128, 16,
+                                                         pa._sm_count(DEV)), DEV)
+    want = pa.window_fwd(*d, *tail, workspace=ws)
+    out, lse = torch.empty_like(want[0]), torch.empty_like(want[1])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        pa.window_fwd(*d, *tail, out=out, lse=lse, workspace=ws)
+    ws.fill_(255)        # the workspace needs no initialisation
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    # shorter sequences in the same graph
+    d[4].copy_(torch.clamp(d[4] - 7, min=0))
+    graph.replay()
+    torch.cuda.synchronize()
+    again = pa.window_fwd(*d, *tail)
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
