@@ -178,11 +178,23 @@ def _check(code: int, where: str):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(device):
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _call(fn, where, device, *args):
+    """Call an entry point whose last argument is the stream, on the tensors'
+    device (entered only if it is not the current one)."""
+    if device.index == torch.cuda.current_device():
+        code = fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
+    else:
+        with torch.cuda.device(device):
+            code = fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
+    if code != PA_OK:
+        raise PAError(code, where)
 
 
 def _need_cuda(*ts):
@@ -587,15 +599,13 @@ def window_fwd(q, key_cache, value_cache, cu_seqlens_q, seqused_k, block_table, 
                                          _sm_count(q.device)), q.device)
     opts = AttnOpts(None if sinks is None else sinks.data_ptr(),
                     None if desc is None else ctypes.pointer(desc))
-    with torch.cuda.device(q.device):
-        code = lib.pa_window_fwd(
-            None if update is None else ctypes.byref(update), _ptr(q), _row_stride(q),
-            _ptr(key_cache), _ptr(value_cache), _cache_stride(key_cache), _ptr(cu_seqlens_q),
-            _ptr(seqused_k), _ptr(block_table), block_table.stride(0), S, T, int(max_seqlen_q),
-            int(max_seqlen_k), H, hk, D, bs, nb, float(softmax_scale), int(window),
-            int(num_first), ctypes.byref(opts), _ptr(out), _ptr(lse), _ptr(workspace),
-            workspace.numel(), dtype, _ptr(dev_status), _stream(q.device))
-    _check(code, "pa_window_fwd")
+    _call(lib.pa_window_fwd, "pa_window_fwd", q.device,
+          None if update is None else ctypes.byref(update), _ptr(q), _row_stride(q),
+          _ptr(key_cache), _ptr(value_cache), _cache_stride(key_cache), _ptr(cu_seqlens_q),
+          _ptr(seqused_k), _ptr(block_table), block_table.stride(0), S, T, int(max_seqlen_q),
+          int(max_seqlen_k), H, hk, D, bs, nb, float(softmax_scale), int(window),
+          int(num_first), ctypes.byref(opts), _ptr(out), _ptr(lse), _ptr(workspace),
+          workspace.numel(), dtype, _ptr(dev_status))
     del keep
     return out, lse
 
@@ -619,10 +629,8 @@ def rope_table(table_len, rot_dim, base=10000.0, scaling="none", factor=1.0, ori
         mscale = 0.1 * math.log(factor) + 1.0 if scaling == "yarn" and factor > 1 else 1.0
     desc = RopeScaling(ROPE_SCALINGS[scaling], factor, orig_len, 1.0 if low is None else low,
                        (32.0 if scaling == "yarn" else 4.0) if high is None else high, mscale)
-    with torch.cuda.device(out.device):
-        code = load_library().pa_rope_table(_ptr(out), int(table_len), int(rot_dim), float(base),
-                                            ctypes.byref(desc), _stream(out.device))
-    _check(code, "pa_rope_table")
+    _call(load_library().pa_rope_table, "pa_rope_table", out.device, _ptr(out), int(table_len),
+          int(rot_dim), float(base), ctypes.byref(desc))
     return out
 
 
@@ -670,14 +678,11 @@ def rope_and_cache(q, key, value, positions, cos_sin, key_cache, value_cache, sl
     rope = Rope(cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], int(bool(interleaved)),
                 None if q_norm is None else q_norm.data_ptr(),
                 None if k_norm is None else k_norm.data_ptr(), float(eps))
-    with torch.cuda.device(q.device):
-        code = lib.pa_rope_and_cache(
-            ctypes.byref(rope), _ptr(positions), _ptr(q), _row_stride(q), _ptr(out),
-            _row_stride(out), ctypes.byref(_kv_update(key, value, slot_mapping)), _ptr(key_cache),
-            _ptr(value_cache), _cache_stride(key_cache), H, hk, d, bs, nb,
-            None if desc is None else ctypes.byref(desc), dtype, _ptr(dev_status),
-            _stream(q.device))
-    _check(code, "pa_rope_and_cache")
+    _call(lib.pa_rope_and_cache, "pa_rope_and_cache", q.device,
+          ctypes.byref(rope), _ptr(positions), _ptr(q), _row_stride(q), _ptr(out),
+          _row_stride(out), ctypes.byref(_kv_update(key, value, slot_mapping)), _ptr(key_cache),
+          _ptr(value_cache), _cache_stride(key_cache), H, hk, d, bs, nb,
+          None if desc is None else ctypes.byref(desc), dtype, _ptr(dev_status))
     del keep
     return out
 
@@ -714,15 +719,13 @@ def attn_weights(q, key_cache, lse, weights, cu_seqlens_q, seqused_k, block_tabl
         _fp8_pool(key_cache)
         desc, keep = _fp8_desc(k_scale, k_scale, hk, q.device)
     dtype = _dtype_code(q) if desc is not None else _dtype_code(q, key_cache)
-    with torch.cuda.device(q.device):
-        code = lib.pa_attn_weights(
-            _ptr(q), _row_stride(q), _ptr(key_cache), _cache_stride(key_cache), _ptr(lse),
-            _ptr(cu_seqlens_q), _ptr(seqused_k), _ptr(block_table), block_table.stride(0),
-            cu_seqlens_q.numel() - 1, T, int(max_seqlen_q), int(max_seqlen_k), H, hk, D, bs, nb,
-            float(softmax_scale), int(bool(causal)), _ptr(weights),
-            _weights_stride(weights, nb, bs, hk), None if desc is None else ctypes.byref(desc),
-            dtype, _ptr(dev_status), _stream(q.device))
-    _check(code, "pa_attn_weights")
+    _call(lib.pa_attn_weights, "pa_attn_weights", q.device,
+          _ptr(q), _row_stride(q), _ptr(key_cache), _cache_stride(key_cache), _ptr(lse),
+          _ptr(cu_seqlens_q), _ptr(seqused_k), _ptr(block_table), block_table.stride(0),
+          cu_seqlens_q.numel() - 1, T, int(max_seqlen_q), int(max_seqlen_k), H, hk, D, bs, nb,
+          float(softmax_scale), int(bool(causal)), _ptr(weights),
+          _weights_stride(weights, nb, bs, hk), None if desc is None else ctypes.byref(desc),
+          dtype, _ptr(dev_status))
     del keep
     return weights
 
@@ -756,12 +759,10 @@ def evict(key_cache, value_cache, weights, seqused_k, block_table, max_seqlen_k,
     for t, shape, name in ((kept, (S, hk, budget), "kept"), (new_lens, (S,), "new_lens")):
         if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape}")
-    with torch.cuda.device(key_cache.device):
-        code = lib.pa_evict(
-            _ptr(key_cache), _ptr(value_cache), _cache_stride(key_cache), _ptr(weights),
-            _weights_stride(weights, nb, bs, hk), _ptr(seqused_k), _ptr(block_table),
-            block_table.stride(0), S, int(max_seqlen_k), hk, d, bs, nb,
-            key_cache.element_size(), int(budget), int(num_first), int(num_recent), _ptr(kept),
-            _ptr(new_lens), _ptr(dev_status), _stream(key_cache.device))
-    _check(code, "pa_evict")
+    _call(lib.pa_evict, "pa_evict", key_cache.device,
+          _ptr(key_cache), _ptr(value_cache), _cache_stride(key_cache), _ptr(weights),
+          _weights_stride(weights, nb, bs, hk), _ptr(seqused_k), _ptr(block_table),
+          block_table.stride(0), S, int(max_seqlen_k), hk, d, bs, nb,
+          key_cache.element_size(), int(budget), int(num_first), int(num_recent), _ptr(kept),
+          _ptr(new_lens), _ptr(dev_status))
     return kept, new_lens

@@ -1040,43 +1040,48 @@ pa_status pa_rope_table(float* cos_sin, int table_len, int rot_dim, double base,
   constexpr double kTwoPi = 6.283185307179586;
   if (table_len < 0 || rot_dim < 2 || rot_dim > 256 || rot_dim % 2 != 0) return PA_ERR_INVALID_ARG;
   if (!std::isfinite(base) || !(base > 0.0)) return PA_ERR_INVALID_ARG;
+  const pa_rope_scaling none{PA_ROPE_NONE, 1.0, 1.0, 1.0, 2.0, 1.0};
+  const pa_rope_scaling& s = scaling ? *scaling : none;
+  if (s.kind < PA_ROPE_NONE || s.kind > PA_ROPE_YARN || !std::isfinite(s.mscale))
+    return PA_ERR_INVALID_ARG;
+  if (s.kind != PA_ROPE_NONE && (!std::isfinite(s.factor) || !(s.factor > 0.0)))
+    return PA_ERR_INVALID_ARG;
+  if (s.kind == PA_ROPE_WAVELENGTH || s.kind == PA_ROPE_YARN) {
+    if (!std::isfinite(s.orig_len) || !(s.orig_len > 0.0) || !std::isfinite(s.high) ||
+        !(s.low > 0.0) || !(s.high > s.low))
+      return PA_ERR_INVALID_ARG;
+  }
+  double ramp_lo = 0.0, ramp_len = 1.0;
+  if (s.kind == PA_ROPE_NTK) {
+    if (rot_dim == 2) return PA_ERR_INVALID_ARG;
+    base *= std::pow(s.factor, rot_dim / (rot_dim - 2.0));
+    if (!std::isfinite(base) || !(base > 0.0)) return PA_ERR_INVALID_ARG;
+  }
+  if (s.kind == PA_ROPE_YARN) {
+    if (!(base > 1.0)) return PA_ERR_INVALID_ARG;
+    auto pair_of = [&](double turns) {
+      return rot_dim * std::log(s.orig_len / (turns * kTwoPi)) / (2.0 * std::log(base));
+    };
+    ramp_lo = std::fmax(std::floor(pair_of(s.high)), 0.0);
+    ramp_len = std::fmax(std::fmin(std::ceil(pair_of(s.low)), rot_dim - 1.0) - ramp_lo, 0.001);
+  }
+  auto unit = [](double x) { return std::fmin(1.0, std::fmax(0.0, x)); };
   RopeTableArgs a{};
   a.table_len = table_len;
   a.rot = rot_dim;
-  a.base = base;
-  a.mscale = 1.f;
-  if (scaling) {
-    const pa_rope_scaling& s = *scaling;
-    a.kind = s.kind;
-    a.factor = s.factor;
-    a.orig_len = s.orig_len;
-    a.low = s.low;
-    a.high = s.high;
-    a.mscale = static_cast<float>(s.mscale);
-    if (!std::isfinite(s.mscale)) return PA_ERR_INVALID_ARG;
-    if (s.kind < PA_ROPE_NONE || s.kind > PA_ROPE_YARN) return PA_ERR_INVALID_ARG;
-    if (s.kind != PA_ROPE_NONE && (!std::isfinite(s.factor) || !(s.factor > 0.0)))
-      return PA_ERR_INVALID_ARG;
-    if (s.kind == PA_ROPE_WAVELENGTH || s.kind == PA_ROPE_YARN) {
-      if (!std::isfinite(s.orig_len) || !(s.orig_len > 0.0) || !std::isfinite(s.high) ||
-          !(s.low > 0.0) || !(s.high > s.low))
-        return PA_ERR_INVALID_ARG;
-    }
-    if (s.kind == PA_ROPE_NTK) {
-      if (rot_dim == 2) return PA_ERR_INVALID_ARG;
-      a.base = base * std::pow(s.factor, rot_dim / (rot_dim - 2.0));
-      if (!std::isfinite(a.base) || !(a.base > 0.0)) return PA_ERR_INVALID_ARG;
-    }
-    if (s.kind == PA_ROPE_YARN) {
-      if (!(base > 1.0)) return PA_ERR_INVALID_ARG;
-      auto pair_of = [&](double turns) {
-        return rot_dim * std::log(s.orig_len / (turns * kTwoPi)) / (2.0 * std::log(base));
-      };
-      const double lo = std::fmax(std::floor(pair_of(s.high)), 0.0);
-      const double hi = std::fmin(std::ceil(pair_of(s.low)), rot_dim - 1.0);
-      a.ramp_lo = lo;
-      a.ramp_len = std::fmax(hi - lo, 0.001);
-    }
+  a.mscale = static_cast<float>(s.mscale);
+  for (int i = 0; i < rot_dim / 2; ++i) {
+    double f = std::pow(base, -2.0 * i / rot_dim), keep = 1.0;   // share of the unscaled rate
+    if (s.kind == PA_ROPE_LINEAR) keep = 0.0;
+    if (s.kind == PA_ROPE_WAVELENGTH)
+      keep = unit((s.orig_len * f / kTwoPi - s.low) / (s.high - s.low));
+    if (s.kind == PA_ROPE_YARN) keep = 1.0 - unit((i - ramp_lo) / ramp_len);
+    f = keep == 1.0 ? f : f / s.factor * (1.0 - keep) + f * keep;
+    const double turns = f / kTwoPi;
+    if (!(turns < 9007199254740992.0)) return PA_ERR_INVALID_ARG;   // 2^53: no fraction left
+    const double frac = (turns - std::floor(turns)) * 0x1p32, hi = std::floor(frac);
+    a.rate[i] = (static_cast<unsigned long long>(hi) << 32) +
+                static_cast<unsigned long long>(std::nearbyint((frac - hi) * 0x1p32));
   }
   if (table_len == 0) return PA_OK;
   if (!cos_sin || !aligned16(cos_sin)) return PA_ERR_INVALID_ARG;
@@ -1094,6 +1099,10 @@ pa_status pa_rope_and_cache(const pa_rope* rope, const int64_t* positions, const
                             int head_size, int block_size, int num_blocks, const pa_kv_fp8* fp8,
                             int dtype, int32_t* dev_status, void* stream) {
   if (!rope || !update || num_heads <= 0) return PA_ERR_INVALID_ARG;
+  // Offsets within a token's row are 32-bit.
+  if (static_cast<int64_t>(num_heads) * head_size > (1 << 28) ||
+      static_cast<int64_t>(num_kv_heads) * head_size > (1 << 28))
+    return PA_ERR_INVALID_ARG;
   const KvFormat kv = fp8 ? fp8_format(fp8) : kKvBf16;
   pa_status st = check_update(update->key, update->value, update->key_token_stride,
                               update->value_token_stride, key_cache, value_cache,

@@ -198,14 +198,12 @@ cudaError_t launch_attn_tc(const CUtensorMap& tmK, const CUtensorMap& tmV, const
 
 // Rotary cos/sin table (rope.cu).
 struct RopeTableArgs {
-  int table_len, rot, kind;       // kind: PA_ROPE_*
-  double base;                    // of pair i's rate base^(-2i / rot) (PA_ROPE_NTK: scaled)
-  double factor, orig_len, low, high;
-  double ramp_lo, ramp_len;       // PA_ROPE_YARN: the ramp over the pairs
+  int table_len, rot;
   float mscale;
   int per_block;                  // positions per block (set by the launcher)
+  unsigned long long rate[128];   // turns per position of each pair, modulo 1, in 2^-64
 };
-cudaError_t launch_rope_table(float* table, RopeTableArgs a, cudaStream_t st, int sms);
+cudaError_t launch_rope_table(float* table, RopeTableArgs& a, cudaStream_t st, int sms);
 
 // Norm, rotation and cache write of new tokens (rope.cu). Strides in
 // elements, the pools' page stride in bytes.
@@ -230,7 +228,8 @@ struct RopeArgs {
   int num_tokens, H, H_kv, bs;
   int64_t num_slots;
   int32_t* status;
-  int items_per_warp, chunks;     // warps a token's heads are shared among (set by the launcher)
+  // Set by the launcher: items per warp, warps per token, those of q among them.
+  int items_per_warp, chunks, q_chunks;
 };
 cudaError_t launch_rope_and_cache(RopeArgs a, int D, bool f16, bool fp8, cudaStream_t st,
                                   int sms);

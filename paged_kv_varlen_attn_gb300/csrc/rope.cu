@@ -12,44 +12,19 @@ namespace pa {
 
 // ---------------------------------------------------------------------------
 // Table. Pair i turns f_i / 2 pi times per position. The turn count of
-// position p is only needed modulo 1, so each thread keeps its pair's rate as
-// a 64-bit fraction F = round(2^64 * frac(f_i / 2 pi)) and multiplies it by
-// p in 64-bit integers, which drop whole turns by themselves: the phase is
-// off by p * 2^-65 turns from F's rounding and p * 2^-53 * f_i / 2 pi from
-// the double behind it (under 1e-9 radian at a million positions), where a
-// float32 angle would be off by p * f_i * 2^-24. The phase is split into the
-// nearest quarter turn and a signed remainder of at most an eighth, so the
-// float32 sinpi / cospi that follow see a remainder with full relative
-// precision.
-// Double precision is slow on this part (2 operations per clock and SM): it
-// is used once per thread, for the rate, and never per entry.
+// position p is only needed modulo 1, so the host hands over each pair's rate
+// as a 64-bit fraction of a turn, round(2^64 * frac(f_i / 2 pi)), and a thread
+// multiplies it by p in 64-bit integers, which drop whole turns by themselves:
+// the phase is off by p * 2^-65 turns from that rounding and p * 2^-53 * f_i /
+// 2 pi from the double behind it (under 1e-9 radian at a million positions),
+// where a float32 angle would be off by p * f_i * 2^-24. The phase is split
+// into the nearest quarter turn and a signed remainder of at most an eighth,
+// so the float32 sinpi / cospi that follow see a remainder with full relative
+// precision. No double arithmetic on the device: it does 2 operations per
+// clock and SM there (computing the rates per thread took 60 us for a table
+// of any size).
 // ---------------------------------------------------------------------------
 constexpr int kTableThreads = 256;
-
-__device__ __forceinline__ double rope_rate(const RopeTableArgs& a, int i) {
-  double f = pow(a.base, -2.0 * i / a.rot);
-  switch (a.kind) {
-    case PA_ROPE_LINEAR:
-      f /= a.factor;
-      break;
-    case PA_ROPE_WAVELENGTH: {
-      // Turns within the original length: at most `low` are interpolated, at
-      // least `high` kept, a linear mix of the two in between.
-      const double mix = fmin(1.0, fmax(0.0, (a.orig_len * f * 0.15915494309189535 - a.low) /
-                                                 (a.high - a.low)));
-      f = f / a.factor * (1.0 - mix) + f * mix;
-      break;
-    }
-    case PA_ROPE_YARN: {
-      const double ramp = fmin(1.0, fmax(0.0, (i - a.ramp_lo) / a.ramp_len));
-      f = f / a.factor * ramp + f * (1.0 - ramp);
-      break;
-    }
-    default:
-      break;   // PA_ROPE_NTK: the host has changed the base
-  }
-  return f * 0.15915494309189535;   // turns per position
-}
 
 __global__ void __launch_bounds__(kTableThreads)
 rope_table_kernel(float* __restrict__ table, const __grid_constant__ RopeTableArgs a) {
@@ -57,13 +32,7 @@ rope_table_kernel(float* __restrict__ table, const __grid_constant__ RopeTableAr
   const int step = kTableThreads / half;   // positions a block writes per step
   const int i = threadIdx.x % half, r = threadIdx.x / half;
   if (r >= step) return;
-  const double turns = rope_rate(a, i);
-  const double frac = turns - floor(turns);
-  // 2^64 frac, rounded: two halves, as frac may carry 53 bits below 2^-11.
-  const double hi = floor(frac * 0x1p32);
-  const unsigned long long rate =
-      (static_cast<unsigned long long>(hi) << 32) +
-      static_cast<unsigned long long>(rint((frac * 0x1p32 - hi) * 0x1p32));
+  const unsigned long long rate = a.rate[i];
   const int p0 = blockIdx.x * a.per_block;
   const int p1 = min(a.table_len, p0 + a.per_block);
   for (int p = p0 + r; p < p1; p += step) {
@@ -80,7 +49,7 @@ rope_table_kernel(float* __restrict__ table, const __grid_constant__ RopeTableAr
   }
 }
 
-cudaError_t launch_rope_table(float* table, RopeTableArgs a, cudaStream_t st, int sms) {
+cudaError_t launch_rope_table(float* table, RopeTableArgs& a, cudaStream_t st, int sms) {
   if (a.table_len == 0) return cudaSuccess;
   const int step = kTableThreads / (a.rot / 2);
   // Eight blocks per SM (every thread resident) share the positions, in
@@ -95,18 +64,22 @@ cudaError_t launch_rope_table(float* table, RopeTableArgs a, cudaStream_t st, in
 
 // ---------------------------------------------------------------------------
 // Norm, rotation and cache write in one pass over the new tokens: every q, k
-// and v element is read once and written once. A warp takes one token (or
-// part of its heads); D / 8 lanes hold a head, 16 bytes each, so an item --
-// 32 * 8 / D heads of q, k or v -- is one coalesced 512-byte access, and
-// kUnroll items are in flight. The token's cos and sin stay in registers for
-// all of its heads. The partner of an element under rotation is in the same
-// lane (interleaved pairs) or rot / 16 lanes away (half layout: one shuffle
-// per element). Everything between the load and the store is float32; the
-// store is the only rounding.
+// and v element is read once and written once. D / 8 lanes hold a head, 16
+// bytes each, so an item -- 32 * 8 / D heads of q, k or v -- is one coalesced
+// 512-byte access, and item i of a token's q (k, v) starts 512 i bytes into
+// the token's row, whatever D is. A warp takes up to kRopeItems items of one
+// token (of q, or of k then v), all of whose loads are in flight before the
+// first is used; none of them waits for the token's position.
+// With w the norm weights (1 without a norm) and r = 1 / rms, an element x_j
+// with partner x_p becomes r (x_j w_j cos -+ x_p w_p sin): the coefficients
+// w_j cos and -+w_p sin of the lane's 8 elements are set up once per warp. The
+// partner is in the same register (interleaved pairs: swapped halves) or rot /
+// 16 lanes away (half layout: one shuffle per pair of elements). Everything
+// between the load and the store is float32; the store is the only rounding.
 // ---------------------------------------------------------------------------
 constexpr int kRopeThreads = 256;
 constexpr int kRopeWarps = kRopeThreads / 32;
-constexpr int kRopeUnroll = 4;
+constexpr int kRopeItems = 8;
 
 template <bool F16>
 __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
@@ -132,156 +105,200 @@ __device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
   f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
 }
 
-template <int D, bool F16, bool FP8>
-__global__ void __launch_bounds__(kRopeThreads)
+// INTER: interleaved pairs. NORM: q or k (or both) are normed.
+template <int D, bool F16, bool FP8, bool INTER, bool NORM>
+__global__ void __launch_bounds__(kRopeThreads, 3)
 rope_and_cache_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int LPH = D / 8;        // lanes per head
   constexpr int HPI = 32 / LPH;     // heads per item
   const int lane = threadIdx.x & 31;
-  const int sub = lane / LPH, l = lane % LPH;
-  const int64_t w = static_cast<int64_t>(blockIdx.x) * kRopeWarps + (threadIdx.x >> 5);
-  const int64_t t = w / a.chunks;
-  const int part = static_cast<int>(w - t * a.chunks);
+  const int l = lane % LPH;
+  const unsigned w = blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
+  const int t = static_cast<int>(w / static_cast<unsigned>(a.chunks));
+  const int part = static_cast<int>(w - static_cast<unsigned>(t) * a.chunks);
   if (t >= a.num_tokens) return;
   const int64_t pos = __ldg(a.positions + t), slot = __ldg(a.slots + t);
+  // This warp's items: q items, or the k items followed by the v items.
+  const bool is_q = part < a.q_chunks;
+  const int nkv = (a.H_kv + HPI - 1) / HPI;
+  const int n_all = is_q ? (a.H + HPI - 1) / HPI : 2 * nkv;
+  const int first = (is_q ? part : part - a.q_chunks) * a.items_per_warp;
+  const int n = min(a.items_per_warp, n_all - first);
+  const int row_bytes = (is_q ? a.H : a.H_kv) * D * 2;
+  const uint8_t* src = reinterpret_cast<const uint8_t*>(is_q ? a.q + t * a.q_stride
+                                                             : a.k + t * a.k_stride) +
+                       lane * 16;
+  const uint8_t* src_v = reinterpret_cast<const uint8_t*>(a.v + t * a.v_stride) + lane * 16;
+
+  uint4 x[kRopeItems];
+#pragma unroll
+  for (int u = 0; u < kRopeItems; ++u) {
+    x[u] = make_uint4(0, 0, 0, 0);
+    if (u >= n) continue;
+    const int item = first + u;
+    const bool v = !is_q && item >= nkv;
+    const int off = (v ? item - nkv : item) * 512;
+    if (off + lane * 16 < row_bytes)
+      x[u] = __ldcs(reinterpret_cast<const uint4*>((v ? src_v : src) + off));
+  }
   if (pos < 0) return;                       // padding token
   if (pos >= a.table_len) {
     if (part == 0 && lane == 0) flag_status(a.status, PA_DEV_BAD_POSITION);
     return;
   }
-  const bool cached = slot >= 0 && slot < a.num_slots;
   if (slot >= a.num_slots && part == 0 && lane == 0) flag_status(a.status, PA_DEV_BAD_SLOT);
-  const int nq = (a.H + HPI - 1) / HPI, nkv = (a.H_kv + HPI - 1) / HPI;
-  const int first = part * a.items_per_warp;
-  const int last = min(first + a.items_per_warp, cached ? nq + 2 * nkv : nq);
+  if (!is_q && (slot < 0 || slot >= a.num_slots)) return;
 
-  // This lane's cos and sin, the latter with the sign of its element's term.
   const bool turns = 8 * l < a.rot;
   const int half = a.rot >> 1;
-  float c[8], s[8];
-  int partner = lane;
-  if (turns) {
+  const bool lower = 8 * l < half;           // half layout: first elements of their pairs
+  const int away = INTER || !turns ? 0 : (lower ? a.rot >> 4 : -(a.rot >> 4));
+  const float* wt = NORM ? (is_q ? a.q_norm : a.k_norm) : nullptr;
+  float ca[8], cb[8];                        // coefficients of x_j and of its partner
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    ca[k] = 1.f;
+    cb[k] = 0.f;
+  }
+  if (turns && first < (is_q ? n_all : nkv)) {   // (not for v items alone)
     const float* row = a.cos_sin + pos * a.rot;
-    if (a.interleaved) {
+    if constexpr (INTER) {
       const float4 cc = __ldg(reinterpret_cast<const float4*>(row + 4 * l));
       const float4 ss = __ldg(reinterpret_cast<const float4*>(row + half + 4 * l));
       const float cv[4] = {cc.x, cc.y, cc.z, cc.w}, sv[4] = {ss.x, ss.y, ss.z, ss.w};
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        c[k] = cv[k >> 1];
-        s[k] = (k & 1) ? sv[k >> 1] : -sv[k >> 1];
+        ca[k] = cv[k >> 1];
+        cb[k] = (k & 1) ? sv[k >> 1] : -sv[k >> 1];
       }
     } else {
-      const bool lower = 8 * l < half;
       const int i0 = lower ? 8 * l : 8 * l - half;
-      partner = lower ? lane + (a.rot >> 4) : lane - (a.rot >> 4);
-      load8(row + i0, c);
-      load8(row + half + i0, s);
+      load8(row + i0, ca);
+      load8(row + half + i0, cb);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) s[k] = lower ? -s[k] : s[k];
+      for (int k = 0; k < 8; ++k) cb[k] = lower ? -cb[k] : cb[k];
     }
   }
-  const int64_t page = cached ? slot / a.bs : 0;
-  // Byte offset of the token's row in a pool (rows hold [H_kv, D]).
-  const int64_t crow = page * a.block_stride_bytes +
-                       (cached ? slot - page * a.bs : 0) * a.H_kv * D * (FP8 ? 1 : 2);
+  if (NORM && wt) {
+    float wv[8];
+    load8(wt + 8 * l, wv);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) ca[k] *= wv[k];
+    if constexpr (INTER) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) cb[k] *= wv[k ^ 1];
+    } else {
+      load8(wt + 8 * (l + away), wv);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) cb[k] *= wv[k];
+    }
+  }
+  // Where item 0's 16 (8 for e4m3) bytes of this lane go: the query row, or
+  // the token's row in the pools (rows hold [H_kv, D]).
+  constexpr int OUT = FP8 ? 256 : 512;       // bytes of a k or v item in the pools
+  uint8_t* dst;
+  int64_t crow = 0;
+  if (is_q) {
+    dst = reinterpret_cast<uint8_t*>(a.q_out + t * a.q_out_stride) + lane * 16;
+  } else {
+    const int64_t page = slot / a.bs;
+    crow = page * a.block_stride_bytes +
+           (slot - page * a.bs) * static_cast<int64_t>(a.H_kv * D * (FP8 ? 1 : 2)) +
+           lane * (FP8 ? 8 : 16);
+    dst = a.kc + crow;
+  }
 
-  for (int it = first; it < last; it += kRopeUnroll) {
-    uint4 x[kRopeUnroll];
 #pragma unroll
-    for (int u = 0; u < kRopeUnroll; ++u) {
-      const int item = it + u;
-      x[u] = make_uint4(0, 0, 0, 0);
-      if (item >= last) continue;
-      const int kind = item < nq ? 0 : (item < nq + nkv ? 1 : 2);
-      const int h = (item - (kind == 0 ? 0 : (kind == 1 ? nq : nq + nkv))) * HPI + sub;
-      if (h >= (kind == 0 ? a.H : a.H_kv)) continue;
-      const uint16_t* src = kind == 0 ? a.q + t * a.q_stride
-                                      : (kind == 1 ? a.k + t * a.k_stride : a.v + t * a.v_stride);
-      x[u] = __ldcs(reinterpret_cast<const uint4*>(src + h * D) + l);
-    }
-#pragma unroll
-    for (int u = 0; u < kRopeUnroll; ++u) {
-      const int item = it + u;
-      if (item >= last) break;               // warp-uniform, like kind below
-      const int kind = item < nq ? 0 : (item < nq + nkv ? 1 : 2);
-      const int h = (item - (kind == 0 ? 0 : (kind == 1 ? nq : nq + nkv))) * HPI + sub;
-      const bool live = h < (kind == 0 ? a.H : a.H_kv);
-      float f[8];
-      if (FP8 || kind < 2) unpack8<F16>(x[u], f);
-      if (kind < 2) {
-        const float* wt = kind == 0 ? a.q_norm : a.k_norm;
-        if (wt) {
-          float ss = 0.f;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) ss = fmaf(f[k], f[k], ss);
-#pragma unroll
-          for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-          const float r = rsqrtf(ss * (1.f / D) + a.eps);
-          float wv[8];
-          load8(wt + 8 * l, wv);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) f[k] = f[k] * r * wv[k];
-        }
-        float g[8];
-        if (a.interleaved) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) g[k] = f[k ^ 1];
-        } else {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) g[k] = __shfl_sync(0xffffffffu, f[k], partner);
-        }
-        if (turns) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) f[k] = fmaf(g[k], s[k], f[k] * c[k]);
-        }
-      }
-      if (!live) continue;
-      // What neither the norm nor the rotation touches keeps its bits.
-      const bool as_is = kind == 2 || (!turns && !(kind == 0 ? a.q_norm : a.k_norm));
-      if (kind == 0) {
-        *(reinterpret_cast<uint4*>(a.q_out + t * a.q_out_stride + h * D) + l) =
-            as_is ? x[u] : pack8<F16>(f);
+  for (int u = 0; u < kRopeItems; ++u) {
+    if (u >= n) break;
+    const int item = first + u;
+    const bool v = !is_q && item >= nkv;
+    const int at = v ? item - nkv : item;
+    const bool live = at * 512 + lane * 16 < row_bytes;
+    float f[8];
+    if (FP8 || !v) unpack8<F16>(x[u], f);
+    if (!v) {
+      uint4 px;
+      if constexpr (INTER) {
+        px = make_uint4(prmt(x[u].x, 0, 0x1032), prmt(x[u].y, 0, 0x1032),
+                        prmt(x[u].z, 0, 0x1032), prmt(x[u].w, 0, 0x1032));
       } else {
-        uint8_t* row = (kind == 1 ? a.kc : a.vc) + crow;
-        if constexpr (FP8) {
-          const ScaleDiv d = scale_div(__ldg((kind == 1 ? a.k_scale : a.v_scale) + h));
-          *(reinterpret_cast<uint2*>(row + h * D) + l) = quantize8(f, d);
-        } else {
-          *(reinterpret_cast<uint4*>(row + h * D * 2) + l) = as_is ? x[u] : pack8<F16>(f);
-        }
+        px.x = __shfl_sync(0xffffffffu, x[u].x, lane + away);
+        px.y = __shfl_sync(0xffffffffu, x[u].y, lane + away);
+        px.z = __shfl_sync(0xffffffffu, x[u].z, lane + away);
+        px.w = __shfl_sync(0xffffffffu, x[u].w, lane + away);
       }
+      if (!turns) px = make_uint4(0, 0, 0, 0);
+      float g[8];
+      unpack8<F16>(px, g);
+      float r = 1.f;
+      if (NORM && wt) {
+        float ss = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) ss = fmaf(f[k], f[k], ss);
+#pragma unroll
+        for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        r = rsqrtf(ss * (1.f / D) + a.eps);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        f[k] = fmaf(g[k], cb[k], f[k] * ca[k]);
+        if (NORM) f[k] *= r;
+      }
+    }
+    if (!live) continue;
+    // What neither the norm nor the rotation touches keeps its bits.
+    const bool as_is = v || (!turns && !wt);
+    if (!FP8 || is_q) {
+      const uint4 y = as_is ? x[u] : pack8<F16>(f);
+      *reinterpret_cast<uint4*>((v ? a.vc + crow : dst) + at * 512) = y;
+    } else if constexpr (FP8) {
+      const int h = at * HPI + lane / LPH;
+      const ScaleDiv d = scale_div(__ldg((v ? a.v_scale : a.k_scale) + h));
+      *reinterpret_cast<uint2*>((v ? a.vc + crow : dst) + at * OUT) = quantize8(f, d);
     }
   }
+}
+
+template <int D, bool F16, bool FP8>
+static cudaError_t launch_rope_d(const RopeArgs& a, unsigned grid, cudaStream_t st) {
+  auto run = [&](auto kernel) {
+    kernel<<<grid, kRopeThreads, 0, st>>>(a);
+    return cudaGetLastError();
+  };
+  const bool norm = a.q_norm || a.k_norm;
+  if (a.interleaved) return norm ? run(rope_and_cache_kernel<D, F16, FP8, true, true>)
+                                 : run(rope_and_cache_kernel<D, F16, FP8, true, false>);
+  return norm ? run(rope_and_cache_kernel<D, F16, FP8, false, true>)
+              : run(rope_and_cache_kernel<D, F16, FP8, false, false>);
 }
 
 cudaError_t launch_rope_and_cache(RopeArgs a, int D, bool f16, bool fp8, cudaStream_t st,
                                   int sms) {
   if (a.num_tokens == 0) return cudaSuccess;
   const int hpi = 256 / D;
-  const int items = (a.H + hpi - 1) / hpi + 2 * ((a.H_kv + hpi - 1) / hpi);
+  const int q_items = (a.H + hpi - 1) / hpi, kv_items = 2 * ((a.H_kv + hpi - 1) / hpi);
   // Few tokens: their heads are shared among more warps, down to one item
-  // each, until about 32 warps per SM have work.
-  const long long want = static_cast<long long>(a.num_tokens) * items / (32LL * sms);
-  const int per = static_cast<int>(want < 1 ? 1 : (want > items ? items : want));
-  a.chunks = (items + per - 1) / per;
-  a.items_per_warp = (items + a.chunks - 1) / a.chunks;
+  // each, until about 24 warps per SM have work.
+  const long long want =
+      static_cast<long long>(a.num_tokens) * (q_items + kv_items) / (24LL * sms);
+  const int per = static_cast<int>(want < 1 ? 1 : (want > kRopeItems ? kRopeItems : want));
+  a.items_per_warp = per;
+  a.q_chunks = (q_items + per - 1) / per;
+  a.chunks = a.q_chunks + (kv_items + per - 1) / per;
   const long long warps = static_cast<long long>(a.num_tokens) * a.chunks;
+  if (warps > 0xffffffffLL - kRopeWarps) return cudaErrorInvalidConfiguration;
   const unsigned grid = static_cast<unsigned>((warps + kRopeWarps - 1) / kRopeWarps);
-  auto run = [&](auto kernel) {
-    kernel<<<grid, kRopeThreads, 0, st>>>(a);
-    return cudaGetLastError();
-  };
-  if (fp8) return f16 ? run(rope_and_cache_kernel<128, true, true>)
-                      : run(rope_and_cache_kernel<128, false, true>);
+  if (fp8) return f16 ? launch_rope_d<128, true, true>(a, grid, st)
+                      : launch_rope_d<128, false, true>(a, grid, st);
   if (f16) {
-    if (D == 256) return run(rope_and_cache_kernel<256, true, false>);
-    if (D == 128) return run(rope_and_cache_kernel<128, true, false>);
-    return run(rope_and_cache_kernel<64, true, false>);
+    if (D == 256) return launch_rope_d<256, true, false>(a, grid, st);
+    if (D == 128) return launch_rope_d<128, true, false>(a, grid, st);
+    return launch_rope_d<64, true, false>(a, grid, st);
   }
-  if (D == 256) return run(rope_and_cache_kernel<256, false, false>);
-  if (D == 128) return run(rope_and_cache_kernel<128, false, false>);
-  return run(rope_and_cache_kernel<64, false, false>);
+  if (D == 256) return launch_rope_d<256, false, false>(a, grid, st);
+  if (D == 128) return launch_rope_d<128, false, false>(a, grid, st);
+  return launch_rope_d<64, false, false>(a, grid, st);
 }
 
 }  // namespace pa
