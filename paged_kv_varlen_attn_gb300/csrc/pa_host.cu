@@ -1200,9 +1200,9 @@ pa_status pa_attn_weights(const void* q, int64_t q_token_stride, const void* key
   if (bt_stride < 0 || num_blocks < 0 || !std::isfinite(softmax_scale) ||
       (causal != 0 && causal != 1))
     return PA_ERR_INVALID_ARG;
-  // Blocks of one launch: 64 keys of a sequence and a KV head each.
+  // Blocks of one launch: 64 keys of a sequence (and 128 of one KV head) each.
   if (num_kv_heads > 65535 ||
-      static_cast<long long>(num_seqs) * cdiv(max_seqlen_k, 64) > 0x7fffffffLL)
+      static_cast<long long>(num_seqs) * cdiv(max_seqlen_k, 64) * num_kv_heads > 0x7fffffffLL)
     return PA_ERR_INVALID_ARG;
   if (num_seqs == 0 || total_q == 0) return PA_OK;
   WeightArgs a{};
@@ -1231,7 +1231,15 @@ pa_status pa_attn_weights(const void* q, int64_t q_token_stride, const void* key
   a.causal = causal;
   a.k_scale = fp8 ? fp8->k_scale : nullptr;
   a.status = dev_status;
-  return launch_attn_weights(a, num_seqs, head_size, dtype == PA_F16, fp8 != nullptr,
+  a.tc_min_rows = 0x7fffffff;
+  CUtensorMap tmQ{};
+  if (tc_tile_rows(a.G) > 0 && static_cast<long long>(max_seqlen_q) * a.G > kWeightsTcMinRows) {
+    if (!encode_q_map(&tmQ, q, head_size, num_heads, total_q, q_token_stride, a.G,
+                      dtype == PA_F16))
+      return PA_ERR_CUDA;
+    a.tc_min_rows = kWeightsTcMinRows;
+  }
+  return launch_attn_weights(tmQ, a, num_seqs, head_size, dtype == PA_F16, fp8 != nullptr,
                              static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? PA_OK
              : PA_ERR_CUDA;

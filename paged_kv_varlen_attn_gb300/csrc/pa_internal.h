@@ -254,6 +254,7 @@ struct EvictArgs {
 cudaError_t launch_evict(const EvictArgs& a, int num_seqs, cudaStream_t st);
 
 // Accumulated attention weight of every cached key (weights.cu).
+constexpr int kWeightsTcMinRows = 64;
 struct WeightArgs {
   const uint16_t* q;
   int64_t q_stride;
@@ -272,8 +273,12 @@ struct WeightArgs {
   int causal;
   const float* k_scale;           // e4m3 pools
   int32_t* status;
+  // Sequences with more packed query rows run on the tensor-core kernel
+  // (INT_MAX: none does, and tmQ is unused).
+  int tc_min_rows;
 };
-cudaError_t launch_attn_weights(const WeightArgs& a, int num_seqs, int D, bool f16, bool fp8,
-                                cudaStream_t st);
+// tmQ: q in tiles of tc_tile_rows(G) packed rows.
+cudaError_t launch_attn_weights(const CUtensorMap& tmQ, const WeightArgs& a, int num_seqs, int D,
+                                bool f16, bool fp8, cudaStream_t st);
 
 }  // namespace pa

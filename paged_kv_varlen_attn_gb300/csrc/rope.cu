@@ -77,7 +77,7 @@ cudaError_t launch_rope_table(float* table, RopeTableArgs& a, cudaStream_t st, i
 // 16 lanes away (half layout: one shuffle per pair of elements). Everything
 // between the load and the store is float32; the store is the only rounding.
 // ---------------------------------------------------------------------------
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;
 constexpr int kRopeWarps = kRopeThreads / 32;
 constexpr int kRopeItems = 8;
 
@@ -107,7 +107,7 @@ __device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
 
 // INTER: interleaved pairs. NORM: q or k (or both) are normed.
 template <int D, bool F16, bool FP8, bool INTER, bool NORM>
-__global__ void __launch_bounds__(kRopeThreads, 3)
+__global__ void __launch_bounds__(kRopeThreads, 6)
 rope_and_cache_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int LPH = D / 8;        // lanes per head
   constexpr int HPI = 32 / LPH;     // heads per item
