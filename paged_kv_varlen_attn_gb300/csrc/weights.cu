@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "device_common.cuh"
 
@@ -181,66 +182,103 @@ weights_kernel(const __grid_constant__ WeightArgs a, int tiles) {
 
 // ---------------------------------------------------------------------------
 // Prompts and prompt chunks: the product on the tensor cores (tcgen05), S^T =
-// K Q^T. A block owns 128 keys of a sequence and KV head -- the M dimension,
-// one TMEM lane each -- and walks the packed query rows that see them in tiles
-// of N = 128 (whole tokens, as in the prefill kernel). The sum over queries is
-// then a sum along a lane's columns: a thread adds up its own key, without
-// shuffles or shared memory, and K is read once.
-//   warp 0        TMA producer: Q tiles into a ring of stages
-//   warp 1        MMA issuer (one lane): S^T of tile t into TMEM buffer t % 2
-//   warps 4-11    two warpgroups; they first bring the K tile into shared
-//                 memory (plain loads through the block table, e4m3 widened to
-//                 the MMA's type), then group g takes tiles g, g + 2, ...:
-//                 p = exp2(S scale log2(e) - lse log2(e)), summed per thread.
-// Bound by the exponentials (16 per clock and SM: 1024 clocks per tile against
-// 620 for its MMAs); two blocks per SM cover each other's start and end. Every
-// wait is bounded; on a timeout the block records PA_DEV_TIMEOUT, waits for its
-// copies in flight, frees its TMEM and returns without writing.
+// K Q^T. A block owns XT * 128 keys of a sequence and KV head -- XT MMA tiles
+// whose M dimension, the TMEM lanes, are keys -- and walks the packed query
+// rows that see them in tiles of N = 128 (whole tokens, as in the prefill
+// kernel). The sum over queries is then a sum along a lane's columns: a thread
+// adds up its own key, without shuffles or shared memory, and K is read once.
+//   warp 0       TMA producer: Q tiles into a ring of stages
+//   warp 1       MMA issuer: the products (query tile t, key tile X) in order,
+//                product n into TMEM buffer n % 3
+//   warps 4-15   three warpgroups; the first XT bring a key tile each from its
+//                pages into TMEM (e4m3 widened to the MMA's type), then group g
+//                takes products g, g + 3, ...: p = exp2(S scale log2(e) - lse
+//                log2(e)), summed per thread and key tile.
+// K is the MMA's A operand and stays in TMEM: from shared memory it would be
+// read again for every query tile, 4 KB beside the 4 KB of Q per 128x128x16
+// MMA, which is all that shared memory gives in the MMA's 64 clocks, and the
+// copies of Q come on top. XT = 2 halves the read of Q (32 KB per tile at head
+// size 128) from L2; at head size 256 K takes the TMEM of both.
+// Under a causal mask the first keys of a sequence are seen by all of its
+// queries and the last by few: a cluster of `parts` blocks shares a key tile
+// (block r takes query tiles r, r + parts, ...) and the first of them adds up
+// the parts' sums in order, read from its own shared memory.
+// Every wait on a barrier in shared memory is bounded; on a timeout the block
+// records PA_DEV_TIMEOUT, waits for its copies in flight, frees its TMEM and
+// returns, and its keys are not written. (Cluster barriers are reached by every
+// thread of the cluster on every path.)
 // ---------------------------------------------------------------------------
 template <int D>
 struct WtCfg {
-  static constexpr int KEYS = 128, COLS = 128;
+  static constexpr int XT = D > 128 ? 1 : 2;           // key tiles of a block
+  static constexpr int KEYS = XT * 128, COLS = 128;
   static constexpr int HALVES = D / 64;
   static constexpr int HALF = 128 * 128;               // 128 rows of 128 bytes
-  static constexpr int TILE = HALVES * HALF;
-  static constexpr int STAGES = D == 64 ? 4 : 2;
-  static constexpr int OFF_Q = TILE;                   // K tile first
-  static constexpr int OFF_NL = OFF_Q + STAGES * TILE; // float[2 groups][2][COLS]
-  static constexpr int OFF_SUM = OFF_NL + 4 * COLS * 4;
-  static constexpr int OFF_BAR = OFF_SUM + KEYS * 4;
-  static constexpr int SMEM_BYTES = OFF_BAR + 256 + 1024;
-  static constexpr int THREADS = 384;
-  static constexpr int BLOCKS = D > 128 ? 1 : 2;       // per SM (shared memory, TMEM)
-  static constexpr int TMEM_COLS = 2 * COLS;
+  static constexpr int TILE = HALVES * HALF;           // a Q tile
+  static constexpr int STAGES = D > 128 ? 3 : 4;
+  static constexpr int GROUPS = 3;                     // warpgroups that add up, S buffers
+  static constexpr int PARTS = 2;                      // largest cluster
+  static constexpr int OFF_NL = STAGES * TILE;         // float[GROUPS][2][COLS]
+  static constexpr int OFF_SUM = OFF_NL + GROUPS * 2 * COLS * 4;   // float[GROUPS][KEYS]
+  static constexpr int OFF_PART = OFF_SUM + GROUPS * KEYS * 4;     // float[PARTS - 1][KEYS]
+  static constexpr int OFF_BAR = OFF_PART + (PARTS - 1) * KEYS * 4;
+  // At least 120 KB: one block per SM, which owns the SM's tensor memory.
+  static constexpr int USED = OFF_BAR + 256 + 1024;
+  static constexpr int SMEM_BYTES = USED > 120 * 1024 ? USED : 120 * 1024;
+  static constexpr int THREADS = 128 + GROUPS * 128;
+  // TMEM columns: K of key tile X at X * D / 2 (two elements a column), S of
+  // buffer b at 128 + 128 b.
+  static constexpr int S_COL = 128, TMEM_COLS = 512;
+  static_assert(XT * D / 2 <= S_COL && S_COL + GROUPS * COLS <= TMEM_COLS, "fits tensor memory");
+  static_assert(SMEM_BYTES <= 227 * 1024, "fits shared memory");
 };
-static_assert(2 * WtCfg<128>::SMEM_BYTES <= 226 * 1024, "two blocks fit an SM");
-static_assert(2 * WtCfg<64>::SMEM_BYTES <= 226 * 1024 && 3 * WtCfg<64>::SMEM_BYTES > 228 * 1024,
-              "two blocks (512 TMEM columns), not three, fit an SM");
-static_assert(WtCfg<256>::SMEM_BYTES <= 227 * 1024, "head size 256 fits shared memory");
 
 struct WtBars {
-  uint64_t k_full;        // K tile in shared memory (256 arrivals)
+  uint64_t k_full;        // K tiles in TMEM (KEYS arrivals)
   uint64_t q_full[4], q_empty[4];
-  uint64_t s_full[2], s_empty[2];
+  uint64_t s_full[3], s_empty[3];   // per S buffer
   uint64_t drain;
   uint32_t tmem_base;
   volatile int abort;
   volatile int issued, consumed;   // Q tiles
+  int part_failed[1];              // of the cluster's other block (written by it)
 };
+static_assert(sizeof(WtBars) <= 256, "the barriers fit their space");
+
+// Clusters: rank, arrive / wait, and a store to this shared-memory location in
+// the block of rank `rank`.
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ void store_remote(const void* p, uint32_t rank, uint32_t v) {
+  uint32_t at;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
 
 template <int D, bool F16, bool FP8>
-__global__ void __launch_bounds__(WtCfg<D>::THREADS, WtCfg<D>::BLOCKS)
+__global__ void __launch_bounds__(WtCfg<D>::THREADS, 1)
 weights_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ WeightArgs a,
-                  int num_seqs) {
+                  int num_seqs, int parts) {
   using C = WtCfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   WtBars* bars = reinterpret_cast<WtBars*>(smem + C::OFF_BAR);
-  // KV head fastest, then sequence, then key tile: under a causal mask the
-  // first keys are seen by the most queries, so blocks start longest first.
-  const int hk = blockIdx.x % a.H_kv;
-  const int ts = blockIdx.x / a.H_kv;
+  // Part fastest, then KV head, sequence, keys: under a causal mask the first
+  // keys are seen by the most queries, so blocks start longest first.
+  const int unit = blockIdx.x / parts;
+  const int part = parts > 1 ? static_cast<int>(cluster_rank()) : 0;
+  const int hk = unit % a.H_kv;
+  const int ts = unit / a.H_kv;
   const int s = ts % num_seqs;
   const int key0 = ts / num_seqs * C::KEYS;
   int q0, q_len, kv;
@@ -249,16 +287,56 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
   const int G = a.G, TR = tc_tile_rows(G), TPT = TR / G;   // rows, tokens of a Q tile
   const int past = kv - q_len;
   const int i0 = a.causal ? max(0, key0 - past) : 0;       // first query that sees a key
-  const int ntiles = (q_len - i0 + TPT - 1) / TPT;
+  // This block's query tiles: tile t starts at query first + t step.
+  const int all_tiles = (q_len - i0 + TPT - 1) / TPT;
+  const int ntiles = (all_tiles - part + parts - 1) / parts;
+  const int step = parts * TPT, first = i0 + part * TPT;
+  // Key tiles of the block that hold keys, and the query tiles that the second
+  // one leaves out (none of their queries is at its first key yet).
+  const int xt = C::XT == 2 && key0 + 128 < kv ? 2 : 1;
+  int skip1 = 0;
+  if (C::XT == 2 && a.causal) {
+    const int d = key0 + 128 - past - first - TPT;
+    skip1 = d >= 0 ? min(ntiles, d / step + 1) : 0;
+  }
+  // Products in order: query tile after query tile, both key tiles of each
+  // (the first skip1 with key tile 0 alone).
+  const int alone = xt == 1 ? ntiles : skip1;
+  const int nprod = alone + 2 * (ntiles - alone);
+  auto tile_of = [&](int n) { return n < alone ? n : alone + ((n - alone) >> 1); };
+  auto key_tile_of = [&](int n) { return n < alone ? 0 : (n - alone) & 1; };
+  if (parts > 1) cluster_arrive();   // this block has started (see the end)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+  // The key rows are asked for first: thread `tid` of warpgroup X brings key
+  // X * 128 + tid (zeros past the sequence and for pages outside the pool).
+  const int wg = (warp - 4) >> 2, tid = threadIdx.x & 127;
+  constexpr int EB = FP8 ? 1 : 2;
+  constexpr int KV16 = D * EB / 16;                    // 16-byte pieces of a key
+  constexpr int KB = KV16 < 16 ? KV16 : 16;            // held at a time
+  const uint4* krow = nullptr;
+  uint4 kx[KB];
+  if (warp >= 4 && wg < C::XT) {
+    const int j = key0 + wg * 128 + tid;
+    if (j < kv) {
+      const int lp = j / a.bs;
+      const int page = __ldg(a.bt + static_cast<int64_t>(s) * a.bt_stride + lp);
+      if (page >= 0 && page < a.num_blocks)
+        krow = reinterpret_cast<const uint4*>(
+            a.kc + page * a.block_stride_bytes +
+            (static_cast<int64_t>(j - lp * a.bs) * a.H_kv + hk) * (D * EB));
+    }
+#pragma unroll
+    for (int u = 0; u < KB; ++u) kx[u] = krow ? __ldg(krow + u) : make_uint4(0, 0, 0, 0);
+  }
+
   if (threadIdx.x == 0) {
-    mbar_init(&bars->k_full, 256);
+    mbar_init(&bars->k_full, C::KEYS);
     for (int i = 0; i < C::STAGES; ++i) {
       mbar_init(&bars->q_full[i], 1);
       mbar_init(&bars->q_empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < C::GROUPS; ++i) {
       mbar_init(&bars->s_full[i], 1);
       mbar_init(&bars->s_empty[i], 128);
     }
@@ -271,12 +349,22 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     tmem_alloc(&bars->tmem_base, C::TMEM_COLS);
     tmem_relinquish();
   }
+  // Rows of a Q stage that no copy fills (groups that do not divide 128):
+  // zeros, so that their columns are finite.
+  if (TR < C::COLS) {
+    for (int st = 0; st < C::STAGES; ++st)
+      for (int idx = threadIdx.x; idx < (C::COLS - TR) * C::HALVES * 8; idx += C::THREADS) {
+        const int r = TR + idx / (C::HALVES * 8), rem = idx % (C::HALVES * 8);
+        *reinterpret_cast<uint4*>(smem + st * C::TILE + (rem >> 3) * C::HALF + r * 128 +
+                                  (rem & 7) * 16) = make_uint4(0, 0, 0, 0);
+      }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
-  float sum = 0.f;
-  bool ok = true;
+  float sum[2] = {0.f, 0.f};   // per key tile
 
   if (warp == 0) {
     // -------------------------------------------------------------- producer
@@ -291,120 +379,97 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         if (bars->abort) break;
         mbar_arrive_expect_tx(&bars->q_full[st], C::HALVES * TR * 128);
         for (int h = 0; h < C::HALVES; ++h)
-          tma_load_3d(smem + C::OFF_Q + st * C::TILE + h * C::HALF, &tmQ, &bars->q_full[st], h * 64,
-                      hk * G, q0 + i0 + t * TPT);
+          tma_load_3d(smem + st * C::TILE + h * C::HALF, &tmQ, &bars->q_full[st], h * 64,
+                      hk * G, q0 + first + t * step);
         bars->issued = t + 1;
       }
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t idesc = mma_idesc(C::KEYS, C::COLS, false, Elem<F16>::kTcFormat);
-      const uint64_t kdesc = smem_desc_sw128(smem_u32(smem), 16, 1024);
-      const uint64_t qdesc = smem_desc_sw128(smem_u32(smem + C::OFF_Q), 16, 1024);
-      ok = mbar_wait(&bars->k_full, 0);
-      for (int t = 0; ok && t < ntiles; ++t) {
-        const int st = t % C::STAGES, b = t & 1;
-        if (bars->abort) { ok = false; break; }
-        if (!(ok = mbar_wait(&bars->q_full[st], (t / C::STAGES) & 1))) break;
-        bars->consumed = t + 1;
-        if (t >= 2 && !(ok = mbar_wait(&bars->s_empty[b], ((t >> 1) - 1) & 1))) break;
-        tc_fence_after();
-        const uint64_t qd = qdesc + static_cast<uint32_t>(st * (C::TILE >> 4));
+    // The whole warp walks the loop and one elected lane issues: with the
+    // control flow uniform, descriptors live in uniform registers.
+    constexpr uint32_t idesc = mma_idesc(128, C::COLS, false, Elem<F16>::kTcFormat);
+    const uint32_t lead = elect_one();
+    const uint64_t qdesc = smem_desc_sw128(smem_u32(smem), 16, 1024);
+    bool ok = __all_sync(0xffffffffu, mbar_wait(&bars->k_full, 0));
+    tc_fence_after();
+    for (int n = 0, b = 0, use = 0; ok && n < nprod; ++n) {
+      const int t = tile_of(n), x = key_tile_of(n);
+      const int st = t % C::STAGES;
+      if (x == 0) {
+        ok = __all_sync(0xffffffffu,
+                        !bars->abort && mbar_wait(&bars->q_full[st], (t / C::STAGES) & 1));
+        if (!ok) break;
+        if (lane == 0) bars->consumed = t + 1;
+      }
+      ok = __all_sync(0xffffffffu, use == 0 || mbar_wait(&bars->s_empty[b], (use - 1) & 1));
+      if (!ok) break;
+      tc_fence_after();
+      const uint64_t qd = qdesc + static_cast<uint32_t>(st * (C::TILE >> 4));
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = ((kk >> 2) * C::HALF + (kk & 3) * 32) >> 4;
-          tc_mma(tmem + b * C::COLS, kdesc + off, qd + off, idesc, kk > 0);
-        }
-        tc_commit(&bars->s_full[b]);
-        tc_commit(&bars->q_empty[st]);
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = ((kk >> 2) * C::HALF + (kk & 3) * 32) >> 4;
+        tc_mma_ts_if(lead, tmem + C::S_COL + b * C::COLS, tmem + x * (D / 2) + kk * 8, qd + off,
+                     idesc, kk > 0);
       }
-      if (!ok) {
-        bars->abort = 1;
-        tc_commit(&bars->drain);   // arrives once every MMA issued above has completed
-        mbar_wait(&bars->drain, 0);
-      }
+      tc_commit_if(lead, &bars->s_full[b]);
+      if (x == 1 || n < alone) tc_commit_if(lead, &bars->q_empty[st]);   // the tile's last product
+      if (++b == C::GROUPS) b = 0, ++use;
+    }
+    if (!ok) {
+      bars->abort = 1;
+      tc_commit_if(lead, &bars->drain);   // arrives once every MMA issued above has completed
+      mbar_wait(&bars->drain, 0);
     }
   } else if (warp >= 4) {
-    // -------------------------------------------------------- K tile, sums
-    const int et = threadIdx.x - 128;      // 0 .. 255
-    const int32_t* bt = a.bt + static_cast<int64_t>(s) * a.bt_stride;
-    {
-      constexpr int EB = FP8 ? 1 : 2;
-      constexpr int CPR = D * EB / 16;     // 16-byte chunks of a key
-      for (int idx = et; idx < C::KEYS * CPR; idx += 256) {
-        const int r = idx / CPR, c = idx % CPR;
-        const int j = key0 + r;
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (j < kv) {
-          const int lp = j / a.bs;
-          const int page = __ldg(bt + lp);
-          if (page >= 0 && page < a.num_blocks)
-            x = __ldg(reinterpret_cast<const uint4*>(
-                          a.kc + page * a.block_stride_bytes +
-                          (static_cast<int64_t>(j - lp * a.bs) * a.H_kv + hk) * (D * EB)) +
-                      c);
+    // -------------------------------------------------------- K tiles, sums
+    const uint32_t tm_row = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    if (wg < C::XT) {
+      // Row tid of key tile wg: element pairs 2c, 2c + 1 in column c.
+#pragma unroll
+      for (int u0 = 0; u0 < KV16; u0 += KB) {
+        if (u0 > 0) {
+#pragma unroll
+          for (int u = 0; u < KB; ++u)
+            kx[u] = krow ? __ldg(krow + u0 + u) : make_uint4(0, 0, 0, 0);
         }
-        auto store = [&](int chunk, const uint4& y) {
-          *reinterpret_cast<uint4*>(smem + (chunk >> 3) * C::HALF + r * 128 +
-                                    (((chunk & 7) ^ (r & 7)) << 4)) = y;
-        };
-        if constexpr (FP8) {
-          store(2 * c, make_uint4(widen_e4m3x2<F16>(x.x), widen_e4m3x2<F16>(x.x >> 16),
-                                  widen_e4m3x2<F16>(x.y), widen_e4m3x2<F16>(x.y >> 16)));
-          store(2 * c + 1, make_uint4(widen_e4m3x2<F16>(x.z), widen_e4m3x2<F16>(x.z >> 16),
-                                      widen_e4m3x2<F16>(x.w), widen_e4m3x2<F16>(x.w >> 16)));
-        } else {
-          store(c, x);
+        constexpr int W = FP8 ? 8 : 4;                 // columns of 16 bytes
+#pragma unroll
+        for (int c0 = 0; c0 < KB * W; c0 += 32) {
+          uint32_t v[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            const uint4& x = kx[(c0 + c) / W];
+            const uint32_t word[4] = {x.x, x.y, x.z, x.w};
+            if constexpr (FP8) {
+              const uint32_t two = word[((c0 + c) % W) / 2];
+              v[c] = widen_e4m3x2<F16>((c & 1) ? two >> 16 : two);
+            } else {
+              v[c] = word[(c0 + c) % W];
+            }
+          }
+          tmem_st32(tm_row + wg * (D / 2) + u0 * W + c0, v);
         }
       }
-      // Rows of a Q stage that no copy fills (groups that do not divide 128):
-      // zeros, so that their columns are finite.
-      for (int st = 0; st < C::STAGES; ++st)
-        for (int idx = et; idx < (C::COLS - TR) * C::HALVES * 8; idx += 256) {
-          const int r = TR + idx / (C::HALVES * 8), rem = idx % (C::HALVES * 8);
-          *reinterpret_cast<uint4*>(smem + C::OFF_Q + st * C::TILE + (rem >> 3) * C::HALF +
-                                    r * 128 + (rem & 7) * 16) = make_uint4(0, 0, 0, 0);
-        }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      tmem_wait_st();
+      tc_fence_before();
       mbar_arrive(&bars->k_full);
     }
-    const int grp = (warp - 4) >> 2;       // warpgroup: tiles grp, grp + 2, ...
-    const int tid = et & 127;              // TMEM lane: key key0 + tid
-    const uint32_t tm = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + grp * C::COLS;
-    float* nl = reinterpret_cast<float*>(smem + C::OFF_NL) + grp * 2 * C::COLS;
+    const uint32_t tm = tm_row + C::S_COL + wg * C::COLS;
+    float* nl = reinterpret_cast<float*>(smem + C::OFF_NL) + wg * 2 * C::COLS;
     const float sl2 = FP8 ? a.scale_log2 * __ldg(a.k_scale + hk) : a.scale_log2;
     // This thread also fetches the LSE of column tid: token tid / G of a tile.
     const int ctok = tid / G;
     const float* lse_row = a.lse + static_cast<int64_t>(hk * G + tid - ctok * G) * a.total_q + q0;
     auto fetch = [&](int t) -> float {
-      const int i = i0 + t * TPT + ctok;
+      const int i = first + t * step + ctok;
       if (tid >= TR || i >= q_len) return -INFINITY;
       const float v = __ldg(lse_row + i);
       return v == -INFINITY ? -INFINITY : -v * kLog2e;   // a row that saw nothing adds nothing
     };
-    float next = grp < ntiles ? fetch(grp) : 0.f;
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int t = grp, it = 0; t < ntiles; t += 2, ++it) {
-      float* nlb = nl + (it & 1) * C::COLS;
-      nlb[tid] = next;
-      asm volatile("bar.sync %0, 128;" ::"r"(1 + grp) : "memory");
-      if (t + 2 < ntiles) next = fetch(t + 2);
-      // Columns [c0, c1) of the tile see this key: queries from its own
-      // position on, rows of the sequence.
-      const int tok0 = i0 + t * TPT;
-      const int c0 = a.causal ? max(0, (key0 + tid - past - tok0) * G) : 0;
-      const int c1 = min(TR, (q_len - tok0) * G);
-      const bool edge = tok0 + TPT > q_len || (a.causal && tok0 < key0 + C::KEYS - 1 - past);
-      // A warp whose wait gave up goes on through the group's barriers without
-      // work, so that no other warp waits for it.
-      if (ok) ok = !bars->abort && mbar_wait(&bars->s_full[grp], it & 1);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) {
-        bars->abort = 1;
-        continue;
-      }
-      tc_fence_after();
+    float next = wg < nprod ? fetch(tile_of(wg)) : 0.f;
+    float acc[4];
+    auto sum_tile = [&](const float* nlb, int c0, int c1, auto masked) {
 #pragma unroll
       for (int c = 0; c < C::COLS / 32; ++c) {
         uint32_t v[32];
@@ -412,51 +477,106 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         tmem_wait_ld();
         if (c == C::COLS / 32 - 1) {
           tc_fence_before();
-          mbar_arrive(&bars->s_empty[grp]);
+          mbar_arrive(&bars->s_empty[wg]);
         }
 #pragma unroll
         for (int e = 0; e < 32; e += 4) {
           const float4 n4 = *reinterpret_cast<const float4*>(nlb + c * 32 + e);
-          float y0, y1, y2, y3;
-          ffma2(y0, y1, __uint_as_float(v[e]), __uint_as_float(v[e + 1]), sl2, sl2, n4.x, n4.y);
-          ffma2(y2, y3, __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]), sl2, sl2, n4.z, n4.w);
-          float p0 = fast_exp2(y0), p1 = fast_exp2(y1), p2 = fast_exp2(y2), p3 = fast_exp2(y3);
-          if (edge) {
-            const int col = c * 32 + e;
-            p0 = col >= c0 && col < c1 ? p0 : 0.f;
-            p1 = col + 1 >= c0 && col + 1 < c1 ? p1 : 0.f;
-            p2 = col + 2 >= c0 && col + 2 < c1 ? p2 : 0.f;
-            p3 = col + 3 >= c0 && col + 3 < c1 ? p3 : 0.f;
+          float y[4];
+          ffma2(y[0], y[1], __uint_as_float(v[e]), __uint_as_float(v[e + 1]), sl2, sl2, n4.x, n4.y);
+          ffma2(y[2], y[3], __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]), sl2, sl2, n4.z,
+                n4.w);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            y[k] = fast_exp2(y[k]);
+            if constexpr (decltype(masked)::value) {
+              const int col = c * 32 + e + k;
+              y[k] = col >= c0 && col < c1 ? y[k] : 0.f;
+            }
           }
-          fadd2(acc[0], acc[1], acc[0], acc[1], p0, p1);
-          fadd2(acc[2], acc[3], acc[2], acc[3], p2, p3);
+          fadd2(acc[0], acc[1], acc[0], acc[1], y[0], y[1]);
+          fadd2(acc[2], acc[3], acc[2], acc[3], y[2], y[3]);
         }
       }
-      sum += (acc[0] + acc[1]) + (acc[2] + acc[3]);
+    };
+    bool ok = true;
+    for (int n = wg, it = 0; n < nprod; n += C::GROUPS, ++it) {
+      const int t = tile_of(n), x = key_tile_of(n);
+      float* nlb = nl + (it & 1) * C::COLS;
+      nlb[tid] = next;
+      asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory");
+      if (n + C::GROUPS < nprod) next = fetch(tile_of(n + C::GROUPS));
+      // Columns [c0, c1) of the tile see this key: queries from its own
+      // position on, rows of the sequence.
+      const int tok0 = first + t * step;
+      const int c0 = a.causal ? max(0, (key0 + x * 128 + tid - past - tok0) * G) : 0;
+      const int c1 = min(TR, (q_len - tok0) * G);
+      const bool edge =
+          tok0 + TPT > q_len || (a.causal && tok0 < key0 + x * 128 + 127 - past);
+      // A warp whose wait gave up goes on through the group's barriers without
+      // work, so that no other warp waits for it.
+      if (ok) ok = !bars->abort && mbar_wait(&bars->s_full[wg], it & 1);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) {
+        bars->abort = 1;
+        continue;
+      }
+      tc_fence_after();
       acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
+      // Two bodies, so that a tile that every key sees whole pays no select.
+      if (edge)
+        sum_tile(nlb, c0, c1, std::true_type{});
+      else
+        sum_tile(nlb, c0, c1, std::false_type{});
+      const float got = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+      sum[0] += x == 0 ? got : 0.f;
+      sum[1] += x == 0 ? 0.f : got;
     }
-    if (grp == 1) reinterpret_cast<float*>(smem + C::OFF_SUM)[tid] = sum;
+    float* mine = reinterpret_cast<float*>(smem + C::OFF_SUM) + wg * C::KEYS + tid;
+    mine[0] = sum[0];
+    if (C::XT == 2) mine[128] = sum[1];
   }
 
   // ---------------------------------------------------------------- teardown
   tc_fence_before();
   __syncthreads();
-  const bool failed = bars->abort != 0;
+  bool failed = bars->abort != 0;
   if (threadIdx.x == 0 && failed) {
     flag_status(a.status, PA_DEV_TIMEOUT);
     for (int t = bars->consumed; t < bars->issued; ++t)
       if (!mbar_wait(&bars->q_full[t % C::STAGES], (t / C::STAGES) & 1)) break;
   }
-  if (!failed && warp >= 4 && warp < 8) {
-    const int j = key0 + threadIdx.x - 128;
+  // One thread per key goes on.
+  const int key = static_cast<int>(threadIdx.x) - 128;
+  const bool adds = key >= 0 && key < C::KEYS;
+  float total = 0.f;
+  if (adds)
+    for (int g = 0; g < C::GROUPS; ++g)
+      total += reinterpret_cast<const float*>(smem + C::OFF_SUM)[g * C::KEYS + key];
+  float* others = reinterpret_cast<float*>(smem + C::OFF_PART);
+  if (parts > 1) {
+    // Every block of the cluster has started (its shared memory is there);
+    // the sums go to block 0; block 0 sees them, and nobody leaves before.
+    cluster_wait();
+    if (part > 0) {
+      if (adds) store_remote(others + (part - 1) * C::KEYS + key, 0, __float_as_uint(total));
+      if (threadIdx.x == 0) store_remote(&bars->part_failed[part - 1], 0, failed);
+    }
+    cluster_arrive();
+    cluster_wait();
+    if (part == 0)
+      for (int r = 1; r < parts; ++r) failed |= bars->part_failed[r - 1] != 0;
+  }
+  if (!failed && adds && part == 0) {
+    const int j = key0 + key;
     if (j < kv) {
       const int lp = j / a.bs;
       const int page = __ldg(a.bt + static_cast<int64_t>(s) * a.bt_stride + lp);
       if (page >= 0 && page < a.num_blocks) {
+        for (int r = 1; r < parts; ++r) total += others[(r - 1) * C::KEYS + key];
         float* w = a.weights + page * a.weights_stride + static_cast<int64_t>(hk) * a.bs +
                    (j - lp * a.bs);
-        *w = (j >= past ? 0.f : *w) +
-             (sum + reinterpret_cast<const float*>(smem + C::OFF_SUM)[threadIdx.x - 128]);
+        *w = (j >= past ? 0.f : *w) + total;
       } else {
         flag_status(a.status, PA_DEV_BAD_PAGE);
       }
@@ -468,6 +588,8 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     tmem_dealloc(tmem, C::TMEM_COLS);
   }
 }
+
+constexpr long long kPairUnits = 304;
 
 template <int D, bool F16, bool FP8>
 static cudaError_t launch_weights_d(const CUtensorMap& tmQ, const WeightArgs& a, int num_seqs,
@@ -489,11 +611,28 @@ static cudaError_t launch_weights_d(const CUtensorMap& tmQ, const WeightArgs& a,
       if (e != cudaSuccess) return e;
       if (known) configured[dev].store(true, std::memory_order_release);
     }
-    const long long blocks =
+    const long long units =
         static_cast<long long>((keys + C::KEYS - 1) / C::KEYS) * num_seqs * a.H_kv;
-    if (blocks > 0) {
-      weights_tc_kernel<D, F16, FP8>
-          <<<static_cast<unsigned>(blocks), C::THREADS, C::SMEM_BYTES, st>>>(tmQ, a, num_seqs);
+    if (units > 0) {
+      // Fewer than two key tiles per SM: two blocks share each, which halves
+      // the longest block. 8 KV heads, prompts of 2,500-4,096 tokens: one
+      // prompt of 4,096 (128 tiles of 256 keys) 74.0 us in pairs against 123.8;
+      // two (184) 85.3 against 96.5; four (about 400) 163 against 147; sixteen
+      // 755 against 647.
+      const int parts = units < kPairUnits ? 2 : 1;
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(static_cast<unsigned>(units * parts));
+      cfg.blockDim = dim3(C::THREADS);
+      cfg.dynamicSmemBytes = C::SMEM_BYTES;
+      cfg.stream = st;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = parts;
+      attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = parts > 1 ? 1 : 0;
+      e = cudaLaunchKernelEx(&cfg, weights_tc_kernel<D, F16, FP8>, tmQ, a, num_seqs, parts);
+      if (e != cudaSuccess) return e;
       e = cudaGetLastError();
       if (e != cudaSuccess) return e;
     }
