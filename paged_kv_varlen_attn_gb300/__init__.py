@@ -188,11 +188,12 @@ def _stream(device):
 def _call(fn, where, device, *args):
     """Call an entry point whose last argument is the stream, on the tensors'
     device (entered only if it is not the current one)."""
-    if device.index == torch.cuda.current_device():
-        code = fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
+    index = device.index
+    if index == torch._C._cuda_getDevice():
+        code = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(device):
-            code = fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
+            code = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     if code != PA_OK:
         raise PAError(code, where)
 
@@ -222,17 +223,20 @@ def _sm_count(device) -> int:
 
 def _row_stride(t):
     """Token stride of a [T, heads, D] tensor whose [heads, D] rows are contiguous."""
-    if t.dim() != 3 or t.stride(2) != 1 or t.stride(1) != t.shape[2]:
+    st = t.stride()
+    if len(st) != 3 or st[2] != 1 or st[1] != t.shape[2]:
         raise ValueError("tensor must be [tokens, heads, head_size] with contiguous rows")
-    return t.stride(0)
+    return st[0]
 
 
 def _cache_stride(c):
-    if c.dim() != 4 or c.stride(3) != 1 or c.stride(2) != c.shape[3] or \
-            c.stride(1) != c.shape[2] * c.shape[3]:
-        raise ValueError("cache must be [num_blocks, block_size, num_kv_heads, head_size] with "
-                         "contiguous pages")
-    return c.stride(0)
+    st = c.stride()
+    if len(st) == 4:
+        _, _, heads, dim = c.shape
+        if st[3] == 1 and st[2] == dim and st[1] == heads * dim:
+            return st[0]
+    raise ValueError("cache must be [num_blocks, block_size, num_kv_heads, head_size] with "
+                     "contiguous pages")
 
 
 # ---------------------------------------------------------------------------
@@ -283,7 +287,8 @@ def alloc_workspace(nbytes, device):
 
 def _attn_common(q, key_cache, value_cache, cu_seqlens_q, seqused_k, block_table):
     _need_cuda(q, key_cache, value_cache, cu_seqlens_q, seqused_k, block_table)
-    if key_cache.stride(0) != value_cache.stride(0) or key_cache.shape != value_cache.shape:
+    if key_cache is not value_cache and (key_cache.stride(0) != value_cache.stride(0) or
+                                         key_cache.shape != value_cache.shape):
         raise ValueError("key and value caches must have the same shape and page stride")
     for t, name in ((cu_seqlens_q, "cu_seqlens_q"), (seqused_k, "seqused_k"),
                     (block_table, "block_table")):
@@ -471,6 +476,8 @@ def _scales(s, hk, device):
     num_kv_heads values."""
     if not torch.is_tensor(s):
         return torch.full((hk,), float(s), dtype=torch.float32, device=device)
+    if s.dtype == torch.float32 and s.shape == (hk,) and s.device == device and s.is_contiguous():
+        return s
     s = s.to(device=device, dtype=torch.float32).reshape(-1)
     if s.numel() == 1:
         s = s.expand(hk)
@@ -649,11 +656,13 @@ def rope_and_cache(q, key, value, positions, cos_sin, key_cache, value_cache, sl
     lib = load_library()
     _need_cuda(q, key, value, positions, cos_sin, key_cache, value_cache, slot_mapping, q_norm,
                k_norm, out, dev_status)
-    if key_cache.stride(0) != value_cache.stride(0) or key_cache.shape != value_cache.shape:
+    shape = key_cache.shape
+    if key_cache.stride() != value_cache.stride() or shape != value_cache.shape:
         raise ValueError("key and value caches must have the same shape and page stride")
-    nb, bs, hk, d = key_cache.shape
-    T, H = q.shape[0], q.shape[1]
-    if q.shape != (T, H, d) or key.shape != (T, hk, d) or value.shape != (T, hk, d):
+    page = _cache_stride(key_cache)
+    nb, bs, hk, d = shape
+    T, H, dq = q.shape
+    if dq != d or key.shape != (T, hk, d) or value.shape != (T, hk, d):
         raise ValueError("q, key and value must be [tokens, heads, head_size] of the caches' "
                          "heads and head size")
     for t, name in ((positions, "positions"), (slot_mapping, "slot_mapping")):
@@ -665,8 +674,9 @@ def rope_and_cache(q, key, value, positions, cos_sin, key_cache, value_cache, sl
     _f32_vector(k_norm, d, "k_norm")
     if (k_scale is None) != (v_scale is None):
         raise ValueError("k_scale and v_scale go together")
+    device = q.device
     if out is None:
-        out = torch.empty((T, H, d), dtype=q.dtype, device=q.device)
+        out = torch.empty((T, H, d), dtype=q.dtype, device=device)
     elif out.shape != q.shape:
         raise ValueError("out must have the shape of q")
     if k_scale is None:
@@ -674,15 +684,17 @@ def rope_and_cache(q, key, value, positions, cos_sin, key_cache, value_cache, sl
     else:
         _fp8_pool(key_cache), _fp8_pool(value_cache)
         dtype = _dtype_code(q, key, value, out)
-        desc, keep = _fp8_desc(k_scale, v_scale, hk, q.device)
-    rope = Rope(cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], int(bool(interleaved)),
-                None if q_norm is None else q_norm.data_ptr(),
-                None if k_norm is None else k_norm.data_ptr(), float(eps))
-    _call(lib.pa_rope_and_cache, "pa_rope_and_cache", q.device,
-          ctypes.byref(rope), _ptr(positions), _ptr(q), _row_stride(q), _ptr(out),
-          _row_stride(out), ctypes.byref(_kv_update(key, value, slot_mapping)), _ptr(key_cache),
-          _ptr(value_cache), _cache_stride(key_cache), H, hk, d, bs, nb,
-          None if desc is None else ctypes.byref(desc), dtype, _ptr(dev_status))
+        desc, keep = _fp8_desc(k_scale, v_scale, hk, device)
+    rows, rot = cos_sin.shape
+    rope = Rope(cos_sin.data_ptr(), rows, rot, 1 if interleaved else 0, _ptr(q_norm),
+                _ptr(k_norm), eps)
+    update = KvUpdate(key.data_ptr(), value.data_ptr(), _row_stride(key), _row_stride(value),
+                      slot_mapping.data_ptr(), T)
+    _call(lib.pa_rope_and_cache, "pa_rope_and_cache", device,
+          ctypes.byref(rope), positions.data_ptr(), q.data_ptr(), _row_stride(q), out.data_ptr(),
+          _row_stride(out), ctypes.byref(update), key_cache.data_ptr(), value_cache.data_ptr(),
+          page, H, hk, d, bs, nb, None if desc is None else ctypes.byref(desc), dtype,
+          _ptr(dev_status))
     del keep
     return out
 
@@ -741,28 +753,30 @@ def evict(key_cache, value_cache, weights, seqused_k, block_table, max_seqlen_k,
     lib = load_library()
     _need_cuda(key_cache, value_cache, weights, seqused_k, block_table, kept, new_lens,
                dev_status)
-    if key_cache.stride(0) != value_cache.stride(0) or key_cache.shape != value_cache.shape or \
+    if key_cache.stride() != value_cache.stride() or key_cache.shape != value_cache.shape or \
             key_cache.dtype != value_cache.dtype:
         raise ValueError("key and value caches must have the same shape, type and page stride")
     nb, bs, hk, d = key_cache.shape
-    S = seqused_k.numel()
-    for t, name in ((seqused_k, "seqused_k"), (block_table, "block_table")):
-        if t.dtype != torch.int32:
-            raise ValueError(f"{name} must be int32")
-    if block_table.dim() != 2 or block_table.stride(1) != 1 or block_table.shape[0] != S:
+    S, = seqused_k.shape
+    if seqused_k.dtype != torch.int32 or block_table.dtype != torch.int32 or \
+            not seqused_k.is_contiguous():
+        raise ValueError("seqused_k (contiguous) and block_table must be int32")
+    row, unit = block_table.stride()
+    if unit != 1 or block_table.shape[0] != S:
         raise ValueError("block_table must be [num_seqs, max_blocks] with unit column stride")
+    device = key_cache.device
     if kept is None:
-        kept = torch.empty((S, hk, max(int(budget), 0)), dtype=torch.int32,
-                           device=key_cache.device)
+        kept = torch.empty((S, hk, max(int(budget), 0)), dtype=torch.int32, device=device)
+    elif kept.dtype != torch.int32 or kept.shape != (S, hk, budget) or not kept.is_contiguous():
+        raise ValueError("kept must be a contiguous int32 [num_seqs, num_kv_heads, budget] tensor")
     if new_lens is None:
-        new_lens = torch.empty(S, dtype=torch.int32, device=key_cache.device)
-    for t, shape, name in ((kept, (S, hk, budget), "kept"), (new_lens, (S,), "new_lens")):
-        if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape}")
-    _call(lib.pa_evict, "pa_evict", key_cache.device,
+        new_lens = torch.empty(S, dtype=torch.int32, device=device)
+    elif new_lens.dtype != torch.int32 or new_lens.shape != (S,) or not new_lens.is_contiguous():
+        raise ValueError("new_lens must be a contiguous int32 tensor of one value per sequence")
+    _call(lib.pa_evict, "pa_evict", device,
           _ptr(key_cache), _ptr(value_cache), _cache_stride(key_cache), _ptr(weights),
           _weights_stride(weights, nb, bs, hk), _ptr(seqused_k), _ptr(block_table),
-          block_table.stride(0), S, int(max_seqlen_k), hk, d, bs, nb,
+          row, S, int(max_seqlen_k), hk, d, bs, nb,
           key_cache.element_size(), int(budget), int(num_first), int(num_recent), _ptr(kept),
           _ptr(new_lens), _ptr(dev_status))
     return kept, new_lens
