@@ -150,12 +150,13 @@ __device__ __forceinline__ void zero_v_hidden(uint8_t* vtile, int tile_key0, int
 // Consumers. RGN = number of 16-row groups (1, 2 or 4); 4 / RGN warps share
 // each group and split every key tile between them.
 // ---------------------------------------------------------------------------
-// WIN: kb and the tiles are numbered as in geo; ke is the last visible key + 1.
+// WIN: keys (kv_len, kb, ke) are numbered as in geo; no query of the item sees
+// keys [a.first, win_lo).
 template <int D, int RGN, bool FP8, bool F16, bool WIN>
 __device__ __forceinline__ void split_consumer(const AttnArgs& a, uint8_t* ring, SplitShared sh,
                                                int hk, int seg, int rt, int j, int q_start,
                                                int q_len, int kv_len, int kb, int ke, int ntiles,
-                                               int nsplit, int slot_base, const WinGeo& geo) {
+                                               int nsplit, int slot_base, int win_lo) {
   using C = SplitCfg<D, FP8>;
   using E = Elem<F16>;
   static_assert(!FP8 || D == 128, "FP8 pools: head size 128");
@@ -242,12 +243,12 @@ __device__ __forceinline__ void split_consumer(const AttnArgs& a, uint8_t* ring,
     consumed = t + 1;
     uint8_t* ktile = ring + s * C::STAGE_BYTES;
     uint8_t* vtile = ktile + C::TILE_BYTES;
-    const int tile_key0 = WIN ? geo.key(kb + t * C::BN) : kb + t * C::BN;
+    const int tile_key0 = kb + t * C::BN;
     const int key_base = tile_key0 + slice0;
     if (key_base < ke && key_base <= lim_max) {
       zero_v_tail<KW, C::HALVES, C::HALF_BYTES>(vtile, tile_key0, slice0, kv_len, lane);
       if constexpr (WIN)
-        zero_v_hidden<KW, C::HALVES, C::HALF_BYTES>(vtile, tile_key0, slice0, a.first, geo.lo, lane);
+        zero_v_hidden<KW, C::HALVES, C::HALF_BYTES>(vtile, tile_key0, slice0, a.first, win_lo, lane);
 #pragma unroll
       for (int ch = 0; ch < NCH; ++ch) {
       const int cs = slice0 + ch * KWC;        // first key of the chunk in the tile
@@ -576,7 +577,7 @@ __device__ __forceinline__ void split_consumer_fp8_dec(const AttnArgs& a, uint8_
                                                        SplitShared sh, int hk, int rt, int j,
                                                        int q_start, int q_len, int kv_len, int kb,
                                                        int ke, int ntiles, int nsplit,
-                                                       int slot_base, const WinGeo& geo) {
+                                                       int slot_base, int win_lo) {
   using C = SplitCfg<128, true>;
   constexpr int D = 128;
   constexpr int KW = C::BN / 4;     // keys per warp per tile
@@ -692,12 +693,12 @@ __device__ __forceinline__ void split_consumer_fp8_dec(const AttnArgs& a, uint8_
     consumed = t + 1;
     const uint8_t* ktile = ring + s * C::STAGE_BYTES;
     uint8_t* vtile = ring + s * C::STAGE_BYTES + C::TILE_BYTES;
-    const int tile_key0 = WIN ? geo.key(kb + t * C::BN) : kb + t * C::BN;
+    const int tile_key0 = kb + t * C::BN;
     const int ckey = tile_key0 + slice0;
     if (ckey < ke && ckey <= lim_max) {
       zero_v_tail<KW, C::HALVES, C::HALF_BYTES>(vtile, tile_key0, slice0, kv_len, lane);
       if constexpr (WIN)
-        zero_v_hidden<KW, C::HALVES, C::HALF_BYTES>(vtile, tile_key0, slice0, a.first, geo.lo, lane);
+        zero_v_hidden<KW, C::HALVES, C::HALF_BYTES>(vtile, tile_key0, slice0, a.first, win_lo, lane);
       // S^T for keys slice0 + g (rows of a0, a2) and slice0 + g + 8 (a1, a3).
       float st[4] = {0.f, 0.f, 0.f, 0.f};
       {
@@ -948,22 +949,18 @@ attn_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
   const int row0 = rt * kRowsSplit;
   const int R = min(kRowsSplit, q_len * G - row0);
   const int kb = j * chunk;
-  int ke = min(kv_len, kb + chunk);
-  int ntiles;
+  // Sliding window: the item works on virtual keys, the sequence is len long.
   WinGeo geo{};
-  if constexpr (WIN) {
+  if constexpr (WIN)
+    geo = win_geo(kv_len, q_len, row0 / G, (row0 + R - 1) / G, a.window, a.first, a.box_rows);
+  const int len = WIN ? kv_len - geo.gap : kv_len;
+  const int win_lo = geo.lo - geo.gap;
+  int ke = min(len, kb + chunk);
+  if (a.causal) {
     const int i_last = (row0 + R - 1) / G;
-    geo = win_geo(kv_len, q_len, row0 / G, i_last, a.window, a.first, C::BN);
-    ke = min(kv_len, kv_len - q_len + i_last + 1);
-    const int vke = min(geo.vend, kb + chunk);
-    ntiles = vke > kb ? (vke - kb + C::BN - 1) / C::BN : 0;
-  } else {
-    if (a.causal) {
-      const int i_last = (row0 + R - 1) / G;
-      ke = min(ke, kv_len - q_len + i_last + 1);
-    }
-    ntiles = ke > kb ? (ke - kb + C::BN - 1) / C::BN : 0;
+    ke = min(ke, len - q_len + i_last + 1);
   }
+  const int ntiles = ke > kb ? (ke - kb + C::BN - 1) / C::BN : 0;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
@@ -987,20 +984,20 @@ attn_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
   }
   if constexpr (FP8) {
     if (R <= 8) {
-      split_consumer_fp8_dec<F16, WIN>(a, ring, sh, hk, rt, j, q_start, q_len, kv_len, kb, ke,
-                                       ntiles, nsplit, slot_base, geo);
+      split_consumer_fp8_dec<F16, WIN>(a, ring, sh, hk, rt, j, q_start, q_len, len, kb, ke,
+                                       ntiles, nsplit, slot_base, win_lo);
       return;
     }
   }
   if (R <= 16)
-    split_consumer<D, 1, FP8, F16, WIN>(a, ring, sh, hk, seg, rt, j, q_start, q_len, kv_len, kb,
-                                          ke, ntiles, nsplit, slot_base, geo);
+    split_consumer<D, 1, FP8, F16, WIN>(a, ring, sh, hk, seg, rt, j, q_start, q_len, len, kb, ke,
+                                          ntiles, nsplit, slot_base, win_lo);
   else if (R <= 32)
-    split_consumer<D, 2, FP8, F16, WIN>(a, ring, sh, hk, seg, rt, j, q_start, q_len, kv_len, kb,
-                                          ke, ntiles, nsplit, slot_base, geo);
+    split_consumer<D, 2, FP8, F16, WIN>(a, ring, sh, hk, seg, rt, j, q_start, q_len, len, kb, ke,
+                                          ntiles, nsplit, slot_base, win_lo);
   else
-    split_consumer<D, 4, FP8, F16, WIN>(a, ring, sh, hk, seg, rt, j, q_start, q_len, kv_len, kb,
-                                          ke, ntiles, nsplit, slot_base, geo);
+    split_consumer<D, 4, FP8, F16, WIN>(a, ring, sh, hk, seg, rt, j, q_start, q_len, len, kb, ke,
+                                          ntiles, nsplit, slot_base, win_lo);
 }
 
 template <int D, bool FP8, bool F16, bool WIN>

@@ -277,12 +277,17 @@ __device__ __forceinline__ void q_split_e4m3(uint8_t* q, float* rs, int tiles, i
   }
 }
 
+// Bits 0 .. n - 1 (none for n <= 0, all from n = 32 on).
+__device__ __forceinline__ uint32_t below_mask(int n) {
+  return n >= 32 ? ~0u : (n <= 0 ? 0u : (1u << n) - 1u);
+}
+
 template <int D, bool F16, bool FP8, bool WIN>
 __device__ __forceinline__ void tc_softmax_tile(const AttnArgs& a, TcBars* bars, uint8_t* smem,
                                                 uint32_t tmem, int X, int q_start, int q_len,
                                                 int kv_len, int kb, int ke, int ntiles, int row0,
                                                 int R, int hk, int nsplit, int slot_base, int rt,
-                                                int j, const WinGeo& geo) {
+                                                int j, int win_lo) {
   using C = TcCfg<D>;
   using E = Elem<F16>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -317,7 +322,7 @@ __device__ __forceinline__ void tc_softmax_tile(const AttnArgs& a, TcBars* bars,
   for (int t = 0; ok && t < ntiles; ++t) {
     if (!mbar_wait(&bars->s_full[X], t & 1)) { ok = false; break; }
     tc_fence_after();
-    const int key0 = WIN ? geo.key(kb + t * C::BN) : kb + t * C::BN;
+    const int key0 = kb + t * C::BN;
     const int vis_end = min(ke, lim + 1);   // keys [key0, vis_end) are visible
     const bool edge = key0 + C::BN > vis_end;
     uint32_t xs_u[C::BN];
@@ -326,19 +331,26 @@ __device__ __forceinline__ void tc_softmax_tile(const AttnArgs& a, TcBars* bars,
       tmem_ld32(tm_row + s_col + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&xs_u[c * 32]));
     tmem_wait_ld();
     float* xs = reinterpret_cast<float*>(xs_u);
-    if (edge) {
+    if constexpr (WIN) {
+      // Visible: keys below vis_end that are first tokens or past lim - window,
+      // as one bit per key, so that the tests of an edge tile cost an element
+      // two instructions.
+      const int win_from = max(lim - a.window + 1, 0);
+      if (edge || (key0 < win_from && key0 + C::BN > a.first)) {
+#pragma unroll
+        for (int c = 0; c < C::BN / 32; ++c) {
+          const int base = key0 + c * 32;
+          const uint32_t seen = below_mask(vis_end - base) &
+                                (below_mask(a.first - base) | ~below_mask(win_from - base));
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (!(seen & (1u << e))) xs[c * 32 + e] = -INFINITY;
+        }
+      }
+    } else if (edge) {
 #pragma unroll
       for (int e = 0; e < C::BN; ++e)
         if (key0 + e >= vis_end) xs[e] = -INFINITY;
-    }
-    if constexpr (WIN) {
-      // Keys [first, lim - window] are behind this row's window.
-      const int hide_from = a.first - key0, hide_to = lim - a.window - key0;
-      if (hide_from < C::BN && hide_to >= 0) {
-#pragma unroll
-        for (int e = 0; e < C::BN; ++e)
-          if (e >= hide_from && e <= hide_to) xs[e] = -INFINITY;
-      }
     }
     // Row max: eight independent chains of three-input maxima over the
     // values j, j+8, j+16, ... of the tile.
@@ -404,9 +416,9 @@ __device__ __forceinline__ void tc_softmax_tile(const AttnArgs& a, TcBars* bars,
         tmem_wait_st();
         // warp-uniform condition and result
         if (!FP8 && X == 0 &&
-            (key0 + C::BN > kv_len || (WIN && key0 < geo.lo && key0 + C::BN > a.first)))
+            (key0 + C::BN > kv_len || (WIN && key0 < win_lo && key0 + C::BN > a.first)))
           ok = __all_sync(0xffffffffu, zero_v_tail<D, WIN>(bars, smem, t, key0, kv_len, tid,
-                                                           a.first, geo.lo));
+                                                           a.first, win_lo));
         if (!ok) break;
         tc_fence_before();
         mbar_arrive(&bars->p_full[0][X]);
@@ -537,19 +549,15 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
   const int R = min(C::TILES * TR, q_len * G - row0);
   const bool two = R > TR;   // tile B has rows
   const int kb = j * chunk;
-  int ke = min(kv_len, kb + chunk);
-  int ntiles;
+  // Sliding window: the item works on virtual keys, the sequence is len long.
   WinGeo geo{};
-  if constexpr (WIN) {
-    const int i_last = (row0 + R - 1) / G;
-    geo = win_geo(kv_len, q_len, row0 / G, i_last, a.window, a.first, C::BN);
-    ke = min(kv_len, kv_len - q_len + i_last + 1);
-    const int vke = min(geo.vend, kb + chunk);
-    ntiles = vke > kb ? (vke - kb + C::BN - 1) / C::BN : 0;
-  } else {
-    if (a.causal) ke = min(ke, kv_len - q_len + (row0 + R - 1) / G + 1);
-    ntiles = ke > kb ? (ke - kb + C::BN - 1) / C::BN : 0;
-  }
+  if constexpr (WIN)
+    geo = win_geo(kv_len, q_len, row0 / G, (row0 + R - 1) / G, a.window, a.first, a.box_rows);
+  const int len = WIN ? kv_len - geo.gap : kv_len;
+  const int win_lo = geo.lo - geo.gap;
+  int ke = min(len, kb + chunk);
+  if (a.causal) ke = min(ke, len - q_len + (row0 + R - 1) / G + 1);
+  const int ntiles = ke > kb ? (ke - kb + C::BN - 1) / C::BN : 0;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -828,9 +836,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
       if (!(ok = mbar_wait(&bars->kv_full[S8 + t % S8], (t / S8) & 1))) break;
       if (ct == 0) bars->consumed[1] = t + 1;
       if (t >= VB && !(ok = mbar_wait(&bars->vw_free[t % VB], ((t / VB) - 1) & 1))) break;
-      const int key0 = WIN ? geo.key(kb + t * C::BN) : kb + t * C::BN;
-      widen_e4m3_tile<WIN>(v8, smem + TcFp8::OFF_VW + (t % VB) * C::KV_TILE, ct, kv_len - key0,
-                           a.first - key0, geo.lo - key0);
+      const int key0 = kb + t * C::BN;
+      widen_e4m3_tile<WIN>(v8, smem + TcFp8::OFF_VW + (t % VB) * C::KV_TILE, ct, len - key0,
+                           a.first - key0, win_lo - key0);
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       mbar_arrive(&bars->vw_full[t % VB]);
       mbar_arrive(&bars->kv_empty[S8 + t % S8]);
@@ -845,8 +853,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     // ------------------------------------------------------------ softmax
     const int X = (warp - 4) >> 2;   // warps 4-7: tile A, 8-11: tile B
     if (X == 0 || two)
-      tc_softmax_tile<D, F16, FP8, WIN>(a, bars, smem, tmem, X, q_start, q_len, kv_len, kb, ke,
-                                        ntiles, row0, R, hk, nsplit, slot_base, rt, j, geo);
+      tc_softmax_tile<D, F16, FP8, WIN>(a, bars, smem, tmem, X, q_start, q_len, len, kb, ke, ntiles,
+                                        row0, R, hk, nsplit, slot_base, rt, j, win_lo);
     if (nsplit > 1 && !a.partials_only) {
       // Both warpgroups (256 threads) take part, active tile or not.
       __threadfence();

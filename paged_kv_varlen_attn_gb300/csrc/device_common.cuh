@@ -242,12 +242,17 @@ __device__ __forceinline__ void fadd2(float& d0, float& d1, float a0, float a1, 
 // The keys a row tile reads under a sliding window with first tokens. Queries
 // i0 .. i1 of a sequence (positions kv_len - q_len + i) see keys [0, first) and,
 // each, the last `window` keys up to its own; no query of the tile sees a key
-// of [first, lo). The tile's key tiles (align keys each) are numbered without
-// the ones between the two parts: virtual key v is key v below fe (`first`
-// rounded up to whole tiles) and key v + gap from there on, up to vend. Where
-// the parts meet or overlap, gap = 0 and the numbering is the plain one.
+// of [first, lo). The tile works on keys numbered without the ones between the
+// two parts: virtual key v is key v below fe (`first` rounded up to whole TMA
+// boxes) and key v + gap from there on, gap a multiple of the box. Where the
+// parts meet or overlap, gap = 0 and the numbering is the plain one. With the
+// sequence's length (hence every row's position) reduced by gap, masks and key
+// ranges are the plain ones on virtual keys -- where gap > 0 every row of the
+// tile lies past the first part -- and only the producer maps boxes to keys.
+// (Numbering by whole 64- or 128-key tiles instead would cost a decode row
+// about one tile in eighteen, a prompt's row tile two in ten at window 1024.)
 struct WinGeo {
-  int fe, gap, vend, lo;
+  int fe, gap, lo;
   __device__ __forceinline__ int key(int v) const { return v < fe ? v : v + gap; }
   // Whether some query of the tile may see a key of [k, k + n).
   __device__ __forceinline__ bool wanted(int k, int n, int first) const {
@@ -255,14 +260,13 @@ struct WinGeo {
   }
 };
 __device__ __forceinline__ WinGeo win_geo(int kv_len, int q_len, int i0, int i1, int window,
-                                          int first, int align) {
+                                          int first, int box) {
   WinGeo w;
   const int ke = max(0, min(kv_len, kv_len - q_len + i1 + 1));
   const long long lo = static_cast<long long>(kv_len) - q_len + i0 - window + 1;
   w.lo = lo > 0 ? static_cast<int>(lo) : 0;
-  w.fe = (min(first, ke) + align - 1) / align * align;
-  w.gap = max(0, w.lo / align * align - w.fe);
-  w.vend = max(0, ke - w.gap);
+  w.fe = (min(first, ke) + box - 1) / box * box;
+  w.gap = max(0, w.lo / box * box - w.fe);
   return w;
 }
 
@@ -506,8 +510,9 @@ __device__ __forceinline__ void abort_call(const AttnArgs& a) {
 // barriers -- full/empty[s] for K, full/empty[STAGES + s] for V -- so a
 // consumer that is done with K(t) before V(t) can release it early, and
 // issued[0] / issued[1] count the issued K / V tiles.
-// WIN = true: kb and the tiles are in the virtual numbering of geo, and a box
-// that no query of the row tile sees reads as zeros, its page id unread.
+// WIN = true: kb and the tiles are in the virtual numbering of geo (kv_len is
+// the sequence's own), and a box that no query of the row tile sees reads as
+// zeros, its page id unread.
 // Returns false on timeout/abort.
 template <int BN, int HALVES, int STAGES, bool SEP = false, bool WIN = false>
 __device__ bool produce_kv(const CUtensorMap* tmK, const CUtensorMap* tmV, const AttnArgs& a,

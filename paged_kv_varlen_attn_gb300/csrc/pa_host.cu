@@ -590,11 +590,12 @@ static pa_status varlen_impl(const pa_kv_update* upd, const void* q, int64_t q_t
   d.tc_allowed = softmax_scale > 0.f;
   if (window > 0) {
     // A window of at least every sequence is no window; else a row tile reads
-    // at most the first tokens, the window and its own tokens, in whole tiles.
+    // at most the first tokens, the window and its own tokens, in whole TMA
+    // boxes (of at most 64 keys).
     if (window >= max_seqlen_k) window = num_first = 0;
     if (num_first > max_seqlen_k) num_first = max_seqlen_k;
-    const long long reach = static_cast<long long>(cdiv(num_first, 128)) * 128 + window +
-                            2 * kTcTileRows + 2 + 128;
+    const long long reach = static_cast<long long>(cdiv(num_first, kKeyTile)) * kKeyTile + window +
+                            2 * kTcTileRows + 2 + kKeyTile;
     if (window > 0 && reach < d.max_kv) d.max_kv = static_cast<int>(reach);
   }
   const PassLayout L = layout_pass(d, 0);
@@ -620,6 +621,7 @@ static pa_status varlen_impl(const pa_kv_update* upd, const void* q, int64_t q_t
                       causal, 0);
   pp.p[0].window = window;
   pp.p[0].first = num_first;
+  pp.p[0].box_rows = box_rows;
   if (launch_plan(pp, 1, c.st) != cudaSuccess) return PA_ERR_CUDA;
   st = launch_kv_update(upd, c, key_cache, value_cache, sms);
   if (st != PA_OK) return st;
@@ -1288,6 +1290,9 @@ pa_status pa_evict(void* key_cache, void* value_cache, int64_t cache_block_strid
   a.bs = block_size;
   a.num_blocks = num_blocks;
   a.row_bytes = head_size * elem_size;
+  a.bs_shift = -1;
+  for (int b = 4; b <= 10; ++b)
+    if (block_size == 1 << b) a.bs_shift = b;
   a.max_k = max_seqlen_k;
   const long long cap = static_cast<long long>(bt_stride) * block_size;
   a.kv_len_cap = cap > 0x7fffffff ? 0x7fffffff : static_cast<int>(cap);

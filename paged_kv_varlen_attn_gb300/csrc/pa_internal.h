@@ -91,6 +91,7 @@ struct PlanArgs {
   int partials_only;     // every item gets a partial-state slot and a zeroed counter (cascade)
   int make_groups;       // list the (segment, row tile) groups of each class (cascade suffix)
   int window, first;     // sliding window (0: none) and first tokens (see WinGeo)
+  int box_rows;          // keys of a TMA box (windowed passes only)
 };
 
 struct PlanPasses {
@@ -245,6 +246,7 @@ struct EvictArgs {
   const int32_t* bt;
   int bt_stride;
   int H_kv, bs, num_blocks, row_bytes;
+  int bs_shift;                   // log2(bs), or -1 where bs is no power of two
   int max_k, kv_len_cap;          // host bound; keys addressable through a block_table row
   int budget, first, recent;
   int32_t* kept;                  // [num_seqs, H_kv, budget]

@@ -70,16 +70,14 @@ constexpr int kPlanThreads = 256;
 constexpr int kSizeBuckets = 1024;
 constexpr int kPlanSmemSegs = 1024;   // segment tables kept in shared memory up to this many
 
-// Sliding window: the keys of one tile of the kernel a class runs on, and a
-// bound on the (virtual, see WinGeo) keys of any row tile of a segment: the
-// first tokens and the window of the tile's first query rounded out to whole
-// tiles, and one key more per further query of the tile.
-__device__ __forceinline__ int win_align(int cls, int D) { return cls && D <= 128 ? 128 : kKeyTile; }
+// Sliding window: a bound on the (virtual, see WinGeo) keys of any row tile of
+// a segment: the first tokens and the window of the tile's first query rounded
+// out to whole TMA boxes, and one key more per further query of the tile.
 __device__ __forceinline__ int win_keys(int4 g, int rows_per_item, const PlanArgs& P) {
-  const int align = win_align(g.w, P.D);
+  const int box = P.box_rows;
   const long long tokens = min(g.y, rows_per_item / P.G + 2);
-  const long long n = static_cast<long long>((min(P.first, g.z) + align - 1) / align) * align +
-                      P.window + tokens + align;
+  const long long n =
+      static_cast<long long>((min(P.first, g.z) + box - 1) / box) * box + P.window + tokens + box;
   return n < g.z ? static_cast<int>(n) : g.z;
 }
 
@@ -93,11 +91,11 @@ __device__ __forceinline__ int item_bucket(int s, int rt, int j, int4 g, int chu
   const int rows = q_len * G;
   const int last_row = min(rows, (rt + 1) * R) - 1;
   const int kb = j * chunk;
-  int ke = min(kv, kb + chunk);
+  int len = kv;
   if constexpr (WIN)
-    ke = min(win_geo(kv, q_len, rt * R / G, last_row / G, P.window, P.first, win_align(cls, D)).vend,
-             kb + chunk);
-  else if (causal) ke = min(ke, kv - q_len + last_row / G + 1);
+    len -= win_geo(kv, q_len, rt * R / G, last_row / G, P.window, P.first, P.box_rows).gap;
+  int ke = min(len, kb + chunk);
+  if (causal) ke = min(ke, len - q_len + last_row / G + 1);
   const int tiles = ke > kb ? (ke - kb + kKeyTile - 1) / kKeyTile : 0;
   return min(tiles, kSizeBuckets - 1);
 }
@@ -231,8 +229,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     else L = (W + tg - 1) / tg;
     const int min_chunk = c ? P.min_chunk_tc : kMinChunkSplit;
     if (L < static_cast<unsigned long long>(min_chunk)) L = min_chunk;
-    const int round_to = WIN ? win_align(c, P.D) : kKeyTile;   // whole key tiles
-    L = (L + round_to - 1) / round_to * round_to;
+    L = (L + kKeyTile - 1) / kKeyTile * kKeyTile;
     if (L > 0x40000000ull) L = 0x40000000ull;
     chunk_max[c] = static_cast<int>(L);
   }
@@ -252,15 +249,14 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
       const int nrt = (g.y * G + R - 1) / R;
       const int kv = WIN ? win_keys(g, R, P) : g.z;
       const int L = cls ? chunk_max[1] : chunk_max[0];
-      const int round_to = WIN ? win_align(cls, P.D) : kKeyTile;
       if (kv > 0) {
         nsplit = (kv + L - 1) / L;
         chunk = (kv + nsplit - 1) / nsplit;
-        chunk = (chunk + round_to - 1) / round_to * round_to;
+        chunk = (chunk + kKeyTile - 1) / kKeyTile * kKeyTile;
         nsplit = (kv + chunk - 1) / chunk;
       } else {
         nsplit = 1;
-        chunk = round_to;
+        chunk = kKeyTile;
       }
       const int n_items = nrt * nsplit;
       const int n_slots = (nsplit > 1 || P.partials_only) ? n_items : 0;
