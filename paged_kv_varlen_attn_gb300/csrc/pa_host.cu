@@ -261,6 +261,12 @@ bool encode_pool_map(CUtensorMap* map, const void* base, int D, int H_kv, int bs
   return r == CUDA_SUCCESS;
 }
 
+int log2_or_none(int n) {
+  for (int b = 0; b < 31; ++b)
+    if (n == 1 << b) return b;
+  return -1;
+}
+
 int gcd_int(int a, int b) {
   while (b) {
     int t = a % b;
@@ -1223,6 +1229,7 @@ pa_status pa_attn_weights(const void* q, int64_t q_token_stride, const void* key
   a.H_kv = num_kv_heads;
   a.G = num_heads / num_kv_heads;
   a.bs = block_size;
+  a.bs_shift = log2_or_none(block_size);
   a.num_blocks = num_blocks;
   a.total_q = total_q;
   a.max_q = max_seqlen_q;
@@ -1290,9 +1297,7 @@ pa_status pa_evict(void* key_cache, void* value_cache, int64_t cache_block_strid
   a.bs = block_size;
   a.num_blocks = num_blocks;
   a.row_bytes = head_size * elem_size;
-  a.bs_shift = -1;
-  for (int b = 4; b <= 10; ++b)
-    if (block_size == 1 << b) a.bs_shift = b;
+  a.bs_shift = log2_or_none(block_size);
   a.max_k = max_seqlen_k;
   const long long cap = static_cast<long long>(bt_stride) * block_size;
   a.kv_len_cap = cap > 0x7fffffff ? 0x7fffffff : static_cast<int>(cap);

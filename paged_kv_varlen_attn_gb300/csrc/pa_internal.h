@@ -270,6 +270,7 @@ struct WeightArgs {
   const int32_t* bt;
   int bt_stride;
   int H, H_kv, G, bs, num_blocks, total_q;
+  int bs_shift;                   // log2(bs), or -1 where bs is no power of two
   int max_q, max_k, kv_len_cap;
   float scale_log2;               // softmax_scale * log2(e)
   int causal;

@@ -14,18 +14,50 @@ namespace pa {
 
 // ---------------------------------------------------------------------------
 // Decode and short queries (at most tc_min_rows packed query rows).
-// One warp per 16 keys of a sequence and KV head. The keys are the M
-// dimension of the warp MMA and 8 packed query rows (token, head of the
-// group) its N, so a key's sum is a sum along the accumulator's columns: no
-// reduction until the end, where the four lanes of a row add up. K goes from
-// global memory straight to the A fragments (held for all query rows) and Q
-// straight to the B fragments: the head dimension is permuted alike in both
-// so that a lane's elements are 16-byte runs and four lanes read 64
-// consecutive bytes. No shared memory, no barriers: at 4 warps a block and 8
-// loads in flight per lane, decode is bound by the read of K.
+// A warp takes kSlices slices of 16 keys of a sequence and KV head. A slice's
+// keys are the M dimension of the warp MMA and 8 packed query rows (token,
+// head of the group) its N, so a key's sum is a sum along the accumulator's
+// columns: no reduction until the end, where the four lanes of a row add up.
+// The head dimension is permuted alike in the K (A) and Q (B) fragments so
+// that a lane's elements are 16-byte runs and four lanes read 64 consecutive
+// bytes; Q goes straight to registers, K through a ring of slots per warp
+// filled by asynchronous copies, where every lane reads back its own bytes
+// (the ring holds what registers could not: no barrier but the warp's own).
+// Decode is bound by the read of K; the ring keeps one to three slices of every
+// warp on their way. On the 64-sequence decode batch (483 MB): 78 us, 6.2 TB/s;
+// with K read straight into registers 92 us (two slices in flight, 16 warps per
+// SM) and 121 us (one slice per warp, the chain of dependent reads in front of
+// it exposed). Two slots of 256-byte rows a warp beat four, 78 against 81 us
+// (more warps per SM), and 8 slices per warp beat 4, 81 against 94.
 // 16 keys never cross a page (pages are multiples of 16 keys).
 // ---------------------------------------------------------------------------
 constexpr int kWeightWarps = 4;
+constexpr int kSlices = 8;
+constexpr int kWeightKeys = kWeightWarps * kSlices * 16;   // keys of a block
+
+template <int D, bool FP8>
+struct WwCfg {
+  static constexpr int ROW = D * (FP8 ? 1 : 2);            // bytes of a key
+  static constexpr int SLOT = 16 * ROW + 64;               // a slice and its old sums
+  static constexpr int SLOTS = ROW >= 256 ? 2 : 4;
+  static constexpr int SMEM_BYTES = kWeightWarps * SLOTS * SLOT;
+};
+
+// Asynchronous copies to shared memory: 16 bytes (past L1), and 4 bytes or, for
+// take = false, a zero.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool take) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
+               "r"(take ? 4 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 // Two e4m3 bytes as a pair of the MMA's element type (exact in both).
 template <bool F16>
@@ -61,84 +93,80 @@ template <int D, bool F16, bool FP8>
 __global__ void __launch_bounds__(kWeightWarps * 32)
 weights_kernel(const __grid_constant__ WeightArgs a, int tiles) {
   using E = Elem<F16>;
-  constexpr int DK = D / 16;        // k-steps
-  const int s = blockIdx.x / tiles;
-  const int hk = blockIdx.y;
+  using C = WwCfg<D, FP8>;
+  constexpr int NQ = D / 32;                    // 16-byte pieces of a query row per lane
+  constexpr int NV = C::ROW / 64;               // of a key row
+  static_assert(kSlices <= 32 && kSlices % C::SLOTS == 0, "a lane holds a slice's page id");
+  extern __shared__ __align__(16) uint8_t ring_raw[];
+  // KV head fastest: a page's heads are read at about the same time (13% on
+  // the decode batch over all of one head's blocks before the next head's).
+  const int unit = blockIdx.x / a.H_kv;
+  const int hk = blockIdx.x - unit * a.H_kv;
+  const int s = unit / tiles;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
-  const int key0 = ((blockIdx.x - s * tiles) * kWeightWarps + warp) * 16;
+  const int base = ((unit - s * tiles) * kWeightWarps + warp) * (kSlices * 16);
   int q0, q_len, kv;
-  if (!weight_lengths(a, s, key0 == 0 && hk == 0 && lane == 0, q0, q_len, kv)) return;
-  if (key0 >= kv || q_len * a.G > a.tc_min_rows) return;
-  const int lp = key0 / a.bs;
-  const int page = __ldg(a.bt + static_cast<int64_t>(s) * a.bt_stride + lp);
-  if (page < 0 || page >= a.num_blocks) {
-    if (lane == 0) flag_status(a.status, PA_DEV_BAD_PAGE);
-    return;
-  }
-  const int prow = key0 - lp * a.bs;   // the slice's first row of the page
-
-  // A fragments: keys key0 + g and key0 + g + 8 (rows past kv are in the page
-  // and feed only their own, unwritten sums).
-  uint32_t kf[DK][4];
-  {
-    constexpr int E16 = FP8 ? 16 : 8;   // elements of 16 bytes
-    constexpr int row_bytes = D * (FP8 ? 1 : 2);
-    const uint8_t* base = a.kc + page * a.block_stride_bytes +
-                          (static_cast<int64_t>(prow) * a.H_kv + hk) * row_bytes;
-    const int64_t rstep = static_cast<int64_t>(a.H_kv) * row_bytes;
-    const uint4* p0 = reinterpret_cast<const uint4*>(base + g * rstep);
-    const uint4* p1 = reinterpret_cast<const uint4*>(base + (g + 8) * rstep);
-    constexpr int NV = D / (4 * E16);
-    uint4 x0[NV], x1[NV];
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      x0[v] = __ldg(p0 + 4 * v + c);
-      x1[v] = __ldg(p1 + 4 * v + c);
-    }
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const uint32_t w0[4] = {x0[v].x, x0[v].y, x0[v].z, x0[v].w};
-      const uint32_t w1[4] = {x1[v].x, x1[v].y, x1[v].z, x1[v].w};
-      if constexpr (FP8) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          kf[4 * v + k][0] = widen_e4m3x2<F16>(w0[k]);
-          kf[4 * v + k][1] = widen_e4m3x2<F16>(w1[k]);
-          kf[4 * v + k][2] = widen_e4m3x2<F16>(w0[k] >> 16);
-          kf[4 * v + k][3] = widen_e4m3x2<F16>(w1[k] >> 16);
-        }
-      } else {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          kf[2 * v + k][0] = w0[2 * k];
-          kf[2 * v + k][1] = w1[2 * k];
-          kf[2 * v + k][2] = w0[2 * k + 1];
-          kf[2 * v + k][3] = w1[2 * k + 1];
-        }
-      }
-    }
-  }
-  const float sl2 = FP8 ? a.scale_log2 * __ldg(a.k_scale + hk) : a.scale_log2;
+  if (!weight_lengths(a, s, base == 0 && hk == 0 && lane == 0, q0, q_len, kv)) return;
+  if (base >= kv || q_len * a.G > a.tc_min_rows) return;
   const int past = kv - q_len;          // query i is at position past + i
   const int rows = q_len * a.G;
-  // The first query that sees a key of the slice.
-  const int i0 = a.causal ? max(0, key0 - past) : 0;
-  float sum[2] = {0.f, 0.f};
-  for (int r = i0 * a.G; r < rows; r += 8) {
-    // B fragments: packed row r + g.
+  const int nslices = min(kSlices, (kv - base + 15) >> 4);
+  uint8_t* ring = ring_raw + warp * (C::SLOTS * C::SLOT);
+
+  // Lane i: page of slice i (-1: none, or outside the pool), its first row.
+  int page_l = -1, row_l = 0;
+  if (lane < nslices) {
+    const int key0 = base + 16 * lane;
+    const int lp = a.bs_shift >= 0 ? key0 >> a.bs_shift : key0 / a.bs;
+    row_l = key0 - lp * a.bs;
+    page_l = __ldg(a.bt + static_cast<int64_t>(s) * a.bt_stride + lp);
+    if (page_l < 0 || page_l >= a.num_blocks) {
+      page_l = -1;
+      flag_status(a.status, PA_DEV_BAD_PAGE);
+    }
+  }
+  // One group of copies per slice, empty or not: keys g and g + 8, pieces
+  // 4 v + c, each to this lane's own places; the old sums (zero for the call's
+  // own keys) behind them. Rows past kv are in the page and feed only their
+  // own, unwritten sums.
+  auto fetch = [&](int i) {
+    const int page = __shfl_sync(0xffffffffu, page_l, i & 31);
+    const int prow = __shfl_sync(0xffffffffu, row_l, i & 31);
+    if (i < nslices && page >= 0) {
+      const uint32_t dst = smem_u32(ring + (i % C::SLOTS) * C::SLOT);
+      const int64_t rstep = static_cast<int64_t>(a.H_kv) * C::ROW;
+      const uint8_t* p = a.kc + page * a.block_stride_bytes + hk * C::ROW + (prow + g) * rstep;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        cp_async16(dst + (2 * v) * 512 + lane * 16, p + (4 * v + c) * 16);
+        cp_async16(dst + (2 * v + 1) * 512 + lane * 16, p + 8 * rstep + (4 * v + c) * 16);
+      }
+      if (lane < 16)
+        cp_async4(dst + 16 * C::ROW + lane * 4,
+                  a.weights + page * a.weights_stride + static_cast<int64_t>(hk) * a.bs + prow + lane,
+                  base + 16 * i + lane < past);
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < C::SLOTS - 1; ++i) fetch(i);
+
+  const float sl2 = FP8 ? a.scale_log2 * __ldg(a.k_scale + hk) : a.scale_log2;
+  // Queries r .. r + 7 of the packed rows: B fragments (row r + g), and LSE and
+  // last visible key of columns r + 2c, r + 2c + 1.
+  uint4 qv[NQ];
+  float nl[2];
+  int lim[2];
+  auto load_queries = [&](int r) {
     const int rq = min(r + g, rows - 1);
     const int iq = rq / a.G;
     const uint4* qrow = reinterpret_cast<const uint4*>(
         a.q + static_cast<int64_t>(q0 + iq) * a.q_stride +
         static_cast<int64_t>(hk * a.G + rq - iq * a.G) * D);
-    uint4 qv[D / 32];
 #pragma unroll
-    for (int v = 0; v < D / 32; ++v)
+    for (int v = 0; v < NQ; ++v)
       qv[v] = __ldg(qrow + (FP8 ? 8 * (v >> 1) + 2 * c + (v & 1) : 4 * v + c));
-    // Columns r + 2c and r + 2c + 1: their LSE and last visible key.
-    float nl[2];
-    int lim[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int re = r + 2 * c + e;
@@ -150,34 +178,71 @@ weights_kernel(const __grid_constant__ WeightArgs a, int tiles) {
       // A row that saw nothing (lse = -inf) or does not exist sees no key here.
       lim[e] = re < rows && lse != -INFINITY ? (a.causal ? past + i : kv - 1) : -1;
     }
-    float st[4] = {0.f, 0.f, 0.f, 0.f};
+  };
+  if (rows <= 8) load_queries(0);
+
+#pragma unroll 1
+  for (int i = 0; i < nslices; ++i) {
+    fetch(i + C::SLOTS - 1);
+    cp_async_wait<C::SLOTS - 1>();
+    __syncwarp();
+    const int page = __shfl_sync(0xffffffffu, page_l, i);
+    const int prow = __shfl_sync(0xffffffffu, row_l, i);
+    if (page < 0) continue;             // warp-uniform
+    const uint8_t* slot = ring + (i % C::SLOTS) * C::SLOT;
+    uint4 x0[NV], x1[NV];
 #pragma unroll
-    for (int v = 0; v < D / 32; ++v) {
-      E::mma(st, kf[2 * v][0], kf[2 * v][1], kf[2 * v][2], kf[2 * v][3], qv[v].x, qv[v].y);
-      E::mma(st, kf[2 * v + 1][0], kf[2 * v + 1][1], kf[2 * v + 1][2], kf[2 * v + 1][3], qv[v].z,
-             qv[v].w);
+    for (int v = 0; v < NV; ++v) {
+      x0[v] = *reinterpret_cast<const uint4*>(slot + (2 * v) * 512 + lane * 16);
+      x1[v] = *reinterpret_cast<const uint4*>(slot + (2 * v + 1) * 512 + lane * 16);
+    }
+    const float* old = reinterpret_cast<const float*>(slot + 16 * C::ROW);
+    const float old0 = old[g], old1 = old[g + 8];
+    __syncwarp();                       // the slot may be filled again
+    const int key0 = base + 16 * i;
+    // The first query that sees a key of the slice.
+    const int i0 = a.causal ? max(0, key0 - past) : 0;
+    float sum[2] = {0.f, 0.f};
+    for (int r = rows > 8 ? i0 * a.G : 0; r < rows; r += 8) {
+      if (rows > 8) load_queries(r);
+      float st[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const uint32_t w0[4] = {x0[v].x, x0[v].y, x0[v].z, x0[v].w};
+        const uint32_t w1[4] = {x1[v].x, x1[v].y, x1[v].z, x1[v].w};
+        if constexpr (FP8) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const uint4& q = qv[2 * v + (x >> 1)];
+            E::mma(st, widen_e4m3x2<F16>(w0[x]), widen_e4m3x2<F16>(w1[x]),
+                   widen_e4m3x2<F16>(w0[x] >> 16), widen_e4m3x2<F16>(w1[x] >> 16),
+                   (x & 1) ? q.z : q.x, (x & 1) ? q.w : q.y);
+          }
+        } else {
+          E::mma(st, w0[0], w1[0], w0[1], w1[1], qv[v].x, qv[v].y);
+          E::mma(st, w0[2], w1[2], w0[3], w1[3], qv[v].z, qv[v].w);
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int j = key0 + g + 8 * x;
+        float p = 0.f;
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (j <= lim[e]) p += fast_exp2(fmaf(st[2 * x + e], sl2, nl[e]));
+        sum[x] += p;
+      }
     }
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int j = key0 + g + 8 * k;
-      float p = 0.f;
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-        if (j <= lim[e]) p += fast_exp2(fmaf(st[2 * k + e], sl2, nl[e]));
-      sum[k] += p;
+    for (int x = 0; x < 2; ++x) {
+      sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], 1);
+      sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], 2);
     }
+    if (c < 2 && key0 + g + 8 * c < kv)
+      a.weights[page * a.weights_stride + static_cast<int64_t>(hk) * a.bs + prow + g + 8 * c] =
+          c == 0 ? old0 + sum[0] : old1 + sum[1];
   }
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], 1);
-    sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], 2);
-    const int j = key0 + g + 8 * k;
-    if (c == 0 && j < kv) {
-      float* w = a.weights + page * a.weights_stride + static_cast<int64_t>(hk) * a.bs + prow + g +
-                 8 * k;
-      *w = (j >= past ? 0.f : *w) + sum[k];
-    }
-  }
+  cp_async_wait<0>();
 }
 
 // ---------------------------------------------------------------------------
@@ -591,26 +656,32 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
 
 constexpr long long kPairUnits = 304;
 
+// The shared-memory opt-in, a per-device function attribute: set on the first
+// launch on each device (before any stream capture), not again.
+template <typename Kernel>
+static cudaError_t opt_in_smem(Kernel kernel, int bytes, std::atomic<bool>* configured) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool known = dev >= 0 && dev < kMaxDevices;
+  if (!known || !configured[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    if (known) configured[dev].store(true, std::memory_order_release);
+  }
+  return cudaSuccess;
+}
+
 template <int D, bool F16, bool FP8>
 static cudaError_t launch_weights_d(const CUtensorMap& tmQ, const WeightArgs& a, int num_seqs,
                                     int keys, cudaStream_t st) {
-  constexpr int kTileKeys = kWeightWarps * 16;
-  const int tiles = keys > 0 ? (keys + kTileKeys - 1) / kTileKeys : 1;
+  const int tiles = keys > 0 ? (keys + kWeightKeys - 1) / kWeightKeys : 1;
   if (a.tc_min_rows < 0x7fffffff) {
     using C = WtCfg<D>;
-    // A per-device function attribute: set on the first launch on each device
-    // (before any stream capture), not again.
-    static std::atomic<bool> configured[kMaxDevices];
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    static std::atomic<bool> configured_tc[kMaxDevices];
+    cudaError_t e =
+        opt_in_smem(weights_tc_kernel<D, F16, FP8>, C::SMEM_BYTES, configured_tc);
     if (e != cudaSuccess) return e;
-    const bool known = dev >= 0 && dev < kMaxDevices;
-    if (!known || !configured[dev].load(std::memory_order_acquire)) {
-      e = cudaFuncSetAttribute(weights_tc_kernel<D, F16, FP8>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
-      if (e != cudaSuccess) return e;
-      if (known) configured[dev].store(true, std::memory_order_release);
-    }
     const long long units =
         static_cast<long long>((keys + C::KEYS - 1) / C::KEYS) * num_seqs * a.H_kv;
     if (units > 0) {
@@ -637,9 +708,12 @@ static cudaError_t launch_weights_d(const CUtensorMap& tmQ, const WeightArgs& a,
       if (e != cudaSuccess) return e;
     }
   }
-  weights_kernel<D, F16, FP8>
-      <<<dim3(static_cast<unsigned>(num_seqs) * tiles, a.H_kv), kWeightWarps * 32, 0, st>>>(a,
-                                                                                            tiles);
+  using W = WwCfg<D, FP8>;
+  static std::atomic<bool> configured[kMaxDevices];
+  cudaError_t e = opt_in_smem(weights_kernel<D, F16, FP8>, W::SMEM_BYTES, configured);
+  if (e != cudaSuccess) return e;
+  weights_kernel<D, F16, FP8><<<static_cast<unsigned>(num_seqs) * tiles * a.H_kv,
+                                kWeightWarps * 32, W::SMEM_BYTES, st>>>(a, tiles);
   return cudaGetLastError();
 }
 
