@@ -209,7 +209,7 @@ def _dtype_code(*ts):
     dts = {t.dtype for t in ts if t is not None}
     if len(dts) != 1:
         raise ValueError(f"tensors must share one element type, got {sorted(map(str, dts))}")
-    dt = dts.pop()
+    dt, = dts
     if dt == torch.bfloat16:
         return PA_BF16
     if dt == torch.float16:
@@ -582,13 +582,13 @@ def window_fwd(q, key_cache, value_cache, cu_seqlens_q, seqused_k, block_table, 
     if (k_scale is None) != (v_scale is None):
         raise ValueError("k_scale and v_scale go together")
     if out is None:
-        out = torch.empty((T, H, D), dtype=q.dtype, device=q.device)
-    if lse is None and return_lse:
-        lse = torch.empty((H, T), dtype=torch.float32, device=q.device)
-    if out.shape != (T, H, D) or not out.is_contiguous():
+        out = q.new_empty((T, H, D))
+    elif out.shape != (T, H, D) or not out.is_contiguous():
         raise ValueError("out must be a contiguous [total_q, num_heads, head_size] tensor")
-    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (H, T) or
-                            not lse.is_contiguous()):
+    if lse is None:
+        if return_lse:
+            lse = q.new_empty((H, T), dtype=torch.float32)
+    elif lse.dtype != torch.float32 or lse.shape != (H, T) or not lse.is_contiguous():
         raise ValueError("lse must be a contiguous float32 [num_heads, total_q] tensor")
     _f32_vector(sinks, H, "sinks")
     new = (key, value) if key is not None else ()
@@ -662,39 +662,41 @@ def rope_and_cache(q, key, value, positions, cos_sin, key_cache, value_cache, sl
     page = _cache_stride(key_cache)
     nb, bs, hk, d = shape
     T, H, dq = q.shape
-    if dq != d or key.shape != (T, hk, d) or value.shape != (T, hk, d):
+    row = (T, hk, d)
+    if dq != d or key.shape != row or value.shape != row:
         raise ValueError("q, key and value must be [tokens, heads, head_size] of the caches' "
                          "heads and head size")
-    for t, name in ((positions, "positions"), (slot_mapping, "slot_mapping")):
-        if t.dtype != torch.int64 or t.shape != (T,) or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous int64 tensor of one value per token")
-    if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+    if positions.dtype != torch.int64 or positions.shape != (T,) or \
+            not positions.is_contiguous() or slot_mapping.dtype != torch.int64 or \
+            slot_mapping.shape != (T,) or not slot_mapping.is_contiguous():
+        raise ValueError("positions and slot_mapping must be contiguous int64 tensors of one "
+                         "value per token")
+    rows, rot = cos_sin.shape
+    if cos_sin.dtype != torch.float32 or not cos_sin.is_contiguous():
         raise ValueError("cos_sin must be a contiguous float32 [positions, rot_dim] tensor")
     _f32_vector(q_norm, d, "q_norm")
     _f32_vector(k_norm, d, "k_norm")
-    if (k_scale is None) != (v_scale is None):
-        raise ValueError("k_scale and v_scale go together")
-    device = q.device
     if out is None:
-        out = torch.empty((T, H, d), dtype=q.dtype, device=device)
+        out = q.new_empty((T, H, d))
     elif out.shape != q.shape:
         raise ValueError("out must have the shape of q")
-    if k_scale is None:
-        dtype, desc, keep = _dtype_code(q, key, value, out, key_cache, value_cache), None, None
+    if k_scale is None and v_scale is None:
+        dtype, fp8, keep = _dtype_code(q, key, value, out, key_cache, value_cache), None, None
+    elif k_scale is None or v_scale is None:
+        raise ValueError("k_scale and v_scale go together")
     else:
         _fp8_pool(key_cache), _fp8_pool(value_cache)
         dtype = _dtype_code(q, key, value, out)
-        desc, keep = _fp8_desc(k_scale, v_scale, hk, device)
-    rows, rot = cos_sin.shape
+        desc, keep = _fp8_desc(k_scale, v_scale, hk, q.device)
+        fp8 = ctypes.byref(desc)
     rope = Rope(cos_sin.data_ptr(), rows, rot, 1 if interleaved else 0, _ptr(q_norm),
                 _ptr(k_norm), eps)
     update = KvUpdate(key.data_ptr(), value.data_ptr(), _row_stride(key), _row_stride(value),
                       slot_mapping.data_ptr(), T)
-    _call(lib.pa_rope_and_cache, "pa_rope_and_cache", device,
+    _call(lib.pa_rope_and_cache, "pa_rope_and_cache", q.device,
           ctypes.byref(rope), positions.data_ptr(), q.data_ptr(), _row_stride(q), out.data_ptr(),
           _row_stride(out), ctypes.byref(update), key_cache.data_ptr(), value_cache.data_ptr(),
-          page, H, hk, d, bs, nb, None if desc is None else ctypes.byref(desc), dtype,
-          _ptr(dev_status))
+          page, H, hk, d, bs, nb, fp8, dtype, _ptr(dev_status))
     del keep
     return out
 

@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstring>
 #include <mutex>
@@ -160,11 +161,16 @@ size_t cascade_bytes(int num_seqs, int total_q, int max_q, int max_k, int G, int
   return a > b ? a : b;
 }
 
+// The count of a device does not change: asked once per device.
 int query_sms(int sm_count) {
+  static std::atomic<int> known[kMaxDevices];
   if (sm_count > 0) return sm_count;
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  const bool cached = dev >= 0 && dev < kMaxDevices;
+  if (cached && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  if (cached) known[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 
