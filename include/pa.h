@@ -245,7 +245,8 @@ pa_status pa_cascade_fwd(const void* q, int64_t q_token_stride, const void* key_
  * pa_use_cascade_attention -- should a batch run as cascade attention?
  * ([FA-vLLM] §6.2, use_cascade_attention: a shared prefix of at least 256
  * tokens, at least 8 requests, no ALiBi / sliding window / local attention
- * and no DCP -- none of which this library has -- then cascade outright if
+ * and no DCP -- a layer with a sliding window calls pa_window_fwd, not a
+ * cascade; the others this library does not have -- then cascade outright if
  * split-KV decoding is off, else whichever of the two is estimated faster.)
  * The pages leave the estimate open; this one compares bytes: flat attention
  * reads the shared prefix once per sequence, cascade reads it once and pays
@@ -502,8 +503,10 @@ pa_status pa_window_fwd(const pa_kv_update* update, const void* q, int64_t q_tok
  * position; row p holds mscale * cos(p f_i) for every i, then mscale *
  * sin(p f_i). Angles are exact to about 1e-9 radian at a million positions.
  *   cos_sin  : float32 [table_len, rot_dim], 16-byte aligned.
+ *   table_len: at most 2^30.
  *   rot_dim  : even, 2 .. 256 (pa_rope_and_cache takes multiples of 16).
- *   base     : finite, > 0.
+ *   base     : finite, > 0 (rates of 2^53 turns per position and more are
+ *              refused).
  *   scaling  : NULL for none, else how the rates change for contexts longer
  *              than the model was trained on (orig_len positions):
  *     PA_ROPE_LINEAR      f_i / factor
@@ -599,6 +602,7 @@ pa_status pa_rope_and_cache(const pa_rope* rope, const int64_t* positions, const
  * keys are left as they were. Sums are float32 in a fixed order: the same
  * call gives the same bits. A sequence's pages must be its own (a page shared
  * with another sequence of the call gets the sum of one of them).
+ * max_seqlen_k and total_q * num_heads / num_kv_heads are at most 2^30.
  * A key in a page outside the pool sets PA_DEV_BAD_PAGE and is skipped; a
  * sequence whose lengths break the stated bounds sets PA_DEV_BAD_SEQLEN, and
  * with inconsistent cu_seqlens_q it is skipped.
@@ -626,8 +630,8 @@ pa_status pa_attn_weights(const void* q, int64_t q_token_stride, const void* key
  * different tokens.
  *   elem_size    : bytes of a cache element: 2, or 1 (e4m3, head_size 128).
  *   weights      : as in pa_attn_weights.
- *   budget       : >= 1, num_first, num_recent >= 0, num_first + num_recent
- *                  <= budget.
+ *   budget       : 1 .. 2^30, num_first, num_recent >= 0, num_first +
+ *                  num_recent <= budget.
  *   kept         : int32 [num_seqs, num_kv_heads, budget], out: the former
  *                  index of each row, ascending; rows past a shorter
  *                  sequence's keys get -1.

@@ -204,6 +204,38 @@ def _need_cuda(*ts):
             raise ValueError("all tensors must be CUDA tensors (no CPU fallback)")
 
 
+def _one_device(first, *rest):
+    """All tensors (None aside) are on the first one's GPU."""
+    index = first.get_device()
+    if index < 0:
+        raise ValueError("all tensors must be CUDA tensors (no CPU fallback)")
+    for t in rest:
+        if t is not None and t.get_device() != index:
+            raise ValueError("all tensors must be on one GPU (no CPU fallback)")
+
+
+def _seq_table(seqused_k, block_table, num_seqs):
+    """Row stride of a block table [num_seqs, columns], which stands for its
+    columns: a row may be read up to it."""
+    if seqused_k.dtype != torch.int32 or seqused_k.shape != (num_seqs,) or \
+            not seqused_k.is_contiguous():
+        raise ValueError("seqused_k must be a contiguous int32 tensor of one value per sequence")
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or \
+            block_table.shape[0] != num_seqs:
+        raise ValueError("block_table must be int32 [num_seqs, max_blocks]")
+    row, unit = block_table.stride()
+    width = block_table.shape[1]
+    if width > 1 and unit != 1:
+        raise ValueError("block_table must have unit column stride")
+    if row != width and num_seqs > 1:
+        end = block_table.storage_offset() + num_seqs * row
+        if row < width or end * 4 > block_table.untyped_storage().nbytes():
+            raise ValueError("block_table rows must not overlap, and its last row must be followed "
+                             "by the rest of a row stride")
+        return row
+    return width
+
+
 def _dtype_code(*ts):
     """PA_BF16 or PA_F16 for tensors that must all share one 2-byte float type."""
     dts = {t.dtype for t in ts if t is not None}
@@ -287,8 +319,7 @@ def alloc_workspace(nbytes, device):
 
 def _attn_common(q, key_cache, value_cache, cu_seqlens_q, seqused_k, block_table):
     _need_cuda(q, key_cache, value_cache, cu_seqlens_q, seqused_k, block_table)
-    if key_cache is not value_cache and (key_cache.stride(0) != value_cache.stride(0) or
-                                         key_cache.shape != value_cache.shape):
+    if key_cache.stride(0) != value_cache.stride(0) or key_cache.shape != value_cache.shape:
         raise ValueError("key and value caches must have the same shape and page stride")
     for t, name in ((cu_seqlens_q, "cu_seqlens_q"), (seqused_k, "seqused_k"),
                     (block_table, "block_table")):
@@ -561,6 +592,13 @@ def cascade_fwd_fp8kv(q, key_cache, value_cache, cu_seqlens_q, seqused_k, block_
 
 # ---------------------------------------------------------------------------
 # Sliding window with first tokens
+def _cu_seqlens(cu):
+    """Number of sequences of cu_seqlens_q."""
+    if cu.dtype != torch.int32 or cu.dim() != 1 or cu.shape[0] < 1 or not cu.is_contiguous():
+        raise ValueError("cu_seqlens_q must be a contiguous int32 tensor of num_seqs + 1 values")
+    return cu.shape[0] - 1
+
+
 def window_fwd(q, key_cache, value_cache, cu_seqlens_q, seqused_k, block_table, max_seqlen_q,
                max_seqlen_k, softmax_scale, window, num_first=0, sinks=None, k_scale=None,
                v_scale=None, key=None, value=None, slot_mapping=None, out=None, lse=None,
@@ -571,14 +609,16 @@ def window_fwd(q, key_cache, value_cache, cu_seqlens_q, seqused_k, block_table, 
     slot_mapping). With k_scale and v_scale the caches hold e4m3 bytes.
     Returns (out, lse or None)."""
     lib = load_library()
-    _attn_common(q, key_cache, value_cache, cu_seqlens_q, seqused_k, block_table)
-    _need_cuda(sinks, out, lse, workspace, dev_status)
+    _one_device(q, key_cache, value_cache, cu_seqlens_q, seqused_k, block_table, sinks, key, value,
+                slot_mapping, out, lse, workspace, dev_status)
+    if key_cache.stride() != value_cache.stride() or key_cache.shape != value_cache.shape:
+        raise ValueError("key and value caches must have the same shape and page stride")
     T, H, D = q.shape
     nb, bs, hk, d = key_cache.shape
-    S = cu_seqlens_q.numel() - 1
-    if d != D or seqused_k.numel() != S or block_table.shape[0] != S:
-        raise ValueError("q and the caches must share the head size; seqused_k and block_table "
-                         "have one row per sequence of cu_seqlens_q")
+    S = _cu_seqlens(cu_seqlens_q)
+    bt_row = _seq_table(seqused_k, block_table, S)
+    if d != D:
+        raise ValueError("q and the caches must share the head size")
     if (k_scale is None) != (v_scale is None):
         raise ValueError("k_scale and v_scale go together")
     if out is None:
@@ -591,8 +631,18 @@ def window_fwd(q, key_cache, value_cache, cu_seqlens_q, seqused_k, block_table, 
     elif lse.dtype != torch.float32 or lse.shape != (H, T) or not lse.is_contiguous():
         raise ValueError("lse must be a contiguous float32 [num_heads, total_q] tensor")
     _f32_vector(sinks, H, "sinks")
-    new = (key, value) if key is not None else ()
-    update = _kv_update(key, value, slot_mapping)
+    new, update = (), None
+    if key is not None:
+        new = (key, value)
+        n = key.shape[0]
+        if key.shape != (n, hk, D) or value.shape != (n, hk, D):
+            raise ValueError("key and value must be [tokens, num_kv_heads, head_size]")
+        if slot_mapping.dtype != torch.int64 or slot_mapping.shape != (n,) or \
+                not slot_mapping.is_contiguous():
+            raise ValueError("slot_mapping must be a contiguous int64 tensor of one value per "
+                             "token")
+        update = KvUpdate(key.data_ptr(), value.data_ptr(), _row_stride(key), _row_stride(value),
+                          slot_mapping.data_ptr(), n)
     desc = keep = None
     if k_scale is None:
         dtype = _dtype_code(q, out, key_cache, value_cache, *new)
@@ -609,7 +659,7 @@ def window_fwd(q, key_cache, value_cache, cu_seqlens_q, seqused_k, block_table, 
     _call(lib.pa_window_fwd, "pa_window_fwd", q.device,
           None if update is None else ctypes.byref(update), _ptr(q), _row_stride(q),
           _ptr(key_cache), _ptr(value_cache), _cache_stride(key_cache), _ptr(cu_seqlens_q),
-          _ptr(seqused_k), _ptr(block_table), block_table.stride(0), S, T, int(max_seqlen_q),
+          _ptr(seqused_k), _ptr(block_table), bt_row, S, T, int(max_seqlen_q),
           int(max_seqlen_k), H, hk, D, bs, nb, float(softmax_scale), int(window),
           int(num_first), ctypes.byref(opts), _ptr(out), _ptr(lse), _ptr(workspace),
           workspace.numel(), dtype, _ptr(dev_status))
@@ -654,8 +704,8 @@ def rope_and_cache(q, key, value, positions, cos_sin, key_cache, value_cache, sl
     their pages (in place on the caches; with k_scale and v_scale the caches
     hold e4m3 bytes). Returns the rotated queries; out may be q itself."""
     lib = load_library()
-    _need_cuda(q, key, value, positions, cos_sin, key_cache, value_cache, slot_mapping, q_norm,
-               k_norm, out, dev_status)
+    _one_device(q, key, value, positions, cos_sin, key_cache, value_cache, slot_mapping, q_norm,
+                k_norm, out, dev_status)
     shape = key_cache.shape
     if key_cache.stride() != value_cache.stride() or shape != value_cache.shape:
         raise ValueError("key and value caches must have the same shape and page stride")
@@ -720,8 +770,9 @@ def attn_weights(q, key_cache, lse, weights, cu_seqlens_q, seqused_k, block_tabl
     own queries start from zero. With k_scale the key cache holds e4m3 bytes.
     Returns weights."""
     lib = load_library()
-    _need_cuda(lse, weights, dev_status)
-    _attn_common(q, key_cache, key_cache, cu_seqlens_q, seqused_k, block_table)
+    _one_device(q, key_cache, lse, weights, cu_seqlens_q, seqused_k, block_table, dev_status)
+    S = _cu_seqlens(cu_seqlens_q)
+    bt_row = _seq_table(seqused_k, block_table, S)
     T, H, D = q.shape
     nb, bs, hk, d = key_cache.shape
     if d != D:
@@ -735,8 +786,8 @@ def attn_weights(q, key_cache, lse, weights, cu_seqlens_q, seqused_k, block_tabl
     dtype = _dtype_code(q) if desc is not None else _dtype_code(q, key_cache)
     _call(lib.pa_attn_weights, "pa_attn_weights", q.device,
           _ptr(q), _row_stride(q), _ptr(key_cache), _cache_stride(key_cache), _ptr(lse),
-          _ptr(cu_seqlens_q), _ptr(seqused_k), _ptr(block_table), block_table.stride(0),
-          cu_seqlens_q.numel() - 1, T, int(max_seqlen_q), int(max_seqlen_k), H, hk, D, bs, nb,
+          _ptr(cu_seqlens_q), _ptr(seqused_k), _ptr(block_table), bt_row,
+          S, T, int(max_seqlen_q), int(max_seqlen_k), H, hk, D, bs, nb,
           float(softmax_scale), int(bool(causal)), _ptr(weights),
           _weights_stride(weights, nb, bs, hk), None if desc is None else ctypes.byref(desc),
           dtype, _ptr(dev_status))
@@ -753,19 +804,14 @@ def evict(key_cache, value_cache, weights, seqused_k, block_table, max_seqlen_k,
     [num_seqs, num_kv_heads, budget], new_lens int32 [num_seqs]); new_lens may
     be seqused_k itself."""
     lib = load_library()
-    _need_cuda(key_cache, value_cache, weights, seqused_k, block_table, kept, new_lens,
-               dev_status)
+    _one_device(key_cache, value_cache, weights, seqused_k, block_table, kept, new_lens,
+                dev_status)
     if key_cache.stride() != value_cache.stride() or key_cache.shape != value_cache.shape or \
             key_cache.dtype != value_cache.dtype:
         raise ValueError("key and value caches must have the same shape, type and page stride")
     nb, bs, hk, d = key_cache.shape
-    S, = seqused_k.shape
-    if seqused_k.dtype != torch.int32 or block_table.dtype != torch.int32 or \
-            not seqused_k.is_contiguous():
-        raise ValueError("seqused_k (contiguous) and block_table must be int32")
-    row, unit = block_table.stride()
-    if unit != 1 or block_table.shape[0] != S:
-        raise ValueError("block_table must be [num_seqs, max_blocks] with unit column stride")
+    S = seqused_k.numel()
+    row = _seq_table(seqused_k, block_table, S)
     device = key_cache.device
     if kept is None:
         kept = torch.empty((S, hk, max(int(budget), 0)), dtype=torch.int32, device=device)

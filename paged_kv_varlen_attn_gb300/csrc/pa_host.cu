@@ -18,6 +18,9 @@ namespace {
 
 constexpr int kAbiVersion = 1;
 constexpr size_t kAlign = 256;
+// Positions, keys and rows of one call that the operators around attention
+// count in 32 bits, with room for a step past the end.
+constexpr int kMaxKeys = 1 << 30;
 
 inline size_t align_up(size_t x, size_t a = kAlign) { return (x + a - 1) / a * a; }
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -1052,7 +1055,8 @@ pa_status pa_window_fwd(const pa_kv_update* update, const void* q, int64_t q_tok
 pa_status pa_rope_table(float* cos_sin, int table_len, int rot_dim, double base,
                         const pa_rope_scaling* scaling, void* stream) {
   constexpr double kTwoPi = 6.283185307179586;
-  if (table_len < 0 || rot_dim < 2 || rot_dim > 256 || rot_dim % 2 != 0) return PA_ERR_INVALID_ARG;
+  if (table_len < 0 || table_len > kMaxKeys || rot_dim < 2 || rot_dim > 256 || rot_dim % 2 != 0)
+    return PA_ERR_INVALID_ARG;
   if (!std::isfinite(base) || !(base > 0.0)) return PA_ERR_INVALID_ARG;
   const pa_rope_scaling none{PA_ROPE_NONE, 1.0, 1.0, 1.0, 2.0, 1.0};
   const pa_rope_scaling& s = scaling ? *scaling : none;
@@ -1215,7 +1219,8 @@ pa_status pa_attn_weights(const void* q, int64_t q_token_stride, const void* key
       (causal != 0 && causal != 1))
     return PA_ERR_INVALID_ARG;
   // Blocks of one launch: 64 keys of a sequence (and 128 of one KV head) each.
-  if (num_kv_heads > 65535 ||
+  if (max_seqlen_k > kMaxKeys ||
+      static_cast<long long>(total_q) * (num_heads / num_kv_heads) > kMaxKeys ||
       static_cast<long long>(num_seqs) * cdiv(max_seqlen_k, 64) * num_kv_heads > 0x7fffffffLL)
     return PA_ERR_INVALID_ARG;
   if (num_seqs == 0 || total_q == 0) return PA_OK;
@@ -1241,7 +1246,7 @@ pa_status pa_attn_weights(const void* q, int64_t q_token_stride, const void* key
   a.max_q = max_seqlen_q;
   a.max_k = max_seqlen_k;
   const long long cap = static_cast<long long>(bt_stride) * block_size;
-  a.kv_len_cap = cap > 0x7fffffff ? 0x7fffffff : static_cast<int>(cap);
+  a.kv_len_cap = cap > kMaxKeys ? kMaxKeys : static_cast<int>(cap);
   a.scale_log2 = softmax_scale * 1.4426950408889634f;
   a.causal = causal;
   a.k_scale = fp8 ? fp8->k_scale : nullptr;
@@ -1269,7 +1274,7 @@ pa_status pa_evict(void* key_cache, void* value_cache, int64_t cache_block_strid
   if (num_seqs < 0 || max_seqlen_k < 0 || num_kv_heads <= 0 || num_kv_heads > 65535 ||
       num_blocks < 0 || bt_stride < 0)
     return PA_ERR_INVALID_ARG;
-  if (budget < 1 || num_first < 0 || num_recent < 0 || num_first > budget ||
+  if (budget < 1 || budget > kMaxKeys || num_first < 0 || num_recent < 0 || num_first > budget ||
       num_recent > budget - num_first)
     return PA_ERR_INVALID_ARG;
   if (elem_size != 1 && elem_size != 2) return PA_ERR_UNSUPPORTED;
@@ -1306,7 +1311,7 @@ pa_status pa_evict(void* key_cache, void* value_cache, int64_t cache_block_strid
   a.bs_shift = log2_or_none(block_size);
   a.max_k = max_seqlen_k;
   const long long cap = static_cast<long long>(bt_stride) * block_size;
-  a.kv_len_cap = cap > 0x7fffffff ? 0x7fffffff : static_cast<int>(cap);
+  a.kv_len_cap = cap > kMaxKeys ? kMaxKeys : static_cast<int>(cap);
   a.budget = budget;
   a.first = num_first;
   a.recent = num_recent;

@@ -88,6 +88,8 @@ def call_weights(lib, **kw):
     (dict(fp8=(FAKE + 2, FAKE)), pa.PA_ERR_INVALID_ARG),
     (dict(fp8=(FAKE, None), D=64, qs=32 * 64, cbs=16 * 8 * 64), pa.PA_ERR_UNSUPPORTED),
     (dict(S=1 << 30, mk=1 << 20), pa.PA_ERR_INVALID_ARG),      # more blocks than a launch has
+    (dict(mk=(1 << 30) + 1), pa.PA_ERR_INVALID_ARG),
+    (dict(T=1 << 29), pa.PA_ERR_INVALID_ARG),                  # packed rows
     (dict(S=0, T=0), pa.PA_OK),
     (dict(T=0, q=None, lse=None), pa.PA_OK),                   # no queries: nothing to add
 ])
@@ -108,6 +110,7 @@ def call_evict(lib, **kw):
 @pytest.mark.parametrize("kw,code", [
     (dict(S=-1), pa.PA_ERR_INVALID_ARG),
     (dict(budget=0), pa.PA_ERR_INVALID_ARG),
+    (dict(budget=(1 << 30) + 1), pa.PA_ERR_INVALID_ARG),
     (dict(first=-1), pa.PA_ERR_INVALID_ARG),
     (dict(recent=-1), pa.PA_ERR_INVALID_ARG),
     (dict(first=20, recent=13), pa.PA_ERR_INVALID_ARG),

@@ -69,7 +69,7 @@ def test_table_refusals(lib):
     def call(out=FAKE, n=8, rot=64, base=1e4, s=None):
         return lib.pa_rope_table(out, n, rot, base, s, None)
     bad = pa.PA_ERR_INVALID_ARG
-    for kw in (dict(n=-1), dict(rot=0), dict(rot=7), dict(rot=258), dict(base=0.0),
+    for kw in (dict(n=-1), dict(n=(1 << 30) + 1), dict(rot=0), dict(rot=7), dict(rot=258), dict(base=0.0),
                dict(base=-2.0), dict(base=float("nan")), dict(base=float("inf")),
                dict(out=None), dict(out=FAKE + 4),
                dict(s=scaling(kind=5)), dict(s=scaling(kind=-1)), dict(s=scaling(factor=0.0)),
@@ -110,6 +110,7 @@ def call_rope(lib, r=None, **kw):
     (dict(update=False), pa.PA_ERR_INVALID_ARG),
     (dict(n=-1), pa.PA_ERR_INVALID_ARG),
     (dict(H=0), pa.PA_ERR_INVALID_ARG),
+    (dict(H=1 << 22, qs=1 << 30, os=1 << 30), pa.PA_ERR_INVALID_ARG),   # row offsets past 32 bits
     (dict(hk=0), pa.PA_ERR_INVALID_ARG),
     (dict(D=96), pa.PA_ERR_UNSUPPORTED),
     (dict(dtype=2), pa.PA_ERR_UNSUPPORTED),
