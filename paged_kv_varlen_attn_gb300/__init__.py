@@ -68,6 +68,7 @@ _lib = None
 _c = ctypes
 _vp, _i64, _i32, _f32, _sz = _c.c_void_p, _c.c_int64, _c.c_int, _c.c_float, _c.c_size_t
 _f64 = _c.c_double
+_INT_MAX = 0x7fffffff
 
 
 class KvUpdate(ctypes.Structure):
@@ -660,8 +661,8 @@ def window_fwd(q, key_cache, value_cache, cu_seqlens_q, seqused_k, block_table, 
           None if update is None else ctypes.byref(update), _ptr(q), _row_stride(q),
           _ptr(key_cache), _ptr(value_cache), _cache_stride(key_cache), _ptr(cu_seqlens_q),
           _ptr(seqused_k), _ptr(block_table), bt_row, S, T, int(max_seqlen_q),
-          int(max_seqlen_k), H, hk, D, bs, nb, float(softmax_scale), int(window),
-          int(num_first), ctypes.byref(opts), _ptr(out), _ptr(lse), _ptr(workspace),
+          int(max_seqlen_k), H, hk, D, bs, nb, float(softmax_scale), min(int(window), _INT_MAX),
+          min(int(num_first), _INT_MAX), ctypes.byref(opts), _ptr(out), _ptr(lse), _ptr(workspace),
           workspace.numel(), dtype, _ptr(dev_status))
     del keep
     return out, lse

@@ -128,6 +128,33 @@ def test_window(seed, S, H, hk, D, bs, mq, mk, dfrac, empty, window, first, dtyp
                         2 * wl.max_seqlen_q + 40, 3 * wl.max_seqlen_k + 500, *tail[2:]), want)
 
 
+MANY = [
+    # q lengths, kv lengths, H, hk, D, window, first, dtype: more units than SMs
+    ([700, 333, 1, 650, 5, 701], [900, 333, 640, 1000, 5, 701], 16, 8, 128, 100, 5, torch.bfloat16),
+    ([700, 333, 0, 650, 129], [750, 400, 0, 650, 500], 24, 8, 64, 64, 0, torch.float16),   # G 3
+    ([64] * 40, [64 + 13 * i for i in range(40)], 32, 8, 128, 37, 20, torch.bfloat16),     # one tile
+    ([2000, 1500], [5000, 4100], 8, 1, 128, 3000, 4, torch.bfloat16),                      # KV splits
+    ([2100, 900], [2100, 2300], 7, 1, 64, 1500, 130, torch.float16),                       # G 7, splits
+]
+
+
+@pytest.mark.parametrize("ql,kv,H,hk,D,window,first,dtype", MANY)
+def test_window_many_units(ql, kv, H, hk, D, window, first, dtype):
+    """Batches of more (item, KV head) units than SMs: items with one and two Q
+    tiles, several and no key tiles, whole and split."""
+    wl = W._build("many", 3, H, hk, D, 16, ql, kv, torch.Generator().manual_seed(3), dtype=dtype)
+    kc, vc = oracle_pools(wl)
+    want = define(wl, kc, vc, window, first)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    tail = (wl.max_seqlen_q, wl.max_seqlen_k, wl.softmax_scale, window, first)
+    got = pa.window_fwd(wl.q.to(DEV), kc.to(DEV), vc.to(DEV), *dev(wl), *tail, dev_status=status)
+    check(got, want)
+    assert int(status) == 0
+    hk_, hv_, hbt = hide(wl, kc, vc, window, first)
+    again = pa.window_fwd(wl.q.to(DEV), hk_.to(DEV), hv_.to(DEV), *dev(wl)[:2], hbt.to(DEV), *tail)
+    assert torch.equal(again[0], got[0]) and torch.equal(again[1], got[1])
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("H,hk,bs,mq,mk,dfrac,window,first", [
     (32, 8, 16, 1, 2500, 1.0, 600, 4),      # the FP8 decode consumer
@@ -251,3 +278,18 @@ def test_window_captured_and_repeatable():
     torch.cuda.synchronize()
     again = pa.window_fwd(*d, *tail)
     assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
+def test_window_wider_than_32_bits():
+    """A window (first tokens) past the C interface's integers is none (all)."""
+    wl = W.random_case(77, num_seqs=3, num_heads=8, num_kv_heads=2, head_size=64, block_size=16,
+                       max_q=40, max_kv=300)
+    kc, vc = (t.to(DEV) for t in oracle_pools(wl))
+    args = (wl.q.to(DEV), kc, vc, *dev(wl), wl.max_seqlen_q, wl.max_seqlen_k, wl.softmax_scale)
+    plain = pa.varlen_fwd(*args, True)
+    for window, first in ((1 << 40, 0), ((1 << 32) + 5, 0), (7, (1 << 32) + 1)):
+        got = pa.window_fwd(*args, window, first)
+        if window > 7:
+            assert torch.equal(got[0], plain[0]) and torch.equal(got[1], plain[1])
+        else:
+            check(got, define(wl, kc.cpu(), vc.cpu(), wl.max_seqlen_k, 0))
