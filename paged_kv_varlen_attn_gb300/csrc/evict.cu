@@ -286,7 +286,7 @@ evict_move_kernel(const __grid_constant__ EvictArgs a) {
   if (b < slices) {
     const int64_t col = static_cast<int64_t>(h) * a.row_bytes + b * (16 * LANES) +
                         threadIdx.x % LANES * 16;
-    const int row_stride = a.H_kv * a.row_bytes;
+    const int64_t row_stride = static_cast<int64_t>(a.H_kv) * a.row_bytes;
     uint4 k[kMoveUnroll], v[kMoveUnroll];
     move_rows<kMoveThreads / LANES>(
         a, kept, bt, threadIdx.x / LANES, bad,
