@@ -588,7 +588,9 @@ pa_status pa_rope_and_cache(const pa_rope* rope, const int64_t* positions, const
  *   q, key_cache, cu_seqlens_q, seqused_k, block_table, max_seqlen_q,
  *   max_seqlen_k, softmax_scale, causal : as in the attention call.
  *   lse       : float32 [num_heads, total_q], that call's log-sum-exp (with
- *               its sinks, if any; a row of -inf saw nothing and adds nothing).
+ *               its sinks, if any; a row of -inf saw nothing and adds nothing,
+ *               whatever its query holds). Not pa_window_fwd's: every key a
+ *               causal query sees counts, a window is not applied.
  *   weights   : float32, one value per cache slot and KV head: key row r of
  *               page b, head h at b * weights_block_stride + h * block_size +
  *               r. weights_block_stride a multiple of 4.

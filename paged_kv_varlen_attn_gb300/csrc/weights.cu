@@ -310,6 +310,17 @@ struct WtBars {
 };
 static_assert(sizeof(WtBars) <= 256, "the barriers fit their space");
 
+// Barrier `id` of 128 threads: does any of them bring p?
+__device__ __forceinline__ bool group_any(int id, bool p) {
+  uint32_t any;
+  asm volatile("{\n.reg .pred a, b;\nsetp.ne.u32 a, %2, 0;\nbar.red.or.pred b, %1, 128, a;\n"
+               "selp.u32 %0, 1, 0, b;\n}"
+               : "=r"(any)
+               : "r"(id), "r"(static_cast<uint32_t>(p))
+               : "memory");
+  return any != 0;
+}
+
 // Clusters: rank, arrive / wait, and a store to this shared-memory location in
 // the block of rank `rank`.
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -556,7 +567,8 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             y[k] = fast_exp2(y[k]);
             if constexpr (decltype(masked)::value) {
               const int col = c * 32 + e + k;
-              y[k] = col >= c0 && col < c1 ? y[k] : 0.f;
+              const float nk = k == 0 ? n4.x : k == 1 ? n4.y : k == 2 ? n4.z : n4.w;
+              y[k] = col >= c0 && col < c1 && nk != -INFINITY ? y[k] : 0.f;
             }
           }
           fadd2(acc[0], acc[1], acc[0], acc[1], y[0], y[1]);
@@ -569,7 +581,9 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       const int t = tile_of(n), x = key_tile_of(n);
       float* nlb = nl + (it & 1) * C::COLS;
       nlb[tid] = next;
-      asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory");
+      // (A query that saw nothing may hold anything: its products are dropped
+      // by a select, not by the exponential.)
+      const bool blind = group_any(1 + wg, tid < TR && next == -INFINITY);
       if (n + C::GROUPS < nprod) next = fetch(tile_of(n + C::GROUPS));
       // Columns [c0, c1) of the tile see this key: queries from its own
       // position on, rows of the sequence.
@@ -577,7 +591,7 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       const int c0 = a.causal ? max(0, (key0 + x * 128 + tid - past - tok0) * G) : 0;
       const int c1 = min(TR, (q_len - tok0) * G);
       const bool edge =
-          tok0 + TPT > q_len || (a.causal && tok0 < key0 + x * 128 + 127 - past);
+          blind || tok0 + TPT > q_len || (a.causal && tok0 < key0 + x * 128 + 127 - past);
       // A warp whose wait gave up goes on through the group's barriers without
       // work, so that no other warp waits for it.
       if (ok) ok = !bars->abort && mbar_wait(&bars->s_full[wg], it & 1);

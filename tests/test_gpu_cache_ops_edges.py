@@ -238,3 +238,31 @@ def test_oracle_weights_match_the_attention_lse():
     # the LSE's own 1e-3
     total = w.double().sum((0, 2)).cpu()
     assert ((total - 4 * wl.total_q).abs() <= 2e-3 * 4 * wl.total_q).all()
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("H,D,mq", [(8, 128, 1), (8, 128, 300), (14, 64, 400), (4, 256, 260)])
+def test_weights_rows_that_saw_nothing_hold_anything(H, D, mq, causal):
+    """Queries whose LSE is -inf (padding rows) hold NaN and infinities: the
+    same bits as with zeros there."""
+    wl = W.random_case(311 + mq, num_seqs=3, num_heads=H, num_kv_heads=2, head_size=D,
+                       block_size=16, max_q=mq, max_kv=700, decode_frac=0.0)
+    kc, vc = oracle_pools(wl)
+    meta = (wl.cu_seqlens_q, wl.seqused_k, wl.block_table)
+    _, lse = oracle.varlen_attention(wl.q, kc, vc, *meta, wl.softmax_scale, causal)
+    lse = lse.float()
+    blind = torch.rand(lse.shape, generator=torch.Generator().manual_seed(5)) < 0.05
+    blind[1, 0] = True
+    lse[blind] = float("-inf")
+    w0 = random_weights(wl)
+    got = []
+    for fill in (0.0, float("nan"), float("inf")):
+        q = wl.q.clone()
+        q[blind.T] = fill
+        got.append(pa.attn_weights(q.to(DEV), kc.to(DEV), lse.to(DEV), w0.to(DEV), *dev(wl),
+                                   wl.max_seqlen_q, wl.max_seqlen_k, wl.softmax_scale, causal))
+    want = ref.attn_weights(torch.where(blind.T[..., None], torch.zeros_like(wl.q), wl.q), kc, lse,
+                            w0, *meta, wl.softmax_scale, causal)
+    rel = rel_bound(wl, kc, lse)
+    assert ((got[0].cpu().double() - want).abs() <= rel * want.abs()).all()
+    assert torch.equal(got[0], got[1]) and torch.equal(got[0], got[2])
