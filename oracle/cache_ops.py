@@ -78,7 +78,7 @@ def _attend(q, k, v, scale, seen, sink=None):
     x = torch.where(seen, x, torch.full_like(x, -math.inf))
     if sink is not None:
         x = torch.cat([x, torch.full((x.shape[0], 1), float(sink), dtype=F64)], 1)
-        v = torch.cat([v, torch.zeros_like(v[:1])])
+        v = torch.cat([v, v.new_zeros((1, v.shape[1]))])
     lse = torch.logsumexp(x, 1) if x.shape[1] else torch.full((x.shape[0],), -math.inf, dtype=F64)
     p = torch.where(torch.isfinite(lse)[:, None], torch.exp(x - lse[:, None]),
                     torch.zeros_like(x))

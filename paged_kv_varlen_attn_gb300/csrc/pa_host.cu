@@ -617,6 +617,54 @@ static pa_status varlen_impl(const pa_kv_update* upd, const void* q, int64_t q_t
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) % kAlign) != 0 ||
       workspace_bytes < L.end)
     return PA_ERR_WORKSPACE;
+  if (window > 0 && !kv.fp8 && head_size <= 128 &&
+      static_cast<long long>(max_seqlen_q) * d.G <= kWinRows) {
+    // Slices of 16 keys that a sequence's queries see: the first tokens, and
+    // window + max_seqlen_q - 1 keys at any offset.
+    const long long slices = cdiv(num_first, 16) +
+                             (static_cast<long long>(window) + max_seqlen_q - 1) / 16 + 2;
+    if (slices <= kWinMaxParts * kWinPartSlices &&
+        static_cast<long long>(num_seqs) * num_kv_heads * kWinMaxParts <= 0x7fffffffLL) {
+      if (upd && upd->num_tokens > 0 &&
+          launch_scatter(upd->key, upd->value, upd->key_token_stride, upd->value_token_stride,
+                         key_cache, value_cache, cache_block_stride, upd->slot_mapping,
+                         upd->num_tokens, num_kv_heads, head_size, block_size, num_blocks, kv,
+                         dev_status, c.st, sms, false, dtype) != cudaSuccess)
+        return PA_ERR_CUDA;
+      WinDecodeArgs w{};
+      w.q = static_cast<const uint16_t*>(q);
+      w.q_stride = q_token_stride;
+      w.kc = static_cast<const uint8_t*>(key_cache);
+      w.vc = static_cast<const uint8_t*>(value_cache);
+      w.block_stride_bytes = cache_block_stride * 2;
+      w.cu = cu_seqlens_q;
+      w.seqused_k = seqused_k;
+      w.bt = block_table;
+      w.bt_stride = bt_stride;
+      w.H = num_heads;
+      w.H_kv = num_kv_heads;
+      w.G = d.G;
+      w.bs = block_size;
+      w.bs_shift = log2_or_none(block_size);
+      w.num_blocks = num_blocks;
+      w.total_q = total_q;
+      w.max_q = max_seqlen_q;
+      w.max_k = max_seqlen_k;
+      const long long cap = static_cast<long long>(bt_stride) * block_size;
+      w.kv_len_cap = cap > 0x7fffff00 ? 0x7fffff00 : static_cast<int>(cap);
+      w.window = window;
+      w.first = num_first;
+      w.scale_log2 = softmax_scale * 1.4426950408889634f;
+      w.sinks = sinks;
+      w.out = static_cast<uint16_t*>(out);
+      w.lse = lse;
+      w.status = dev_status;
+      return launch_window_decode(w, num_seqs, static_cast<int>(slices), head_size,
+                                  dtype == PA_F16, c.st, sms) == cudaSuccess
+                 ? PA_OK
+                 : PA_ERR_CUDA;
+    }
+  }
   const int box_rows = gcd_int(block_size, kKeyTile);
   CUtensorMap tmK, tmV;
   if (!encode_pool_map(&tmK, key_cache, head_size, num_kv_heads, block_size, num_blocks,

@@ -197,6 +197,37 @@ cudaError_t launch_cascade_combine(const AttnArgs& a0, const AttnArgs& a1, int g
 cudaError_t launch_attn_tc(const CUtensorMap& tmK, const CUtensorMap& tmV, const CUtensorMap& tmQ,
                            const AttnArgs& a, int items_bound, cudaStream_t st);
 
+// Decode under a sliding window (window_decode.cu): sequences of at most
+// kWinRows packed query rows whose visible keys span at most
+// kWinMaxParts * kWinPartSlices slices of 16.
+constexpr int kWinRows = 8;
+constexpr int kWinMaxParts = 8;          // blocks (of a cluster) per sequence and KV head
+constexpr int kWinPartSlices = 4 * 32;   // four warps, a page id per lane
+struct WinDecodeArgs {
+  const uint16_t* q;
+  int64_t q_stride;
+  const uint8_t* kc;
+  const uint8_t* vc;
+  int64_t block_stride_bytes;
+  const int32_t* cu;
+  const int32_t* seqused_k;
+  const int32_t* bt;
+  int bt_stride;
+  int H, H_kv, G, bs, num_blocks, total_q;
+  int bs_shift;                   // log2(bs), or -1 where bs is no power of two
+  int max_q, max_k, kv_len_cap;
+  int window, first;
+  float scale_log2;               // softmax_scale * log2(e)
+  const float* sinks;             // [H] or NULL
+  uint16_t* out;                  // [total_q, H, D]
+  float* lse;                     // [H, total_q] or NULL
+  int32_t* status;
+  int parts;                      // set by the launcher
+};
+// slices: a bound on the slices of 16 keys that a sequence's queries see.
+cudaError_t launch_window_decode(WinDecodeArgs a, int num_seqs, int slices, int D, bool f16,
+                                 cudaStream_t st, int sms);
+
 // Rotary cos/sin table (rope.cu).
 struct RopeTableArgs {
   int table_len, rot;

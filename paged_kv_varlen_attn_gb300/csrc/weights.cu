@@ -5,7 +5,6 @@
 // sums are the same bits on every run.
 #include <cuda_runtime.h>
 
-#include <atomic>
 #include <type_traits>
 
 #include "device_common.cuh"
@@ -42,22 +41,6 @@ struct WwCfg {
   static constexpr int SLOTS = ROW >= 256 ? 2 : 4;
   static constexpr int SMEM_BYTES = kWeightWarps * SLOTS * SLOT;
 };
-
-// Asynchronous copies to shared memory: 16 bytes (past L1), and 4 bytes or, for
-// take = false, a zero.
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool take) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
-               "r"(take ? 4 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 
 // Two e4m3 bytes as a pair of the MMA's element type (exact in both).
 template <bool F16>
@@ -319,25 +302,6 @@ __device__ __forceinline__ bool group_any(int id, bool p) {
                : "r"(id), "r"(static_cast<uint32_t>(p))
                : "memory");
   return any != 0;
-}
-
-// Clusters: rank, arrive / wait, and a store to this shared-memory location in
-// the block of rank `rank`.
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
-}
-__device__ __forceinline__ void store_remote(const void* p, uint32_t rank, uint32_t v) {
-  uint32_t at;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
 }
 
 template <int D, bool F16, bool FP8>
@@ -669,22 +633,6 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
 }
 
 constexpr long long kPairUnits = 304;
-
-// The shared-memory opt-in, a per-device function attribute: set on the first
-// launch on each device (before any stream capture), not again.
-template <typename Kernel>
-static cudaError_t opt_in_smem(Kernel kernel, int bytes, std::atomic<bool>* configured) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const bool known = dev >= 0 && dev < kMaxDevices;
-  if (!known || !configured[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess) return e;
-    if (known) configured[dev].store(true, std::memory_order_release);
-  }
-  return cudaSuccess;
-}
 
 template <int D, bool F16, bool FP8>
 static cudaError_t launch_weights_d(const CUtensorMap& tmQ, const WeightArgs& a, int num_seqs,

@@ -293,3 +293,89 @@ def test_window_wider_than_32_bits():
             assert torch.equal(got[0], plain[0]) and torch.equal(got[1], plain[1])
         else:
             check(got, define(wl, kc.cpu(), vc.cpu(), wl.max_seqlen_k, 0))
+
+
+DECODE = [
+    # q lengths, kv lengths, H, hk, D, bs, window, first, dtype: at most 8 packed rows
+    ([1], [5000], 8, 1, 128, 16, 4000, 7, torch.bfloat16),          # few sequences: several blocks
+    ([1, 1], [17000, 900], 2, 1, 128, 16, 16000, 40, torch.float16),
+    ([1], [16700], 1, 1, 64, 64, 16400, 0, torch.bfloat16),         # a window past the kernel's
+    ([1] * 40, [1 + 23 * i for i in range(40)], 8, 8, 64, 32, 200, 33, torch.bfloat16),
+    ([2, 0, 1, 2, 2], [2, 40, 300, 301, 2], 8, 2, 128, 16, 100, 5, torch.bfloat16),
+    ([1, 1, 1], [1, 16, 17], 8, 1, 64, 16, 16, 0, torch.float16),   # one key, a slice, one more
+    ([8, 3, 5], [8, 500, 77], 4, 4, 128, 48, 31, 17, torch.float16),   # q rows of one head
+    ([1] * 100, [700 + i for i in range(100)], 16, 8, 128, 16, 640, 4, torch.bfloat16),
+    ([2] * 90, [600] * 90, 12, 4, 64, 16, 300, 300, torch.bfloat16),   # G 3: 6 rows
+]
+
+
+@pytest.mark.parametrize("ql,kv,H,hk,D,bs,window,first,dtype", DECODE)
+def test_window_decode(ql, kv, H, hk, D, bs, window, first, dtype):
+    """Few packed query rows: every split of the keys over warps and blocks,
+    with sinks, and pages that nobody sees."""
+    wl = W._build("decode", 5, H, hk, D, bs, ql, kv, torch.Generator().manual_seed(9), dtype=dtype)
+    kc, vc = oracle_pools(wl)
+    sinks = torch.linspace(-1, 2, H)
+    tail = (wl.max_seqlen_q, max(wl.max_seqlen_k, window + 1), wl.softmax_scale, window, first)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    for sk in (None, sinks):
+        want = define(wl, kc, vc, window, first, sinks=sk)
+        skd = None if sk is None else sk.to(DEV)
+        got = pa.window_fwd(wl.q.to(DEV), kc.to(DEV), vc.to(DEV), *dev(wl), *tail, sinks=skd,
+                            dev_status=status)
+        check(got, want)
+        hk_, hv_, hbt = hide(wl, kc, vc, window, first)
+        again = pa.window_fwd(wl.q.to(DEV), hk_.to(DEV), hv_.to(DEV), *dev(wl)[:2], hbt.to(DEV),
+                              *tail, sinks=skd, dev_status=status)
+        assert torch.equal(again[0], got[0]) and torch.equal(again[1], got[1])
+    assert int(status) == 0
+
+
+@pytest.mark.parametrize("sink", [False, True])
+def test_window_decode_more_queries_than_keys(sink):
+    """Queries in front of the first key, and sequences without keys, see
+    nothing (a sink apart)."""
+    wl = W._build("decode", 7, 8, 2, 64, 16, [2, 2, 1, 2], [60, 60, 60, 60],
+                  torch.Generator().manual_seed(4), dtype=torch.float16)
+    kc, vc = oracle_pools(wl)
+    lens = torch.tensor([1, 0, 0, 60], dtype=torch.int32)
+    sinks = torch.linspace(-1, 1, 8) if sink else None
+    meta = (wl.cu_seqlens_q, lens, wl.block_table)
+    got = pa.window_fwd(wl.q.to(DEV), kc.to(DEV), vc.to(DEV), *(t.to(DEV) for t in meta), 2, 60,
+                        wl.softmax_scale, 20, 3, sinks=None if sinks is None else sinks.to(DEV))
+    tail = (*meta, wl.softmax_scale, 20, 3)
+    sinks = None if sinks is None else sinks.double()
+    o, l = ref.window_attention(wl.q, kc, vc, *tail, sinks=sinks)
+    check(got, (o, l, ref.window_attention(wl.q, kc, vc.abs(), *tail, sinks=sinks)[0]))
+
+
+def test_window_decode_bad_metadata():
+    """A page outside the pool reads as zeros and is reported, as are lengths
+    past the bounds; a sequence with inconsistent offsets writes nothing."""
+    wl = W._build("decode", 6, 8, 2, 128, 16, [1, 1, 1], [400, 300, 200],
+                  torch.Generator().manual_seed(4))
+    kc, vc = oracle_pools(wl)
+    bt = wl.block_table.clone()
+    page = int(bt[1, 10])
+    bt[1, 10] = wl.num_blocks
+    zk, zv = kc.clone(), vc.clone()
+    zk[page] = 0
+    zv[page] = 0
+    args = (wl.q.to(DEV), kc.to(DEV), vc.to(DEV))
+    cu, lens, _ = dev(wl)
+    tail = (1, wl.max_seqlen_k, wl.softmax_scale, 250, 3)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    got = pa.window_fwd(*args, cu, lens, bt.to(DEV), *tail, dev_status=status)
+    assert int(status) == pa.PA_DEV_BAD_PAGE
+    check(got, define(wl, zk, zv, 250, 3))
+    status.zero_()
+    pa.window_fwd(*args, *dev(wl), 1, 350, *tail[2:], dev_status=status)
+    assert int(status) == pa.PA_DEV_BAD_SEQLEN
+    status.zero_()
+    bad = torch.tensor([0, 1, 5, 3], dtype=torch.int32, device=DEV)
+    out = torch.full_like(args[0], 7.0)
+    pa.window_fwd(*args, bad, lens, dev(wl)[2], *tail, out=out, dev_status=status)
+    assert int(status) == pa.PA_DEV_BAD_SEQLEN
+    want = define(wl, kc, vc, 250, 3)[0]
+    assert (out[0].cpu().double() - want[0]).abs().max() < 0.05
+    assert (out[1:] == 7.0).all()
