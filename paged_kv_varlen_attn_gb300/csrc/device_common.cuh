@@ -281,6 +281,18 @@ struct Elem<true> {
   static constexpr uint32_t kTcFormat = 0;   // tcgen05 kind::f16 operand format: f16
 };
 
+// Two e4m3 bytes as a pair of the MMA's element type (exact in both).
+template <bool F16>
+__device__ __forceinline__ uint32_t widen_e4m3x2(uint32_t two) {
+  const uint32_t h = e4m3x2_to_f16x2(two);
+  if constexpr (F16) {
+    return h;
+  } else {
+    const float2 f = Elem<true>::unpack(h);
+    return Elem<false>::pack(f.x, f.y);
+  }
+}
+
 // Two-lane float32 arithmetic (sm_100 and later): one instruction computes a
 // pair, each lane rounded exactly as the scalar fmaf / add would be.
 __device__ __forceinline__ void ffma2(float& d0, float& d1, float a0, float a1, float b0,

@@ -617,14 +617,18 @@ static pa_status varlen_impl(const pa_kv_update* upd, const void* q, int64_t q_t
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) % kAlign) != 0 ||
       workspace_bytes < L.end)
     return PA_ERR_WORKSPACE;
-  if (window > 0 && !kv.fp8 && head_size <= 128 &&
-      static_cast<long long>(max_seqlen_q) * d.G <= kWinRows) {
+  if (window > 0 && static_cast<long long>(max_seqlen_q) * d.G <= kWinRows) {
     // Slices of 16 keys that a sequence's queries see: the first tokens, and
     // window + max_seqlen_q - 1 keys at any offset.
     const long long slices = cdiv(num_first, 16) +
                              (static_cast<long long>(window) + max_seqlen_q - 1) / 16 + 2;
-    if (slices <= kWinMaxParts * kWinPartSlices &&
-        static_cast<long long>(num_seqs) * num_kv_heads * kWinMaxParts <= 0x7fffffffLL) {
+    // A long window of a few (sequence, KV head) pairs is read faster by the
+    // planned kernel's finer splits: one sequence of 8 KV heads of 128 takes
+    // 24.2 us (25.3 planned) at window 12000, 30.1 (26.8) at 16000; two take
+    // 36.7 (50.0).
+    const long long units = static_cast<long long>(num_seqs) * num_kv_heads;
+    if (slices <= (units * kWinMaxParts < sms ? 3 : 4) * (kWinMaxParts * kWinPartSlices / 4) &&
+        units * kWinMaxParts <= 0x7fffffffLL) {
       if (upd && upd->num_tokens > 0 &&
           launch_scatter(upd->key, upd->value, upd->key_token_stride, upd->value_token_stride,
                          key_cache, value_cache, cache_block_stride, upd->slot_mapping,
@@ -636,7 +640,7 @@ static pa_status varlen_impl(const pa_kv_update* upd, const void* q, int64_t q_t
       w.q_stride = q_token_stride;
       w.kc = static_cast<const uint8_t*>(key_cache);
       w.vc = static_cast<const uint8_t*>(value_cache);
-      w.block_stride_bytes = cache_block_stride * 2;
+      w.block_stride_bytes = cache_block_stride * (kv.fp8 ? 1 : 2);
       w.cu = cu_seqlens_q;
       w.seqused_k = seqused_k;
       w.bt = block_table;
@@ -655,6 +659,8 @@ static pa_status varlen_impl(const pa_kv_update* upd, const void* q, int64_t q_t
       w.window = window;
       w.first = num_first;
       w.scale_log2 = softmax_scale * 1.4426950408889634f;
+      w.k_scale = kv.k_scale;
+      w.v_scale = kv.v_scale;
       w.sinks = sinks;
       w.out = static_cast<uint16_t*>(out);
       w.lse = lse;

@@ -218,6 +218,8 @@ struct WinDecodeArgs {
   int max_q, max_k, kv_len_cap;
   int window, first;
   float scale_log2;               // softmax_scale * log2(e)
+  const float* k_scale;           // [H_kv], e4m3 pools (head size 128); else NULL
+  const float* v_scale;
   const float* sinks;             // [H] or NULL
   uint16_t* out;                  // [total_q, H, D]
   float* lse;                     // [H, total_q] or NULL

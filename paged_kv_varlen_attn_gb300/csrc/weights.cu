@@ -42,18 +42,6 @@ struct WwCfg {
   static constexpr int SMEM_BYTES = kWeightWarps * SLOTS * SLOT;
 };
 
-// Two e4m3 bytes as a pair of the MMA's element type (exact in both).
-template <bool F16>
-__device__ __forceinline__ uint32_t widen_e4m3x2(uint32_t two) {
-  const uint32_t h = e4m3x2_to_f16x2(two);
-  if constexpr (F16) {
-    return h;
-  } else {
-    const float2 f = Elem<true>::unpack(h);
-    return Elem<false>::pack(f.x, f.y);
-  }
-}
-
 // Lengths of sequence s for both kernels: false if the call has nothing to add
 // for it. Blocks with `reports` set flag metadata outside the stated bounds.
 __device__ __forceinline__ bool weight_lengths(const WeightArgs& a, int s, bool reports, int& q0,
@@ -509,7 +497,7 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     };
     float next = wg < nprod ? fetch(tile_of(wg)) : 0.f;
     float acc[4];
-    auto sum_tile = [&](const float* nlb, int c0, int c1, auto masked) {
+    auto sum_tile = [&](const float* nlb, int c0, int c1, auto mask) {
 #pragma unroll
       for (int c = 0; c < C::COLS / 32; ++c) {
         uint32_t v[32];
@@ -529,10 +517,13 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             y[k] = fast_exp2(y[k]);
-            if constexpr (decltype(masked)::value) {
+            if constexpr (decltype(mask)::value > 0) {
               const int col = c * 32 + e + k;
+              y[k] = col >= c0 && col < c1 ? y[k] : 0.f;
+            }
+            if constexpr (decltype(mask)::value > 1) {
               const float nk = k == 0 ? n4.x : k == 1 ? n4.y : k == 2 ? n4.z : n4.w;
-              y[k] = col >= c0 && col < c1 && nk != -INFINITY ? y[k] : 0.f;
+              y[k] = nk != -INFINITY ? y[k] : 0.f;
             }
           }
           fadd2(acc[0], acc[1], acc[0], acc[1], y[0], y[1]);
@@ -555,7 +546,7 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       const int c0 = a.causal ? max(0, (key0 + x * 128 + tid - past - tok0) * G) : 0;
       const int c1 = min(TR, (q_len - tok0) * G);
       const bool edge =
-          blind || tok0 + TPT > q_len || (a.causal && tok0 < key0 + x * 128 + 127 - past);
+          tok0 + TPT > q_len || (a.causal && tok0 < key0 + x * 128 + 127 - past);
       // A warp whose wait gave up goes on through the group's barriers without
       // work, so that no other warp waits for it.
       if (ok) ok = !bars->abort && mbar_wait(&bars->s_full[wg], it & 1);
@@ -566,11 +557,14 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       }
       tc_fence_after();
       acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
-      // Two bodies, so that a tile that every key sees whole pays no select.
-      if (edge)
-        sum_tile(nlb, c0, c1, std::true_type{});
+      // Three bodies, so that a tile that every key sees whole pays no select
+      // (one for all: 4 us of 84 on two prompts of 2,500-4,096 tokens).
+      if (blind)
+        sum_tile(nlb, c0, c1, std::integral_constant<int, 2>{});
+      else if (edge)
+        sum_tile(nlb, c0, c1, std::integral_constant<int, 1>{});
       else
-        sum_tile(nlb, c0, c1, std::false_type{});
+        sum_tile(nlb, c0, c1, std::integral_constant<int, 0>{});
       const float got = (acc[0] + acc[1]) + (acc[2] + acc[3]);
       sum[0] += x == 0 ? got : 0.f;
       sum[1] += x == 0 ? 0.f : got;

@@ -23,18 +23,29 @@ namespace pa {
 //     weights inside the element type)
 //   O^T[D x 8 rows] += V^T P^T         V by transposed matrix loads from a
 //     swizzled slice; P^T as the B operand by two 8x8 register transposes
+// e4m3 pools: both products on f16 MMAs, which hold every e4m3 value and the
+// query (see below) exactly; the K scale joins the scores', the V scale the
+// final division.
 // Rows of a slice that no query sees (before the window, past the sequence)
 // are filled with zeros in V and masked in S: what their memory holds does not
 // matter. The states (maximum, sum, O) of the warps meet in shared memory,
 // those of the blocks of a cluster through distributed shared memory, always
 // in the same order: no workspace, no atomics, the same bits on every run.
+// Bound by the read of K and V: 64 sequences, 32/8 heads of 128, 46.0 us at
+// window 1024 (276 MB, 6.0 TB/s), where the planned split kernel takes 73.5,
+// and 169 us at window 4096 (6.35 TB/s; 203). e4m3 pools 36.7 us (54.0), by
+// the conversions of K and V; head size 256 (16/8 heads) 89 us (149). Three
+// slots per warp: two gave 43.5 us where four sequences' worth of warps read
+// window 16000 instead of 36.7, four leave three blocks on an SM (57.6 us
+// against 51.7 on the 64 sequences, uncached).
 // ---------------------------------------------------------------------------
 constexpr int kWdWarps = 4;
 
-template <int D>
+template <int D, bool FP8>
 struct WdCfg {
   static constexpr int SLOTS = 3;
-  static constexpr int ROW = D * 2;                    // bytes of a key
+  static constexpr int BLOCKS = D > 128 ? 2 : 4;       // per SM
+  static constexpr int ROW = D * (FP8 ? 1 : 2);        // bytes of a key
   static constexpr int TILE = 16 * ROW;                // a slice of K or of V
   static constexpr int RING = SLOTS * TILE;            // of a warp
   // A warp's state, in its ring: O[row][PITCH] (pitch of 4 banks mod 32: the
@@ -45,12 +56,13 @@ struct WdCfg {
   static_assert(kWinRows * PITCH * 4 <= RING, "the state fits the ring");
 };
 
-template <int D, bool F16>
-__global__ void __launch_bounds__(kWdWarps * 32, 4)
+template <int D, bool F16, bool FP8>
+__global__ void __launch_bounds__(kWdWarps * 32, WdCfg<D, FP8>::BLOCKS)
 window_decode_kernel(const __grid_constant__ WinDecodeArgs a) {
   using E = Elem<F16>;
-  using C = WdCfg<D>;
-  constexpr int NV = C::ROW / 64;                      // 16-byte pieces of a row per lane
+  using C = WdCfg<D, FP8>;
+  constexpr int NV = C::ROW / 64;                      // 16-byte pieces of a key row per lane
+  constexpr int NQ = D / 32;                           // of a query row
   constexpr int PIECES = C::ROW / 16;                  // of a row
   extern __shared__ __align__(128) uint8_t smem[];
   // Parts fastest, then KV head: a page's heads are read at about the same time.
@@ -138,14 +150,15 @@ window_decode_kernel(const __grid_constant__ WinDecodeArgs a) {
   for (int u = 0; u < C::SLOTS - 1; ++u) fetch_next(u >> 1, u & 1);
 
   // Q as B fragments: packed row g (rows past the last repeat it, unwritten).
-  uint4 qv[NV];
+  uint4 qv[NQ];
   {
     const int r = min(g, rows - 1), i = r / a.G;
     const uint4* qrow = reinterpret_cast<const uint4*>(
         a.q + static_cast<int64_t>(q0 + i) * a.q_stride +
         static_cast<int64_t>(hk * a.G + r - i * a.G) * D);
 #pragma unroll
-    for (int v = 0; v < NV; ++v) qv[v] = __ldg(qrow + 4 * v + c);
+    for (int v = 0; v < NQ; ++v)
+      qv[v] = __ldg(qrow + (FP8 ? 8 * (v >> 1) + 2 * c + (v & 1) : 4 * v + c));
   }
   // This lane's rows 2c, 2c + 1: their positions.
   int pos[2];
@@ -158,8 +171,48 @@ window_decode_kernel(const __grid_constant__ WinDecodeArgs a) {
   for (int t = 0; t < D / 16; ++t)
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[t][e] = 0.f;
-  // Row of the transposed loads of V: matrices (keys 0-7 | 8-15) x (dims 0-7 | 8-15).
-  const int vr = (lane & 7) + ((lane >> 4) & 1) * 8, vx = (lane >> 3) & 1;
+  // Row and piece of this lane in the transposed loads of V, two pieces at a
+  // time: matrices keys 0-7 | 8-15 of a piece (e4m3), or pieces of keys 0-7,
+  // then of keys 8-15.
+  const int vr = (lane & 7) + ((lane >> (FP8 ? 3 : 4)) & 1) * 8;
+  const int vx = (lane >> (FP8 ? 4 : 3)) & 1;
+  // Scale of the scores of rows 2c, 2c + 1.
+  float sl2[2] = {a.scale_log2, a.scale_log2};
+  using P = Elem<F16 || FP8>;                          // the MMA's type (e4m3 is exact in f16)
+  if constexpr (FP8) {
+    float qs = __ldg(a.k_scale + hk);
+    if constexpr (!F16) {
+      // A bf16 query as f16, its row brought to a maximum of 2^14 to 2^15 by a
+      // power of two: exact but for elements of less than 2^-32 of the row's
+      // largest, which are off by 2^-40 of it at most.
+      float q[NQ][8], top = 0.f;
+#pragma unroll
+      for (int v = 0; v < NQ; ++v) {
+        const uint32_t x[4] = {qv[v].x, qv[v].y, qv[v].z, qv[v].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 f = E::unpack(x[k]);
+          q[v][2 * k] = f.x;
+          q[v][2 * k + 1] = f.y;
+          top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+        }
+      }
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // Exponent field of top; none for zeros, and infinities stay themselves.
+      const int ex = static_cast<int>(__float_as_uint(top) >> 23);
+      const int up = ex == 0 || ex == 255 ? 0 : max(-100, min(100, 141 - ex));
+      const float by = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+#pragma unroll
+      for (int v = 0; v < NQ; ++v)
+        qv[v] = make_uint4(pack_f16(q[v][0] * by, q[v][1] * by), pack_f16(q[v][2] * by, q[v][3] * by),
+                           pack_f16(q[v][4] * by, q[v][5] * by), pack_f16(q[v][6] * by, q[v][7] * by));
+      qs *= __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      sl2[e] = a.scale_log2 * __shfl_sync(0xffffffffu, qs, (2 * c + e) * 4);
+  }
 
   int from = 0;                                        // slot of the slice in use
 #pragma unroll 1
@@ -176,8 +229,19 @@ window_decode_kernel(const __grid_constant__ WinDecodeArgs a) {
       for (int v = 0; v < NV; ++v) {
         const uint4 x0 = *reinterpret_cast<const uint4*>(slot + (2 * v) * 512);
         const uint4 x1 = *reinterpret_cast<const uint4*>(slot + (2 * v + 1) * 512);
-        E::mma(st, x0.x, x1.x, x0.y, x1.y, qv[v].x, qv[v].y);
-        E::mma(st, x0.z, x1.z, x0.w, x1.w, qv[v].z, qv[v].w);
+        if constexpr (FP8) {
+          const uint32_t w0[4] = {x0.x, x0.y, x0.z, x0.w}, w1[4] = {x1.x, x1.y, x1.z, x1.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint4& q = qv[2 * v + (k >> 1)];
+            P::mma(st, e4m3x2_to_f16x2(w0[k]), e4m3x2_to_f16x2(w1[k]),
+                   e4m3x2_to_f16x2(w0[k] >> 16), e4m3x2_to_f16x2(w1[k] >> 16),
+                   (k & 1) ? q.z : q.x, (k & 1) ? q.w : q.y);
+          }
+        } else {
+          P::mma(st, x0.x, x1.x, x0.y, x1.y, qv[v].x, qv[v].y);
+          P::mma(st, x0.z, x1.z, x0.w, x1.w, qv[v].z, qv[v].w);
+        }
       }
     }
     if (++from == C::SLOTS) from = 0;
@@ -186,7 +250,7 @@ window_decode_kernel(const __grid_constant__ WinDecodeArgs a) {
     // ------------------------------------------------------------- softmax
     float x[4];                                        // (key g, rows) (key g + 8, rows)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = st[e] * a.scale_log2;
+    for (int e = 0; e < 4; ++e) x[e] = st[e] * sl2[e & 1];
     const bool whole = key0 + 15 <= past &&
                        (key0 > past + q_len - 1 - a.window || key0 + 15 < first);
     if (!whole) {
@@ -220,17 +284,29 @@ window_decode_kernel(const __grid_constant__ WinDecodeArgs a) {
       p[e] = fast_exp2(x[e] - (m[e & 1] == -INFINITY ? 0.f : m[e & 1]));
     l[0] += p[0] + p[2];
     l[1] += p[1] + p[3];
-    const uint32_t pb0 = movmatrix_trans(E::pack(p[0], p[1]));
-    const uint32_t pb1 = movmatrix_trans(E::pack(p[2], p[3]));
+    const uint32_t pb0 = movmatrix_trans(P::pack(p[0], p[1]));
+    const uint32_t pb1 = movmatrix_trans(P::pack(p[2], p[3]));
     // ------------------------------------------------------------- O^T += V^T P^T
     cp_async_wait<C::SLOTS - 1>();
     __syncwarp();
     const uint32_t vrow = ring_at + from * C::TILE + vr * C::ROW;
 #pragma unroll
-    for (int t = 0; t < D / 16; ++t) {
-      uint32_t r0, r1, r2, r3;
-      ldsm_x4_t(vrow + (((2 * t + vx) ^ (vr & 7)) << 4), r0, r1, r2, r3);
-      E::mma(acc[t], r0, r1, r2, r3, pb0, pb1);
+    for (int t = 0; t < C::ROW / 32; ++t) {
+      uint32_t r[4];
+      ldsm_x4_t(vrow + (((2 * t + vx) ^ (vr & 7)) << 4), r[0], r[1], r[2], r[3]);
+      if constexpr (FP8) {
+        // A lane holds bytes (keys 2c, 2c + 1) x (dims 2g, 2g + 1) of a piece:
+        // even dims become rows 0-7 of the MMA, odd ones rows 8-15.
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t lo8 = r[2 * k], hi8 = r[2 * k + 1];
+          P::mma(acc[2 * t + k], e4m3x2_to_f16x2(prmt(lo8, 0, 0x4420)),
+                 e4m3x2_to_f16x2(prmt(lo8, 0, 0x4431)), e4m3x2_to_f16x2(prmt(hi8, 0, 0x4420)),
+                 e4m3x2_to_f16x2(prmt(hi8, 0, 0x4431)), pb0, pb1);
+        }
+      } else {
+        P::mma(acc[t], r[0], r[1], r[2], r[3], pb0, pb1);
+      }
     }
     if (++from == C::SLOTS) from = 0;
     __syncwarp();
@@ -253,20 +329,22 @@ window_decode_kernel(const __grid_constant__ WinDecodeArgs a) {
     }
 #pragma unroll
     for (int t = 0; t < D / 16; ++t) {
-      mine[(2 * c + e) * C::PITCH + 16 * t + g] = acc[t][e];
-      mine[(2 * c + e) * C::PITCH + 16 * t + 8 + g] = acc[t][2 + e];
+      const int d = 16 * t + (FP8 ? 2 * g : g);
+      mine[(2 * c + e) * C::PITCH + d] = acc[t][e];
+      mine[(2 * c + e) * C::PITCH + d + (FP8 ? 1 : 8)] = acc[t][2 + e];
     }
   }
   __syncthreads();
 
   // Four dims of a row, finished: the sink joins, the sum divides.
+  const float vs = FP8 ? __ldg(a.v_scale + hk) : 1.f;
   auto finish = [&](int row, int d, float M, float L, float4 o) {
     const int i = row / a.G, head = hk * a.G + row - i * a.G;
     if (a.sinks) {
       const float f = add_sink(M, L, __ldg(a.sinks + head) * kLog2e);
       o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
     }
-    const float inv = L == 0.f ? 0.f : 1.f / L;
+    const float inv = L == 0.f ? 0.f : vs / L;
     *reinterpret_cast<uint2*>(a.out + (static_cast<int64_t>(q0 + i) * a.H + head) * D + d) =
         make_uint2(E::pack(o.x * inv, o.y * inv), E::pack(o.z * inv, o.w * inv));
     if (d == 0 && a.lse)
@@ -326,11 +404,11 @@ window_decode_kernel(const __grid_constant__ WinDecodeArgs a) {
   cluster_wait();
 }
 
-template <int D, bool F16>
+template <int D, bool F16, bool FP8>
 static cudaError_t launch_window_decode_d(const WinDecodeArgs& a, unsigned grid, cudaStream_t st) {
-  using C = WdCfg<D>;
+  using C = WdCfg<D, FP8>;
   static std::atomic<bool> configured[kMaxDevices];
-  cudaError_t e = opt_in_smem(window_decode_kernel<D, F16>, C::SMEM_BYTES, configured);
+  cudaError_t e = opt_in_smem(window_decode_kernel<D, F16, FP8>, C::SMEM_BYTES, configured);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
@@ -343,23 +421,34 @@ static cudaError_t launch_window_decode_d(const WinDecodeArgs& a, unsigned grid,
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = a.parts > 1 ? 1 : 0;
-  e = cudaLaunchKernelEx(&cfg, window_decode_kernel<D, F16>, a);
+  e = cudaLaunchKernelEx(&cfg, window_decode_kernel<D, F16, FP8>, a);
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
 cudaError_t launch_window_decode(WinDecodeArgs a, int num_seqs, int slices, int D, bool f16,
                                  cudaStream_t st, int sms) {
   const long long units = static_cast<long long>(num_seqs) * a.H_kv;
+  // Blocks per (sequence, KV head): what the page ids of a warp's lanes ask
+  // for, and then two waves of one block per SM as long as a warp keeps two
+  // slices. 16 sequences of 8 KV heads, window 1024: 15.0 us with 4 parts, 16.3
+  // with 2, 19.8 with 8; 32 sequences 29.8, 27.9 (one) and 32.6; one sequence
+  // 8.0 with 8 parts.
   int parts = 1;
   while (parts < kWinMaxParts && (slices > parts * kWinPartSlices ||
                                   (units * parts < 2LL * sms && slices > 2 * kWdWarps * parts)))
     parts *= 2;
   a.parts = parts;
   const unsigned grid = static_cast<unsigned>(units * parts);
-  if (D == 128) return f16 ? launch_window_decode_d<128, true>(a, grid, st)
-                           : launch_window_decode_d<128, false>(a, grid, st);
-  return f16 ? launch_window_decode_d<64, true>(a, grid, st)
-             : launch_window_decode_d<64, false>(a, grid, st);
+  if (a.k_scale) return f16 ? launch_window_decode_d<128, true, true>(a, grid, st)
+                            : launch_window_decode_d<128, false, true>(a, grid, st);
+  if (f16) {
+    if (D == 256) return launch_window_decode_d<256, true, false>(a, grid, st);
+    if (D == 128) return launch_window_decode_d<128, true, false>(a, grid, st);
+    return launch_window_decode_d<64, true, false>(a, grid, st);
+  }
+  if (D == 256) return launch_window_decode_d<256, false, false>(a, grid, st);
+  if (D == 128) return launch_window_decode_d<128, false, false>(a, grid, st);
+  return launch_window_decode_d<64, false, false>(a, grid, st);
 }
 
 }  // namespace pa

@@ -306,6 +306,8 @@ DECODE = [
     ([8, 3, 5], [8, 500, 77], 4, 4, 128, 48, 31, 17, torch.float16),   # q rows of one head
     ([1] * 100, [700 + i for i in range(100)], 16, 8, 128, 16, 640, 4, torch.bfloat16),
     ([2] * 90, [600] * 90, 12, 4, 64, 16, 300, 300, torch.bfloat16),   # G 3: 6 rows
+    ([1, 1], [3500, 40], 8, 1, 256, 16, 2000, 9, torch.bfloat16),
+    ([2] * 30, [300 + 7 * i for i in range(30)], 4, 2, 256, 32, 150, 20, torch.float16),
 ]
 
 
@@ -328,6 +330,35 @@ def test_window_decode(ql, kv, H, hk, D, bs, window, first, dtype):
         again = pa.window_fwd(wl.q.to(DEV), hk_.to(DEV), hv_.to(DEV), *dev(wl)[:2], hbt.to(DEV),
                               *tail, sinks=skd, dev_status=status)
         assert torch.equal(again[0], got[0]) and torch.equal(again[1], got[1])
+    assert int(status) == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("ql,kv,H,hk,bs,window,first", [
+    ([1], [5000], 8, 1, 16, 4000, 7),
+    ([1] * 60, [400 + 11 * i for i in range(60)], 16, 8, 16, 500, 4),
+    ([2, 1, 0, 2], [2, 33, 50, 900], 8, 2, 48, 65, 40),
+])
+def test_window_decode_fp8(ql, kv, H, hk, bs, window, first, dtype):
+    """e4m3 pools: keys and values are exact in the MMA's types and a query
+    keeps its bits, so the tolerance is the 2-byte pools' one."""
+    wl = W._build("decode", 8, H, hk, 128, bs, ql, kv, torch.Generator().manual_seed(6),
+                  dtype=dtype)
+    ks, vs = torch.linspace(0.01, 0.03, hk), torch.linspace(0.02, 0.04, hk)
+    codes = [(c.float() / s[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn)
+             for c, s in zip(oracle_pools(wl), (ks, vs))]
+    kd, vd = (c.double() * s.double()[:, None] for c, s in zip(codes, (ks, vs)))
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    tail = (wl.max_seqlen_q, max(wl.max_seqlen_k, window + 1), wl.softmax_scale, window, first)
+    kw = dict(k_scale=ks.to(DEV), v_scale=vs.to(DEV), dev_status=status)
+    raw = [c.view(torch.uint8) for c in codes]
+    got = pa.window_fwd(wl.q.to(DEV), *(c.to(DEV) for c in raw), *dev(wl), *tail, **kw)
+    check(got, define(wl, kd, vd, window, first))
+    nan = hide(wl, *(c.float() for c in codes), window, first)
+    raw = [c.to(torch.float8_e4m3fn).view(torch.uint8) for c in nan[:2]]   # NaN bytes
+    again = pa.window_fwd(wl.q.to(DEV), *(c.to(DEV) for c in raw), *dev(wl)[:2], nan[2].to(DEV),
+                          *tail, **kw)
+    assert torch.equal(again[0], got[0]) and torch.equal(again[1], got[1])
     assert int(status) == 0
 
 
