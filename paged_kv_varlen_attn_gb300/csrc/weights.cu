@@ -68,6 +68,12 @@ weights_kernel(const __grid_constant__ WeightArgs a, int tiles) {
   constexpr int NQ = D / 32;                    // 16-byte pieces of a query row per lane
   constexpr int NV = C::ROW / 64;               // of a key row
   static_assert(kSlices <= 32 && kSlices % C::SLOTS == 0, "a lane holds a slice's page id");
+  // Beside the tensor-core kernel (see launch_weights_d) one more block, which
+  // has no keys, holds this grid's end back until that kernel's.
+  if (blockIdx.x == gridDim.x - 1) {
+    pdl_wait();
+    return;
+  }
   extern __shared__ __align__(16) uint8_t ring_raw[];
   // KV head fastest: a page's heads are read at about the same time (13% on
   // the decode batch over all of one head's blocks before the next head's).
@@ -301,6 +307,7 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   WtBars* bars = reinterpret_cast<WtBars*>(smem + C::OFF_BAR);
+  pdl_trigger();   // the other kernel may start: it takes the other sequences
   // Part fastest, then KV head, sequence, keys: under a causal mask the first
   // keys are seen by the most queries, so blocks start longest first.
   const int unit = blockIdx.x / parts;
@@ -632,6 +639,7 @@ template <int D, bool F16, bool FP8>
 static cudaError_t launch_weights_d(const CUtensorMap& tmQ, const WeightArgs& a, int num_seqs,
                                     int keys, cudaStream_t st) {
   const int tiles = keys > 0 ? (keys + kWeightKeys - 1) / kWeightKeys : 1;
+  bool tc = false;   // the tensor-core kernel was launched
   if (a.tc_min_rows < 0x7fffffff) {
     using C = WtCfg<D>;
     static std::atomic<bool> configured_tc[kMaxDevices];
@@ -662,14 +670,28 @@ static cudaError_t launch_weights_d(const CUtensorMap& tmQ, const WeightArgs& a,
       if (e != cudaSuccess) return e;
       e = cudaGetLastError();
       if (e != cudaSuccess) return e;
+      tc = true;
     }
   }
   using W = WwCfg<D, FP8>;
   static std::atomic<bool> configured[kMaxDevices];
   cudaError_t e = opt_in_smem(weights_kernel<D, F16, FP8>, W::SMEM_BYTES, configured);
   if (e != cudaSuccess) return e;
-  weights_kernel<D, F16, FP8><<<static_cast<unsigned>(num_seqs) * tiles * a.H_kv,
-                                kWeightWarps * 32, W::SMEM_BYTES, st>>>(a, tiles);
+  // Behind the tensor-core kernel as its programmatic dependent: the two add
+  // to different sequences' keys, so the blocks of one fill in beside the
+  // other's, or find nothing to do while it runs.
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(num_seqs) * tiles * a.H_kv + 1u);
+  cfg.blockDim = dim3(kWeightWarps * 32);
+  cfg.dynamicSmemBytes = W::SMEM_BYTES;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = tc ? 1 : 0;
+  e = cudaLaunchKernelEx(&cfg, weights_kernel<D, F16, FP8>, a, tiles);
+  if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
 
