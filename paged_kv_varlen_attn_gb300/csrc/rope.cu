@@ -243,17 +243,19 @@ rope_and_cache_kernel(const __grid_constant__ RopeArgs a) {
       unpack8<F16>(px, g);
       float r = 1.f;
       if (NORM && wt) {
-        float ss = 0.f;
+        float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) ss = fmaf(f[k], f[k], ss);
+        for (int k = 0; k < 8; k += 2) ffma2(s0, s1, f[k], f[k + 1], f[k], f[k + 1], s0, s1);
+        float ss = s0 + s1;
 #pragma unroll
         for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
         r = rsqrtf(ss * (1.f / D) + a.eps);
       }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        f[k] = fmaf(g[k], cb[k], f[k] * ca[k]);
-        if (NORM) f[k] *= r;
+      for (int k = 0; k < 8; k += 2) {
+        fmul2(f[k], f[k + 1], f[k], f[k + 1], ca[k], ca[k + 1]);
+        ffma2(f[k], f[k + 1], g[k], g[k + 1], cb[k], cb[k + 1], f[k], f[k + 1]);
+        if (NORM) fmul2(f[k], f[k + 1], f[k], f[k + 1], r, r);
       }
     }
     if (!live) continue;
