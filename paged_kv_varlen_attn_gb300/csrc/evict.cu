@@ -26,9 +26,7 @@ namespace pa {
 // owns a contiguous run of candidates, counts its kept ones by ballots, and
 // one scan over the warps gives its first output position.
 // ---------------------------------------------------------------------------
-constexpr int kSelUnroll = 4;            // weights on their way per thread
-constexpr int kRadixBits = 11;
-constexpr int kRadixBins = 1 << kRadixBits;
+constexpr int kSelUnroll = 4;            // groups of four weights on their way per thread
 
 // Logical page of key j (a shift for the usual page sizes).
 __device__ __forceinline__ int page_of(const EvictArgs& a, int j) {
@@ -41,11 +39,12 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return (b >> 31) ? ~b : b | 0x80000000u;
 }
 
-template <int kSelThreads>
-__global__ void __launch_bounds__(kSelThreads)
+template <int kSelThreads, int kRadixBits>
+__global__ void __launch_bounds__(kSelThreads, 1)
 evict_select_kernel(const __grid_constant__ EvictArgs a, int staged_max) {
-  constexpr int kSelWarps = kSelThreads / 32;
-  extern __shared__ uint32_t staged[];   // [staged_max]
+  constexpr int kSelWarps = kSelThreads / 32, kRadixBins = 1 << kRadixBits;
+  static_assert(kRadixBins % kSelThreads == 0, "whole bins per thread");
+  extern __shared__ __align__(16) uint32_t staged[];   // [staged_max]
   __shared__ int hist[kRadixBins];
   __shared__ int warp_sum[kSelWarps][2];
   __shared__ int found[3];               // digit of this pass, candidates above it, in it
@@ -80,26 +79,48 @@ evict_select_kernel(const __grid_constant__ EvictArgs a, int staged_max) {
     }
     return weight_key(__ldg(a.weights + page * a.weights_stride + h * a.bs + (j - lp * a.bs)));
   };
-  const bool in_smem = n <= staged_max;
+  // The keys are read in groups of four (rows of one page, 16 bytes), from the
+  // group that holds the first candidate on.
+  const int off = a.first & 3, groups = (off + n + 3) >> 2;
+  const bool in_smem = 4 * groups <= staged_max;
   for (int i = tid; i < kRadixBins; i += kSelThreads) hist[i] = 0;
   __syncthreads();
-  for (int i0 = tid; i0 < n; i0 += kSelThreads * kSelUnroll) {
-    uint32_t k[kSelUnroll];
+  for (int g0 = tid; g0 < groups; g0 += kSelThreads * kSelUnroll) {
+    int page[kSelUnroll], row[kSelUnroll];
 #pragma unroll
     for (int u = 0; u < kSelUnroll; ++u) {
-      const int i = i0 + u * kSelThreads;
-      k[u] = i < n ? load_key(i) : 0u;
+      const int j = a.first - off + 4 * (g0 + u * kSelThreads);
+      const int lp = page_of(a, j);
+      row[u] = j - lp * a.bs;
+      page[u] = g0 + u * kSelThreads < groups ? __ldg(bt + lp) : 0;
+    }
+    uint4 k[kSelUnroll];
+#pragma unroll
+    for (int u = 0; u < kSelUnroll; ++u) {
+      k[u] = make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u);   // -inf
+      if (g0 + u * kSelThreads >= groups) continue;
+      if (page[u] < 0 || page[u] >= a.num_blocks)
+        bad |= PA_DEV_BAD_PAGE;
+      else
+        k[u] = __ldg(reinterpret_cast<const uint4*>(a.weights + page[u] * a.weights_stride +
+                                                    h * a.bs + row[u]));
     }
 #pragma unroll
     for (int u = 0; u < kSelUnroll; ++u) {
-      const int i = i0 + u * kSelThreads;
-      if (i >= n) break;
-      if (in_smem) staged[i] = k[u];
-      atomicAdd(&hist[k[u] >> (32 - kRadixBits)], 1);
+      const int gi = g0 + u * kSelThreads;
+      if (gi >= groups) break;
+      uint32_t x[4] = {k[u].x, k[u].y, k[u].z, k[u].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[e] = weight_key(__uint_as_float(x[e]));
+        const int i = 4 * gi + e - off;
+        if (i >= 0 && i < n) atomicAdd(&hist[x[e] >> (32 - kRadixBits)], 1);
+      }
+      if (in_smem) reinterpret_cast<uint4*>(staged)[gi] = make_uint4(x[0], x[1], x[2], x[3]);
     }
   }
   __syncthreads();
-  auto key_of = [&](int i) -> uint32_t { return in_smem ? staged[i] : load_key(i); };
+  auto key_of = [&](int i) -> uint32_t { return in_smem ? staged[off + i] : load_key(i); };
 
   // Radix selection of the need-th largest key (none for need = 0).
   uint32_t prefix = 0, matched = 0;   // the digits found so far, and their bits
@@ -341,7 +362,7 @@ static cudaError_t launch_move(const EvictArgs& a, int num_seqs, cudaStream_t st
 // keys (192 KB, one block per SM).
 constexpr int kStageCap = 48 * 1024;
 
-template <int THREADS>
+template <int THREADS, int BITS>
 static cudaError_t launch_select(const EvictArgs& a, int num_seqs, int bound, cudaStream_t st) {
   // A per-device function attribute: set on the first launch on each device
   // (before any stream capture), not again.
@@ -351,13 +372,13 @@ static cudaError_t launch_select(const EvictArgs& a, int num_seqs, int bound, cu
   if (e != cudaSuccess) return e;
   const bool known = dev >= 0 && dev < kMaxDevices;
   if (!known || !configured[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(evict_select_kernel<THREADS>,
+    e = cudaFuncSetAttribute(evict_select_kernel<THREADS, BITS>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, kStageCap * 4);
     if (e != cudaSuccess) return e;
     if (known) configured[dev].store(true, std::memory_order_release);
   }
-  const int staged = bound < kStageCap ? bound : kStageCap;
-  evict_select_kernel<THREADS><<<dim3(num_seqs, a.H_kv), THREADS, static_cast<size_t>(staged) * 4,
+  const int staged = bound < kStageCap ? (bound + 3) & ~3 : kStageCap;
+  evict_select_kernel<THREADS, BITS><<<dim3(num_seqs, a.H_kv), THREADS, static_cast<size_t>(staged) * 4,
                                  st>>>(a, staged);
   return cudaGetLastError();
 }
@@ -365,16 +386,20 @@ static cudaError_t launch_select(const EvictArgs& a, int num_seqs, int bound, cu
 cudaError_t launch_evict(const EvictArgs& a, int num_seqs, cudaStream_t st) {
   if (num_seqs == 0) return cudaSuccess;
   const int bound = a.max_k < a.kv_len_cap ? a.max_k : a.kv_len_cap;
-  // Long sequences: twice the threads walk the candidates.
-  cudaError_t e = bound > kLongKeys ? launch_select<1024>(a, num_seqs, bound, st)
-                                    : launch_select<512>(a, num_seqs, bound, st);
+  // Short sequences: many small blocks, digits of as many bins as threads, so
+  // that a pass costs little beside the candidates (512 threads and 11 bits:
+  // 66.1 us instead of 64.5 in all for 512 pairs to 1024 keys). Long ones: all
+  // threads of a block walk the candidates (512: 30.7 us instead of 27.6 for 32
+  // pairs from 14,000 keys to 2048; 10 and 12 bits 30.0 and 28.2).
+  cudaError_t e = bound > kLongKeys ? launch_select<1024, 11>(a, num_seqs, bound, st)
+                                    : launch_select<256, 8>(a, num_seqs, bound, st);
   if (e != cudaSuccess) return e;
   // Rows of one head move in order, chunk by chunk: where there are few
   // (sequence, head) pairs, narrower slices make longer chunks and more blocks.
-  // 64-byte slices against 32: 512 pairs to 1024 keys 69 us against 77, 32
-  // pairs to 2048 keys 43 against 38. (Launched as a programmatic dependent of
-  // the selection the move was no faster: 73 and 35 against 69 and 32 us in
-  // all.)
+  // 64-byte slices against 32 (with an earlier selection): 512 pairs to 1024
+  // keys 69 us against 77, 32 pairs to 2048 keys 43 against 38. (Launched as a
+  // programmatic dependent of the selection the move was no faster: 73 and 35
+  // against 69 and 32 us in all.)
   return static_cast<long long>(num_seqs) * a.H_kv >= kWidePairs
              ? launch_move<4>(a, num_seqs, st)
              : launch_move<2>(a, num_seqs, st);
