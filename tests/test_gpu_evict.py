@@ -344,3 +344,18 @@ def test_prompt_evict_decode():
             ref_o = torch.softmax(x, 0) @ vals
             assert abs(l1[h, s].item() - ref_l.item()) <= 2e-2   # q, k may round apart by a step
             assert (o1[s, h].cpu().double() - ref_o).abs().max().item() <= 2e-2
+
+
+@pytest.mark.parametrize("kv,bound,first", [(60000, 60000, 5), (5000, 700, 6), (5000, 4999, 3)])
+def test_evict_candidates_past_shared_memory(kv, bound, first):
+    """More candidates than the selection keeps in shared memory (48k, or what
+    the stated bound asks for, which is reported): the same result."""
+    kb, vb, w, bt, lens = pools(13, [kv], 1, 64, 64, 2)
+    rk, rv, rw, kept, rlens = ref.evict(kb, vb, w, lens, bt, 333, first, 2)
+    dk, dv, dw = typed(kb, 2).to(DEV), typed(vb, 2).to(DEV), w.to(DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    got, glens = pa.evict(dk, dv, dw, lens.to(DEV), bt.to(DEV), bound, 333, first, 2,
+                          dev_status=status)
+    assert int(status) == (pa.PA_DEV_BAD_SEQLEN if kv > bound else 0)
+    assert torch.equal(got.cpu(), kept) and torch.equal(glens.cpu(), rlens)
+    assert torch.equal(dk.cpu().view(torch.uint8), rk) and torch.equal(dw.cpu(), rw)
