@@ -623,7 +623,7 @@ def window_fwd(q, key_cache, value_cache, cu_seqlens_q, seqused_k, block_table, 
     if (k_scale is None) != (v_scale is None):
         raise ValueError("k_scale and v_scale go together")
     if out is None:
-        out = q.new_empty((T, H, D))
+        out = torch.empty_like(q) if q.is_contiguous() else q.new_empty((T, H, D))
     elif out.shape != (T, H, D) or not out.is_contiguous():
         raise ValueError("out must be a contiguous [total_q, num_heads, head_size] tensor")
     if lse is None:
@@ -728,7 +728,7 @@ def rope_and_cache(q, key, value, positions, cos_sin, key_cache, value_cache, sl
     _f32_vector(q_norm, d, "q_norm")
     _f32_vector(k_norm, d, "k_norm")
     if out is None:
-        out = q.new_empty((T, H, d))
+        out = torch.empty_like(q) if q.is_contiguous() else q.new_empty((T, H, d))
     elif out.shape != q.shape:
         raise ValueError("out must have the shape of q")
     if k_scale is None and v_scale is None:
@@ -815,11 +815,11 @@ def evict(key_cache, value_cache, weights, seqused_k, block_table, max_seqlen_k,
     row = _seq_table(seqused_k, block_table, S)
     device = key_cache.device
     if kept is None:
-        kept = torch.empty((S, hk, max(int(budget), 0)), dtype=torch.int32, device=device)
+        kept = seqused_k.new_empty((S, hk, max(int(budget), 0)))
     elif kept.dtype != torch.int32 or kept.shape != (S, hk, budget) or not kept.is_contiguous():
         raise ValueError("kept must be a contiguous int32 [num_seqs, num_kv_heads, budget] tensor")
     if new_lens is None:
-        new_lens = torch.empty(S, dtype=torch.int32, device=device)
+        new_lens = torch.empty_like(seqused_k)
     elif new_lens.dtype != torch.int32 or new_lens.shape != (S,) or not new_lens.is_contiguous():
         raise ValueError("new_lens must be a contiguous int32 tensor of one value per sequence")
     _call(lib.pa_evict, "pa_evict", device,
