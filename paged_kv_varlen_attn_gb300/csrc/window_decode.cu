@@ -35,9 +35,9 @@ namespace pa {
 // window 1024 (276 MB, 6.0 TB/s), where the planned split kernel takes 73.5,
 // and 169 us at window 4096 (6.35 TB/s; 203). e4m3 pools 36.7 us (54.0), by
 // the conversions of K and V; head size 256 (16/8 heads) 89 us (149). Three
-// slots per warp: two gave 43.5 us where four sequences' worth of warps read
-// window 16000 instead of 36.7, four leave three blocks on an SM (57.6 us
-// against 51.7 on the 64 sequences, uncached).
+// slots per warp: with two, two sequences at window 16000 take 43.5 us instead
+// of 36.7; with four, three blocks fit an SM (64 sequences in pages that are
+// not cached 57.6 us instead of 51.7).
 // ---------------------------------------------------------------------------
 constexpr int kWdWarps = 4;
 

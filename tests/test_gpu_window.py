@@ -300,6 +300,8 @@ DECODE = [
     ([1], [5000], 8, 1, 128, 16, 4000, 7, torch.bfloat16),          # few sequences: several blocks
     ([1, 1], [17000, 900], 2, 1, 128, 16, 16000, 40, torch.float16),
     ([1], [16700], 1, 1, 64, 64, 16400, 0, torch.bfloat16),         # a window past the kernel's
+    ([1], [12500], 2, 1, 128, 16, 12000, 40, torch.float16),        # nearly the longest run of a
+    ([1] * 20, [16100 + i for i in range(20)], 1, 1, 64, 32, 16000, 200, torch.bfloat16),   # warp
     ([1] * 40, [1 + 23 * i for i in range(40)], 8, 8, 64, 32, 200, 33, torch.bfloat16),
     ([2, 0, 1, 2, 2], [2, 40, 300, 301, 2], 8, 2, 128, 16, 100, 5, torch.bfloat16),
     ([1, 1, 1], [1, 16, 17], 8, 1, 64, 16, 16, 0, torch.float16),   # one key, a slice, one more
@@ -336,6 +338,7 @@ def test_window_decode(ql, kv, H, hk, D, bs, window, first, dtype):
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("ql,kv,H,hk,bs,window,first", [
     ([1], [5000], 8, 1, 16, 4000, 7),
+    ([1], [12900], 2, 1, 16, 11000, 9),
     ([1] * 60, [400 + 11 * i for i in range(60)], 16, 8, 16, 500, 4),
     ([2, 1, 0, 2], [2, 33, 50, 900], 8, 2, 48, 65, 40),
 ])
@@ -360,6 +363,17 @@ def test_window_decode_fp8(ql, kv, H, hk, bs, window, first, dtype):
                           *tail, **kw)
     assert torch.equal(again[0], got[0]) and torch.equal(again[1], got[1])
     assert int(status) == 0
+
+
+def test_window_decode_fp8_planned():
+    """A window past the unplanned kernel's, over e4m3 pools (bf16 queries are
+    exact there too)."""
+    wl = W._build("decode", 8, 8, 1, 128, 16, [1], [13000], torch.Generator().manual_seed(6))
+    codes = [(c.float() / 0.02).clamp(-448, 448).to(torch.float8_e4m3fn) for c in oracle_pools(wl)]
+    kd, vd = (c.double() * torch.tensor([0.02]).double() for c in codes)
+    got = pa.window_fwd(wl.q.to(DEV), *(c.view(torch.uint8).to(DEV) for c in codes), *dev(wl), 1,
+                        13000, wl.softmax_scale, 12800, 4, k_scale=0.02, v_scale=0.02)
+    check(got, define(wl, kd, vd, 12800, 4))
 
 
 @pytest.mark.parametrize("sink", [False, True])
