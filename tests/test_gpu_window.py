@@ -424,3 +424,44 @@ def test_window_decode_bad_metadata():
     want = define(wl, kc, vc, 250, 3)[0]
     assert (out[0].cpu().double() - want[0]).abs().max() < 0.05
     assert (out[1:] == 7.0).all()
+
+
+def test_window_decode_captured_scaled_and_on_two_streams():
+    """A decode step in a graph, replayed on other lengths, and on two streams
+    at once; softmax scales of zero and below."""
+    wl = W._build("decode", 11, 16, 4, 128, 16, [1] * 12, [90 + 60 * i for i in range(12)],
+                  torch.Generator().manual_seed(2))
+    kc, vc = (t.to(DEV) for t in oracle_pools(wl))
+    cu, lens, bt = dev(wl)
+    q = wl.q.to(DEV)
+    tail = (wl.max_seqlen_q, wl.max_seqlen_k, wl.softmax_scale, 300, 4)
+    for scale in (0.0, -0.1):
+        check(pa.window_fwd(q, kc, vc, cu, lens, bt, 1, wl.max_seqlen_k, scale, 300, 4),
+              define(wl, kc.cpu(), vc.cpu(), 300, 4, scale=scale))
+    want = pa.window_fwd(q, kc, vc, cu, lens, bt, *tail)
+    ws = pa.alloc_workspace(pa.varlen_fwd_workspace_size(12, 12, 1, wl.max_seqlen_k, 16, 4, 128, 16,
+                                                         pa._sm_count(DEV)), DEV)
+    out, lse = torch.empty_like(want[0]), torch.empty_like(want[1])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        pa.window_fwd(q, kc, vc, cu, lens, bt, *tail, out=out, lse=lse, workspace=ws)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    short = torch.clamp(lens - 77, min=0)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for _ in range(3):
+        for st, n in zip(streams, (lens, short)):
+            with torch.cuda.stream(st):
+                got.append(pa.window_fwd(q, kc, vc, cu, n, bt, *tail))
+    torch.cuda.synchronize()
+    lens.copy_(short)
+    graph.replay()
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        for x, y in zip(g, (out, lse) if i % 2 else want):
+            assert torch.equal(x, y)
