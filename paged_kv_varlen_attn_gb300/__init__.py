@@ -215,17 +215,30 @@ def _one_device(first, *rest):
             raise ValueError("all tensors must be on one GPU (no CPU fallback)")
 
 
+def _pools(key_cache, value_cache):
+    """(shape, page stride) of a pair of pools laid out alike."""
+    shape, st = key_cache.shape, key_cache.stride()
+    if st != value_cache.stride() or shape != value_cache.shape:
+        raise ValueError("key and value caches must have the same shape and page stride")
+    if len(st) == 4:
+        _, _, heads, dim = shape
+        if st[3] == 1 and st[2] == dim and st[1] == heads * dim:
+            return shape, st[0]
+    raise ValueError("cache must be [num_blocks, block_size, num_kv_heads, head_size] with "
+                     "contiguous pages")
+
+
 def _seq_table(seqused_k, block_table, num_seqs):
     """Row stride of a block table [num_seqs, columns], which stands for its
     columns: a row may be read up to it."""
-    if seqused_k.dtype != torch.int32 or seqused_k.shape != (num_seqs,) or \
+    if seqused_k.dtype is not torch.int32 or seqused_k.shape != (num_seqs,) or \
             not seqused_k.is_contiguous():
         raise ValueError("seqused_k must be a contiguous int32 tensor of one value per sequence")
-    if block_table.dtype != torch.int32 or block_table.dim() != 2 or \
-            block_table.shape[0] != num_seqs:
+    shape = block_table.shape
+    if block_table.dtype is not torch.int32 or len(shape) != 2 or shape[0] != num_seqs:
         raise ValueError("block_table must be int32 [num_seqs, max_blocks]")
+    width = shape[1]
     row, unit = block_table.stride()
-    width = block_table.shape[1]
     if width > 1 and unit != 1:
         raise ValueError("block_table must have unit column stride")
     if row != width and num_seqs > 1:
@@ -239,10 +252,11 @@ def _seq_table(seqused_k, block_table, num_seqs):
 
 def _dtype_code(*ts):
     """PA_BF16 or PA_F16 for tensors that must all share one 2-byte float type."""
-    dts = {t.dtype for t in ts if t is not None}
-    if len(dts) != 1:
-        raise ValueError(f"tensors must share one element type, got {sorted(map(str, dts))}")
-    dt, = dts
+    dt = ts[0].dtype
+    for t in ts:
+        if t is not None and t.dtype is not dt:
+            names = sorted({str(t.dtype) for t in ts if t is not None})
+            raise ValueError(f"tensors must share one element type, got {names}")
     if dt == torch.bfloat16:
         return PA_BF16
     if dt == torch.float16:
@@ -595,9 +609,10 @@ def cascade_fwd_fp8kv(q, key_cache, value_cache, cu_seqlens_q, seqused_k, block_
 # Sliding window with first tokens
 def _cu_seqlens(cu):
     """Number of sequences of cu_seqlens_q."""
-    if cu.dtype != torch.int32 or cu.dim() != 1 or cu.shape[0] < 1 or not cu.is_contiguous():
+    shape = cu.shape
+    if cu.dtype is not torch.int32 or len(shape) != 1 or shape[0] < 1 or not cu.is_contiguous():
         raise ValueError("cu_seqlens_q must be a contiguous int32 tensor of num_seqs + 1 values")
-    return cu.shape[0] - 1
+    return shape[0] - 1
 
 
 def window_fwd(q, key_cache, value_cache, cu_seqlens_q, seqused_k, block_table, max_seqlen_q,
@@ -612,10 +627,8 @@ def window_fwd(q, key_cache, value_cache, cu_seqlens_q, seqused_k, block_table, 
     lib = load_library()
     _one_device(q, key_cache, value_cache, cu_seqlens_q, seqused_k, block_table, sinks, key, value,
                 slot_mapping, out, lse, workspace, dev_status)
-    if key_cache.stride() != value_cache.stride() or key_cache.shape != value_cache.shape:
-        raise ValueError("key and value caches must have the same shape and page stride")
+    (nb, bs, hk, d), page = _pools(key_cache, value_cache)
     T, H, D = q.shape
-    nb, bs, hk, d = key_cache.shape
     S = _cu_seqlens(cu_seqlens_q)
     bt_row = _seq_table(seqused_k, block_table, S)
     if d != D:
@@ -655,14 +668,15 @@ def window_fwd(q, key_cache, value_cache, cu_seqlens_q, seqused_k, block_table, 
         size = varlen_fwd_workspace_size if desc is None else varlen_fwd_fp8kv_workspace_size
         workspace = alloc_workspace(size(S, T, max_seqlen_q, max_seqlen_k, H, hk, D, bs,
                                          _sm_count(q.device)), q.device)
-    opts = AttnOpts(None if sinks is None else sinks.data_ptr(),
-                    None if desc is None else ctypes.pointer(desc))
+    opts = None
+    if sinks is not None or desc is not None:
+        opts = ctypes.byref(AttnOpts(_ptr(sinks), None if desc is None else ctypes.pointer(desc)))
     _call(lib.pa_window_fwd, "pa_window_fwd", q.device,
-          None if update is None else ctypes.byref(update), _ptr(q), _row_stride(q),
-          _ptr(key_cache), _ptr(value_cache), _cache_stride(key_cache), _ptr(cu_seqlens_q),
-          _ptr(seqused_k), _ptr(block_table), bt_row, S, T, int(max_seqlen_q),
+          None if update is None else ctypes.byref(update), q.data_ptr(), _row_stride(q),
+          key_cache.data_ptr(), value_cache.data_ptr(), page, cu_seqlens_q.data_ptr(),
+          seqused_k.data_ptr(), block_table.data_ptr(), bt_row, S, T, int(max_seqlen_q),
           int(max_seqlen_k), H, hk, D, bs, nb, float(softmax_scale), min(int(window), _INT_MAX),
-          min(int(num_first), _INT_MAX), ctypes.byref(opts), _ptr(out), _ptr(lse), _ptr(workspace),
+          min(int(num_first), _INT_MAX), opts, out.data_ptr(), _ptr(lse), workspace.data_ptr(),
           workspace.numel(), dtype, _ptr(dev_status))
     del keep
     return out, lse
@@ -707,18 +721,14 @@ def rope_and_cache(q, key, value, positions, cos_sin, key_cache, value_cache, sl
     lib = load_library()
     _one_device(q, key, value, positions, cos_sin, key_cache, value_cache, slot_mapping, q_norm,
                 k_norm, out, dev_status)
-    shape = key_cache.shape
-    if key_cache.stride() != value_cache.stride() or shape != value_cache.shape:
-        raise ValueError("key and value caches must have the same shape and page stride")
-    page = _cache_stride(key_cache)
-    nb, bs, hk, d = shape
+    (nb, bs, hk, d), page = _pools(key_cache, value_cache)
     T, H, dq = q.shape
     row = (T, hk, d)
     if dq != d or key.shape != row or value.shape != row:
         raise ValueError("q, key and value must be [tokens, heads, head_size] of the caches' "
                          "heads and head size")
-    if positions.dtype != torch.int64 or positions.shape != (T,) or \
-            not positions.is_contiguous() or slot_mapping.dtype != torch.int64 or \
+    if positions.dtype is not torch.int64 or positions.shape != (T,) or \
+            not positions.is_contiguous() or slot_mapping.dtype is not torch.int64 or \
             slot_mapping.shape != (T,) or not slot_mapping.is_contiguous():
         raise ValueError("positions and slot_mapping must be contiguous int64 tensors of one "
                          "value per token")
@@ -729,8 +739,11 @@ def rope_and_cache(q, key, value, positions, cos_sin, key_cache, value_cache, sl
     _f32_vector(k_norm, d, "k_norm")
     if out is None:
         out = torch.empty_like(q) if q.is_contiguous() else q.new_empty((T, H, d))
+        out_row = H * d
     elif out.shape != q.shape:
         raise ValueError("out must have the shape of q")
+    else:
+        out_row = _row_stride(out)
     if k_scale is None and v_scale is None:
         dtype, fp8, keep = _dtype_code(q, key, value, out, key_cache, value_cache), None, None
     elif k_scale is None or v_scale is None:
@@ -746,7 +759,7 @@ def rope_and_cache(q, key, value, positions, cos_sin, key_cache, value_cache, sl
                       slot_mapping.data_ptr(), T)
     _call(lib.pa_rope_and_cache, "pa_rope_and_cache", q.device,
           ctypes.byref(rope), positions.data_ptr(), q.data_ptr(), _row_stride(q), out.data_ptr(),
-          _row_stride(out), ctypes.byref(update), key_cache.data_ptr(), value_cache.data_ptr(),
+          out_row, ctypes.byref(update), key_cache.data_ptr(), value_cache.data_ptr(),
           page, H, hk, d, bs, nb, fp8, dtype, _ptr(dev_status))
     del keep
     return out
@@ -756,11 +769,12 @@ def rope_and_cache(q, key, value, positions, cos_sin, key_cache, value_cache, sl
 # Accumulated attention weight of the cached keys, and eviction by it
 def _weights_stride(weights, nb, bs, hk):
     """Page stride of a weights tensor [num_blocks, num_kv_heads, block_size]."""
-    if weights.dtype != torch.float32 or weights.shape != (nb, hk, bs) or \
-            weights.stride(2) != 1 or weights.stride(1) != bs:
+    st = weights.stride()
+    if weights.dtype is not torch.float32 or weights.shape != (nb, hk, bs) or st[2] != 1 or \
+            st[1] != bs:
         raise ValueError("weights must be float32 [num_blocks, num_kv_heads, block_size] with "
                          "contiguous pages")
-    return weights.stride(0)
+    return st[0]
 
 
 def attn_weights(q, key_cache, lse, weights, cu_seqlens_q, seqused_k, block_table, max_seqlen_q,
@@ -807,10 +821,9 @@ def evict(key_cache, value_cache, weights, seqused_k, block_table, max_seqlen_k,
     lib = load_library()
     _one_device(key_cache, value_cache, weights, seqused_k, block_table, kept, new_lens,
                 dev_status)
-    if key_cache.stride() != value_cache.stride() or key_cache.shape != value_cache.shape or \
-            key_cache.dtype != value_cache.dtype:
-        raise ValueError("key and value caches must have the same shape, type and page stride")
-    nb, bs, hk, d = key_cache.shape
+    (nb, bs, hk, d), page = _pools(key_cache, value_cache)
+    if key_cache.dtype is not value_cache.dtype:
+        raise ValueError("key and value caches must have the same type")
     S = seqused_k.numel()
     row = _seq_table(seqused_k, block_table, S)
     device = key_cache.device
@@ -823,9 +836,9 @@ def evict(key_cache, value_cache, weights, seqused_k, block_table, max_seqlen_k,
     elif new_lens.dtype != torch.int32 or new_lens.shape != (S,) or not new_lens.is_contiguous():
         raise ValueError("new_lens must be a contiguous int32 tensor of one value per sequence")
     _call(lib.pa_evict, "pa_evict", device,
-          _ptr(key_cache), _ptr(value_cache), _cache_stride(key_cache), _ptr(weights),
-          _weights_stride(weights, nb, bs, hk), _ptr(seqused_k), _ptr(block_table),
+          key_cache.data_ptr(), value_cache.data_ptr(), page, weights.data_ptr(),
+          _weights_stride(weights, nb, bs, hk), seqused_k.data_ptr(), block_table.data_ptr(),
           row, S, int(max_seqlen_k), hk, d, bs, nb,
-          key_cache.element_size(), int(budget), int(num_first), int(num_recent), _ptr(kept),
-          _ptr(new_lens), _ptr(dev_status))
+          key_cache.element_size(), int(budget), int(num_first), int(num_recent), kept.data_ptr(),
+          new_lens.data_ptr(), _ptr(dev_status))
     return kept, new_lens
