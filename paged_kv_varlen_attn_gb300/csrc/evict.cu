@@ -7,14 +7,14 @@
 // out. Neither waits for another block.
 #include <cuda_runtime.h>
 
-#include <atomic>
-
 #include "device_common.cuh"
 
 namespace pa {
 
 // ---------------------------------------------------------------------------
-// Selection. One block per (KV head, sequence). The weights of the candidate
+// Selection. One block per (KV head, sequence), or a cluster whose blocks share
+// its candidates, add up each other's histograms and write one after another's
+// kept indices (all read from the others' shared memory). The weights of the candidate
 // keys [first, kv - recent) become 32-bit keys whose unsigned order is the
 // weights' order (NaN as -inf, -0 as +0) and stay in shared memory if they
 // fit (else every pass reads them again). A radix selection from the top
@@ -22,10 +22,11 @@ namespace pa {
 // read) finds the smallest key prefix whose candidates are kept, and how many
 // of the candidates with that prefix: it stops at the digit where that is all
 // of them, or after the last digit, where they are equal and the ones of
-// lowest index are kept. A last pass writes the kept indices in ascending order: each warp
-// owns a contiguous run of candidates, counts its kept ones by ballots, and
-// one scan over the warps gives its first output position.
+// lowest index are kept. A last pass writes the kept indices in ascending
+// order: each warp owns a contiguous run of candidates, counts its kept ones
+// by ballots, and one scan over the warps gives its first output position.
 // ---------------------------------------------------------------------------
+constexpr int kSelParts = 4;             // blocks of a cluster at most
 constexpr int kSelUnroll = 4;            // groups of four weights on their way per thread
 
 // Logical page of key j (a shift for the usual page sizes).
@@ -39,16 +40,32 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return (b >> 31) ? ~b : b | 0x80000000u;
 }
 
-template <int kSelThreads, int kRadixBits>
+template <int kSelThreads, int kRadixBits, bool CLUSTER>
 __global__ void __launch_bounds__(kSelThreads, 1)
-evict_select_kernel(const __grid_constant__ EvictArgs a, int staged_max) {
+evict_select_kernel(const __grid_constant__ EvictArgs a, int staged_max, int parts) {
   constexpr int kSelWarps = kSelThreads / 32, kRadixBins = 1 << kRadixBits;
   static_assert(kRadixBins % kSelThreads == 0, "whole bins per thread");
   extern __shared__ __align__(16) uint32_t staged[];   // [staged_max]
-  __shared__ int hist[kRadixBins];
-  __shared__ int warp_sum[kSelWarps][2];
+  // One histogram, or one per pass where other blocks read them.
+  constexpr int kHists = CLUSTER ? (32 + kRadixBits - 1) / kRadixBits : 1;
+  __shared__ int hist[kHists][kRadixBins];
+  __shared__ int warp_sum[kSelWarps][2], block_sum[2];
   __shared__ int found[3];               // digit of this pass, candidates above it, in it
-  const int s = blockIdx.x, h = blockIdx.y;
+  const int part = CLUSTER ? static_cast<int>(cluster_rank()) : 0;
+  const int s = CLUSTER ? blockIdx.x / parts : blockIdx.x, h = blockIdx.y;
+  // What this block has written to its shared memory is seen by its threads,
+  // and by the cluster's.
+  auto sync = [&]() {
+    if constexpr (CLUSTER) {
+      cluster_arrive();
+      cluster_wait();
+    } else {
+      __syncthreads();
+    }
+  };
+  auto remote = [&](const int* at, int rank) {
+    return __float_as_int(load_remote(reinterpret_cast<const float*>(at), rank));
+  };
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int kv = __ldg(a.seqused_k + s);
   int bad = 0;
@@ -60,6 +77,7 @@ evict_select_kernel(const __grid_constant__ EvictArgs a, int staged_max) {
   }
   int32_t* kept = a.kept + (static_cast<int64_t>(s) * a.H_kv + h) * a.budget;
   if (kv <= a.budget) {   // nothing to evict
+    if (part > 0) return;
     if (bad && h == 0 && tid == 0) flag_status(a.status, bad);
     for (int d = tid; d < a.budget; d += kSelThreads) kept[d] = d < kv ? d : -1;
     return;
@@ -81,11 +99,14 @@ evict_select_kernel(const __grid_constant__ EvictArgs a, int staged_max) {
   };
   // The keys are read in groups of four (rows of one page, 16 bytes), from the
   // group that holds the first candidate on.
-  const int off = a.first & 3, groups = (off + n + 3) >> 2;
-  const bool in_smem = 4 * groups <= staged_max;
-  for (int i = tid; i < kRadixBins; i += kSelThreads) hist[i] = 0;
+  const int off = a.first & 3, all = (off + n + 3) >> 2;
+  const int base = static_cast<int>(static_cast<long long>(all) * part / parts);
+  const int groups = static_cast<int>(static_cast<long long>(all) * (part + 1) / parts);
+  const int i_lo = max(0, 4 * base - off), i_hi = min(n, 4 * groups - off);   // this block's
+  const bool in_smem = 4 * (groups - base) <= staged_max;
+  for (int i = tid; i < kHists * kRadixBins; i += kSelThreads) hist[0][i] = 0;
   __syncthreads();
-  for (int g0 = tid; g0 < groups; g0 += kSelThreads * kSelUnroll) {
+  for (int g0 = base + tid; g0 < groups; g0 += kSelThreads * kSelUnroll) {
     int page[kSelUnroll], row[kSelUnroll];
 #pragma unroll
     for (int u = 0; u < kSelUnroll; ++u) {
@@ -114,27 +135,41 @@ evict_select_kernel(const __grid_constant__ EvictArgs a, int staged_max) {
       for (int e = 0; e < 4; ++e) {
         x[e] = weight_key(__uint_as_float(x[e]));
         const int i = 4 * gi + e - off;
-        if (i >= 0 && i < n) atomicAdd(&hist[x[e] >> (32 - kRadixBits)], 1);
+        if (i >= 0 && i < n) atomicAdd(&hist[0][x[e] >> (32 - kRadixBits)], 1);
       }
-      if (in_smem) reinterpret_cast<uint4*>(staged)[gi] = make_uint4(x[0], x[1], x[2], x[3]);
+      if (in_smem) reinterpret_cast<uint4*>(staged)[gi - base] = make_uint4(x[0], x[1], x[2], x[3]);
     }
   }
-  __syncthreads();
-  auto key_of = [&](int i) -> uint32_t { return in_smem ? staged[off + i] : load_key(i); };
+  sync();
+  auto key_of = [&](int i) -> uint32_t {
+    return in_smem ? staged[off + i - 4 * base] : load_key(i);
+  };
 
   // Radix selection of the need-th largest key (none for need = 0).
   uint32_t prefix = 0, matched = 0;   // the digits found so far, and their bits
   int left = need;                    // kept candidates that match the prefix
   if (need > 0) {
-    int shift = 32 - kRadixBits, bins = kRadixBins;
+    int shift = 32 - kRadixBits, bins = kRadixBins, pass = 0;
     while (true) {
       // Bins from the top: thread t takes the bins of ranks [t*per, t*per+per).
       constexpr int per = kRadixBins / kSelThreads;
-      int sum = 0;
+      int count[per], sum = 0;
 #pragma unroll
       for (int k = 0; k < per; ++k) {
         const int b = bins - 1 - (tid * per + k);
-        sum += b >= 0 ? hist[b] : 0;
+        count[k] = 0;
+        if (b >= 0) {
+          if constexpr (CLUSTER) {
+            int c[kSelParts];                              // all on their way at once
+#pragma unroll
+            for (int r = 0; r < kSelParts; ++r) c[r] = r < parts ? remote(&hist[pass][b], r) : 0;
+#pragma unroll
+            for (int r = 0; r < kSelParts; ++r) count[k] += c[r];
+          } else {
+            count[k] = hist[0][b];
+          }
+        }
+        sum += count[k];
       }
       int incl = sum;
 #pragma unroll
@@ -150,14 +185,12 @@ evict_select_kernel(const __grid_constant__ EvictArgs a, int staged_max) {
       if (above < left && left <= above + sum) {   // exactly one thread
 #pragma unroll
         for (int k = 0; k < per; ++k) {
-          const int b = bins - 1 - (tid * per + k);
-          const int c = b >= 0 ? hist[b] : 0;
-          if (above < left && left <= above + c) {
-            found[0] = b;
+          if (above < left && left <= above + count[k]) {
+            found[0] = bins - 1 - (tid * per + k);
             found[1] = above;
-            found[2] = c;
+            found[2] = count[k];
           }
-          above += c;
+          above += count[k];
         }
       }
       __syncthreads();
@@ -168,18 +201,22 @@ evict_select_kernel(const __grid_constant__ EvictArgs a, int staged_max) {
       const int bits = min(kRadixBits, shift);
       shift -= bits;
       bins = 1 << bits;
-      for (int i = tid; i < bins; i += kSelThreads) hist[i] = 0;
-      __syncthreads();
-      for (int i = tid; i < n; i += kSelThreads) {
-        const uint32_t k = key_of(i);
-        if ((k & matched) == prefix) atomicAdd(&hist[(k >> shift) & (bins - 1)], 1);
+      if constexpr (CLUSTER) {
+        ++pass;
+      } else {
+        for (int i = tid; i < bins; i += kSelThreads) hist[0][i] = 0;
+        __syncthreads();
       }
-      __syncthreads();
+      for (int i = i_lo + tid; i < i_hi; i += kSelThreads) {
+        const uint32_t k = key_of(i);
+        if ((k & matched) == prefix) atomicAdd(&hist[pass][(k >> shift) & (bins - 1)], 1);
+      }
+      sync();
     }
   }
   // Kept: the candidates above the prefix, and the first `left` that match it.
-  const int run = (n + kSelThreads - 1) / kSelThreads * 32;   // candidates per warp
-  const int r0 = min(n, warp * run), r1 = min(n, r0 + run);
+  const int run = (i_hi - i_lo + kSelThreads - 1) / kSelThreads * 32;   // candidates per warp
+  const int r0 = min(i_hi, i_lo + warp * run), r1 = min(i_hi, r0 + run);
   int gt = 0, eq = 0;
   if (need > 0) {
     for (int i = r0 + lane; i < r1; i += 32) {
@@ -204,6 +241,19 @@ evict_select_kernel(const __grid_constant__ EvictArgs a, int staged_max) {
     gt0 += warp_sum[w][0];
     eq0 += warp_sum[w][1];
   }
+  if constexpr (CLUSTER) {
+    // The blocks before this one come first.
+    if (tid == kSelThreads - 1) {
+      block_sum[0] = gt0 + warp_sum[warp][0];
+      block_sum[1] = eq0 + warp_sum[warp][1];
+    }
+    sync();
+#pragma unroll
+    for (int r = 0; r < kSelParts - 1; ++r) {
+      gt0 += r < part ? remote(&block_sum[0], r) : 0;
+      eq0 += r < part ? remote(&block_sum[1], r) : 0;
+    }
+  }
   if (need > 0) {
     const uint32_t below = (1u << lane) - 1u;
     for (int i0 = r0; i0 < r1; i0 += 32) {
@@ -218,9 +268,13 @@ evict_select_kernel(const __grid_constant__ EvictArgs a, int staged_max) {
       eq0 += __popc(me);
     }
   }
-  for (int d = tid; d < a.first; d += kSelThreads) kept[d] = d;
-  for (int d = tid; d < a.recent; d += kSelThreads) kept[a.budget - a.recent + d] = kv - a.recent + d;
+  if (part == 0) {
+    for (int d = tid; d < a.first; d += kSelThreads) kept[d] = d;
+    for (int d = tid; d < a.recent; d += kSelThreads)
+      kept[a.budget - a.recent + d] = kv - a.recent + d;
+  }
   if (bad) flag_status(a.status, bad);
+  if constexpr (CLUSTER) sync();   // nobody leaves while its sums are read
 }
 
 // ---------------------------------------------------------------------------
@@ -237,9 +291,9 @@ evict_select_kernel(const __grid_constant__ EvictArgs a, int staged_max) {
 // stay where they are (kept[d] = d, a prefix) are skipped.
 // Bound by HBM where many sequences are cut (selection and move 64.5 us for 64
 // sequences of 900-1400 keys and 8 heads of 128 to 1024: 380 MB, 87% of the
-// measured copy rate), by the chain of dependent chunks and the one block per
-// (sequence, KV head) of the selection where few are (4 sequences of 14,000
-// keys to 2048: 27.3 us, 37%).
+// measured copy rate), by the passes of the selection and the chain of
+// dependent chunks where few are (4 sequences of 14,000 keys to 2048: 25.4 us,
+// 40%).
 // ---------------------------------------------------------------------------
 constexpr int kMoveThreads = 256;
 constexpr int kMoveUnroll = 4;
@@ -367,25 +421,29 @@ static cudaError_t launch_move(const EvictArgs& a, int num_seqs, cudaStream_t st
 // keys (192 KB, one block per SM).
 constexpr int kStageCap = 48 * 1024;
 
-template <int THREADS, int BITS>
-static cudaError_t launch_select(const EvictArgs& a, int num_seqs, int bound, cudaStream_t st) {
-  // A per-device function attribute: set on the first launch on each device
-  // (before any stream capture), not again.
+template <int THREADS, int BITS, bool CLUSTER>
+static cudaError_t launch_select(const EvictArgs& a, int num_seqs, int bound, int parts,
+                                 cudaStream_t st) {
+  auto kernel = evict_select_kernel<THREADS, BITS, CLUSTER>;
   static std::atomic<bool> configured[kMaxDevices];
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  cudaError_t e = opt_in_smem(kernel, kStageCap * 4, configured);
   if (e != cudaSuccess) return e;
-  const bool known = dev >= 0 && dev < kMaxDevices;
-  if (!known || !configured[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(evict_select_kernel<THREADS, BITS>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, kStageCap * 4);
-    if (e != cudaSuccess) return e;
-    if (known) configured[dev].store(true, std::memory_order_release);
-  }
-  const int staged = bound < kStageCap ? (bound + 3) & ~3 : kStageCap;
-  evict_select_kernel<THREADS, BITS><<<dim3(num_seqs, a.H_kv), THREADS, static_cast<size_t>(staged) * 4,
-                                 st>>>(a, staged);
-  return cudaGetLastError();
+  // A block's share of the groups of four, one more at either end.
+  const int share = (bound / parts + 11) & ~3;
+  const int staged = share < kStageCap ? share : kStageCap;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(num_seqs * parts, a.H_kv);
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = static_cast<size_t>(staged) * 4;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = parts;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = CLUSTER ? 1 : 0;
+  e = cudaLaunchKernelEx(&cfg, kernel, a, staged, parts);
+  return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
 cudaError_t launch_evict(const EvictArgs& a, int num_seqs, cudaStream_t st) {
@@ -393,11 +451,18 @@ cudaError_t launch_evict(const EvictArgs& a, int num_seqs, cudaStream_t st) {
   const int bound = a.max_k < a.kv_len_cap ? a.max_k : a.kv_len_cap;
   // Short sequences: many small blocks, digits of as many bins as threads, so
   // that a pass costs little beside the candidates (512 threads and 11 bits:
-  // 66.1 us instead of 64.5 in all for 512 pairs to 1024 keys). Long ones: all
-  // threads of a block walk the candidates (512: 30.7 us instead of 27.6 for 32
-  // pairs from 14,000 keys to 2048; 10 and 12 bits 30.0 and 28.2).
-  cudaError_t e = bound > kLongKeys ? launch_select<1024, 11>(a, num_seqs, bound, st)
-                                    : launch_select<256, 8>(a, num_seqs, bound, st);
+  // 66.1 us instead of 64.5 in all for 512 pairs to 1024 keys). Long ones:
+  // clusters of such blocks while there are fewer blocks than SMs (32 pairs
+  // from 14,000 keys to 2048: 25.4 us, 24.9 with 8 blocks, whose first, uncached
+  // call is slower; 27.9 with one block of 1024 threads and 11 bits; 28 with 9
+  // bits, 94 with 11, by the remote reads), one large block each from there on
+  // (half the threads: 30.7).
+  const long long units = static_cast<long long>(num_seqs) * a.H_kv;
+  int parts = 1;
+  while (parts < kSelParts && units * parts < kWidePairs && bound > kLongKeys) parts *= 2;
+  cudaError_t e = bound <= kLongKeys ? launch_select<256, 8, false>(a, num_seqs, bound, 1, st)
+                  : parts == 1       ? launch_select<1024, 11, false>(a, num_seqs, bound, 1, st)
+                                     : launch_select<256, 8, true>(a, num_seqs, bound, parts, st);
   if (e != cudaSuccess) return e;
   // Rows of one head move in order, chunk by chunk: where there are few
   // (sequence, head) pairs, narrower slices make longer chunks and more blocks.
@@ -405,7 +470,7 @@ cudaError_t launch_evict(const EvictArgs& a, int num_seqs, cudaStream_t st) {
   // keys 69 us against 77, 32 pairs to 2048 keys 43 against 38. (Launched as a
   // programmatic dependent of the selection the move was no faster: 73 and 35
   // against 69 and 32 us in all.)
-  return static_cast<long long>(num_seqs) * a.H_kv >= kWidePairs
+  return units >= kWidePairs
              ? launch_move<4>(a, num_seqs, st)
              : launch_move<2>(a, num_seqs, st);
 }

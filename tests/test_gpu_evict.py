@@ -359,3 +359,39 @@ def test_evict_candidates_past_shared_memory(kv, bound, first):
     assert int(status) == (pa.PA_DEV_BAD_SEQLEN if kv > bound else 0)
     assert torch.equal(got.cpu(), kept) and torch.equal(glens.cpu(), rlens)
     assert torch.equal(dk.cpu().view(torch.uint8), rk) and torch.equal(dw.cpu(), rw)
+
+
+@pytest.mark.parametrize("budget,first,recent", [(1500, 5, 7), (12, 5, 7), (8999, 1, 0), (1, 0, 0)])
+@pytest.mark.parametrize("seqs", [1, 9, 40])
+def test_evict_long_sequences_with_ties(seqs, budget, first, recent):
+    """Few distinct weights (kept ties spread over the blocks that share a
+    sequence), no candidate kept, all but one, sequences on both sides of the
+    budget; with few and many (sequence, head) pairs."""
+    kv = [9000, 4800, 6001, 700, 5, 0, 8191, 5003, 9000][:seqs]
+    kv += [5000 + 3 * i for i in range(seqs - len(kv))]
+    if seqs == 40:
+        kv[10:] = [50] * 30
+    kb, vb, w, bt, lens = pools(21, kv, 4, 64, 16, 2)
+    w = (w * 5).floor()
+    rk, rv, rw, kept, rlens = ref.evict(kb, vb, w, lens, bt, budget, first, recent)
+    dk, dv, dw = typed(kb, 2).to(DEV), typed(vb, 2).to(DEV), w.to(DEV)
+    got, glens = pa.evict(dk, dv, dw, lens.to(DEV), bt.to(DEV), max(kv), budget, first, recent)
+    assert torch.equal(got.cpu(), kept) and torch.equal(glens.cpu(), rlens)
+    assert torch.equal(dk.cpu().view(torch.uint8), rk)
+    assert torch.equal(dv.cpu().view(torch.uint8), rv) and torch.equal(dw.cpu(), rw)
+
+
+def test_evict_long_bad_page():
+    """A page outside the pool in a sequence whose candidates several blocks
+    share: reported, and the selection is the one with its keys at -inf."""
+    kb, vb, w, bt, lens = pools(22, [6000], 2, 64, 16, 2)
+    bad = int(bt[0, 200])
+    wi = w.clone()
+    wi[bad] = float("-inf")
+    kept = ref.evict(kb, vb, wi, lens, bt, 1000, 3, 9)[3]
+    bt[0, 200] = -5
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    got, _ = pa.evict(typed(kb, 2).to(DEV), typed(vb, 2).to(DEV), w.to(DEV), lens.to(DEV),
+                      bt.to(DEV), 6000, 1000, 3, 9, dev_status=status)
+    assert int(status) == pa.PA_DEV_BAD_PAGE
+    assert torch.equal(got.cpu(), kept)
