@@ -87,15 +87,14 @@ cudaError_t launch_rope_table(float* table, RopeTableArgs& a, cudaStream_t st, i
 // partner is in the same register (interleaved pairs: swapped halves) or rot /
 // 16 lanes away (half layout: one shuffle per pair of elements). Everything
 // between the load and the store is float32; the store is the only rounding.
-// Bound by HBM: 16,384 tokens of 32/8 heads of 128 without norms (405 MB) take
-// 70.6 us, 84% of the measured copy rate; 4,109 tokens of 64/8 heads with norms
-// into e4m3 pools (162 MB) 42.2 us, 57%, with 56% of the issue slots used --
-// the norm's shuffles and the quantization run while a warp has no load in
-// flight, and 80 registers leave 24 warps per SM to fill the gap (4 items per
-// warp and more warps: 44.6 us). A decode step's 64 tokens take 3.0 us.
+// A block is one warp: its place on the SM is taken by the next one as soon as
+// it is done, so loads are always on their way. Bound by HBM: 16,384 tokens of
+// 32/8 heads of 128 without norms (405 MB) take 62.2 us, 96% of the measured
+// copy rate (blocks of two warps 67.5, of four 70.8; 28 blocks per SM 66.6);
+// 4,109 tokens of 64/8 heads with norms into e4m3 pools (162 MB) 33.2 us, 72%,
+// beside the norm's shuffles and the quantization (two warps 41, four 42.2; 24
+// blocks per SM 33.8). A decode step's 64 tokens take 3.0 us.
 // ---------------------------------------------------------------------------
-constexpr int kRopeThreads = 128;
-constexpr int kRopeWarps = kRopeThreads / 32;
 constexpr int kRopeItems = 8;
 
 template <bool F16>
@@ -124,16 +123,14 @@ __device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
 
 // INTER: interleaved pairs. NORM: q or k (or both) are normed.
 template <int D, bool F16, bool FP8, bool INTER, bool NORM>
-__global__ void __launch_bounds__(kRopeThreads, 6)
+__global__ void __launch_bounds__(32, NORM ? 28 : 32)
 rope_and_cache_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int LPH = D / 8;        // lanes per head
   constexpr int HPI = 32 / LPH;     // heads per item
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x;
   const int l = lane % LPH;
-  const unsigned w = blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
-  const int t = static_cast<int>(w / static_cast<unsigned>(a.chunks));
-  const int part = static_cast<int>(w - static_cast<unsigned>(t) * a.chunks);
-  if (t >= a.num_tokens) return;
+  const int t = static_cast<int>(blockIdx.x / static_cast<unsigned>(a.chunks));
+  const int part = static_cast<int>(blockIdx.x - static_cast<unsigned>(t) * a.chunks);
   const int64_t pos = __ldg(a.positions + t), slot = __ldg(a.slots + t);
   // This warp's items: q items, or the k items followed by the v items.
   const bool is_q = part < a.q_chunks;
@@ -282,7 +279,7 @@ rope_and_cache_kernel(const __grid_constant__ RopeArgs a) {
 template <int D, bool F16, bool FP8>
 static cudaError_t launch_rope_d(const RopeArgs& a, unsigned grid, cudaStream_t st) {
   auto run = [&](auto kernel) {
-    kernel<<<grid, kRopeThreads, 0, st>>>(a);
+    kernel<<<grid, 32, 0, st>>>(a);
     return cudaGetLastError();
   };
   const bool norm = a.q_norm || a.k_norm;
@@ -306,8 +303,8 @@ cudaError_t launch_rope_and_cache(RopeArgs a, int D, bool f16, bool fp8, cudaStr
   a.q_chunks = (q_items + per - 1) / per;
   a.chunks = a.q_chunks + (kv_items + per - 1) / per;
   const long long warps = static_cast<long long>(a.num_tokens) * a.chunks;
-  if (warps > 0xffffffffLL - kRopeWarps) return cudaErrorInvalidConfiguration;
-  const unsigned grid = static_cast<unsigned>((warps + kRopeWarps - 1) / kRopeWarps);
+  if (warps > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  const unsigned grid = static_cast<unsigned>(warps);
   if (fp8) return f16 ? launch_rope_d<128, true, true>(a, grid, st)
                       : launch_rope_d<128, false, true>(a, grid, st);
   if (f16) {
