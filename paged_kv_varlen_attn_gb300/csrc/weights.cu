@@ -23,14 +23,16 @@ namespace pa {
 // filled by asynchronous copies, where every lane reads back its own bytes
 // (the ring holds what registers could not: no barrier but the warp's own).
 // Decode is bound by the read of K; the ring keeps one to three slices of every
-// warp on their way. On the 64-sequence decode batch (483 MB): 78 us, 6.2 TB/s;
-// with K read straight into registers 92 us (two slices in flight, 16 warps per
-// SM) and 121 us (one slice per warp, the chain of dependent reads in front of
-// it exposed). Two slots of 256-byte rows a warp beat four, 78 against 81 us
-// (more warps per SM), and 8 slices per warp beat 4, 81 against 94.
+// warp on their way. A block is one warp, whose place the next one takes as soon
+// as it is done. On the 64-sequence decode batch (483 MB): 77.3 us, 6.2 TB/s, 92%
+// of the measured copy rate (blocks of four warps 77.9); with K read straight
+// into registers 92 us (two slices in flight, 16 warps per SM) and 121 us (one
+// slice per warp, the chain of dependent reads in front of it exposed). Two
+// slots of 256-byte rows a warp beat four by 1.4 us (more warps per SM), and 8
+// slices per warp beat 4 and 16 by 2.3.
 // 16 keys never cross a page (pages are multiples of 16 keys).
 // ---------------------------------------------------------------------------
-constexpr int kWeightWarps = 4;
+constexpr int kWeightWarps = 1;
 constexpr int kSlices = 8;
 constexpr int kWeightKeys = kWeightWarps * kSlices * 16;   // keys of a block
 
