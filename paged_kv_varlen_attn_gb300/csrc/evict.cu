@@ -289,13 +289,12 @@ evict_select_kernel(const __grid_constant__ EvictArgs a, int staged_max, int par
 // head; the weights are one more slice, of 4 bytes. While a chunk's rows are
 // on their way the next chunk's indices and pages are looked up. Rows that
 // stay where they are (kept[d] = d, a prefix) are skipped.
-// Bound by HBM where many sequences are cut (selection and move 64.5 us for 64
-// sequences of 900-1400 keys and 8 heads of 128 to 1024: 380 MB, 87% of the
+// Bound by HBM where many sequences are cut (selection and move 61.5 us for 64
+// sequences of 900-1400 keys and 8 heads of 128 to 1024: 380 MB, 91% of the
 // measured copy rate), by the passes of the selection and the chain of
-// dependent chunks where few are (4 sequences of 14,000 keys to 2048: 25.4 us,
+// dependent chunks where few are (4 sequences of 14,000 keys to 2048: 25.2 us,
 // 40%).
 // ---------------------------------------------------------------------------
-constexpr int kMoveThreads = 256;
 constexpr int kMoveUnroll = 4;
 
 // Page-relative place of key j: page id (or -1 for a page outside the pool)
@@ -352,7 +351,7 @@ __device__ __forceinline__ void move_rows(const EvictArgs& a, const int32_t* kep
   }
 }
 
-template <int LANES>
+template <int LANES, int kMoveThreads>
 __global__ void __launch_bounds__(kMoveThreads)
 evict_move_kernel(const __grid_constant__ EvictArgs a) {
   // The slices of a sequence's rows are neighbouring blocks, so that the
@@ -410,10 +409,11 @@ evict_move_kernel(const __grid_constant__ EvictArgs a) {
 constexpr int kWidePairs = 152;
 constexpr int kLongKeys = 4096;
 
-template <int LANES>
+template <int LANES, int THREADS>
 static cudaError_t launch_move(const EvictArgs& a, int num_seqs, cudaStream_t st) {
   const int slices = a.row_bytes / (16 * LANES);
-  evict_move_kernel<LANES><<<dim3(num_seqs * (slices + 1), a.H_kv), kMoveThreads, 0, st>>>(a);
+  evict_move_kernel<LANES, THREADS>
+      <<<dim3(num_seqs * (slices + 1), a.H_kv), THREADS, 0, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -465,14 +465,15 @@ cudaError_t launch_evict(const EvictArgs& a, int num_seqs, cudaStream_t st) {
                                      : launch_select<256, 8, true>(a, num_seqs, bound, parts, st);
   if (e != cudaSuccess) return e;
   // Rows of one head move in order, chunk by chunk: where there are few
-  // (sequence, head) pairs, narrower slices make longer chunks and more blocks.
-  // 64-byte slices against 32 (with an earlier selection): 512 pairs to 1024
-  // keys 69 us against 77, 32 pairs to 2048 keys 43 against 38. (Launched as a
-  // programmatic dependent of the selection the move was no faster: 73 and 35
-  // against 69 and 32 us in all.)
-  return units >= kWidePairs
-             ? launch_move<4>(a, num_seqs, st)
-             : launch_move<2>(a, num_seqs, st);
+  // (sequence, head) pairs, narrower slices and larger blocks make longer chunks
+  // and more blocks (32 pairs to 2048 keys: 25.2 us with 32-byte slices and 256
+  // threads, 28.2 with 128; 64-byte slices 32.6, 16-byte ones 41). Where there
+  // are many, smaller blocks leave less of an SM waiting at a chunk's end (512
+  // pairs to 1024 keys: 61.5 us with 64-byte slices and 128 threads, 64.4 with
+  // 256, 63.5 with 64; 32-byte slices 73). As a programmatic dependent of the
+  // selection the move was no faster.
+  return units >= kWidePairs ? launch_move<4, 128>(a, num_seqs, st)
+                             : launch_move<2, 256>(a, num_seqs, st);
 }
 
 }  // namespace pa
