@@ -557,7 +557,9 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       // Columns [c0, c1) of the tile see this key: queries from its own
       // position on, rows of the sequence.
       const int tok0 = first + t * step;
-      const int c0 = a.causal ? max(0, (key0 + x * 128 + tid - past - tok0) * G) : 0;
+      // (A key far in front of the queries: clamped in tokens, since keys x heads
+      // of the group may pass 32 bits. The other side is at most 255 tokens.)
+      const int c0 = a.causal ? max(0, key0 + x * 128 + tid - past - tok0) * G : 0;
       const int c1 = min(TR, (q_len - tok0) * G);
       const bool edge =
           tok0 + TPT > q_len || (a.causal && tok0 < key0 + x * 128 + 127 - past);
