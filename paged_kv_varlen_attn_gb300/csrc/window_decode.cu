@@ -199,9 +199,11 @@ window_decode_kernel(const __grid_constant__ WinDecodeArgs a) {
       }
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      // Exponent field of top; none for zeros, and infinities stay themselves.
+      // By the exponent field of top: a finite row goes down by 2^113 at most and
+      // up by 2^126 (so that 2^up and 2^-up are normal numbers; a smaller row's
+      // maximum then stays below 2^14, zeros stay zeros). Infinities, too.
       const int ex = static_cast<int>(__float_as_uint(top) >> 23);
-      const int up = ex == 0 || ex == 255 ? 0 : max(-100, min(100, 141 - ex));
+      const int up = ex == 255 ? 0 : min(126, 141 - ex);
       const float by = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
 #pragma unroll
       for (int v = 0; v < NQ; ++v)
