@@ -604,7 +604,9 @@ pa_status pa_rope_and_cache(const pa_rope* rope, const int64_t* positions, const
  * keys are left as they were. Sums are float32 in a fixed order: the same
  * call gives the same bits. A sequence's pages must be its own (a page shared
  * with another sequence of the call gets the sum of one of them).
- * max_seqlen_k and total_q * num_heads / num_kv_heads are at most 2^30.
+ * max_seqlen_k and total_q * num_heads / num_kv_heads are at most 2^30, and
+ * num_seqs * num_kv_heads * ceil(max_seqlen_k / 128) is at most 2^31 - 2
+ * (PA_ERR_INVALID_ARG).
  * A key in a page outside the pool sets PA_DEV_BAD_PAGE and is skipped; a
  * sequence whose lengths break the stated bounds sets PA_DEV_BAD_SEQLEN, and
  * with inconsistent cu_seqlens_q it is skipped.

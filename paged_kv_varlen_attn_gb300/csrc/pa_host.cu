@@ -1272,10 +1272,12 @@ pa_status pa_attn_weights(const void* q, int64_t q_token_stride, const void* key
   if (bt_stride < 0 || num_blocks < 0 || !std::isfinite(softmax_scale) ||
       (causal != 0 && causal != 1))
     return PA_ERR_INVALID_ARG;
-  // Blocks of one launch: 64 keys of a sequence (and 128 of one KV head) each.
+  // The larger of the two launches: a block per kWeightKeys keys of a sequence
+  // and KV head, and one more. (Divided, since the product may pass 64 bits.)
   if (max_seqlen_k > kMaxKeys ||
       static_cast<long long>(total_q) * (num_heads / num_kv_heads) > kMaxKeys ||
-      static_cast<long long>(num_seqs) * cdiv(max_seqlen_k, 64) * num_kv_heads > 0x7fffffffLL)
+      static_cast<long long>(num_seqs) * (max_seqlen_k > 0 ? cdiv(max_seqlen_k, kWeightKeys) : 1) >
+          0x7ffffffeLL / num_kv_heads)
     return PA_ERR_INVALID_ARG;
   if (num_seqs == 0 || total_q == 0) return PA_OK;
   WeightArgs a{};

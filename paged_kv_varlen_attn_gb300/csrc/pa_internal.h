@@ -290,6 +290,7 @@ cudaError_t launch_evict(const EvictArgs& a, int num_seqs, cudaStream_t st);
 
 // Accumulated attention weight of every cached key (weights.cu).
 constexpr int kWeightsTcMinRows = 64;
+constexpr int kWeightKeys = 128;   // of a sequence and KV head, per block of decode rows
 struct WeightArgs {
   const uint16_t* q;
   int64_t q_stride;

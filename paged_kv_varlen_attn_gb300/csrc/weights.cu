@@ -34,7 +34,7 @@ namespace pa {
 // ---------------------------------------------------------------------------
 constexpr int kWeightWarps = 1;
 constexpr int kSlices = 8;
-constexpr int kWeightKeys = kWeightWarps * kSlices * 16;   // keys of a block
+static_assert(kWeightWarps * kSlices * 16 == kWeightKeys, "the keys of a block");
 
 template <int D, bool FP8>
 struct WwCfg {
