@@ -215,6 +215,13 @@ def _one_device(first, *rest):
             raise ValueError("all tensors must be on one GPU (no CPU fallback)")
 
 
+def _fit32(*values):
+    """Integers for the C interface, whose low 32 bits ctypes would pass on."""
+    for v in values:
+        if v > _INT_MAX or v < -_INT_MAX:
+            raise ValueError(f"integer arguments must fit 32 bits, got {v}")
+
+
 def _pools(key_cache, value_cache):
     """(shape, page stride) of a pair of pools laid out alike."""
     shape, st = key_cache.shape, key_cache.stride()
@@ -625,6 +632,8 @@ def window_fwd(q, key_cache, value_cache, cu_seqlens_q, seqused_k, block_table, 
     slot_mapping). With k_scale and v_scale the caches hold e4m3 bytes.
     Returns (out, lse or None)."""
     lib = load_library()
+    window, num_first = min(int(window), _INT_MAX), min(int(num_first), _INT_MAX)
+    _fit32(max_seqlen_q, max_seqlen_k, window, num_first)
     _one_device(q, key_cache, value_cache, cu_seqlens_q, seqused_k, block_table, sinks, key, value,
                 slot_mapping, out, lse, workspace, dev_status)
     (nb, bs, hk, d), page = _pools(key_cache, value_cache)
@@ -675,9 +684,9 @@ def window_fwd(q, key_cache, value_cache, cu_seqlens_q, seqused_k, block_table, 
           None if update is None else ctypes.byref(update), q.data_ptr(), _row_stride(q),
           key_cache.data_ptr(), value_cache.data_ptr(), page, cu_seqlens_q.data_ptr(),
           seqused_k.data_ptr(), block_table.data_ptr(), bt_row, S, T, int(max_seqlen_q),
-          int(max_seqlen_k), H, hk, D, bs, nb, float(softmax_scale), min(int(window), _INT_MAX),
-          min(int(num_first), _INT_MAX), opts, out.data_ptr(), _ptr(lse), workspace.data_ptr(),
-          workspace.numel(), dtype, _ptr(dev_status))
+          int(max_seqlen_k), H, hk, D, bs, nb, float(softmax_scale), window, num_first, opts,
+          out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.numel(), dtype,
+          _ptr(dev_status))
     del keep
     return out, lse
 
@@ -692,6 +701,7 @@ def rope_table(table_len, rot_dim, base=10000.0, scaling="none", factor=1.0, ori
     mscale default 0.1 ln factor + 1 for factor > 1)."""
     if scaling not in ROPE_SCALINGS:
         raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}, got {scaling!r}")
+    _fit32(table_len, rot_dim)
     if out is None:
         out = torch.empty((table_len, rot_dim), dtype=torch.float32, device=device)
     _need_cuda(out)
@@ -719,6 +729,8 @@ def rope_and_cache(q, key, value, positions, cos_sin, key_cache, value_cache, sl
     their pages (in place on the caches; with k_scale and v_scale the caches
     hold e4m3 bytes). Returns the rotated queries; out may be q itself."""
     lib = load_library()
+    rows, rot = cos_sin.shape
+    _fit32(rows)
     _one_device(q, key, value, positions, cos_sin, key_cache, value_cache, slot_mapping, q_norm,
                 k_norm, out, dev_status)
     (nb, bs, hk, d), page = _pools(key_cache, value_cache)
@@ -732,7 +744,6 @@ def rope_and_cache(q, key, value, positions, cos_sin, key_cache, value_cache, sl
             slot_mapping.shape != (T,) or not slot_mapping.is_contiguous():
         raise ValueError("positions and slot_mapping must be contiguous int64 tensors of one "
                          "value per token")
-    rows, rot = cos_sin.shape
     if cos_sin.dtype != torch.float32 or not cos_sin.is_contiguous():
         raise ValueError("cos_sin must be a contiguous float32 [positions, rot_dim] tensor")
     _f32_vector(q_norm, d, "q_norm")
@@ -785,6 +796,7 @@ def attn_weights(q, key_cache, lse, weights, cu_seqlens_q, seqused_k, block_tabl
     own queries start from zero. With k_scale the key cache holds e4m3 bytes.
     Returns weights."""
     lib = load_library()
+    _fit32(max_seqlen_q, max_seqlen_k)
     _one_device(q, key_cache, lse, weights, cu_seqlens_q, seqused_k, block_table, dev_status)
     S = _cu_seqlens(cu_seqlens_q)
     bt_row = _seq_table(seqused_k, block_table, S)
@@ -819,6 +831,7 @@ def evict(key_cache, value_cache, weights, seqused_k, block_table, max_seqlen_k,
     [num_seqs, num_kv_heads, budget], new_lens int32 [num_seqs]); new_lens may
     be seqused_k itself."""
     lib = load_library()
+    _fit32(max_seqlen_k, budget, num_first, num_recent)
     _one_device(key_cache, value_cache, weights, seqused_k, block_table, kept, new_lens,
                 dev_status)
     (nb, bs, hk, d), page = _pools(key_cache, value_cache)

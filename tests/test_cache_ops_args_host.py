@@ -1,6 +1,7 @@
 """Argument checks of the operators around attention that need no GPU: the
 limits of a launch, integers past 32 bits, outputs beside their inputs."""
 import pytest
+import torch
 
 import paged_kv_varlen_attn_gb300 as pa
 from paged_kv_varlen_attn_gb300 import _build
@@ -27,3 +28,41 @@ def test_weights_largest_grid(lib, S, mk, hk, ok):
     got = call_weights(lib, S=S, mk=mk, H=hk, hk=hk, D=64, qs=hk * 64, cbs=16 * hk * 64,
                        ws=16 * hk, T=0, mq=0)
     assert got == (pa.PA_OK if ok else pa.PA_ERR_INVALID_ARG)
+
+
+BIG = [(1 << 32) + 5, -(1 << 32) + 5, 1 << 31, -(1 << 31) - 1]
+
+
+@pytest.mark.parametrize("v", BIG)
+def test_integers_past_32_bits_are_refused(lib, v):
+    """ctypes passes the low 32 bits of an integer; the binding refuses what
+    does not fit, before it looks at any tensor."""
+    c = torch.zeros(4, 16, 8, 128, dtype=torch.bfloat16)
+    q, w = torch.zeros(2, 8, 128, dtype=torch.bfloat16), torch.zeros(4, 8, 16)
+    n, bt = torch.zeros(2, dtype=torch.int32), torch.zeros((2, 4), dtype=torch.int32)
+    cu, lse = torch.zeros(3, dtype=torch.int32), torch.zeros(8, 2)
+    calls = [lambda: pa.evict(c, c, w, n, bt, v, 32),
+             lambda: pa.evict(c, c, w, n, bt, 64, v),
+             lambda: pa.evict(c, c, w, n, bt, 64, 32, v),
+             lambda: pa.evict(c, c, w, n, bt, 64, 32, 0, v),
+             lambda: pa.attn_weights(q, c, lse, w, cu, n, bt, v, 64, 0.1, True),
+             lambda: pa.attn_weights(q, c, lse, w, cu, n, bt, 1, v, 0.1, True),
+             lambda: pa.window_fwd(q, c, c, cu, n, bt, v, 64, 0.1, 16),
+             lambda: pa.window_fwd(q, c, c, cu, n, bt, 1, v, 0.1, 16),
+             lambda: pa.rope_table(v, 2, device="meta"),
+             lambda: pa.rope_table(2, v, device="meta")]
+    if v < 0:      # a window (first tokens) past the integers is all; below them, nothing
+        calls += [lambda: pa.window_fwd(q, c, c, cu, n, bt, 1, 64, 0.1, v),
+                  lambda: pa.window_fwd(q, c, c, cu, n, bt, 1, 64, 0.1, 16, v)]
+    for call in calls:
+        with pytest.raises(ValueError, match="32 bits"):
+            call()
+
+
+def test_rope_table_longer_than_32_bits_is_refused(lib):
+    q = torch.empty((1, 2, 128), dtype=torch.bfloat16, device="meta")
+    c = torch.empty((1, 16, 2, 128), dtype=torch.bfloat16, device="meta")
+    i = torch.empty(1, dtype=torch.int64, device="meta")
+    table = torch.empty(((1 << 32) + 8, 64), device="meta")
+    with pytest.raises(ValueError, match="32 bits"):
+        pa.rope_and_cache(q, q, q, i, table, c, c, i)
