@@ -552,8 +552,9 @@ pa_status pa_rope_table(float* cos_sin, int table_len, int rot_dim, double base,
  *               PA_DEV_BAD_POSITION and its token is skipped likewise.
  *   q         : [num_tokens, num_heads, head_size] in dtype, token t at
  *               q + t*q_token_stride; q_out likewise. q_out may be q (same
- *               pointer and stride); it must not overlap q otherwise
- *               (PA_ERR_INVALID_ARG), nor the update's keys and values.
+ *               pointer and stride), or its rows may lie between q's (same
+ *               stride); it must not overlap q otherwise (PA_ERR_INVALID_ARG),
+ *               nor the update's keys and values.
  *   update    : the new tokens' k and v, their slots and num_tokens, as in
  *               pa_varlen_fwd_with_update. slot < 0: the token's k and v are
  *               not written (its q is).

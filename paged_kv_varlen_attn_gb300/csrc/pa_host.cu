@@ -1197,12 +1197,17 @@ pa_status pa_rope_and_cache(const pa_rope* rope, const int64_t* positions, const
       q_out_token_stride % 8 != 0)
     return PA_ERR_INVALID_ARG;
   if (q_out != q || q_out_token_stride != q_token_stride) {
-    // Rows are read and written by different warps: in place or apart.
+    // Rows are read and written by different warps: in place or apart, or, with
+    // one stride, q_out's rows between those of q.
     const char* lo = static_cast<const char*>(q);
     const char* out = static_cast<const char*>(q_out);
     if (out < lo + 2 * ((T - 1) * q_token_stride + row) &&
-        lo < out + 2 * ((T - 1) * q_out_token_stride + row))
-      return PA_ERR_INVALID_ARG;
+        lo < out + 2 * ((T - 1) * q_out_token_stride + row)) {
+      const int64_t step = 2 * q_token_stride;
+      const int64_t at = ((out - lo) % step + step) % step;   // in the rows of q
+      if (q_out_token_stride != q_token_stride || at < 2 * row || step - at < 2 * row)
+        return PA_ERR_INVALID_ARG;
+    }
   }
   const int sms = query_sms(0);
   if (sms <= 0) return PA_ERR_CUDA;

@@ -6,6 +6,7 @@ import torch
 import paged_kv_varlen_attn_gb300 as pa
 from paged_kv_varlen_attn_gb300 import _build
 from test_evict_host import call_weights
+from test_rope_host import call_rope
 
 
 @pytest.fixture(scope="module")
@@ -66,3 +67,22 @@ def test_rope_table_longer_than_32_bits_is_refused(lib):
     table = torch.empty(((1 << 32) + 8, 64), device="meta")
     with pytest.raises(ValueError, match="32 bits"):
         pa.rope_and_cache(q, q, q, i, table, c, c, i)
+
+
+ROW = 32 * 128
+FAR = 1 << 24    # 16-byte aligned, never dereferenced: validation fails first
+
+
+@pytest.mark.parametrize("n,os,off", [
+    (4, 4 * ROW, 3 * ROW + 8),        # the next row of q begins inside
+    (4, 4 * ROW, ROW - 8),
+    (4, 4 * ROW, -ROW + 8),
+    (4, 4 * ROW, 4 * ROW),            # other rows of q
+    (4, 4 * ROW, -8 * ROW),
+    (4, 2 * ROW, 3 * ROW),            # strides apart: any common range
+    (1, 2 * ROW, ROW - 8),
+])
+def test_rope_output_that_overlaps_its_input(lib, n, os, off):
+    """q_out lies off elements from q, whose rows are four rows apart."""
+    assert call_rope(lib, n=n, q=FAR, qs=4 * ROW, out=FAR + 2 * off, os=os) == \
+        pa.PA_ERR_INVALID_ARG
