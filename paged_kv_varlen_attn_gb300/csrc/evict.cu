@@ -406,7 +406,6 @@ evict_move_kernel(const __grid_constant__ EvictArgs a) {
   if (bad) flag_status(a.status, bad);
 }
 
-constexpr int kWidePairs = 152;
 constexpr int kLongKeys = 4096;
 
 template <int LANES, int THREADS>
@@ -446,7 +445,7 @@ static cudaError_t launch_select(const EvictArgs& a, int num_seqs, int bound, in
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
-cudaError_t launch_evict(const EvictArgs& a, int num_seqs, cudaStream_t st) {
+cudaError_t launch_evict(const EvictArgs& a, int num_seqs, cudaStream_t st, int sms) {
   if (num_seqs == 0) return cudaSuccess;
   const int bound = a.max_k < a.kv_len_cap ? a.max_k : a.kv_len_cap;
   // Short sequences: many small blocks, digits of as many bins as threads, so
@@ -459,21 +458,21 @@ cudaError_t launch_evict(const EvictArgs& a, int num_seqs, cudaStream_t st) {
   // (half the threads: 30.7).
   const long long units = static_cast<long long>(num_seqs) * a.H_kv;
   int parts = 1;
-  while (parts < kSelParts && units * parts < kWidePairs && bound > kLongKeys) parts *= 2;
+  while (parts < kSelParts && units * parts < sms && bound > kLongKeys) parts *= 2;
   cudaError_t e = bound <= kLongKeys ? launch_select<256, 8, false>(a, num_seqs, bound, 1, st)
                   : parts == 1       ? launch_select<1024, 11, false>(a, num_seqs, bound, 1, st)
                                      : launch_select<256, 8, true>(a, num_seqs, bound, parts, st);
   if (e != cudaSuccess) return e;
-  // Rows of one head move in order, chunk by chunk: where there are few
-  // (sequence, head) pairs, narrower slices and larger blocks make longer chunks
+  // Rows of one head move in order, chunk by chunk: where there are fewer
+  // (sequence, head) pairs than SMs, narrower slices and larger blocks make longer chunks
   // and more blocks (32 pairs to 2048 keys: 25.2 us with 32-byte slices and 256
   // threads, 28.2 with 128; 64-byte slices 32.6, 16-byte ones 41). Where there
   // are many, smaller blocks leave less of an SM waiting at a chunk's end (512
   // pairs to 1024 keys: 61.5 us with 64-byte slices and 128 threads, 64.4 with
   // 256, 63.5 with 64; 32-byte slices 73). As a programmatic dependent of the
   // selection the move was no faster.
-  return units >= kWidePairs ? launch_move<4, 128>(a, num_seqs, st)
-                             : launch_move<2, 256>(a, num_seqs, st);
+  return units >= sms ? launch_move<4, 128>(a, num_seqs, st)
+                      : launch_move<2, 256>(a, num_seqs, st);
 }
 
 }  // namespace pa

@@ -1285,6 +1285,8 @@ pa_status pa_attn_weights(const void* q, int64_t q_token_stride, const void* key
           0x7ffffffeLL / num_kv_heads)
     return PA_ERR_INVALID_ARG;
   if (num_seqs == 0 || total_q == 0) return PA_OK;
+  const int sms = query_sms(0);
+  if (sms <= 0) return PA_ERR_CUDA;
   WeightArgs a{};
   a.q = static_cast<const uint16_t*>(q);
   a.q_stride = q_token_stride;
@@ -1321,7 +1323,7 @@ pa_status pa_attn_weights(const void* q, int64_t q_token_stride, const void* key
     a.tc_min_rows = kWeightsTcMinRows;
   }
   return launch_attn_weights(tmQ, a, num_seqs, head_size, dtype == PA_F16, fp8 != nullptr,
-                             static_cast<cudaStream_t>(stream)) == cudaSuccess
+                             static_cast<cudaStream_t>(stream), sms) == cudaSuccess
              ? PA_OK
              : PA_ERR_CUDA;
 }
@@ -1356,6 +1358,8 @@ pa_status pa_evict(void* key_cache, void* value_cache, int64_t cache_block_strid
   if (weights_block_stride < static_cast<int64_t>(block_size) * num_kv_heads ||
       weights_block_stride % 4 != 0)
     return PA_ERR_INVALID_ARG;
+  const int sms = query_sms(0);
+  if (sms <= 0) return PA_ERR_CUDA;
   EvictArgs a{};
   a.kc = static_cast<uint8_t*>(key_cache);
   a.vc = static_cast<uint8_t*>(value_cache);
@@ -1379,7 +1383,7 @@ pa_status pa_evict(void* key_cache, void* value_cache, int64_t cache_block_strid
   a.kept = kept;
   a.new_lens = new_lens;
   a.status = dev_status;
-  return launch_evict(a, num_seqs, static_cast<cudaStream_t>(stream)) == cudaSuccess
+  return launch_evict(a, num_seqs, static_cast<cudaStream_t>(stream), sms) == cudaSuccess
              ? PA_OK
              : PA_ERR_CUDA;
 }

@@ -286,7 +286,7 @@ struct EvictArgs {
   int32_t* new_lens;              // [num_seqs]
   int32_t* status;
 };
-cudaError_t launch_evict(const EvictArgs& a, int num_seqs, cudaStream_t st);
+cudaError_t launch_evict(const EvictArgs& a, int num_seqs, cudaStream_t st, int sms);
 
 // Accumulated attention weight of every cached key (weights.cu).
 constexpr int kWeightsTcMinRows = 64;
@@ -316,6 +316,6 @@ struct WeightArgs {
 };
 // tmQ: q in tiles of tc_tile_rows(G) packed rows.
 cudaError_t launch_attn_weights(const CUtensorMap& tmQ, const WeightArgs& a, int num_seqs, int D,
-                                bool f16, bool fp8, cudaStream_t st);
+                                bool f16, bool fp8, cudaStream_t st, int sms);
 
 }  // namespace pa

@@ -642,11 +642,9 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
   }
 }
 
-constexpr long long kPairUnits = 304;
-
 template <int D, bool F16, bool FP8>
 static cudaError_t launch_weights_d(const CUtensorMap& tmQ, const WeightArgs& a, int num_seqs,
-                                    int keys, cudaStream_t st) {
+                                    int keys, cudaStream_t st, int sms) {
   const int tiles = keys > 0 ? (keys + kWeightKeys - 1) / kWeightKeys : 1;
   bool tc = false;   // the tensor-core kernel was launched
   if (a.tc_min_rows < 0x7fffffff) {
@@ -663,7 +661,7 @@ static cudaError_t launch_weights_d(const CUtensorMap& tmQ, const WeightArgs& a,
       // prompt of 4,096 (128 tiles of 256 keys) 74.0 us in pairs against 123.8;
       // two (184) 85.3 against 96.5; four (about 400) 163 against 147; sixteen
       // 755 against 647.
-      const int parts = units < kPairUnits ? 2 : 1;
+      const int parts = units < 2LL * sms ? 2 : 1;
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3(static_cast<unsigned>(units * parts));
       cfg.blockDim = dim3(C::THREADS);
@@ -705,18 +703,18 @@ static cudaError_t launch_weights_d(const CUtensorMap& tmQ, const WeightArgs& a,
 }
 
 cudaError_t launch_attn_weights(const CUtensorMap& tmQ, const WeightArgs& a, int num_seqs, int D,
-                                bool f16, bool fp8, cudaStream_t st) {
+                                bool f16, bool fp8, cudaStream_t st, int sms) {
   const int keys = a.max_k < a.kv_len_cap ? a.max_k : a.kv_len_cap;
-  if (fp8) return f16 ? launch_weights_d<128, true, true>(tmQ, a, num_seqs, keys, st)
-                      : launch_weights_d<128, false, true>(tmQ, a, num_seqs, keys, st);
+  if (fp8) return f16 ? launch_weights_d<128, true, true>(tmQ, a, num_seqs, keys, st, sms)
+                      : launch_weights_d<128, false, true>(tmQ, a, num_seqs, keys, st, sms);
   if (f16) {
-    if (D == 256) return launch_weights_d<256, true, false>(tmQ, a, num_seqs, keys, st);
-    if (D == 128) return launch_weights_d<128, true, false>(tmQ, a, num_seqs, keys, st);
-    return launch_weights_d<64, true, false>(tmQ, a, num_seqs, keys, st);
+    if (D == 256) return launch_weights_d<256, true, false>(tmQ, a, num_seqs, keys, st, sms);
+    if (D == 128) return launch_weights_d<128, true, false>(tmQ, a, num_seqs, keys, st, sms);
+    return launch_weights_d<64, true, false>(tmQ, a, num_seqs, keys, st, sms);
   }
-  if (D == 256) return launch_weights_d<256, false, false>(tmQ, a, num_seqs, keys, st);
-  if (D == 128) return launch_weights_d<128, false, false>(tmQ, a, num_seqs, keys, st);
-  return launch_weights_d<64, false, false>(tmQ, a, num_seqs, keys, st);
+  if (D == 256) return launch_weights_d<256, false, false>(tmQ, a, num_seqs, keys, st, sms);
+  if (D == 128) return launch_weights_d<128, false, false>(tmQ, a, num_seqs, keys, st, sms);
+  return launch_weights_d<64, false, false>(tmQ, a, num_seqs, keys, st, sms);
 }
 
 }  // namespace pa
