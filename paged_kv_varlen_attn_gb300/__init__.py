@@ -216,7 +216,8 @@ def _one_device(first, *rest):
 
 
 def _fit32(*values):
-    """Integers for the C interface, whose low 32 bits ctypes would pass on."""
+    """Refuse integers that the C interface does not hold (ctypes would pass
+    their low 32 bits on). Called where one may be such: v >> 31 is not 0."""
     for v in values:
         if v > _INT_MAX or v < -_INT_MAX:
             raise ValueError(f"integer arguments must fit 32 bits, got {v}")
@@ -632,8 +633,10 @@ def window_fwd(q, key_cache, value_cache, cu_seqlens_q, seqused_k, block_table, 
     slot_mapping). With k_scale and v_scale the caches hold e4m3 bytes.
     Returns (out, lse or None)."""
     lib = load_library()
-    window, num_first = min(int(window), _INT_MAX), min(int(num_first), _INT_MAX)
-    _fit32(max_seqlen_q, max_seqlen_k, window, num_first)
+    mq, mk, window, first = int(max_seqlen_q), int(max_seqlen_k), int(window), int(num_first)
+    if (mq | mk | window | first) >> 31:
+        window, first = min(window, _INT_MAX), min(first, _INT_MAX)
+        _fit32(mq, mk, window, first)
     _one_device(q, key_cache, value_cache, cu_seqlens_q, seqused_k, block_table, sinks, key, value,
                 slot_mapping, out, lse, workspace, dev_status)
     (nb, bs, hk, d), page = _pools(key_cache, value_cache)
@@ -675,18 +678,17 @@ def window_fwd(q, key_cache, value_cache, cu_seqlens_q, seqused_k, block_table, 
         desc, keep = _fp8_desc(k_scale, v_scale, hk, q.device)
     if workspace is None:
         size = varlen_fwd_workspace_size if desc is None else varlen_fwd_fp8kv_workspace_size
-        workspace = alloc_workspace(size(S, T, max_seqlen_q, max_seqlen_k, H, hk, D, bs,
-                                         _sm_count(q.device)), q.device)
+        workspace = alloc_workspace(size(S, T, mq, mk, H, hk, D, bs, _sm_count(q.device)),
+                                    q.device)
     opts = None
     if sinks is not None or desc is not None:
         opts = ctypes.byref(AttnOpts(_ptr(sinks), None if desc is None else ctypes.pointer(desc)))
     _call(lib.pa_window_fwd, "pa_window_fwd", q.device,
           None if update is None else ctypes.byref(update), q.data_ptr(), _row_stride(q),
           key_cache.data_ptr(), value_cache.data_ptr(), page, cu_seqlens_q.data_ptr(),
-          seqused_k.data_ptr(), block_table.data_ptr(), bt_row, S, T, int(max_seqlen_q),
-          int(max_seqlen_k), H, hk, D, bs, nb, float(softmax_scale), window, num_first, opts,
-          out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.numel(), dtype,
-          _ptr(dev_status))
+          seqused_k.data_ptr(), block_table.data_ptr(), bt_row, S, T, mq, mk, H, hk, D, bs, nb,
+          float(softmax_scale), window, first, opts, out.data_ptr(), _ptr(lse),
+          workspace.data_ptr(), workspace.numel(), dtype, _ptr(dev_status))
     del keep
     return out, lse
 
@@ -730,7 +732,8 @@ def rope_and_cache(q, key, value, positions, cos_sin, key_cache, value_cache, sl
     hold e4m3 bytes). Returns the rotated queries; out may be q itself."""
     lib = load_library()
     rows, rot = cos_sin.shape
-    _fit32(rows)
+    if rows >> 31:
+        _fit32(rows)
     _one_device(q, key, value, positions, cos_sin, key_cache, value_cache, slot_mapping, q_norm,
                 k_norm, out, dev_status)
     (nb, bs, hk, d), page = _pools(key_cache, value_cache)
@@ -796,7 +799,9 @@ def attn_weights(q, key_cache, lse, weights, cu_seqlens_q, seqused_k, block_tabl
     own queries start from zero. With k_scale the key cache holds e4m3 bytes.
     Returns weights."""
     lib = load_library()
-    _fit32(max_seqlen_q, max_seqlen_k)
+    mq, mk = int(max_seqlen_q), int(max_seqlen_k)
+    if (mq | mk) >> 31:
+        _fit32(mq, mk)
     _one_device(q, key_cache, lse, weights, cu_seqlens_q, seqused_k, block_table, dev_status)
     S = _cu_seqlens(cu_seqlens_q)
     bt_row = _seq_table(seqused_k, block_table, S)
@@ -814,8 +819,7 @@ def attn_weights(q, key_cache, lse, weights, cu_seqlens_q, seqused_k, block_tabl
     _call(lib.pa_attn_weights, "pa_attn_weights", q.device,
           _ptr(q), _row_stride(q), _ptr(key_cache), _cache_stride(key_cache), _ptr(lse),
           _ptr(cu_seqlens_q), _ptr(seqused_k), _ptr(block_table), bt_row,
-          S, T, int(max_seqlen_q), int(max_seqlen_k), H, hk, D, bs, nb,
-          float(softmax_scale), int(bool(causal)), _ptr(weights),
+          S, T, mq, mk, H, hk, D, bs, nb, float(softmax_scale), int(bool(causal)), _ptr(weights),
           _weights_stride(weights, nb, bs, hk), None if desc is None else ctypes.byref(desc),
           dtype, _ptr(dev_status))
     del keep
@@ -831,7 +835,9 @@ def evict(key_cache, value_cache, weights, seqused_k, block_table, max_seqlen_k,
     [num_seqs, num_kv_heads, budget], new_lens int32 [num_seqs]); new_lens may
     be seqused_k itself."""
     lib = load_library()
-    _fit32(max_seqlen_k, budget, num_first, num_recent)
+    mk, budget, first, recent = int(max_seqlen_k), int(budget), int(num_first), int(num_recent)
+    if (mk | budget | first | recent) >> 31:
+        _fit32(mk, budget, first, recent)
     _one_device(key_cache, value_cache, weights, seqused_k, block_table, kept, new_lens,
                 dev_status)
     (nb, bs, hk, d), page = _pools(key_cache, value_cache)
@@ -841,7 +847,7 @@ def evict(key_cache, value_cache, weights, seqused_k, block_table, max_seqlen_k,
     row = _seq_table(seqused_k, block_table, S)
     device = key_cache.device
     if kept is None:
-        kept = seqused_k.new_empty((S, hk, max(int(budget), 0)))
+        kept = seqused_k.new_empty((S, hk, max(budget, 0)))
     elif kept.dtype != torch.int32 or kept.shape != (S, hk, budget) or not kept.is_contiguous():
         raise ValueError("kept must be a contiguous int32 [num_seqs, num_kv_heads, budget] tensor")
     if new_lens is None:
@@ -851,7 +857,6 @@ def evict(key_cache, value_cache, weights, seqused_k, block_table, max_seqlen_k,
     _call(lib.pa_evict, "pa_evict", device,
           key_cache.data_ptr(), value_cache.data_ptr(), page, weights.data_ptr(),
           _weights_stride(weights, nb, bs, hk), seqused_k.data_ptr(), block_table.data_ptr(),
-          row, S, int(max_seqlen_k), hk, d, bs, nb,
-          key_cache.element_size(), int(budget), int(num_first), int(num_recent), kept.data_ptr(),
-          new_lens.data_ptr(), _ptr(dev_status))
+          row, S, mk, hk, d, bs, nb, key_cache.element_size(), budget, first, recent,
+          kept.data_ptr(), new_lens.data_ptr(), _ptr(dev_status))
     return kept, new_lens
