@@ -13,18 +13,19 @@ namespace pa {
 
 // ---------------------------------------------------------------------------
 // Decode and short queries (at most tc_min_rows packed query rows).
-// A warp takes kSlices slices of 16 keys of a sequence and KV head. A slice's
-// keys are the M dimension of the warp MMA and 8 packed query rows (token,
-// head of the group) its N, so a key's sum is a sum along the accumulator's
-// columns: no reduction until the end, where the four lanes of a row add up.
+// A block, one warp, takes kSlices slices of 16 keys of a sequence and KV head.
+// A slice's keys are the M dimension of the warp MMA and 8 packed query rows
+// (token, head of the group) its N, so a key's sum is a sum along the
+// accumulator's columns: no reduction until the end, where the four lanes of a
+// row add up.
 // The head dimension is permuted alike in the K (A) and Q (B) fragments so
 // that a lane's elements are 16-byte runs and four lanes read 64 consecutive
-// bytes; Q goes straight to registers, K through a ring of slots per warp
+// bytes; Q goes straight to registers, K through a ring of slots
 // filled by asynchronous copies, where every lane reads back its own bytes
 // (the ring holds what registers could not: no barrier but the warp's own).
 // Decode is bound by the read of K; the ring keeps one to three slices of every
-// warp on their way. A block is one warp, whose place the next one takes as soon
-// as it is done. On the 64-sequence decode batch (483 MB): 77.3 us, 6.2 TB/s, 92%
+// warp on their way, and a block's place is taken by the next one as soon as it
+// is done. On the 64-sequence decode batch (483 MB): 77.3 us, 6.2 TB/s, 92%
 // of the measured copy rate (blocks of four warps 77.9); with K read straight
 // into registers 92 us (two slices in flight, 16 warps per SM) and 121 us (one
 // slice per warp, the chain of dependent reads in front of it exposed). Two
@@ -32,16 +33,14 @@ namespace pa {
 // slices per warp beat 4 and 16 by 2.3.
 // 16 keys never cross a page (pages are multiples of 16 keys).
 // ---------------------------------------------------------------------------
-constexpr int kWeightWarps = 1;
-constexpr int kSlices = 8;
-static_assert(kWeightWarps * kSlices * 16 == kWeightKeys, "the keys of a block");
+constexpr int kSlices = kWeightKeys / 16;
 
 template <int D, bool FP8>
 struct WwCfg {
   static constexpr int ROW = D * (FP8 ? 1 : 2);            // bytes of a key
   static constexpr int SLOT = 16 * ROW + 64;               // a slice and its old sums
   static constexpr int SLOTS = ROW >= 256 ? 2 : 4;
-  static constexpr int SMEM_BYTES = kWeightWarps * SLOTS * SLOT;
+  static constexpr int SMEM_BYTES = SLOTS * SLOT;
 };
 
 // Lengths of sequence s for both kernels: false if the call has nothing to add
@@ -63,7 +62,7 @@ __device__ __forceinline__ bool weight_lengths(const WeightArgs& a, int s, bool 
 }
 
 template <int D, bool F16, bool FP8>
-__global__ void __launch_bounds__(kWeightWarps * 32)
+__global__ void __launch_bounds__(32)
 weights_kernel(const __grid_constant__ WeightArgs a, int tiles) {
   using E = Elem<F16>;
   using C = WwCfg<D, FP8>;
@@ -76,22 +75,21 @@ weights_kernel(const __grid_constant__ WeightArgs a, int tiles) {
     pdl_wait();
     return;
   }
-  extern __shared__ __align__(16) uint8_t ring_raw[];
+  extern __shared__ __align__(16) uint8_t ring[];
   // KV head fastest: a page's heads are read at about the same time (13% on
   // the decode batch over all of one head's blocks before the next head's).
   const int unit = blockIdx.x / a.H_kv;
   const int hk = blockIdx.x - unit * a.H_kv;
   const int s = unit / tiles;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int lane = threadIdx.x;
   const int g = lane >> 2, c = lane & 3;
-  const int base = ((unit - s * tiles) * kWeightWarps + warp) * (kSlices * 16);
+  const int base = (unit - s * tiles) * kWeightKeys;
   int q0, q_len, kv;
   if (!weight_lengths(a, s, base == 0 && hk == 0 && lane == 0, q0, q_len, kv)) return;
   if (base >= kv || q_len * a.G > a.tc_min_rows) return;
   const int past = kv - q_len;          // query i is at position past + i
   const int rows = q_len * a.G;
   const int nslices = min(kSlices, (kv - base + 15) >> 4);
-  uint8_t* ring = ring_raw + warp * (C::SLOTS * C::SLOT);
 
   // Lane i: page of slice i (-1: none, or outside the pool), its first row.
   int page_l = -1, row_l = 0;
@@ -689,7 +687,7 @@ static cudaError_t launch_weights_d(const CUtensorMap& tmQ, const WeightArgs& a,
   // other's, or find nothing to do while it runs.
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(num_seqs) * tiles * a.H_kv + 1u);
-  cfg.blockDim = dim3(kWeightWarps * 32);
+  cfg.blockDim = dim3(32);
   cfg.dynamicSmemBytes = W::SMEM_BYTES;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
