@@ -372,8 +372,13 @@ pa_status pa_varlen_fwd_noalloc(const void* q, int64_t q_token_stride, const voi
  * Shorter segments run on the split-KV kernel: items of at most 8 packed
  * rows (decode with GQA <= 8) take q.k on the e4m3 MMA too, wider ones form
  * q.k from f16 q (there |q| must stay below 65504). Wherever q.k is on the
- * e4m3 MMA, q is taken as two e4m3 terms after a power-of-two row scale
- * (exact for every element of at least 2^-9 of its row's largest).
+ * e4m3 MMA, q is taken as two e4m3 terms after a power-of-two row scale:
+ * exact for every bf16 element of at least 2^-9 of its row's largest; an f16
+ * element, which has eleven significant bits, is rounded to about eight (off
+ * by at most 2^-9 of its power of two). pa_window_fwd takes the query as it is,
+ * on the f16 MMA, in calls of at most 8 packed rows per sequence and KV head
+ * (max_seqlen_q * num_heads / num_kv_heads; long windows of few sequences
+ * apart).
  * Layout: the NHD pools of pa_reshape_and_cache with 1-byte elements;
  * cache_block_stride is in elements (= bytes) and a multiple of 16.
  * head_size must be 128 (PA_ERR_UNSUPPORTED otherwise).

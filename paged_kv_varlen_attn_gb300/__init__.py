@@ -797,7 +797,8 @@ def attn_weights(q, key_cache, lse, weights, cu_seqlens_q, seqused_k, block_tabl
     (recomputed from K and the attention call's lse) to weights, float32
     [num_blocks, num_kv_heads, block_size], in place; the keys of the call's
     own queries start from zero. With k_scale the key cache holds e4m3 bytes.
-    Returns weights."""
+    A sequence's pages must be its own: a page that two sequences of the call
+    share (a common prefix) gets the sum of one of them. Returns weights."""
     lib = load_library()
     mq, mk = int(max_seqlen_q), int(max_seqlen_k)
     if (mq | mk) >> 31:
@@ -831,9 +832,10 @@ def evict(key_cache, value_cache, weights, seqused_k, block_table, max_seqlen_k,
     """Cut every sequence of more than budget keys down to budget, per KV head:
     its first num_first keys, its last num_recent and the heaviest of the rest
     by weights; kept rows of the caches (2-byte or e4m3 elements) and of
-    weights move to the front of the sequence's pages. Returns (kept int32
-    [num_seqs, num_kv_heads, budget], new_lens int32 [num_seqs]); new_lens may
-    be seqused_k itself."""
+    weights move to the front of the sequence's pages, which must be its own
+    (none shared with another sequence: rows are rewritten in place). Returns
+    (kept int32 [num_seqs, num_kv_heads, budget], new_lens int32 [num_seqs]);
+    new_lens may be seqused_k itself."""
     lib = load_library()
     mk, budget, first, recent = int(max_seqlen_k), int(budget), int(num_first), int(num_recent)
     if (mk | budget | first | recent) >> 31:

@@ -89,12 +89,14 @@ cudaError_t launch_rope_table(float* table, RopeTableArgs& a, cudaStream_t st, i
 // 16 lanes away (half layout: one shuffle per pair of elements). Everything
 // between the load and the store is float32; the store is the only rounding.
 // A block is one warp: its place on the SM is taken by the next one as soon as
-// it is done, so loads are always on their way. Bound by HBM: 16,384 tokens of
-// 32/8 heads of 128 without norms (405 MB) take 62.2 us, 96% of the measured
-// copy rate (blocks of two warps 67.5, of four 70.8; 28 blocks per SM 66.6);
-// 4,109 tokens of 64/8 heads with norms into e4m3 pools (162 MB) 33.2 us, 72%,
-// beside the norm's shuffles and the quantization (two warps 41, four 42.2; 24
-// blocks per SM 33.8). A decode step's 64 tokens take 3.0 us.
+// it is done, so loads are always on their way. Bound by HBM without norms:
+// 16,384 tokens of 32/8 heads of 128 (405 MB) take 62.2 us, 96% of the measured
+// copy rate (blocks of two warps 67.5, of four 70.8; 28 blocks per SM 66.6).
+// 4,109 tokens of 64/8 heads with norms into e4m3 pools (162 MB) take 33.2 us,
+// 72% (two warps 41, four 42.2; 24 blocks per SM 33.8); there nothing is full
+// (profiler: DRAM 36%, issue slots 63%, resident warps 38%): a warp waits for the
+// shuffles of its items one after another, four of the norm's sum and four of
+// the partners each. A decode step's 64 tokens take 3.0 us.
 // ---------------------------------------------------------------------------
 constexpr int kRopeItems = 8;
 

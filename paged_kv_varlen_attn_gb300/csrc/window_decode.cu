@@ -20,7 +20,11 @@ namespace pa {
 //     bytes it copied itself
 //   P^T by exponentials against a running maximum that is raised only when a
 //     score passes it by more than 2^8 (the sums stay far inside float32, the
-//     weights inside the element type)
+//     weights inside the element type). The weights are rounded to that type (f16
+//     over e4m3 pools) for the second product, as in every attention kernel here:
+//     at most 2^-8 (f16 2^-11) of each, the size of the output's own rounding;
+//     their sum is taken in float32 before that. An f16 weight below 2^-25 of the
+//     running maximum's is lost.
 //   O^T[D x 8 rows] += V^T P^T         V by transposed matrix loads from a
 //     swizzled slice; P^T as the B operand by two 8x8 register transposes
 // e4m3 pools: both products on f16 MMAs, which hold every e4m3 value and the
