@@ -637,6 +637,8 @@ def window_fwd(q, key_cache, value_cache, cu_seqlens_q, seqused_k, block_table, 
     if (mq | mk | window | first) >> 31:
         window, first = min(window, _INT_MAX), min(first, _INT_MAX)
         _fit32(mq, mk, window, first)
+    if (key is None) is not (value is None) or (key is None) is not (slot_mapping is None):
+        raise ValueError("key, value and slot_mapping go together")
     _one_device(q, key_cache, value_cache, cu_seqlens_q, seqused_k, block_table, sinks, key, value,
                 slot_mapping, out, lse, workspace, dev_status)
     (nb, bs, hk, d), page = _pools(key_cache, value_cache)

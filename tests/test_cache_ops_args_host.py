@@ -86,3 +86,17 @@ def test_rope_output_that_overlaps_its_input(lib, n, os, off):
     """q_out lies off elements from q, whose rows are four rows apart."""
     assert call_rope(lib, n=n, q=FAR, qs=4 * ROW, out=FAR + 2 * off, os=os) == \
         pa.PA_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("given", [("key",), ("value",), ("slot_mapping",), ("key", "value"),
+                                   ("value", "slot_mapping"), ("key", "slot_mapping")])
+def test_window_update_is_whole_or_none(lib, given):
+    """New tokens without one of key, value and slots: refused, not left out."""
+    m = dict(device="meta")
+    q = torch.empty((2, 8, 128), dtype=torch.bfloat16, **m)
+    c = torch.empty((4, 16, 8, 128), dtype=torch.bfloat16, **m)
+    n, bt = torch.empty(2, dtype=torch.int32, **m), torch.empty((2, 4), dtype=torch.int32, **m)
+    cu = torch.empty(3, dtype=torch.int32, **m)
+    new = dict(key=q, value=q, slot_mapping=torch.empty(2, dtype=torch.int64, **m))
+    with pytest.raises(ValueError, match="go together"):
+        pa.window_fwd(q, c, c, cu, n, bt, 1, 64, 0.1, 16, **{k: new[k] for k in given})
