@@ -657,6 +657,100 @@ pa_status pa_evict(void* key_cache, void* value_cache, int64_t cache_block_strid
                    int budget, int num_first, int num_recent, int32_t* kept, int32_t* new_lens,
                    int32_t* dev_status, void* stream);
 
+/*
+ * 4-bit K/V cache. The pools hold codes of four bits, and every row (one token
+ * of one KV head) has a scale and a minimum of its own:
+ *   value of an element = code * scale + minimum, codes 0 .. 15.
+ *   codes  : page b of a pool starts at b * cache_block_stride (in bytes, a
+ *            multiple of 16) and holds [block_size, num_kv_heads, head_size / 2]
+ *            bytes contiguous. Of each 8 consecutive elements 8w .. 8w + 7 the
+ *            32-bit little-endian word w holds element 8w + 2i in bits 4i .. 4i +
+ *            3 and element 8w + 2i + 1 in bits 16 + 4i .. 19 + 4i.
+ *   params : pairs of f16, (scale, minimum); row r of page b, KV head h is pair
+ *            b * params_block_stride + h * block_size + r, 4-byte aligned.
+ * A row x is written as follows, in float32 with every operation rounded once:
+ *   elements beyond +-32752 count as +-32752;
+ *   scale = f16((max x - min x) * (1 / 15)), minimum = f16(min x);
+ *   code = (x - minimum) * (1 / scale), brought into [0, 15] and rounded to
+ *   the nearest integer, ties to even (0 for a scale of 0).
+ * A row with a NaN gets NaN for scale and minimum, so all of it reads as NaN.
+ * Head sizes 64 and 128 (PA_ERR_UNSUPPORTED otherwise).
+ */
+typedef struct pa_kv_int4 {
+  void* k_params; /* device f16 pairs, written by the cache writes */
+  void* v_params;
+  int64_t params_block_stride; /* in pairs, >= num_kv_heads * block_size */
+} pa_kv_int4;
+
+/*
+ * pa_reshape_and_cache_int4 -- pa_reshape_and_cache into 4-bit pools.
+ */
+pa_status pa_reshape_and_cache_int4(const void* key, const void* value, int64_t key_token_stride,
+                                    int64_t value_token_stride, void* key_cache, void* value_cache,
+                                    int64_t cache_block_stride, const pa_kv_int4* int4,
+                                    const int64_t* slot_mapping, int num_tokens, int num_kv_heads,
+                                    int head_size, int block_size, int num_blocks, int dtype,
+                                    int32_t* dev_status, void* stream);
+
+/*
+ * pa_rope_and_cache_int4 -- pa_rope_and_cache into 4-bit pools: the rotated
+ * key is quantized from its float32 value. A rotated element is a cos - b sin
+ * (b cos + a sin) with both products and the sum rounded to float32; norm
+ * weights are multiplied into cos and sin before, and the norm's 1 / rms is
+ * multiplied on last.
+ */
+pa_status pa_rope_and_cache_int4(const pa_rope* rope, const int64_t* positions, const void* q,
+                                 int64_t q_token_stride, void* q_out, int64_t q_out_token_stride,
+                                 const pa_kv_update* update, void* key_cache, void* value_cache,
+                                 int64_t cache_block_stride, const pa_kv_int4* int4, int num_heads,
+                                 int num_kv_heads, int head_size, int block_size, int num_blocks,
+                                 int dtype, int32_t* dev_status, void* stream);
+
+/*
+ * pa_gather_cache_int4 -- rows of a 4-bit cache back as values, to move them
+ * into 2-byte pools or to look at them: key and value, [num_tokens,
+ * num_kv_heads, head_size] in dtype and contiguous, get code * scale + minimum
+ * (float32, rounded once to dtype) of the rows at slot_mapping. A slot may
+ * occur more than once; a token whose slot is negative, or past the pool
+ * (PA_DEV_BAD_SLOT), gets zeros. The outputs must not overlap the pools.
+ */
+pa_status pa_gather_cache_int4(const void* key_cache, const void* value_cache,
+                               int64_t cache_block_stride, const pa_kv_int4* int4,
+                               const int64_t* slot_mapping, int num_tokens, int num_kv_heads,
+                               int head_size, int block_size, int num_blocks, void* key,
+                               void* value, int dtype, int32_t* dev_status, void* stream);
+
+/*
+ * pa_varlen_fwd_int4kv -- pa_varlen_fwd_ex over 4-bit pools: the optional
+ * update (NULL or num_tokens = 0 for none) is written as by
+ * pa_reshape_and_cache_int4, then the attention reads the cache's values code *
+ * scale + minimum. sinks as in pa_attn_opts (NULL for none). Groups of at most
+ * 128 query heads per KV head (PA_ERR_UNSUPPORTED otherwise); max_seqlen_k at
+ * most 2^30 (PA_ERR_INVALID_ARG).
+ * Sequences of at most 32 packed query rows (tokens x heads of the group; decode
+ * and short queries) form q.k from the codes themselves, which are exact in
+ * f16, and apply scale and minimum to the sums; q is taken as f16 after a
+ * power-of-two row scale, exact for every bf16 element of at least 2^-28 of its
+ * row's largest. The weights times V's scale are rounded to f16 after a
+ * power-of-two row scale. Longer sequences run on the tensor-core kernel with K
+ * and V widened to f16 values (one rounding, at most 2^-11 of a value) and the
+ * weights in f16.
+ * In pages that are read, rows past a sequence's keys do not matter.
+ */
+size_t pa_varlen_fwd_int4kv_workspace_size(int num_seqs, int total_q, int max_seqlen_q,
+                                           int max_seqlen_k, int num_heads, int num_kv_heads,
+                                           int head_size, int block_size, int sm_count);
+pa_status pa_varlen_fwd_int4kv(const pa_kv_update* update, const void* q, int64_t q_token_stride,
+                               void* key_cache, void* value_cache, int64_t cache_block_stride,
+                               const int32_t* cu_seqlens_q, const int32_t* seqused_k,
+                               const int32_t* block_table, int bt_stride, int num_seqs,
+                               int total_q, int max_seqlen_q, int max_seqlen_k, int num_heads,
+                               int num_kv_heads, int head_size, int block_size, int num_blocks,
+                               float softmax_scale, int causal, const pa_kv_int4* int4,
+                               const float* sinks, void* out, float* lse, void* workspace,
+                               size_t workspace_bytes, int dtype, int32_t* dev_status,
+                               void* stream);
+
 #ifdef __cplusplus
 }
 #endif

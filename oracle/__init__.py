@@ -21,4 +21,4 @@ from .paged_attention import (  # noqa: F401
     reshape_and_cache_e4m3,
     varlen_attention_e4m3,
 )
-from . import cache_ops  # noqa: F401
+from . import cache_ops, changed_scores  # noqa: F401

@@ -61,6 +61,11 @@ EXPORTS = (
     "pa_rope_and_cache",
     "pa_attn_weights",
     "pa_evict",
+    "pa_reshape_and_cache_int4",
+    "pa_rope_and_cache_int4",
+    "pa_gather_cache_int4",
+    "pa_varlen_fwd_int4kv_workspace_size",
+    "pa_varlen_fwd_int4kv",
 )
 
 _lib = None
@@ -97,6 +102,11 @@ class Rope(ctypes.Structure):
     """struct pa_rope of include/pa.h."""
     _fields_ = [("cos_sin", _vp), ("table_len", _i32), ("rot_dim", _i32), ("interleaved", _i32),
                 ("q_norm", _vp), ("k_norm", _vp), ("norm_eps", _f32)]
+
+
+class KvInt4(ctypes.Structure):
+    """struct pa_kv_int4 of include/pa.h."""
+    _fields_ = [("k_params", _vp), ("v_params", _vp), ("params_block_stride", _i64)]
 
 
 _ATTN_ARGS = [_vp, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i32,
@@ -141,6 +151,16 @@ _SIGS = {
         _f32, _i32, _vp, _i64, ctypes.POINTER(KvFp8), _i32, _vp, _vp], _i32),
     "pa_evict": ([_vp, _vp, _i64, _vp, _i64, _vp, _vp] + [_i32] * 11 + [_vp, _vp, _vp, _vp],
                  _i32),
+    "pa_reshape_and_cache_int4": ([_vp, _vp, _i64, _i64, _vp, _vp, _i64, ctypes.POINTER(KvInt4),
+                                   _vp] + [_i32] * 6 + [_vp, _vp], _i32),
+    "pa_rope_and_cache_int4": ([ctypes.POINTER(Rope), _vp, _vp, _i64, _vp, _i64,
+                                ctypes.POINTER(KvUpdate), _vp, _vp, _i64,
+                                ctypes.POINTER(KvInt4)] + [_i32] * 6 + [_vp, _vp], _i32),
+    "pa_gather_cache_int4": ([_vp, _vp, _i64, ctypes.POINTER(KvInt4), _vp] + [_i32] * 5 +
+                             [_vp, _vp, _i32, _vp, _vp], _i32),
+    "pa_varlen_fwd_int4kv_workspace_size": ([_i32] * 9, _sz),
+    "pa_varlen_fwd_int4kv": ([ctypes.POINTER(KvUpdate)] + _ATTN_ARGS[:20] +
+                             [ctypes.POINTER(KvInt4), _vp] + _ATTN_ARGS[20:], _i32),
     "pa_cascade_fwd_fp8kv_workspace_size": ([_i32] * 9, _sz),
     "pa_varlen_fwd_fp8kv": ([ctypes.POINTER(KvUpdate)] + _ATTN_ARGS[:20] +
                             [ctypes.POINTER(KvFp8)] + _ATTN_ARGS[20:], _i32),
@@ -864,3 +884,192 @@ def evict(key_cache, value_cache, weights, seqused_k, block_table, max_seqlen_k,
           row, S, mk, hk, d, bs, nb, key_cache.element_size(), budget, first, recent,
           kept.data_ptr(), new_lens.data_ptr(), _ptr(dev_status))
     return kept, new_lens
+
+
+# ---------------------------------------------------------------------------
+# 4-bit K/V cache: uint8 pools [num_blocks, block_size, num_kv_heads, head_size
+# / 2] of codes, and float16 params [num_blocks, num_kv_heads, block_size, 2] of
+# a scale and a minimum per row (the format is described in include/pa.h).
+def int4_pools(num_blocks, block_size, num_kv_heads, head_size, device="cuda"):
+    """Empty (zeroed) 4-bit pools: (key_cache, value_cache, key_params,
+    value_params)."""
+    codes = (num_blocks, block_size, num_kv_heads, head_size // 2)
+    params = (num_blocks, num_kv_heads, block_size, 2)
+    return tuple(torch.zeros(codes, dtype=torch.uint8, device=device) for _ in range(2)) + \
+        tuple(torch.zeros(params, dtype=torch.float16, device=device) for _ in range(2))
+
+
+def _int4_pools(key_cache, value_cache, key_params, value_params):
+    """(num_blocks, block_size, kv heads, head size), page stride, descriptor."""
+    (nb, bs, hk, half), page = _pools(key_cache, value_cache)
+    if key_cache.dtype is not torch.uint8 or value_cache.dtype is not torch.uint8:
+        raise ValueError("4-bit caches are uint8 [num_blocks, block_size, num_kv_heads, "
+                         "head_size / 2]")
+    shape, st = (nb, hk, bs, 2), key_params.stride()
+    if key_params.dtype is not torch.float16 or value_params.dtype is not torch.float16 or \
+            key_params.shape != shape or value_params.shape != shape or \
+            value_params.stride() != st or st[3] != 1 or st[2] != 2 or \
+            (st[1] != 2 * bs and hk > 1) or st[0] % 2:
+        raise ValueError("params must be float16 [num_blocks, num_kv_heads, block_size, 2] with "
+                         "contiguous pages, laid out alike")
+    return (nb, bs, hk, 2 * half), page, KvInt4(key_params.data_ptr(), value_params.data_ptr(),
+                                                st[0] // 2)
+
+
+def _slots(slot_mapping, n):
+    if slot_mapping.dtype is not torch.int64 or slot_mapping.shape != (n,) or \
+            not slot_mapping.is_contiguous():
+        raise ValueError("slot_mapping must be a contiguous int64 tensor of one value per token")
+
+
+def _new_tokens(key, value, slot_mapping, hk, d):
+    """struct pa_kv_update of new tokens [n, hk, d]."""
+    n = key.shape[0]
+    if key.shape != (n, hk, d) or value.shape != (n, hk, d):
+        raise ValueError("key and value must be [tokens, num_kv_heads, head_size]")
+    _slots(slot_mapping, n)
+    return KvUpdate(key.data_ptr(), value.data_ptr(), _row_stride(key), _row_stride(value),
+                    slot_mapping.data_ptr(), n)
+
+
+def reshape_and_cache_int4(key, value, key_cache, value_cache, key_params, value_params,
+                           slot_mapping, dev_status=None):
+    """Quantize new K/V rows to 4 bits and scatter them into their pages (in
+    place on the caches and params)."""
+    _one_device(key, value, key_cache, value_cache, key_params, value_params, slot_mapping,
+                dev_status)
+    (nb, bs, hk, d), page, desc = _int4_pools(key_cache, value_cache, key_params, value_params)
+    u = _new_tokens(key, value, slot_mapping, hk, d)
+    _call(load_library().pa_reshape_and_cache_int4, "pa_reshape_and_cache_int4", key.device,
+          u.key, u.value, u.key_token_stride, u.value_token_stride, key_cache.data_ptr(),
+          value_cache.data_ptr(), page, ctypes.byref(desc), u.slot_mapping, u.num_tokens, hk, d, bs,
+          nb, _dtype_code(key, value), _ptr(dev_status))
+
+
+def rope_and_cache_int4(q, key, value, positions, cos_sin, key_cache, value_cache, key_params,
+                        value_params, slot_mapping, interleaved=False, q_norm=None, k_norm=None,
+                        eps=1e-6, out=None, dev_status=None):
+    """rope_and_cache into 4-bit pools: norm (optional) and rotate the new
+    queries and keys, and write keys and values into their pages in 4 bits (in
+    place on the caches and params). Returns the rotated queries; out may be q
+    itself."""
+    lib = load_library()
+    rows, rot = cos_sin.shape
+    if rows >> 31:
+        _fit32(rows)
+    _one_device(q, key, value, positions, cos_sin, key_cache, value_cache, key_params,
+                value_params, slot_mapping, q_norm, k_norm, out, dev_status)
+    (nb, bs, hk, d), page, desc = _int4_pools(key_cache, value_cache, key_params, value_params)
+    T, H, dq = q.shape
+    if dq != d or key.shape[0] != T:
+        raise ValueError("q, key and value must be [tokens, heads, head_size] of the caches' "
+                         "heads and head size")
+    update = _new_tokens(key, value, slot_mapping, hk, d)
+    if positions.dtype is not torch.int64 or positions.shape != (T,) or \
+            not positions.is_contiguous():
+        raise ValueError("positions must be a contiguous int64 tensor of one value per token")
+    if cos_sin.dtype != torch.float32 or not cos_sin.is_contiguous():
+        raise ValueError("cos_sin must be a contiguous float32 [positions, rot_dim] tensor")
+    _f32_vector(q_norm, d, "q_norm")
+    _f32_vector(k_norm, d, "k_norm")
+    if out is None:
+        out = torch.empty_like(q) if q.is_contiguous() else q.new_empty((T, H, d))
+        out_row = H * d
+    elif out.shape != q.shape:
+        raise ValueError("out must have the shape of q")
+    else:
+        out_row = _row_stride(out)
+    rope = Rope(cos_sin.data_ptr(), rows, rot, 1 if interleaved else 0, _ptr(q_norm),
+                _ptr(k_norm), eps)
+    _call(lib.pa_rope_and_cache_int4, "pa_rope_and_cache_int4", q.device,
+          ctypes.byref(rope), positions.data_ptr(), q.data_ptr(), _row_stride(q), out.data_ptr(),
+          out_row, ctypes.byref(update), key_cache.data_ptr(), value_cache.data_ptr(), page,
+          ctypes.byref(desc), H, hk, d, bs, nb, _dtype_code(q, key, value, out), _ptr(dev_status))
+    return out
+
+
+def gather_cache_int4(key_cache, value_cache, key_params, value_params, slot_mapping, dtype,
+                      key=None, value=None, dev_status=None):
+    """Rows of a 4-bit cache back as values: (key, value) [tokens, num_kv_heads,
+    head_size] in dtype of the rows at slot_mapping (zeros for a negative slot)."""
+    _one_device(key_cache, value_cache, key_params, value_params, slot_mapping, key, value,
+                dev_status)
+    (nb, bs, hk, d), page, desc = _int4_pools(key_cache, value_cache, key_params, value_params)
+    n = slot_mapping.numel()
+    _slots(slot_mapping, n)
+    shape, got = (n, hk, d), []
+    for t in (key, value):
+        if t is None:
+            t = torch.empty(shape, dtype=dtype, device=key_cache.device)
+        elif t.shape != shape or not t.is_contiguous() or t.dtype is not dtype:
+            raise ValueError("key and value must be contiguous [tokens, num_kv_heads, head_size] "
+                             "tensors of dtype")
+        got.append(t)
+    _call(load_library().pa_gather_cache_int4, "pa_gather_cache_int4", key_cache.device,
+          key_cache.data_ptr(), value_cache.data_ptr(), page, ctypes.byref(desc),
+          slot_mapping.data_ptr(), n, hk, d, bs, nb, got[0].data_ptr(), got[1].data_ptr(),
+          _dtype_code(*got), _ptr(dev_status))
+    return tuple(got)
+
+
+def varlen_fwd_int4kv_workspace_size(num_seqs, total_q, max_seqlen_q, max_seqlen_k, num_heads,
+                                     num_kv_heads, head_size, block_size, sm_count):
+    return load_library().pa_varlen_fwd_int4kv_workspace_size(
+        num_seqs, total_q, max_seqlen_q, max_seqlen_k, num_heads, num_kv_heads, head_size,
+        block_size, sm_count)
+
+
+def _outputs(q, out, lse, return_lse):
+    """out and lse of an attention call, allocated where they are None."""
+    T, H, D = q.shape
+    if out is None:
+        out = torch.empty_like(q) if q.is_contiguous() else q.new_empty((T, H, D))
+    elif out.shape != (T, H, D) or not out.is_contiguous():
+        raise ValueError("out must be a contiguous [total_q, num_heads, head_size] tensor")
+    if lse is None:
+        if return_lse:
+            lse = q.new_empty((H, T), dtype=torch.float32)
+    elif lse.dtype != torch.float32 or lse.shape != (H, T) or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous float32 [num_heads, total_q] tensor")
+    return out, lse
+
+
+def varlen_fwd_int4kv(q, key_cache, value_cache, key_params, value_params, cu_seqlens_q, seqused_k,
+                      block_table, max_seqlen_q, max_seqlen_k, softmax_scale, causal, key=None,
+                      value=None, slot_mapping=None, out=None, lse=None, return_lse=True,
+                      workspace=None, dev_status=None, sinks=None):
+    """Varlen attention over 4-bit pools, optionally first quantizing and
+    scattering the new tokens' K/V (key, value, slot_mapping). Returns (out, lse
+    or None)."""
+    lib = load_library()
+    mq, mk = int(max_seqlen_q), int(max_seqlen_k)
+    if (mq | mk) >> 31:
+        _fit32(mq, mk)
+    if (key is None) is not (value is None) or (key is None) is not (slot_mapping is None):
+        raise ValueError("key, value and slot_mapping go together")
+    _one_device(q, key_cache, value_cache, key_params, value_params, cu_seqlens_q, seqused_k,
+                block_table, key, value, slot_mapping, out, lse, workspace, dev_status, sinks)
+    (nb, bs, hk, d), page, desc = _int4_pools(key_cache, value_cache, key_params, value_params)
+    T, H, D = q.shape
+    S = _cu_seqlens(cu_seqlens_q)
+    bt_row = _seq_table(seqused_k, block_table, S)
+    if d != D:
+        raise ValueError("q and the caches must share the head size")
+    out, lse = _outputs(q, out, lse, return_lse)
+    _f32_vector(sinks, H, "sinks")
+    update = None
+    if key is None:
+        dtype = _dtype_code(q, out)
+    else:
+        update = ctypes.byref(_new_tokens(key, value, slot_mapping, hk, D))
+        dtype = _dtype_code(q, out, key, value)
+    if workspace is None:
+        workspace = alloc_workspace(varlen_fwd_int4kv_workspace_size(
+            S, T, mq, mk, H, hk, D, bs, _sm_count(q.device)), q.device)
+    _call(lib.pa_varlen_fwd_int4kv, "pa_varlen_fwd_int4kv", q.device,
+          update, q.data_ptr(), _row_stride(q), key_cache.data_ptr(), value_cache.data_ptr(), page,
+          cu_seqlens_q.data_ptr(), seqused_k.data_ptr(), block_table.data_ptr(), bt_row, S, T, mq,
+          mk, H, hk, D, bs, nb, float(softmax_scale), 1 if causal else 0, ctypes.byref(desc),
+          _ptr(sinks), out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.numel(), dtype,
+          _ptr(dev_status))
+    return out, lse

@@ -188,13 +188,42 @@ pa_status check_shape(int num_seqs, int total_q, int max_seqlen_q, int max_seqle
   return PA_OK;
 }
 
-// Element type of the K/V pools: bf16, or e4m3 codes with per-KV-head scales.
+// Element type of the K/V pools: bf16, e4m3 codes with per-KV-head scales, or
+// 4-bit codes with a scale and a minimum per row.
 struct KvFormat {
   bool fp8;
   const float* k_scale;
   const float* v_scale;
+  bool int4 = false;
+  uint32_t* k_params = nullptr;
+  uint32_t* v_params = nullptr;
+  int64_t params_stride = 0;
 };
 constexpr KvFormat kKvBf16{false, nullptr, nullptr};
+
+KvFormat int4_format(const pa_kv_int4* p) {
+  KvFormat f{false, nullptr, nullptr, true};
+  if (p) {
+    f.k_params = static_cast<uint32_t*>(p->k_params);
+    f.v_params = static_cast<uint32_t*>(p->v_params);
+    f.params_stride = p->params_block_stride;
+  }
+  return f;
+}
+
+// Checks of a 4-bit cache.
+pa_status check_int4(const KvFormat& kv, const void* kc, const void* vc, int64_t block_stride,
+                     int H_kv, int D, int bs) {
+  if (D != 64 && D != 128) return PA_ERR_UNSUPPORTED;
+  if (!kc || !vc || !aligned16(kc) || !aligned16(vc) || !kv.k_params || !kv.v_params)
+    return PA_ERR_INVALID_ARG;
+  if (((reinterpret_cast<uintptr_t>(kv.k_params) | reinterpret_cast<uintptr_t>(kv.v_params)) & 3u))
+    return PA_ERR_INVALID_ARG;
+  if (block_stride < static_cast<int64_t>(bs) * H_kv * (D / 2) || block_stride % 16 != 0 ||
+      kv.params_stride < static_cast<int64_t>(bs) * H_kv)
+    return PA_ERR_INVALID_ARG;
+  return PA_OK;
+}
 
 pa_status check_attn_ptrs(const void* q, int64_t q_stride, const void* kc, const void* vc,
                           int64_t block_stride, const int32_t* cu, const int32_t* lens,
@@ -207,6 +236,10 @@ pa_status check_attn_ptrs(const void* q, int64_t q_stride, const void* kc, const
   if (!aligned16(q) || !aligned16(kc) || !aligned16(vc) || !aligned16(out)) return PA_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(lse) & 3u) != 0) return PA_ERR_INVALID_ARG;
   if (q_stride < static_cast<int64_t>(H) * D || q_stride % 8 != 0) return PA_ERR_INVALID_ARG;
+  if (kv.int4) {
+    const pa_status st = check_int4(kv, kc, vc, block_stride, H_kv, D, bs);
+    if (st != PA_OK) return st;
+  } else
   // Page strides are whole 16-byte units (a TMA rule): 8 bf16 or 16 e4m3 elements.
   if (block_stride < static_cast<int64_t>(bs) * H_kv * D || block_stride % (kv.fp8 ? 16 : 8) != 0)
     return PA_ERR_INVALID_ARG;
@@ -436,6 +469,7 @@ pa_status check_update(const void* key, const void* value, int64_t key_token_str
   if (dtype != PA_BF16 && dtype != PA_F16) return PA_ERR_UNSUPPORTED;
   if (head_size != 64 && head_size != 128 && head_size != 256) return PA_ERR_UNSUPPORTED;
   if (kv.fp8 && head_size != 128) return PA_ERR_UNSUPPORTED;
+  if (kv.int4 && head_size != 64 && head_size != 128) return PA_ERR_UNSUPPORTED;
   if (block_size <= 0 || block_size % 16 != 0 || block_size > 1024) return PA_ERR_BLOCK_SIZE;
   if (num_tokens == 0) return PA_OK;
   if (kv.fp8 && (!kv.k_scale || !kv.v_scale ||
@@ -450,17 +484,41 @@ pa_status check_update(const void* key, const void* value, int64_t key_token_str
   if (key_token_stride < row || value_token_stride < row || key_token_stride % 8 ||
       value_token_stride % 8)
     return PA_ERR_INVALID_ARG;
+  if (kv.int4 && row > (1 << 28)) return PA_ERR_INVALID_ARG;   // 32-bit offsets in a token's row
+  if (kv.int4)
+    return check_int4(kv, key_cache, value_cache, cache_block_stride, num_kv_heads, head_size,
+                      block_size);
   if (cache_block_stride < row * block_size || cache_block_stride % (kv.fp8 ? 16 : 8))
     return PA_ERR_INVALID_ARG;
   return PA_OK;
 }
 
-// The scatter of pa_reshape_and_cache(_fp8) for the cache format kv.
+// The scatter of pa_reshape_and_cache(_fp8, _int4) for the cache format kv.
 cudaError_t launch_scatter(const void* key, const void* value, int64_t kstride, int64_t vstride,
                            void* kc, void* vc, int64_t block_stride, const int64_t* slots,
                            int num_tokens, int H_kv, int D, int bs, int num_blocks,
                            const KvFormat& kv, int32_t* status, cudaStream_t st, int sms,
                            bool pdl, int dtype) {
+  if (kv.int4) {   // the rotation's pass, without queries and positions
+    RopeArgs a{};
+    a.k = static_cast<const uint16_t*>(key);
+    a.v = static_cast<const uint16_t*>(value);
+    a.k_stride = kstride;
+    a.v_stride = vstride;
+    a.kc = static_cast<uint8_t*>(kc);
+    a.vc = static_cast<uint8_t*>(vc);
+    a.block_stride_bytes = block_stride;
+    a.slots = slots;
+    a.k_params = kv.k_params;
+    a.v_params = kv.v_params;
+    a.params_stride = kv.params_stride;
+    a.num_tokens = num_tokens;
+    a.H_kv = H_kv;
+    a.bs = bs;
+    a.num_slots = static_cast<int64_t>(num_blocks) * bs;
+    a.status = status;
+    return launch_rope_and_cache(a, D, dtype == PA_F16, CachePool::int4, st, sms);
+  }
   if (kv.fp8)
     return launch_reshape_and_cache_fp8(key, value, kstride, vstride, kc, vc, block_stride, slots,
                                         num_tokens, H_kv, D, bs, num_blocks, kv.k_scale,
@@ -1164,18 +1222,17 @@ pa_status pa_rope_table(float* cos_sin, int table_len, int rot_dim, double base,
              : PA_ERR_CUDA;
 }
 
-pa_status pa_rope_and_cache(const pa_rope* rope, const int64_t* positions, const void* q,
-                            int64_t q_token_stride, void* q_out, int64_t q_out_token_stride,
-                            const pa_kv_update* update, void* key_cache, void* value_cache,
-                            int64_t cache_block_stride, int num_heads, int num_kv_heads,
-                            int head_size, int block_size, int num_blocks, const pa_kv_fp8* fp8,
-                            int dtype, int32_t* dev_status, void* stream) {
+static pa_status rope_impl(const pa_rope* rope, const int64_t* positions, const void* q,
+                           int64_t q_token_stride, void* q_out, int64_t q_out_token_stride,
+                           const pa_kv_update* update, void* key_cache, void* value_cache,
+                           int64_t cache_block_stride, int num_heads, int num_kv_heads,
+                           int head_size, int block_size, int num_blocks, const KvFormat& kv,
+                           int dtype, int32_t* dev_status, void* stream) {
   if (!rope || !update || num_heads <= 0) return PA_ERR_INVALID_ARG;
   // Offsets within a token's row are 32-bit.
   if (static_cast<int64_t>(num_heads) * head_size > (1 << 28) ||
       static_cast<int64_t>(num_kv_heads) * head_size > (1 << 28))
     return PA_ERR_INVALID_ARG;
-  const KvFormat kv = fp8 ? fp8_format(fp8) : kKvBf16;
   pa_status st = check_update(update->key, update->value, update->key_token_stride,
                               update->value_token_stride, key_cache, value_cache,
                               cache_block_stride, update->slot_mapping, update->num_tokens,
@@ -1222,7 +1279,7 @@ pa_status pa_rope_and_cache(const pa_rope* rope, const int64_t* positions, const
   a.q_out_stride = q_out_token_stride;
   a.kc = static_cast<uint8_t*>(key_cache);
   a.vc = static_cast<uint8_t*>(value_cache);
-  a.block_stride_bytes = cache_block_stride * (kv.fp8 ? 1 : 2);
+  a.block_stride_bytes = cache_block_stride * (kv.fp8 || kv.int4 ? 1 : 2);
   a.slots = update->slot_mapping;
   a.positions = positions;
   a.cos_sin = rope->cos_sin;
@@ -1234,16 +1291,263 @@ pa_status pa_rope_and_cache(const pa_rope* rope, const int64_t* positions, const
   a.eps = rope->norm_eps;
   a.k_scale = kv.k_scale;
   a.v_scale = kv.v_scale;
+  a.k_params = kv.k_params;
+  a.v_params = kv.v_params;
+  a.params_stride = kv.params_stride;
   a.num_tokens = T;
   a.H = num_heads;
   a.H_kv = num_kv_heads;
   a.bs = block_size;
   a.num_slots = static_cast<int64_t>(num_blocks) * block_size;
   a.status = dev_status;
-  return launch_rope_and_cache(a, head_size, dtype == PA_F16, kv.fp8,
+  return launch_rope_and_cache(a, head_size, dtype == PA_F16,
+                               kv.fp8    ? CachePool::e4m3
+                               : kv.int4 ? CachePool::int4
+                                         : CachePool::same,
                                static_cast<cudaStream_t>(stream), sms) == cudaSuccess
              ? PA_OK
              : PA_ERR_CUDA;
+}
+
+pa_status pa_rope_and_cache(const pa_rope* rope, const int64_t* positions, const void* q,
+                            int64_t q_token_stride, void* q_out, int64_t q_out_token_stride,
+                            const pa_kv_update* update, void* key_cache, void* value_cache,
+                            int64_t cache_block_stride, int num_heads, int num_kv_heads,
+                            int head_size, int block_size, int num_blocks, const pa_kv_fp8* fp8,
+                            int dtype, int32_t* dev_status, void* stream) {
+  return rope_impl(rope, positions, q, q_token_stride, q_out, q_out_token_stride, update,
+                   key_cache, value_cache, cache_block_stride, num_heads, num_kv_heads, head_size,
+                   block_size, num_blocks, fp8 ? fp8_format(fp8) : kKvBf16, dtype, dev_status,
+                   stream);
+}
+
+// ---------------------------------------------------------------- 4-bit cache
+pa_status pa_rope_and_cache_int4(const pa_rope* rope, const int64_t* positions, const void* q,
+                                 int64_t q_token_stride, void* q_out, int64_t q_out_token_stride,
+                                 const pa_kv_update* update, void* key_cache, void* value_cache,
+                                 int64_t cache_block_stride, const pa_kv_int4* int4, int num_heads,
+                                 int num_kv_heads, int head_size, int block_size, int num_blocks,
+                                 int dtype, int32_t* dev_status, void* stream) {
+  if (!int4) return PA_ERR_INVALID_ARG;
+  return rope_impl(rope, positions, q, q_token_stride, q_out, q_out_token_stride, update,
+                   key_cache, value_cache, cache_block_stride, num_heads, num_kv_heads, head_size,
+                   block_size, num_blocks, int4_format(int4), dtype, dev_status, stream);
+}
+
+pa_status pa_reshape_and_cache_int4(const void* key, const void* value, int64_t key_token_stride,
+                                    int64_t value_token_stride, void* key_cache, void* value_cache,
+                                    int64_t cache_block_stride, const pa_kv_int4* int4,
+                                    const int64_t* slot_mapping, int num_tokens, int num_kv_heads,
+                                    int head_size, int block_size, int num_blocks, int dtype,
+                                    int32_t* dev_status, void* stream) {
+  if (!int4) return PA_ERR_INVALID_ARG;
+  const KvFormat kv = int4_format(int4);
+  const pa_status st =
+      check_update(key, value, key_token_stride, value_token_stride, key_cache, value_cache,
+                   cache_block_stride, slot_mapping, num_tokens, num_kv_heads, head_size,
+                   block_size, num_blocks, dtype, kv);
+  if (st != PA_OK || num_tokens == 0) return st;
+  const int sms = query_sms(0);
+  if (sms <= 0) return PA_ERR_CUDA;
+  return launch_scatter(key, value, key_token_stride, value_token_stride, key_cache, value_cache,
+                        cache_block_stride, slot_mapping, num_tokens, num_kv_heads, head_size,
+                        block_size, num_blocks, kv, dev_status, static_cast<cudaStream_t>(stream),
+                        sms, false, dtype) == cudaSuccess
+             ? PA_OK
+             : PA_ERR_CUDA;
+}
+
+pa_status pa_gather_cache_int4(const void* key_cache, const void* value_cache,
+                               int64_t cache_block_stride, const pa_kv_int4* int4,
+                               const int64_t* slot_mapping, int num_tokens, int num_kv_heads,
+                               int head_size, int block_size, int num_blocks, void* key,
+                               void* value, int dtype, int32_t* dev_status, void* stream) {
+  if (!int4 || num_tokens < 0 || num_kv_heads <= 0 || num_blocks < 0) return PA_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(num_kv_heads) * head_size > (1 << 28)) return PA_ERR_INVALID_ARG;
+  if (dtype != PA_BF16 && dtype != PA_F16) return PA_ERR_UNSUPPORTED;
+  if (head_size != 64 && head_size != 128) return PA_ERR_UNSUPPORTED;
+  if (block_size <= 0 || block_size % 16 != 0 || block_size > 1024) return PA_ERR_BLOCK_SIZE;
+  if (num_tokens == 0) return PA_OK;
+  const KvFormat kv = int4_format(int4);
+  const pa_status st = check_int4(kv, key_cache, value_cache, cache_block_stride, num_kv_heads,
+                                  head_size, block_size);
+  if (st != PA_OK) return st;
+  if (!slot_mapping || (reinterpret_cast<uintptr_t>(slot_mapping) & 7u) != 0 || !key || !value ||
+      !aligned16(key) || !aligned16(value))
+    return PA_ERR_INVALID_ARG;
+  const int sms = query_sms(0);
+  if (sms <= 0) return PA_ERR_CUDA;
+  Int4RowsArgs a{};
+  a.kc = static_cast<const uint8_t*>(key_cache);
+  a.vc = static_cast<const uint8_t*>(value_cache);
+  a.block_stride_bytes = cache_block_stride;
+  a.k_params = kv.k_params;
+  a.v_params = kv.v_params;
+  a.params_stride = kv.params_stride;
+  a.slots = slot_mapping;
+  a.key = static_cast<uint16_t*>(key);
+  a.value = static_cast<uint16_t*>(value);
+  a.num_tokens = num_tokens;
+  a.H_kv = num_kv_heads;
+  a.bs = block_size;
+  a.num_slots = static_cast<int64_t>(num_blocks) * block_size;
+  a.status = dev_status;
+  return launch_int4_rows(a, head_size, dtype == PA_F16, static_cast<cudaStream_t>(stream), sms) ==
+                 cudaSuccess
+             ? PA_OK
+             : PA_ERR_CUDA;
+}
+
+// The kernels of a call over 4-bit pools, from host-known bounds only: decode of
+// at most 8 packed rows (nr = 1), short queries of more (nr = 2 or 4), prompts.
+struct Int4Plan {
+  bool few, some, many;
+  int nr;                // of `some`
+  PassLayout tc;         // of `many`
+  size_t parts, end;     // partial states of the decode kernels; all bytes
+  size_t part_rows;
+};
+
+static Int4Plan plan_int4(const PassDims& d) {
+  Int4Plan p{};
+  const long long rows = static_cast<long long>(d.max_q) * d.G;
+  p.few = d.G <= 8;
+  p.nr = rows <= 16 || 2 * d.G > kI4MaxRows ? 2 : 4;
+  if (d.G > 16) p.nr = 4;
+  p.some = d.max_q > 8 / d.G && kI4MaxRows / d.G > 8 / d.G;
+  p.many = rows > kI4MaxRows;
+  size_t off = 0;
+  if (p.many) {
+    p.tc = layout_pass(d, 0);
+    off = p.tc.end;
+  }
+  p.parts = align_up(off);
+  if (p.few) p.part_rows = int4_decode_part_rows(d.sms, d.H_kv, 1);
+  if (p.some) {
+    const size_t n = int4_decode_part_rows(d.sms, d.H_kv, p.nr);
+    if (n > p.part_rows) p.part_rows = n;
+  }
+  p.end = align_up(p.parts + p.part_rows * 4) + p.part_rows * d.D * 4;
+  return p;
+}
+
+static PassDims int4_dims(int num_seqs, int total_q, int max_q, int max_k, int H, int H_kv, int D,
+                          int sms) {
+  PassDims d{num_seqs, total_q, max_q, false, H / H_kv, H, H_kv, D, sms};
+  d.max_kv = max_k;
+  return d;
+}
+
+size_t pa_varlen_fwd_int4kv_workspace_size(int num_seqs, int total_q, int max_seqlen_q,
+                                           int max_seqlen_k, int num_heads, int num_kv_heads,
+                                           int head_size, int block_size, int sm_count) {
+  if (check_shape(num_seqs, total_q, max_seqlen_q, max_seqlen_k, num_heads, num_kv_heads,
+                  head_size, block_size, PA_BF16) != PA_OK ||
+      (head_size != 64 && head_size != 128) || num_heads / num_kv_heads > kTcTileRows)
+    return 0;
+  const int sms = query_sms(sm_count);
+  if (sms <= 0) return 0;
+  return plan_int4(int4_dims(num_seqs, total_q, max_seqlen_q, max_seqlen_k, num_heads,
+                             num_kv_heads, head_size, sms)).end;
+}
+
+pa_status pa_varlen_fwd_int4kv(const pa_kv_update* update, const void* q, int64_t q_token_stride,
+                               void* key_cache, void* value_cache, int64_t cache_block_stride,
+                               const int32_t* cu_seqlens_q, const int32_t* seqused_k,
+                               const int32_t* block_table, int bt_stride, int num_seqs,
+                               int total_q, int max_seqlen_q, int max_seqlen_k, int num_heads,
+                               int num_kv_heads, int head_size, int block_size, int num_blocks,
+                               float softmax_scale, int causal, const pa_kv_int4* int4,
+                               const float* sinks, void* out, float* lse, void* workspace,
+                               size_t workspace_bytes, int dtype, int32_t* dev_status,
+                               void* stream) {
+  if (!int4) return PA_ERR_INVALID_ARG;
+  const KvFormat kv = int4_format(int4);
+  pa_status st = check_shape(num_seqs, total_q, max_seqlen_q, max_seqlen_k, num_heads,
+                             num_kv_heads, head_size, block_size, dtype);
+  if (st != PA_OK) return st;
+  if (head_size > 128 || num_heads / num_kv_heads > kTcTileRows) return PA_ERR_UNSUPPORTED;
+  st = check_attn_ptrs(q, q_token_stride, key_cache, value_cache, cache_block_stride, cu_seqlens_q,
+                       seqused_k, block_table, bt_stride, num_seqs, total_q, num_blocks, num_heads,
+                       num_kv_heads, head_size, block_size, softmax_scale, causal, out, lse, kv);
+  if (st != PA_OK) return st;
+  if ((reinterpret_cast<uintptr_t>(sinks) & 3u) != 0) return PA_ERR_INVALID_ARG;
+  if (max_seqlen_k > kMaxKeys || static_cast<int64_t>(num_kv_heads) * head_size > (1 << 28) ||
+      static_cast<int64_t>(num_seqs) * num_kv_heads > 0x7fffffff)
+    return PA_ERR_INVALID_ARG;
+  CommonAttn c{q, q_token_stride, key_cache, value_cache, cache_block_stride, cu_seqlens_q,
+               seqused_k, block_table, bt_stride, num_seqs, total_q, max_seqlen_q, max_seqlen_k,
+               num_heads, num_kv_heads, head_size, block_size, num_blocks, softmax_scale,
+               dev_status, static_cast<cudaStream_t>(stream), kv, sinks, dtype};
+  st = check_kv_update(update, c, key_cache, value_cache, dtype);
+  if (st != PA_OK) return st;
+  const bool attends = num_seqs > 0 && total_q > 0;
+  const bool writes = update && update->num_tokens > 0;
+  if (!attends && !writes) return PA_OK;
+  const int sms = query_sms(0);
+  if (sms <= 0) return PA_ERR_CUDA;
+  const PassDims d = int4_dims(num_seqs, total_q, max_seqlen_q, max_seqlen_k, num_heads,
+                               num_kv_heads, head_size, sms);
+  const Int4Plan p = plan_int4(d);
+  if (attends && (!workspace || (reinterpret_cast<uintptr_t>(workspace) % kAlign) != 0 ||
+                  workspace_bytes < p.end))
+    return PA_ERR_WORKSPACE;
+  if (writes &&
+      launch_scatter(update->key, update->value, update->key_token_stride,
+                     update->value_token_stride, key_cache, value_cache, cache_block_stride,
+                     update->slot_mapping, update->num_tokens, num_kv_heads, head_size, block_size,
+                     num_blocks, kv, dev_status, c.st, sms, false, dtype) != cudaSuccess)
+    return PA_ERR_CUDA;
+  if (!attends) return PA_OK;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const long long cap = static_cast<long long>(bt_stride) * block_size;
+  const int kv_cap = cap > kMaxKeys ? kMaxKeys : static_cast<int>(cap);
+  if (p.many) return PA_ERR_UNSUPPORTED;
+  Int4DecodeArgs a{};
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_stride = q_token_stride;
+  a.kc = static_cast<const uint8_t*>(key_cache);
+  a.vc = static_cast<const uint8_t*>(value_cache);
+  a.block_stride_bytes = cache_block_stride;
+  a.k_params = kv.k_params;
+  a.v_params = kv.v_params;
+  a.params_stride = kv.params_stride;
+  a.cu = cu_seqlens_q;
+  a.seqused_k = seqused_k;
+  a.bt = block_table;
+  a.bt_stride = bt_stride;
+  a.num_seqs = num_seqs;
+  a.H = num_heads;
+  a.H_kv = num_kv_heads;
+  a.G = d.G;
+  a.bs = block_size;
+  a.bs_shift = log2_or_none(block_size);
+  a.num_blocks = num_blocks;
+  a.total_q = total_q;
+  a.max_q = max_seqlen_q;
+  a.max_k = max_seqlen_k;
+  a.kv_len_cap = kv_cap;
+  a.causal = causal;
+  a.scale_log2 = softmax_scale * 1.4426950408889634f;
+  a.sinks = sinks;
+  a.out = static_cast<uint16_t*>(out);
+  a.lse = lse;
+  a.part_lse = reinterpret_cast<float*>(ws + p.parts);
+  a.part_o = reinterpret_cast<float*>(ws + align_up(p.parts + p.part_rows * 4));
+  a.status = dev_status;
+  if (p.few) {
+    a.tokens_min = 0;
+    a.tokens_max = 8 / d.G;
+    if (launch_int4_decode(a, head_size, dtype == PA_F16, 1, sms, c.st) != cudaSuccess)
+      return PA_ERR_CUDA;
+  }
+  if (p.some) {
+    a.tokens_min = 8 / d.G;
+    a.tokens_max = kI4MaxRows / d.G;
+    if (launch_int4_decode(a, head_size, dtype == PA_F16, p.nr, sms, c.st) != cudaSuccess)
+      return PA_ERR_CUDA;
+  }
+  return PA_OK;
 }
 
 // ---------------------------------------------------------------- weights, eviction

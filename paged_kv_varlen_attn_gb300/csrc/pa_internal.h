@@ -239,6 +239,10 @@ struct RopeTableArgs {
 };
 cudaError_t launch_rope_table(float* table, RopeTableArgs& a, cudaStream_t st, int sms);
 
+// What the pools hold: elements of the activations' type, e4m3 bytes, or 4-bit
+// codes with a scale and a minimum per row (see pa.h).
+enum class CachePool { same, e4m3, int4 };
+
 // Norm, rotation and cache write of new tokens (rope.cu). Strides in
 // elements, the pools' page stride in bytes.
 struct RopeArgs {
@@ -251,7 +255,7 @@ struct RopeArgs {
   uint8_t* vc;
   int64_t block_stride_bytes;
   const int64_t* slots;
-  const int64_t* positions;
+  const int64_t* positions;       // NULL (4-bit pools only): no rotation, rot = 0
   const float* cos_sin;           // [table_len, rot]
   int table_len, rot, interleaved;
   const float* q_norm;            // [D] or NULL
@@ -259,14 +263,69 @@ struct RopeArgs {
   float eps;
   const float* k_scale;           // [H_kv], e4m3 pools only
   const float* v_scale;
-  int num_tokens, H, H_kv, bs;
+  uint32_t* k_params;             // 4-bit pools only: (scale, minimum) f16 pairs; page b,
+  uint32_t* v_params;             // head h, row r at b * params_stride + h * bs + r
+  int64_t params_stride;
+  int num_tokens, H, H_kv, bs;    // H = 0 (4-bit pools only): no queries
   int64_t num_slots;
   int32_t* status;
   // Set by the launcher: items per warp, warps per token, those of q among them.
   int items_per_warp, chunks, q_chunks;
 };
-cudaError_t launch_rope_and_cache(RopeArgs a, int D, bool f16, bool fp8, cudaStream_t st,
+cudaError_t launch_rope_and_cache(RopeArgs a, int D, bool f16, CachePool pool, cudaStream_t st,
                                   int sms);
+
+// Rows of a 4-bit cache back as values (int4_cache.cu).
+struct Int4RowsArgs {
+  const uint8_t* kc;
+  const uint8_t* vc;
+  int64_t block_stride_bytes;
+  const uint32_t* k_params;
+  const uint32_t* v_params;
+  int64_t params_stride;          // in (scale, minimum) pairs
+  const int64_t* slots;
+  uint16_t* key;                  // [num_tokens, H_kv, D]
+  uint16_t* value;
+  int num_tokens, H_kv, bs;
+  int64_t num_slots;
+  int32_t* status;
+};
+cudaError_t launch_int4_rows(const Int4RowsArgs& a, int D, bool f16, cudaStream_t st, int sms);
+
+// Decode and short queries over 4-bit pools (int4_decode.cu): the sequences
+// with tokens_min < q_len <= tokens_max, at most 8 nr packed rows each (nr: 1,
+// 2 or 4).
+constexpr int kI4MaxRows = 32;
+struct Int4DecodeArgs {
+  const uint16_t* q;
+  int64_t q_stride;
+  const uint8_t* kc;
+  const uint8_t* vc;
+  int64_t block_stride_bytes;
+  const uint32_t* k_params;       // (scale, minimum) f16 pairs: page b, head h, row r at
+  const uint32_t* v_params;       // b * params_stride + h * bs + r
+  int64_t params_stride;
+  const int32_t* cu;
+  const int32_t* seqused_k;
+  const int32_t* bt;
+  int bt_stride;
+  int num_seqs, H, H_kv, G, bs, num_blocks, total_q;
+  int bs_shift;                   // log2(bs), or -1 where bs is no power of two
+  int max_q, max_k, kv_len_cap;
+  int tokens_min, tokens_max;
+  int causal;
+  float scale_log2;               // softmax_scale * log2(e)
+  const float* sinks;             // [H] or NULL
+  uint16_t* out;                  // [total_q, H, D]
+  float* lse;                     // [H, total_q] or NULL
+  float* part_o;                  // [int4_decode_part_rows][D]
+  float* part_lse;                // [int4_decode_part_rows]
+  int32_t* status;
+  int ranges;                     // set by the launcher
+};
+size_t int4_decode_part_rows(int sms, int H_kv, int nr);
+cudaError_t launch_int4_decode(Int4DecodeArgs a, int D, bool f16, int nr, int sms,
+                               cudaStream_t st);
 
 // Eviction (evict.cu). Rows of head_size elements are row_bytes long.
 struct EvictArgs {

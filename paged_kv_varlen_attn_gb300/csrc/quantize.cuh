@@ -1,4 +1,4 @@
-// Quantization of K/V values into e4m3 pools, shared by the cache writers.
+// Quantization of K/V values into e4m3 and 4-bit pools, shared by the cache writers.
 #pragma once
 
 #include "device_common.cuh"
@@ -66,6 +66,52 @@ __device__ __forceinline__ uint2 quantize8(uint4 x, const ScaleDiv& d) {
     v[2 * k + 1] = a.y;
   }
   return quantize8(v, d);
+}
+
+// The 4-bit codes of a head's row, 8 consecutive elements per lane, LPH lanes
+// per row (see pa.h for the format and its roundings): a word of this lane's 8
+// codes, and in *params the row's f16 scale (low half) and minimum. The
+// quotient is a product with the float32 reciprocal of the rounded scale, and
+// adding 1.5 * 2^23 rounds it to the nearest integer, ties to even, into the low
+// bits of the sum; eight multiply-adds (modulo 2^32) place those, and what the
+// exponents add up to is a constant. A NaN anywhere in the row makes scale and
+// minimum NaN, hence the row's values.
+template <int LPH>
+__device__ __forceinline__ uint32_t quantize8_int4(const float (&x)[8], int lane,
+                                                   uint32_t* params) {
+  constexpr float kTop = 32752.f;   // (2 * kTop) / 15 and kTop are f16 numbers' size
+  float f[8], lo = INFINITY, hi = -INFINITY;
+  bool nan = false;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    nan |= isnan(x[k]);
+    f[k] = fminf(fmaxf(x[k], -kTop), kTop);
+    lo = fminf(lo, f[k]);
+    hi = fmaxf(hi, f[k]);
+  }
+#pragma unroll
+  for (int o = LPH / 2; o > 0; o >>= 1) {
+    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+  }
+  const uint32_t row = ((LPH == 32 ? 0u : 1u << LPH) - 1u) << (lane / LPH * LPH);
+  nan = (__ballot_sync(0xffffffffu, nan) & row) != 0;
+  const __half s = __float2half_rn(__fmul_rn(__fsub_rn(hi, lo), 1.f / 15.f));
+  const __half m = __float2half_rn(lo);
+  *params = nan ? 0x7fff7fffu
+                : static_cast<uint32_t>(__half_as_ushort(s)) |
+                      static_cast<uint32_t>(__half_as_ushort(m)) << 16;
+  const float sf = __half2float(s), mf = __half2float(m);
+  const float inv = sf > 0.f && !nan ? __frcp_rn(sf) : 0.f;
+  uint32_t w = 0;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const float q = fminf(fmaxf(__fmul_rn(__fsub_rn(f[k], mf), inv), 0.f), 15.f);
+    w += __float_as_uint(__fadd_rn(q, 12582912.f)) << (4 * (k >> 1) + 16 * (k & 1));
+  }
+  // Eight times the bits of 1.5 * 2^23, each at its shift.
+  constexpr uint32_t kBase = 0x4B400000u * 0x11111111u;
+  return w - kBase;
 }
 
 }  // namespace pa

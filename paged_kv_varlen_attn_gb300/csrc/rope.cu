@@ -125,16 +125,19 @@ __device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
 }
 
 // INTER: interleaved pairs. NORM: q or k (or both) are normed.
-template <int D, bool F16, bool FP8, bool INTER, bool NORM>
-__global__ void __launch_bounds__(32, NORM ? 28 : 32)
+template <int D, bool F16, CachePool POOL, bool INTER, bool NORM>
+__global__ void __launch_bounds__(32, NORM || POOL == CachePool::int4 ? 28 : 32)
 rope_and_cache_kernel(const __grid_constant__ RopeArgs a) {
+  constexpr bool FP8 = POOL == CachePool::e4m3, INT4 = POOL == CachePool::int4;
   constexpr int LPH = D / 8;        // lanes per head
   constexpr int HPI = 32 / LPH;     // heads per item
   const int lane = threadIdx.x;
   const int l = lane % LPH;
   const int t = static_cast<int>(blockIdx.x / static_cast<unsigned>(a.chunks));
   const int part = static_cast<int>(blockIdx.x - static_cast<unsigned>(t) * a.chunks);
-  const int64_t pos = __ldg(a.positions + t), slot = __ldg(a.slots + t);
+  // Without positions (4-bit pools only) nothing turns.
+  const int64_t pos = INT4 && !a.positions ? 0 : __ldg(a.positions + t);
+  const int64_t slot = __ldg(a.slots + t);
   // This warp's items: q items, or the k items followed by the v items.
   const bool is_q = part < a.q_chunks;
   const int nkv = (a.H_kv + HPI - 1) / HPI;
@@ -159,7 +162,7 @@ rope_and_cache_kernel(const __grid_constant__ RopeArgs a) {
       x[u] = __ldcs(reinterpret_cast<const uint4*>((v ? src_v : src) + off));
   }
   if (pos < 0) return;                       // padding token
-  if (pos >= a.table_len) {
+  if (pos >= a.table_len && !(INT4 && !a.positions)) {
     if (part == 0 && lane == 0) flag_status(a.status, PA_DEV_BAD_POSITION);
     return;
   }
@@ -210,19 +213,21 @@ rope_and_cache_kernel(const __grid_constant__ RopeArgs a) {
       for (int k = 0; k < 8; ++k) cb[k] *= wv[k];
     }
   }
-  // Where item 0's 16 (8 for e4m3) bytes of this lane go: the query row, or
+  // Where item 0's 16 (8 for e4m3, 4 for 4-bit codes) bytes of this lane go: the query row, or
   // the token's row in the pools (rows hold [H_kv, D]).
-  constexpr int OUT = FP8 ? 256 : 512;       // bytes of a k or v item in the pools
+  constexpr int OUT = INT4 ? 128 : FP8 ? 256 : 512;   // bytes of a k or v item in the pools
   uint8_t* dst;
-  int64_t crow = 0;
+  int64_t crow = 0, prow = 0;
   if (is_q) {
     dst = reinterpret_cast<uint8_t*>(a.q_out + t * a.q_out_stride) + lane * 16;
   } else {
     const int64_t page = slot / a.bs;
     crow = page * a.block_stride_bytes +
-           (slot - page * a.bs) * static_cast<int64_t>(a.H_kv * D * (FP8 ? 1 : 2)) +
-           lane * (FP8 ? 8 : 16);
+           (slot - page * a.bs) * static_cast<int64_t>(INT4 ? a.H_kv * (D / 2)
+                                                            : a.H_kv * D * (FP8 ? 1 : 2)) +
+           lane * (INT4 ? 4 : FP8 ? 8 : 16);
     dst = a.kc + crow;
+    if constexpr (INT4) prow = page * a.params_stride + (slot - page * a.bs);
   }
 
 #pragma unroll
@@ -233,7 +238,7 @@ rope_and_cache_kernel(const __grid_constant__ RopeArgs a) {
     const int at = v ? item - nkv : item;
     const bool live = at * 512 + lane * 16 < row_bytes;
     float f[8];
-    if (FP8 || !v) unpack8<F16>(x[u], f);
+    if (FP8 || INT4 || !v) unpack8<F16>(x[u], f);
     if (!v) {
       uint4 px;
       if constexpr (INTER) {
@@ -260,15 +265,34 @@ rope_and_cache_kernel(const __grid_constant__ RopeArgs a) {
       }
 #pragma unroll
       for (int k = 0; k < 8; k += 2) {
-        fmul2(f[k], f[k + 1], f[k], f[k + 1], ca[k], ca[k + 1]);
-        ffma2(f[k], f[k + 1], g[k], g[k + 1], cb[k], cb[k + 1], f[k], f[k + 1]);
+        if constexpr (INT4) {
+          // Each product is rounded, as pa.h has it (ptxas contracts a two-lane
+          // product and sum).
+          f[k] = __fadd_rn(__fmul_rn(f[k], ca[k]), __fmul_rn(g[k], cb[k]));
+          f[k + 1] = __fadd_rn(__fmul_rn(f[k + 1], ca[k + 1]), __fmul_rn(g[k + 1], cb[k + 1]));
+        } else {
+          fmul2(f[k], f[k + 1], f[k], f[k + 1], ca[k], ca[k + 1]);
+          ffma2(f[k], f[k + 1], g[k], g[k + 1], cb[k], cb[k + 1], f[k], f[k + 1]);
+        }
         if (NORM) fmul2(f[k], f[k + 1], f[k], f[k + 1], r, r);
+      }
+    }
+    if constexpr (INT4) {
+      // (All lanes: the reductions of a head are shuffles.)
+      if (!is_q) {
+        uint32_t params;
+        const uint32_t word = quantize8_int4<LPH>(f, lane, &params);
+        if (!live) continue;
+        *reinterpret_cast<uint32_t*>((v ? a.vc + crow : dst) + at * OUT) = word;
+        const int h = at * HPI + lane / LPH;
+        if (l == 0) (v ? a.v_params : a.k_params)[prow + static_cast<int64_t>(h) * a.bs] = params;
+        continue;
       }
     }
     if (!live) continue;
     // What neither the norm nor the rotation touches keeps its bits.
     const bool as_is = v || (!turns && !wt);
-    if (!FP8 || is_q) {
+    if (INT4 || !FP8 || is_q) {
       const uint4 y = as_is ? x[u] : pack8<F16>(f);
       *reinterpret_cast<uint4*>((v ? a.vc + crow : dst) + at * 512) = y;
     } else if constexpr (FP8) {
@@ -279,21 +303,21 @@ rope_and_cache_kernel(const __grid_constant__ RopeArgs a) {
   }
 }
 
-template <int D, bool F16, bool FP8>
+template <int D, bool F16, CachePool POOL>
 static cudaError_t launch_rope_d(const RopeArgs& a, unsigned grid, cudaStream_t st) {
   auto run = [&](auto kernel) {
     kernel<<<grid, 32, 0, st>>>(a);
     return cudaGetLastError();
   };
   const bool norm = a.q_norm || a.k_norm;
-  if (a.interleaved) return norm ? run(rope_and_cache_kernel<D, F16, FP8, true, true>)
-                                 : run(rope_and_cache_kernel<D, F16, FP8, true, false>);
-  return norm ? run(rope_and_cache_kernel<D, F16, FP8, false, true>)
-              : run(rope_and_cache_kernel<D, F16, FP8, false, false>);
+  if (a.interleaved) return norm ? run(rope_and_cache_kernel<D, F16, POOL, true, true>)
+                                 : run(rope_and_cache_kernel<D, F16, POOL, true, false>);
+  return norm ? run(rope_and_cache_kernel<D, F16, POOL, false, true>)
+              : run(rope_and_cache_kernel<D, F16, POOL, false, false>);
 }
 
-cudaError_t launch_rope_and_cache(RopeArgs a, int D, bool f16, bool fp8, cudaStream_t st,
-                                  int sms) {
+cudaError_t launch_rope_and_cache(RopeArgs a, int D, bool f16, CachePool pool,
+                                  cudaStream_t st, int sms) {
   if (a.num_tokens == 0) return cudaSuccess;
   const int hpi = 256 / D;
   const int q_items = (a.H + hpi - 1) / hpi, kv_items = 2 * ((a.H_kv + hpi - 1) / hpi);
@@ -308,16 +332,23 @@ cudaError_t launch_rope_and_cache(RopeArgs a, int D, bool f16, bool fp8, cudaStr
   const long long warps = static_cast<long long>(a.num_tokens) * a.chunks;
   if (warps > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   const unsigned grid = static_cast<unsigned>(warps);
-  if (fp8) return f16 ? launch_rope_d<128, true, true>(a, grid, st)
-                      : launch_rope_d<128, false, true>(a, grid, st);
-  if (f16) {
-    if (D == 256) return launch_rope_d<256, true, false>(a, grid, st);
-    if (D == 128) return launch_rope_d<128, true, false>(a, grid, st);
-    return launch_rope_d<64, true, false>(a, grid, st);
+  constexpr CachePool k16 = CachePool::same, k8 = CachePool::e4m3, k4 = CachePool::int4;
+  if (pool == k8) return f16 ? launch_rope_d<128, true, k8>(a, grid, st)
+                             : launch_rope_d<128, false, k8>(a, grid, st);
+  if (pool == k4) {
+    if (D == 128) return f16 ? launch_rope_d<128, true, k4>(a, grid, st)
+                             : launch_rope_d<128, false, k4>(a, grid, st);
+    return f16 ? launch_rope_d<64, true, k4>(a, grid, st)
+               : launch_rope_d<64, false, k4>(a, grid, st);
   }
-  if (D == 256) return launch_rope_d<256, false, false>(a, grid, st);
-  if (D == 128) return launch_rope_d<128, false, false>(a, grid, st);
-  return launch_rope_d<64, false, false>(a, grid, st);
+  if (f16) {
+    if (D == 256) return launch_rope_d<256, true, k16>(a, grid, st);
+    if (D == 128) return launch_rope_d<128, true, k16>(a, grid, st);
+    return launch_rope_d<64, true, k16>(a, grid, st);
+  }
+  if (D == 256) return launch_rope_d<256, false, k16>(a, grid, st);
+  if (D == 128) return launch_rope_d<128, false, k16>(a, grid, st);
+  return launch_rope_d<64, false, k16>(a, grid, st);
 }
 
 }  // namespace pa
