@@ -751,6 +751,43 @@ pa_status pa_varlen_fwd_int4kv(const pa_kv_update* update, const void* q, int64_
                                size_t workspace_bytes, int dtype, int32_t* dev_status,
                                void* stream);
 
+/*
+ * pa_score_fwd -- pa_varlen_fwd_ex (causal) with changed scores and masks: the
+ * query of head h at position p (p = kv_len - q_len + i) gives a key j that it
+ * sees the score
+ *   s = softmax_scale q.k_j,
+ *   s = softcap tanh(s / softcap)              (softcap > 0),
+ *   s = s - alibi_slopes[h] |p - j|            (alibi_slopes given),
+ * and it sees key j if
+ *   j >= first_key[its token]                  (first_key given: documents packed
+ *                                               into one sequence), and
+ *   j <= p, or j < prefix_lens[its sequence]   (prefix_lens given: a prefix that
+ *                                               sees itself whole).
+ * score may be NULL, its pointers too; without any, this is pa_varlen_fwd_ex. A
+ * row that sees no key gets out = 0 and lse = -inf (with a sink: lse = the sink).
+ * Pools in dtype only: opts->fp8 must be NULL (PA_ERR_UNSUPPORTED). Workspace as
+ * for pa_varlen_fwd.
+ * Key tiles in front of the first key of all of a tile's queries are not read.
+ * What a page holds past its sequence's keys, or in keys that no query of a row
+ * tile sees in front of its first key, does not matter; keys that some of its
+ * queries see must be finite in V.
+ */
+typedef struct pa_score {
+  float softcap;              /* >= 0, 0: none; 2 log2(e) softmax_scale / softcap must be finite */
+  const float* alibi_slopes;  /* device float32 [num_heads] or NULL */
+  const int32_t* prefix_lens; /* device int32 [num_seqs] or NULL; outside [0, kv_len]: clamped */
+  const int32_t* first_key;   /* device int32 [total_q] or NULL; negative: 0 */
+} pa_score;
+pa_status pa_score_fwd(const pa_kv_update* update, const void* q, int64_t q_token_stride,
+                       void* key_cache, void* value_cache, int64_t cache_block_stride,
+                       const int32_t* cu_seqlens_q, const int32_t* seqused_k,
+                       const int32_t* block_table, int bt_stride, int num_seqs, int total_q,
+                       int max_seqlen_q, int max_seqlen_k, int num_heads, int num_kv_heads,
+                       int head_size, int block_size, int num_blocks, float softmax_scale,
+                       const pa_score* score, const pa_attn_opts* opts, void* out, float* lse,
+                       void* workspace, size_t workspace_bytes, int dtype, int32_t* dev_status,
+                       void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -66,6 +66,7 @@ EXPORTS = (
     "pa_gather_cache_int4",
     "pa_varlen_fwd_int4kv_workspace_size",
     "pa_varlen_fwd_int4kv",
+    "pa_score_fwd",
 )
 
 _lib = None
@@ -107,6 +108,12 @@ class Rope(ctypes.Structure):
 class KvInt4(ctypes.Structure):
     """struct pa_kv_int4 of include/pa.h."""
     _fields_ = [("k_params", _vp), ("v_params", _vp), ("params_block_stride", _i64)]
+
+
+class Score(ctypes.Structure):
+    """struct pa_score of include/pa.h."""
+    _fields_ = [("softcap", _f32), ("alibi_slopes", _vp), ("prefix_lens", _vp),
+                ("first_key", _vp)]
 
 
 _ATTN_ARGS = [_vp, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i32,
@@ -161,6 +168,8 @@ _SIGS = {
     "pa_varlen_fwd_int4kv_workspace_size": ([_i32] * 9, _sz),
     "pa_varlen_fwd_int4kv": ([ctypes.POINTER(KvUpdate)] + _ATTN_ARGS[:20] +
                              [ctypes.POINTER(KvInt4), _vp] + _ATTN_ARGS[20:], _i32),
+    "pa_score_fwd": ([ctypes.POINTER(KvUpdate)] + _ATTN_ARGS[:19] +
+                     [ctypes.POINTER(Score), ctypes.POINTER(AttnOpts)] + _ATTN_ARGS[20:], _i32),
     "pa_cascade_fwd_fp8kv_workspace_size": ([_i32] * 9, _sz),
     "pa_varlen_fwd_fp8kv": ([ctypes.POINTER(KvUpdate)] + _ATTN_ARGS[:20] +
                             [ctypes.POINTER(KvFp8)] + _ATTN_ARGS[20:], _i32),
@@ -1072,4 +1081,60 @@ def varlen_fwd_int4kv(q, key_cache, value_cache, key_params, value_params, cu_se
           mk, H, hk, D, bs, nb, float(softmax_scale), 1 if causal else 0, ctypes.byref(desc),
           _ptr(sinks), out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.numel(), dtype,
           _ptr(dev_status))
+    return out, lse
+
+
+# ---------------------------------------------------------------------------
+# Changed scores and masks
+def _i32_vector(t, n, name):
+    if t is not None and (t.dtype != torch.int32 or t.shape != (n,) or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous int32 tensor of {n} values")
+
+
+def score_fwd(q, key_cache, value_cache, cu_seqlens_q, seqused_k, block_table, max_seqlen_q,
+              max_seqlen_k, softmax_scale, softcap=0.0, alibi_slopes=None, prefix_lens=None,
+              first_key=None, sinks=None, key=None, value=None, slot_mapping=None, out=None,
+              lse=None, return_lse=True, workspace=None, dev_status=None):
+    """Causal varlen attention whose scores are capped (softcap tanh(s / softcap))
+    and biased (alibi_slopes float32 [num_heads] times the distance, subtracted),
+    and in which a query sees no key below first_key (int32 [total_q]) and,
+    causal or not, those below its sequence's prefix_lens (int32 [num_seqs]);
+    optionally the new tokens' K/V are first scattered into the caches (key,
+    value, slot_mapping). Returns (out, lse or None)."""
+    lib = load_library()
+    mq, mk = int(max_seqlen_q), int(max_seqlen_k)
+    if (mq | mk) >> 31:
+        _fit32(mq, mk)
+    if (key is None) is not (value is None) or (key is None) is not (slot_mapping is None):
+        raise ValueError("key, value and slot_mapping go together")
+    _one_device(q, key_cache, value_cache, cu_seqlens_q, seqused_k, block_table, alibi_slopes,
+                prefix_lens, first_key, sinks, key, value, slot_mapping, out, lse, workspace,
+                dev_status)
+    (nb, bs, hk, d), page = _pools(key_cache, value_cache)
+    T, H, D = q.shape
+    S = _cu_seqlens(cu_seqlens_q)
+    bt_row = _seq_table(seqused_k, block_table, S)
+    if d != D:
+        raise ValueError("q and the caches must share the head size")
+    out, lse = _outputs(q, out, lse, return_lse)
+    _f32_vector(sinks, H, "sinks")
+    _f32_vector(alibi_slopes, H, "alibi_slopes")
+    _i32_vector(prefix_lens, S, "prefix_lens")
+    _i32_vector(first_key, T, "first_key")
+    update = None
+    if key is None:
+        dtype = _dtype_code(q, out, key_cache, value_cache)
+    else:
+        update = ctypes.byref(_new_tokens(key, value, slot_mapping, hk, D))
+        dtype = _dtype_code(q, out, key_cache, value_cache, key, value)
+    if workspace is None:
+        workspace = alloc_workspace(varlen_fwd_workspace_size(
+            S, T, mq, mk, H, hk, D, bs, _sm_count(q.device)), q.device)
+    score = Score(softcap, _ptr(alibi_slopes), _ptr(prefix_lens), _ptr(first_key))
+    opts = None if sinks is None else ctypes.byref(AttnOpts(sinks.data_ptr(), None))
+    _call(lib.pa_score_fwd, "pa_score_fwd", q.device,
+          update, q.data_ptr(), _row_stride(q), key_cache.data_ptr(), value_cache.data_ptr(), page,
+          cu_seqlens_q.data_ptr(), seqused_k.data_ptr(), block_table.data_ptr(), bt_row, S, T, mq,
+          mk, H, hk, D, bs, nb, float(softmax_scale), ctypes.byref(score), opts, out.data_ptr(),
+          _ptr(lse), workspace.data_ptr(), workspace.numel(), dtype, _ptr(dev_status))
     return out, lse

@@ -152,11 +152,14 @@ __device__ __forceinline__ void zero_v_hidden(uint8_t* vtile, int tile_key0, int
 // ---------------------------------------------------------------------------
 // WIN: keys (kv_len, kb, ke) are numbered as in geo; no query of the item sees
 // keys [a.first, win_lo).
-template <int D, int RGN, bool FP8, bool F16, bool WIN>
+// SC (changed scores and masks, always causal): every row sees the first prefix
+// keys, causal or not, and no row sees keys below win_lo.
+template <int D, int RGN, bool FP8, bool F16, bool WIN, bool SC>
 __device__ __forceinline__ void split_consumer(const AttnArgs& a, uint8_t* ring, SplitShared sh,
                                                int hk, int seg, int rt, int j, int q_start,
                                                int q_len, int kv_len, int kb, int ke, int ntiles,
-                                               int nsplit, int slot_base, int win_lo) {
+                                               int nsplit, int slot_base, int win_lo,
+                                               int prefix) {
   using C = SplitCfg<D, FP8>;
   using E = Elem<F16>;
   static_assert(!FP8 || D == 128, "FP8 pools: head size 128");
@@ -181,6 +184,8 @@ __device__ __forceinline__ void split_consumer(const AttnArgs& a, uint8_t* ring,
   int lim[2];
   bool rvalid[2];
   int tok[2], head[2];
+  int pos[2], low[2] = {0, 0};      // SC: the rows' positions, first keys, and
+  float slope[2] = {0.f, 0.f};      // biases per key of distance (base 2)
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
     const int rl = rg * 16 + gq + 8 * r;
@@ -190,6 +195,14 @@ __device__ __forceinline__ void split_consumer(const AttnArgs& a, uint8_t* ring,
     tok[r] = q_start + i;
     head[r] = hk * G + (pr - i * G);
     lim[r] = !rvalid[r] ? -1 : (a.causal ? kv_len - q_len + i : 0x7fffffff);
+    pos[r] = lim[r];
+    if constexpr (SC) {
+      if (rvalid[r]) {
+        lim[r] = max(lim[r], prefix - 1);
+        if (a.first_key) low[r] = __ldg(a.first_key + tok[r]);
+        if (a.slopes) slope[r] = __ldg(a.slopes + head[r]) * kLog2e;
+      }
+    }
   }
   int lim_max = max(lim[0], lim[1]);
 #pragma unroll
@@ -198,6 +211,13 @@ __device__ __forceinline__ void split_consumer(const AttnArgs& a, uint8_t* ring,
   int lim_min = min(rvalid[0] ? lim[0] : 0x7fffffff, rvalid[1] ? lim[1] : 0x7fffffff);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) lim_min = min(lim_min, __shfl_xor_sync(0xffffffffu, lim_min, o));
+
+  // SC: the largest first key of the warp's valid rows.
+  int low_max = 0;
+  if constexpr (SC) {
+    low_max = max(rvalid[0] ? low[0] : 0, rvalid[1] ? low[1] : 0);
+    low_max = __reduce_max_sync(0xffffffffu, low_max);
+  }
 
   // Q fragments (A operand, 16 x D), loaded once from global memory: bf16,
   // or for FP8 pools f16 in the permuted dim order of the K fragments.
@@ -247,8 +267,9 @@ __device__ __forceinline__ void split_consumer(const AttnArgs& a, uint8_t* ring,
     const int key_base = tile_key0 + slice0;
     if (key_base < ke && key_base <= lim_max) {
       zero_v_tail<KW, C::HALVES, C::HALF_BYTES>(vtile, tile_key0, slice0, kv_len, lane);
-      if constexpr (WIN)
-        zero_v_hidden<KW, C::HALVES, C::HALF_BYTES>(vtile, tile_key0, slice0, a.first, win_lo, lane);
+      if constexpr (WIN || SC)
+        zero_v_hidden<KW, C::HALVES, C::HALF_BYTES>(vtile, tile_key0, slice0, SC ? 0 : a.first,
+                                                    win_lo, lane);
 #pragma unroll
       for (int ch = 0; ch < NCH; ++ch) {
       const int cs = slice0 + ch * KWC;        // first key of the chunk in the tile
@@ -293,13 +314,23 @@ __device__ __forceinline__ void split_consumer(const AttnArgs& a, uint8_t* ring,
       // Mask, scale into the log2 domain, running max. A chunk inside every
       // valid row's visible range needs no mask.
       float mx[2] = {-INFINITY, -INFINITY};
+      // The score of a product, in base 2.
+      auto score = [&](float x, int r, int key) {
+        if constexpr (!SC) {
+          return x * sl2;
+        } else {
+          const float y = a.cap > 0.f ? capped_score(x, a.cap_in, a.cap) : x * sl2;
+          return a.slopes ? fmaf(-slope[r], fabsf(static_cast<float>(key - pos[r])), y) : y;
+        }
+      };
       if (ckey + KWC <= ke && ckey + KWC - 1 <= lim_min &&
-          (!WIN || ckey + KWC <= a.first || ckey > lim_max - a.window)) {
+          (!WIN || ckey + KWC <= a.first || ckey > lim_max - a.window) &&
+          (!SC || ckey >= low_max)) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float v = sacc[n][e] * sl2;
+            const float v = score(sacc[n][e], e >> 1, ckey + n * 8 + 2 * cq + (e & 1));
             sacc[n][e] = v;
             mx[e >> 1] = fmaxf(mx[e >> 1], v);
           }
@@ -313,7 +344,8 @@ __device__ __forceinline__ void split_consumer(const AttnArgs& a, uint8_t* ring,
           const int r = e >> 1;
           bool ok = key < ke && key <= lim[r];
           if constexpr (WIN) ok = ok && (key > lim[r] - a.window || key < a.first);
-          const float v = ok ? sacc[n][e] * sl2 : -INFINITY;
+          if constexpr (SC) ok = ok && key >= low[r];
+          const float v = ok ? score(sacc[n][e], r, key) : -INFINITY;
           sacc[n][e] = v;
           mx[r] = fmaxf(mx[r], v);
         }
@@ -920,7 +952,7 @@ __device__ __forceinline__ void split_consumer_fp8_dec(const AttnArgs& a, uint8_
   finish_group<D, F16>(a, sh, slot_base, rt, nsplit, hk, R, row0, q_start);
 }
 
-template <int D, bool FP8, bool F16, bool WIN>
+template <int D, bool FP8, bool F16, bool WIN, bool SC>
 __global__ void __launch_bounds__(SplitCfg<D, FP8>::THREADS, SplitCfg<D, FP8>::CTAS_PER_SM)
 attn_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                   const __grid_constant__ AttnArgs a) {
@@ -948,15 +980,28 @@ attn_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
   const int G = a.G;
   const int row0 = rt * kRowsSplit;
   const int R = min(kRowsSplit, q_len * G - row0);
-  const int kb = j * chunk;
+  int kb = j * chunk;
   // Sliding window: the item works on virtual keys, the sequence is len long.
   WinGeo geo{};
   if constexpr (WIN)
     geo = win_geo(kv_len, q_len, row0 / G, (row0 + R - 1) / G, a.window, a.first, a.box_rows);
   const int len = WIN ? kv_len - geo.gap : kv_len;
-  const int win_lo = geo.lo - geo.gap;
+  int win_lo = geo.lo - geo.gap;
   int ke = min(len, kb + chunk);
-  if (a.causal) {
+  int prefix = 0;
+  if constexpr (SC) {
+    if (a.prefix) prefix = min(max(__ldg(a.prefix + seg), 0), len);
+    ke = min(ke, max(len - q_len + (row0 + R - 1) / G + 1, prefix));   // (always causal)
+    if (a.first_key) {
+      // Whole tiles in front of every row's first key are left out.
+      const int lane = threadIdx.x & 31;
+      int low = 0x7fffffff;
+      for (int i = row0 / G + lane; i <= (row0 + R - 1) / G; i += 32)
+        low = min(low, __ldg(a.first_key + q_start + i));
+      win_lo = max(__reduce_min_sync(0xffffffffu, low), 0);
+      if (win_lo > kb) kb += min(win_lo - kb, max(ke - kb, 0)) / C::BN * C::BN;
+    }
+  } else if (a.causal) {
     const int i_last = (row0 + R - 1) / G;
     ke = min(ke, len - q_len + i_last + 1);
   }
@@ -990,17 +1035,17 @@ attn_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     }
   }
   if (R <= 16)
-    split_consumer<D, 1, FP8, F16, WIN>(a, ring, sh, hk, seg, rt, j, q_start, q_len, len, kb, ke,
-                                          ntiles, nsplit, slot_base, win_lo);
+    split_consumer<D, 1, FP8, F16, WIN, SC>(a, ring, sh, hk, seg, rt, j, q_start, q_len, len, kb,
+                                            ke, ntiles, nsplit, slot_base, win_lo, prefix);
   else if (R <= 32)
-    split_consumer<D, 2, FP8, F16, WIN>(a, ring, sh, hk, seg, rt, j, q_start, q_len, len, kb, ke,
-                                          ntiles, nsplit, slot_base, win_lo);
+    split_consumer<D, 2, FP8, F16, WIN, SC>(a, ring, sh, hk, seg, rt, j, q_start, q_len, len, kb,
+                                            ke, ntiles, nsplit, slot_base, win_lo, prefix);
   else
-    split_consumer<D, 4, FP8, F16, WIN>(a, ring, sh, hk, seg, rt, j, q_start, q_len, len, kb, ke,
-                                          ntiles, nsplit, slot_base, win_lo);
+    split_consumer<D, 4, FP8, F16, WIN, SC>(a, ring, sh, hk, seg, rt, j, q_start, q_len, len, kb,
+                                            ke, ntiles, nsplit, slot_base, win_lo, prefix);
 }
 
-template <int D, bool FP8, bool F16, bool WIN>
+template <int D, bool FP8, bool F16, bool WIN, bool SC = false>
 static cudaError_t launch_split_w(const CUtensorMap& tmK, const CUtensorMap& tmV,
                                   const AttnArgs& a, int items_bound, cudaStream_t st) {
   using C = SplitCfg<D, FP8>;
@@ -1014,8 +1059,8 @@ static cudaError_t launch_split_w(const CUtensorMap& tmK, const CUtensorMap& tmV
   if (e != cudaSuccess) return e;
   const bool known = dev >= 0 && dev < kMaxDevices;
   if (!known || !configured[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(attn_split_kernel<D, FP8, F16, WIN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             C::SMEM_BYTES);
+    e = cudaFuncSetAttribute(attn_split_kernel<D, FP8, F16, WIN, SC>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
     if (e != cudaSuccess) return e;
     if (known) configured[dev].store(true, std::memory_order_release);
   }
@@ -1031,7 +1076,7 @@ static cudaError_t launch_split_w(const CUtensorMap& tmK, const CUtensorMap& tmV
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, attn_split_kernel<D, FP8, F16, WIN>, tmK, tmV, a);
+  e = cudaLaunchKernelEx(&cfg, attn_split_kernel<D, FP8, F16, WIN, SC>, tmK, tmV, a);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
@@ -1039,6 +1084,8 @@ static cudaError_t launch_split_w(const CUtensorMap& tmK, const CUtensorMap& tmV
 template <int D, bool FP8, bool F16>
 static cudaError_t launch_split_d(const CUtensorMap& tmK, const CUtensorMap& tmV,
                                   const AttnArgs& a, int items_bound, cudaStream_t st) {
+  if constexpr (!FP8)   // changed scores: 2-byte pools
+    if (a.scored) return launch_split_w<D, FP8, F16, false, true>(tmK, tmV, a, items_bound, st);
   return a.window > 0 ? launch_split_w<D, FP8, F16, true>(tmK, tmV, a, items_bound, st)
                       : launch_split_w<D, FP8, F16, false>(tmK, tmV, a, items_bound, st);
 }

@@ -60,120 +60,9 @@
 
 #include <atomic>
 
-#include "device_common.cuh"
-#include "epilogue.cuh"
+#include "attn_tc.cuh"
 
 namespace pa {
-
-// Head sizes 64 and 128: two Q tiles per CTA and 128-key K/V tiles. Head
-// size 256: one Q tile (its O takes 256 TMEM columns) and 64-key K/V tiles,
-// so that two ring stages fit beside the 64 KB Q tile.
-template <int D>
-struct TcCfg {
-  static constexpr int BM = 128;         // rows per Q tile (TMEM lanes)
-  static constexpr int TILES = tc_tiles(D);   // Q tiles per CTA
-  static constexpr int BN = D > 128 ? 64 : 128;   // keys per K/V tile
-  static constexpr int HALVES = D / 64;
-  static constexpr int Q_HALF = BM * 128;
-  static constexpr int Q_TILE = HALVES * Q_HALF;
-  static constexpr int KV_HALF = BN * 128;
-  static constexpr int KV_TILE = HALVES * KV_HALF;
-  static constexpr int STAGE = 2 * KV_TILE;
-  static constexpr int STAGES = D == 64 ? 4 : 2;
-  static constexpr int OFF_Q = 0;
-  static constexpr int OFF_KV = TILES * Q_TILE;
-  static constexpr int OFF_BAR = OFF_KV + STAGES * STAGE;
-  static constexpr int SMEM_BYTES = OFF_BAR + 512 + 1024;
-  static constexpr int THREADS = 384;   // 3 warpgroups: control, softmax A, softmax B
-  static constexpr int TMEM_COLS = 512;
-  // TMEM columns: S of tile X at X*128 (P of tile X as bf16 or f16 pairs in
-  // its first BN / 2 columns); O of tile X at 256 + X*D.
-  static constexpr int O_COL = 256;
-  static constexpr float RESCALE_LOG2 = 8.0f;
-};
-// FP8 (e4m3) pools, head size 128. S = Q K^T runs on the e4m3 tensor MMA
-// (kind::f8f6f4) straight from the TMA-staged key bytes, with Q taken as two
-// e4m3 terms Qh + Ql after a power-of-two row scale (split in place, in the Q
-// tiles' own shared memory, by two converter warps); P V stays on kind::f16:
-// the converter warps widen each e4m3 V tile (exactly) into f16 tiles laid
-// out as the 2-byte kernel's TMA tiles. Shared memory: Q 64 KB (Qh and Ql of
-// tile X in its two 16 KB halves after the split), two widened V buffers
-// (64 KB: V(t + 1) is widened while the P V products of tile t still read
-// V(t)), two e4m3 stages of 32 KB, 1 KB of row scales. Measured on the 70B
-// prefill with the keys widened too (one K buffer): 831 TFLOP/s; without
-// widening the keys the converters' work halves.
-struct TcFp8 {
-  using C = TcCfg<128>;
-  static constexpr int VBUF = 2;                          // widened V buffers
-  static constexpr int OFF_VW = C::TILES * C::Q_TILE;     // widened V tiles
-  static constexpr int OFF_R8 = OFF_VW + VBUF * C::KV_TILE;   // e4m3 ring
-  static constexpr int TILE8 = C::BN * 128;               // 128 keys x 128 bytes
-  static constexpr int STAGE8 = 2 * TILE8;
-  static constexpr int STAGES8 = 2;                       // e4m3 ring stages
-  static constexpr int OFF_RS = OFF_R8 + STAGES8 * STAGE8;   // float[TILES * BM]: 2^-k per row
-  static constexpr int OFF_BAR = OFF_RS + C::TILES * C::BM * 4;
-  static constexpr int SMEM_BYTES = OFF_BAR + 512 + 1024;
-  static constexpr int CONV_THREADS = 64;                 // warps 2 and 3
-};
-static_assert(TcFp8::SMEM_BYTES <= 227 * 1024, "the FP8 layout fits shared memory");
-static_assert(kTcTileRows == TcCfg<128>::BM, "a Q tile spans the 128 TMEM lanes");
-static_assert(TcCfg<256>::SMEM_BYTES <= 227 * 1024, "head size 256 fits shared memory");
-static_assert(TcCfg<256>::O_COL + 256 <= TcCfg<256>::TMEM_COLS, "head size 256 fits TMEM");
-
-struct TcBars {
-  uint64_t q_full;
-  uint64_t kv_full[8];     // [s]: K of stage s, [STAGES + s]: V of stage s
-  uint64_t kv_empty[8];
-  uint64_t s_full[2];      // [tile]: S = Q K^T of the current key tile is in TMEM
-  uint64_t p_full[2][2];   // [half][tile]: P of keys [64 half, +64) of the tile is in TMEM
-  uint64_t pv_done[2];     // [tile]: O += P V of the current key tile completed
-  uint64_t drain;
-  // FP8 pools: Q split into e4m3 terms (64 converter arrivals); [buffer]:
-  // widened V tile ready (64 arrivals), widened V buffer free again (MMA
-  // commit). Buffer b holds tiles b, b + VBUF, ... (phase t / VBUF).
-  uint64_t q_conv, vw_full[2], vw_free[2];
-  uint32_t tmem_base;
-  volatile int abort;
-  volatile int last;
-  volatile int issued[2];    // K / V tiles issued by the producer
-  volatile int consumed[2];  // K / V tiles whose arrival the MMA issuer observed
-};
-
-// V rows past the sequence end hold arbitrary bytes: zero them so the P V
-// product (P = 0 there) cannot pick up NaN. Tile A's warps do it for key
-// tile t before they publish the first half of its P; the MMA thread issues
-// every product on V(t) -- tile A's and tile B's -- after observing that, so
-// they all see the zeros. V(t) has its own barrier and may land after S(t):
-// wait for it first, so the copy cannot overwrite the zeros. False on
-// timeout.
-// Sliding window (WIN): likewise the rows of keys [first, lo), which no query
-// of the item sees.
-template <int D, bool WIN>
-__device__ __forceinline__ bool zero_v_tail(TcBars* bars, uint8_t* smem, int t, int key0,
-                                            int kv_len, int tid, int first_key, int lo) {
-  using C = TcCfg<D>;
-  if (!mbar_wait(&bars->kv_full[C::STAGES + t % C::STAGES], (t / C::STAGES) & 1)) return false;
-  const int first = max(0, kv_len - key0);
-  uint8_t* vt = smem + C::OFF_KV + (t % C::STAGES) * C::STAGE + C::KV_TILE;
-  const int n16 = (C::BN - first) * C::HALVES * 8;
-  for (int idx = tid; idx < n16; idx += 128) {
-    const int rr = first + idx / (C::HALVES * 8);
-    const int rem = idx % (C::HALVES * 8);
-    *reinterpret_cast<uint4*>(vt + (rem >> 3) * C::KV_HALF + rr * 128 + (rem & 7) * 16) =
-        make_uint4(0, 0, 0, 0);
-  }
-  if constexpr (WIN) {
-    const int from = max(0, first_key - key0), to = min(C::BN, lo - key0);
-    for (int idx = tid; idx < (to - from) * C::HALVES * 8; idx += 128) {
-      const int rr = from + idx / (C::HALVES * 8);
-      const int rem = idx % (C::HALVES * 8);
-      *reinterpret_cast<uint4*>(vt + (rem >> 3) * C::KV_HALF + rr * 128 + (rem & 7) * 16) =
-          make_uint4(0, 0, 0, 0);
-    }
-  }
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-  return true;
-}
 
 // Widen an e4m3 K or V tile (BN keys x 128 bytes, TMA 128-byte swizzle:
 // 16-byte chunk j of row r at r*128 + ((j ^ r%8) << 4)) to f16 in the layout
@@ -285,256 +174,12 @@ __device__ __forceinline__ void q_split_e4m3(uint8_t* q, float* rs, int tiles, i
   }
 }
 
-// Bits 0 .. n - 1 (none for n <= 0, all from n = 32 on).
-__device__ __forceinline__ uint32_t below_mask(int n) {
-  return n >= 32 ? ~0u : (n <= 0 ? 0u : (1u << n) - 1u);
-}
-
-template <int D, bool F16, bool FP8, bool WIN>
-__device__ __forceinline__ void tc_softmax_tile(const AttnArgs& a, TcBars* bars, uint8_t* smem,
-                                                uint32_t tmem, int X, int q_start, int q_len,
-                                                int kv_len, int kb, int ke, int ntiles, int row0,
-                                                int R, int hk, int nsplit, int slot_base, int rt,
-                                                int j, int win_lo) {
-  using C = TcCfg<D>;
-  using E = Elem<F16>;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int quarter = warp & 3;
-  const int r = quarter * 32 + lane;              // TMEM lane
-  const int TR = tc_tile_rows(a.G);               // rows of a Q tile (whole tokens)
-  const int rl = X * TR + r;                      // row within the work item
-  const uint32_t tm_row = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-  const uint32_t s_col = X * 128, o_col = C::O_COL + X * D;   // S / P and O columns
-  const int G = a.G;
-  const bool rvalid = r < TR && rl < R;
-  const int pr = row0 + (rvalid ? rl : 0);
-  const int ti = pr / G;
-  const int tok = q_start + ti;
-  const int head = hk * G + (pr - ti * G);
-  // Last key this row may see (bottom-right causal), or the last key.
-  const int lim = !rvalid ? -1 : (a.causal ? kv_len - q_len + ti : kv_len - 1);
-  // FP8 pools: scores use the stored codes, so k_scale joins the softmax
-  // scale and v_scale the final normalisation.
-  float sl2 = FP8 ? a.scale_log2 * __ldg(a.k_scale + hk) : a.scale_log2;
-  const int tid = threadIdx.x - 128 - X * 128;     // 0..127 within the warpgroup
-  float m_use = -INFINITY, l = 0.f;
-  bool ok = true;
-  if constexpr (FP8) {
-    // S holds q 2^k . k for the row's power of two 2^k (Q entered the e4m3
-    // products as two e4m3 terms): 2^-k joins the softmax scale.
-    if (ntiles > 0) {
-      ok = mbar_wait(&bars->q_conv, 0);
-      sl2 *= reinterpret_cast<const float*>(smem + TcFp8::OFF_RS)[X * C::BM + r];
-    }
-  }
-  for (int t = 0; ok && t < ntiles; ++t) {
-    if (!mbar_wait(&bars->s_full[X], t & 1)) { ok = false; break; }
-    tc_fence_after();
-    const int key0 = kb + t * C::BN;
-    const int vis_end = min(ke, lim + 1);   // keys [key0, vis_end) are visible
-    const bool edge = key0 + C::BN > vis_end;
-    uint32_t xs_u[C::BN];
-#pragma unroll
-    for (int c = 0; c < C::BN / 32; ++c)
-      tmem_ld32(tm_row + s_col + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&xs_u[c * 32]));
-    tmem_wait_ld();
-    float* xs = reinterpret_cast<float*>(xs_u);
-    if constexpr (WIN) {
-      // Visible: keys below vis_end that are first tokens or past lim - window,
-      // as one bit per key, so that the tests of an edge tile cost an element
-      // two instructions.
-      const int win_from = max(lim - a.window + 1, 0);
-      if (edge || (key0 < win_from && key0 + C::BN > a.first)) {
-#pragma unroll
-        for (int c = 0; c < C::BN / 32; ++c) {
-          const int base = key0 + c * 32;
-          const uint32_t seen = below_mask(vis_end - base) &
-                                (below_mask(a.first - base) | ~below_mask(win_from - base));
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (!(seen & (1u << e))) xs[c * 32 + e] = -INFINITY;
-        }
-      }
-    } else if (edge) {
-#pragma unroll
-      for (int e = 0; e < C::BN; ++e)
-        if (key0 + e >= vis_end) xs[e] = -INFINITY;
-    }
-    // Row max: eight independent chains of three-input maxima over the
-    // values j, j+8, j+16, ... of the tile.
-    static_assert(C::BN % 16 == 0, "max chains take two values per step");
-    float mx8[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) mx8[j] = fmaxf(xs[j], xs[8 + j]);
-#pragma unroll
-    for (int e = 16; e < C::BN; e += 16)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) mx8[j] = fmax3(mx8[j], xs[e + j], xs[e + 8 + j]);
-    const float tmax = fmaxf(fmax3(mx8[0], mx8[1], mx8[2]),
-                             fmax3(fmax3(mx8[3], mx8[4], mx8[5]), mx8[6], mx8[7])) * sl2;
-    float m_new = m_use;
-    bool need = false;
-    if (tmax > m_use) {
-      if (m_use == -INFINITY) m_new = tmax;                 // O holds only zeros so far
-      else if (tmax - m_use > C::RESCALE_LOG2) { need = true; m_new = tmax; }
-    }
-    // O_X is final here: this tile's S was issued after the previous P V
-    // completed, and its commit covers that product.
-    if (__any_sync(0xffffffffu, need)) {
-      const float alpha = need ? fast_exp2(m_use - m_new) : 1.f;
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t v[32];
-        tmem_ld32(tm_row + o_col + c * 32, v);
-        tmem_wait_ld();
-#pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
-        tmem_st32(tm_row + o_col + c * 32, v);
-      }
-      l *= alpha;
-    }
-    m_use = m_new;
-    const float mu = m_use == -INFINITY ? 0.f : m_use;
-    // Pass 2: P = exp2(S * scale * log2(e) - m) as bf16 pairs into the first
-    // 64 columns of this tile's S region (key k -> column k / 2). Chunk c
-    // reads S columns [32c, 32c+32) and writes P columns [16c, 16c+16), which
-    // only the already-read chunks occupy.
-    // P is published in two halves (keys 0-63, then 64-127), so the tensor
-    // core multiplies the first half by V while the second is computed.
-    float ls[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int c = 0; c < C::BN / 32; ++c) {
-      uint32_t pk[16];
-#pragma unroll
-      for (int e = 0; e < 32; e += 2) {
-        // Pairs in the two-lane FMA / add: half the arithmetic instructions,
-        // the same roundings and summation order as the scalar forms. The
-        // MMA-issuing thread shares issue slots with these warps, and dense
-        // FMA streams beside it starve it (measured: a single issuing thread
-        // next to eight warps of FMA/max arithmetic issued one 128x128x16 MMA
-        // per ~220 clocks instead of 64; next to exp2-only warps, 64).
-        float y0, y1;
-        ffma2(y0, y1, xs[c * 32 + e], xs[c * 32 + e + 1], sl2, sl2, -mu, -mu);
-        const float p0 = fast_exp2(y0), p1 = fast_exp2(y1);
-        fadd2(ls[e & 7], ls[(e + 1) & 7], ls[e & 7], ls[(e + 1) & 7], p0, p1);
-        pk[e >> 1] = Elem<F16 || FP8>::pack(p0, p1);   // P has the MMA's operand type
-      }
-      tmem_st16(tm_row + s_col + c * 16, pk);
-      if (c == C::BN / 64 - 1) {   // the first half of the tile's keys
-        tmem_wait_st();
-        // warp-uniform condition and result
-        if (!FP8 && X == 0 &&
-            (key0 + C::BN > kv_len || (WIN && key0 < win_lo && key0 + C::BN > a.first)))
-          ok = __all_sync(0xffffffffu, zero_v_tail<D, WIN>(bars, smem, t, key0, kv_len, tid,
-                                                           a.first, win_lo));
-        if (!ok) break;
-        tc_fence_before();
-        mbar_arrive(&bars->p_full[0][X]);
-      }
-    }
-    if (!ok) break;
-    l += ((ls[0] + ls[1]) + (ls[2] + ls[3])) + ((ls[4] + ls[5]) + (ls[6] + ls[7]));
-    tmem_wait_st();
-    tc_fence_before();
-    mbar_arrive(&bars->p_full[1][X]);
-  }
-  if (!ok) {
-    abort_call(a);
-    bars->abort = 1;
-  }
-  // ---------------------------------------------------------- epilogue
-  ok = __all_sync(0xffffffffu, ok);   // TMEM loads below are warp-collective
-  if (ok && ntiles > 0) {
-    if (!mbar_wait(&bars->pv_done[X], (ntiles - 1) & 1)) {
-      abort_call(a);
-      bars->abort = 1;
-      ok = false;
-    }
-    ok = __all_sync(0xffffffffu, ok);
-    tc_fence_after();
-  }
-  const bool partial = nsplit > 1 || a.partials_only;
-  float mf = m_use, lf = ok ? l : 0.f, of = 1.f;
-  if (a.sinks && !partial && rvalid) of = add_sink(mf, lf, __ldg(a.sinks + head) * kLog2e);
-  const bool any = ok && lf > 0.f;
-  const float inv_l = any ? (FP8 ? __ldg(a.v_scale + hk) : 1.f) * of / lf : 0.f;
-  float lse_nat = any ? (mf + fast_log2(lf)) * kLn2 : -INFINITY;
-  const int slot = slot_base + rt * nsplit + j;
-  const int64_t srow = slot_row(a, slot, hk, rl);
-  // The output leaves through shared memory: each warp stages 32 rows x 32
-  // columns in its quarter of Q tile X (free once the last S_X product has
-  // completed, which the pv_done wait above implies) and stores them so that
-  // every instruction writes whole row segments (fp32 partial rows of 128 B,
-  // bf16 output rows of 64 B) instead of one 8- or 16-byte piece per row.
-  // 16-byte granules are XOR-swizzled by row to keep the shared-memory
-  // accesses free of bank conflicts.
-  uint8_t* stage = smem + C::OFF_Q + X * C::Q_TILE + quarter * (C::Q_TILE / 4);
-  const int rl0 = X * TR + quarter * 32;             // first row of this warp in the item
-  const int64_t srow0 = slot_row(a, slot, hk, rl0);  // rows of a slot are consecutive
-  // Rows of this warp that exist: inside the tile and inside the item.
-  const int wrows = max(0, min(TR - quarter * 32, R - rl0));
-#pragma unroll 1
-  for (int c = 0; c < D / 32; ++c) {
-    uint32_t v[32];
-    if (ntiles > 0 && ok) {
-      tmem_ld32(tm_row + o_col + c * 32, v);
-      tmem_wait_ld();
-    } else {
-#pragma unroll
-      for (int e = 0; e < 32; ++e) v[e] = 0u;
-    }
-    if (partial) {
-#pragma unroll
-      for (int g = 0; g < 8; ++g)
-        *reinterpret_cast<float4*>(stage + lane * 128 + ((g ^ (lane & 7)) << 4)) =
-            make_float4(__uint_as_float(v[4 * g]) * inv_l, __uint_as_float(v[4 * g + 1]) * inv_l,
-                        __uint_as_float(v[4 * g + 2]) * inv_l, __uint_as_float(v[4 * g + 3]) * inv_l);
-      __syncwarp();
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = i * 4 + (lane >> 3), g = lane & 7;
-        if (r < wrows)
-          __stcg(reinterpret_cast<float4*>(a.part_o + (srow0 + r) * D + c * 32 + g * 4),
-                 *reinterpret_cast<const float4*>(stage + r * 128 + ((g ^ (r & 7)) << 4)));
-      }
-    } else {
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        uint4 pk;
-        pk.x = E::pack(__uint_as_float(v[8 * g]) * inv_l, __uint_as_float(v[8 * g + 1]) * inv_l);
-        pk.y = E::pack(__uint_as_float(v[8 * g + 2]) * inv_l, __uint_as_float(v[8 * g + 3]) * inv_l);
-        pk.z = E::pack(__uint_as_float(v[8 * g + 4]) * inv_l, __uint_as_float(v[8 * g + 5]) * inv_l);
-        pk.w = E::pack(__uint_as_float(v[8 * g + 6]) * inv_l, __uint_as_float(v[8 * g + 7]) * inv_l);
-        *reinterpret_cast<uint4*>(stage + lane * 64 + ((g ^ ((lane >> 1) & 3)) << 4)) = pk;
-      }
-      __syncwarp();
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = i * 8 + (lane >> 2), g = lane & 3;
-        if (r < wrows) {
-          const int prr = row0 + rl0 + r;
-          const int tr = prr / G;
-          const int64_t ob = (static_cast<int64_t>(q_start + tr) * a.H + hk * G + (prr - tr * G)) * D;
-          *reinterpret_cast<uint4*>(a.out + ob + c * 32 + g * 8) =
-              *reinterpret_cast<const uint4*>(stage + r * 64 + ((g ^ ((r >> 1) & 3)) << 4));
-        }
-      }
-    }
-    __syncwarp();
-  }
-  if (rvalid) {
-    if (nsplit > 1 || a.partials_only) {
-      __stcg(a.part_lse + srow, lse_nat);
-    } else if (a.lse) {
-      a.lse[static_cast<int64_t>(head) * a.lse_stride + tok] = lse_nat;
-    }
-  }
-}
-
-template <int D, bool F16, bool FP8, bool WIN>
-__global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
+template <class Kind>
+__global__ void __launch_bounds__(TcCfg<Kind::D>::THREADS, 1)
 attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ AttnArgs a) {
+  constexpr int D = Kind::D;
+  constexpr bool F16 = Kind::F16, FP8 = Kind::FP8, WIN = Kind::WIN, SC = Kind::SC;
   using C = TcCfg<D>;
   static_assert(!FP8 || D == 128, "FP8 pools: head size 128");
   extern __shared__ uint8_t smem_raw[];
@@ -556,16 +201,20 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
   const int row0 = rt * C::TILES * TR;
   const int R = min(C::TILES * TR, q_len * G - row0);
   const bool two = R > TR;   // tile B has rows
-  const int kb = j * chunk;
+  int kb = j * chunk;
   // Sliding window: the item works on virtual keys, the sequence is len long.
   WinGeo geo{};
   if constexpr (WIN)
     geo = win_geo(kv_len, q_len, row0 / G, (row0 + R - 1) / G, a.window, a.first, a.box_rows);
   const int len = WIN ? kv_len - geo.gap : kv_len;
-  const int win_lo = geo.lo - geo.gap;
+  int win_lo = geo.lo - geo.gap;
   int ke = min(len, kb + chunk);
-  if (a.causal) ke = min(ke, len - q_len + (row0 + R - 1) / G + 1);
-  const int ntiles = ke > kb ? (ke - kb + C::BN - 1) / C::BN : 0;
+  const int prefix = SC && a.prefix ? min(max(__ldg(a.prefix + seg), 0), len) : 0;
+  if constexpr (SC)
+    ke = min(ke, max(len - q_len + (row0 + R - 1) / G + 1, prefix));   // (always causal)
+  else if (a.causal)
+    ke = min(ke, len - q_len + (row0 + R - 1) / G + 1);
+  int ntiles = ke > kb ? (ke - kb + C::BN - 1) / C::BN : 0;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -601,9 +250,26 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     tmem_alloc(&bars->tmem_base, C::TMEM_COLS);
     tmem_relinquish();
   }
+  if constexpr (SC) {
+    if (a.first_key && warp == 2) {
+      int low = 0x7fffffff;
+      for (int i = row0 / G + lane; i <= (row0 + R - 1) / G; i += 32)
+        low = min(low, __ldg(a.first_key + q_start + i));
+      low = __reduce_min_sync(0xffffffffu, low);
+      if (lane == 0) bars->first_key = low;
+    }
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if constexpr (SC) {
+    // Whole tiles in front of every row's first key are left out.
+    if (a.first_key) {
+      win_lo = max(bars->first_key, 0);
+      if (win_lo > kb) kb += min(win_lo - kb, max(ke - kb, 0)) / C::BN * C::BN;
+      ntiles = ke > kb ? (ke - kb + C::BN - 1) / C::BN : 0;
+    }
+  }
   const uint32_t tmem = bars->tmem_base;
   // Register split: the block is launched with 384 x 168 registers. The
   // control warpgroup (producer, MMA issuer, two idle warps) drops to 104 and
@@ -861,8 +527,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     // ------------------------------------------------------------ softmax
     const int X = (warp - 4) >> 2;   // warps 4-7: tile A, 8-11: tile B
     if (X == 0 || two)
-      tc_softmax_tile<D, F16, FP8, WIN>(a, bars, smem, tmem, X, q_start, q_len, len, kb, ke, ntiles,
-                                        row0, R, hk, nsplit, slot_base, rt, j, win_lo);
+      tc_softmax_tile<Kind>(a, bars, smem, tmem, X, q_start, q_len, len, kb, ke, ntiles, row0, R,
+                            hk, nsplit, slot_base, rt, j, win_lo, prefix);
     if (nsplit > 1 && !a.partials_only) {
       // Both warpgroups (256 threads) take part, active tile or not.
       __threadfence();
@@ -899,11 +565,12 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
   }
 }
 
-template <int D, bool F16, bool FP8, bool WIN>
-static cudaError_t launch_tc_w(const CUtensorMap& tmK, const CUtensorMap& tmV,
+template <class Kind>
+static cudaError_t launch_tc_kind(const CUtensorMap& tmK, const CUtensorMap& tmV,
                                const CUtensorMap& tmQ, const AttnArgs& a, int items_bound,
                                cudaStream_t st) {
-  using C = TcCfg<D>;
+  using C = TcCfg<Kind::D>;
+  constexpr bool FP8 = Kind::FP8;
   // The shared-memory opt-in is a per-device function attribute: set it on
   // the first launch on each device (before any stream capture), not again.
   // The flags are atomics, so first calls from several host threads are
@@ -914,7 +581,7 @@ static cudaError_t launch_tc_w(const CUtensorMap& tmK, const CUtensorMap& tmV,
   if (e != cudaSuccess) return e;
   const bool known = dev >= 0 && dev < kMaxDevices;
   if (!known || !configured[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(attn_tc_kernel<D, F16, FP8, WIN>,
+    e = cudaFuncSetAttribute(attn_tc_kernel<Kind>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                              FP8 ? TcFp8::SMEM_BYTES : C::SMEM_BYTES);
     if (e != cudaSuccess) return e;
@@ -932,7 +599,7 @@ static cudaError_t launch_tc_w(const CUtensorMap& tmK, const CUtensorMap& tmV,
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, attn_tc_kernel<D, F16, FP8, WIN>, tmK, tmV, tmQ, a);
+  e = cudaLaunchKernelEx(&cfg, attn_tc_kernel<Kind>, tmK, tmV, tmQ, a);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
@@ -941,8 +608,12 @@ template <int D, bool F16, bool FP8 = false>
 static cudaError_t launch_tc_d(const CUtensorMap& tmK, const CUtensorMap& tmV,
                                const CUtensorMap& tmQ, const AttnArgs& a, int items_bound,
                                cudaStream_t st) {
-  return a.window > 0 ? launch_tc_w<D, F16, FP8, true>(tmK, tmV, tmQ, a, items_bound, st)
-                      : launch_tc_w<D, F16, FP8, false>(tmK, tmV, tmQ, a, items_bound, st);
+  if constexpr (!FP8)   // changed scores: 2-byte pools
+    if (a.scored)
+      return launch_tc_kind<TcKind<D, F16, false, false, true>>(tmK, tmV, tmQ, a, items_bound, st);
+  return a.window > 0
+             ? launch_tc_kind<TcKind<D, F16, FP8, true>>(tmK, tmV, tmQ, a, items_bound, st)
+             : launch_tc_kind<TcKind<D, F16, FP8, false>>(tmK, tmV, tmQ, a, items_bound, st);
 }
 
 cudaError_t launch_attn_tc(const CUtensorMap& tmK, const CUtensorMap& tmV, const CUtensorMap& tmQ,

@@ -251,6 +251,17 @@ __device__ __forceinline__ float fast_log2(float x) {
   return y;
 }
 
+__device__ __forceinline__ float fast_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// cap tanh(s / cap) of a raw product x, as cap - 2 cap / (1 + 2^(x cap_in)) with
+// cap_in = 2 log2(e) softmax_scale / cap; in the base of cap.
+__device__ __forceinline__ float capped_score(float x, float cap_in, float cap) {
+  return fmaf(-2.f * cap, fast_rcp(1.f + fast_exp2(x * cap_in)), cap);
+}
+
 // Element type of Q, the bf16/f16 K/V pools and the outputs: bfloat16
 // (F16 = false) or IEEE half (F16 = true). Both are 2-byte types moved as raw
 // bits; the kernels differ only in the MMA operand type and the conversions.

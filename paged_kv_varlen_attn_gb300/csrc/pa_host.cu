@@ -618,6 +618,12 @@ size_t pa_cascade_fwd_workspace_size(int num_seqs, int total_q, int max_seqlen_q
                        num_heads, num_kv_heads, head_size, sms, false);
 }
 
+// The factor of a product in the exponential of a capped score.
+constexpr double kLog2e64 = 1.4426950408889634;
+static float score_cap_in(float scale, float cap) {
+  return static_cast<float>(2.0 * kLog2e64 * scale / cap);
+}
+
 // pa_varlen_fwd, optionally preceded by a K/V update of the same cache.
 static pa_status varlen_impl(const pa_kv_update* upd, const void* q, int64_t q_token_stride,
                              void* key_cache, void* value_cache, int64_t cache_block_stride,
@@ -628,7 +634,8 @@ static pa_status varlen_impl(const pa_kv_update* upd, const void* q, int64_t q_t
                              int causal, void* out, float* lse, void* workspace,
                              size_t workspace_bytes, int dtype, int32_t* dev_status,
                              void* stream, const KvFormat& kv, const float* sinks = nullptr,
-                             int window = 0, int num_first = 0) {
+                             int window = 0, int num_first = 0,
+                             const pa_score* score = nullptr) {
   pa_status st = check_shape(num_seqs, total_q, max_seqlen_q, max_seqlen_k, num_heads,
                              num_kv_heads, head_size, block_size, dtype);
   if (st != PA_OK) return st;
@@ -755,6 +762,14 @@ static pa_status varlen_impl(const pa_kv_update* upd, const void* q, int64_t q_t
   AttnArgs a = make_attn(c, ws, L, bt_stride, 0, causal, out, lse);
   a.window = window;
   a.first = num_first;
+  if (score) {
+    a.scored = 1;
+    a.cap = score->softcap * kLog2e64;
+    a.cap_in = score->softcap > 0.f ? score_cap_in(softmax_scale, score->softcap) : 0.f;
+    a.slopes = score->alibi_slopes;
+    a.prefix = score->prefix_lens;
+    a.first_key = score->first_key;
+  }
   bool first = true;
   return launch_pass(c, tmK, tmV, tmQ, a, ws, L, &first);
 }
@@ -1161,6 +1176,37 @@ pa_status pa_window_fwd(const pa_kv_update* update, const void* q, int64_t q_tok
                      max_seqlen_q, max_seqlen_k, num_heads, num_kv_heads, head_size, block_size,
                      num_blocks, softmax_scale, 1, out, lse, workspace, workspace_bytes, dtype,
                      dev_status, stream, kv, opts ? opts->sinks : nullptr, window, num_first);
+}
+
+// ---------------------------------------------------------------- changed scores
+pa_status pa_score_fwd(const pa_kv_update* update, const void* q, int64_t q_token_stride,
+                       void* key_cache, void* value_cache, int64_t cache_block_stride,
+                       const int32_t* cu_seqlens_q, const int32_t* seqused_k,
+                       const int32_t* block_table, int bt_stride, int num_seqs, int total_q,
+                       int max_seqlen_q, int max_seqlen_k, int num_heads, int num_kv_heads,
+                       int head_size, int block_size, int num_blocks, float softmax_scale,
+                       const pa_score* score, const pa_attn_opts* opts, void* out, float* lse,
+                       void* workspace, size_t workspace_bytes, int dtype, int32_t* dev_status,
+                       void* stream) {
+  if (opts && opts->fp8) return PA_ERR_UNSUPPORTED;
+  if (score) {
+    if (!std::isfinite(score->softcap) || score->softcap < 0.f ||
+        !std::isfinite(static_cast<float>(score->softcap * kLog2e64)))
+      return PA_ERR_INVALID_ARG;
+    if (score->softcap > 0.f && !std::isfinite(score_cap_in(softmax_scale, score->softcap)))
+      return PA_ERR_INVALID_ARG;
+    if (((reinterpret_cast<uintptr_t>(score->alibi_slopes) |
+          reinterpret_cast<uintptr_t>(score->prefix_lens) |
+          reinterpret_cast<uintptr_t>(score->first_key)) & 3u) != 0)
+      return PA_ERR_INVALID_ARG;
+    if (score->softcap == 0.f && !score->alibi_slopes && !score->prefix_lens && !score->first_key)
+      score = nullptr;
+  }
+  return varlen_impl(update, q, q_token_stride, key_cache, value_cache, cache_block_stride,
+                     cu_seqlens_q, seqused_k, block_table, bt_stride, num_seqs, total_q,
+                     max_seqlen_q, max_seqlen_k, num_heads, num_kv_heads, head_size, block_size,
+                     num_blocks, softmax_scale, 1, out, lse, workspace, workspace_bytes, dtype,
+                     dev_status, stream, kKvBf16, opts ? opts->sinks : nullptr, 0, 0, score);
 }
 
 // ---------------------------------------------------------------- rotary positions

@@ -149,6 +149,15 @@ struct AttnArgs {
   // Sliding window: a query at position p sees key j <= p if j > p - window or
   // j < first. window = 0: none (the kernels' plain instantiations).
   int window, first;
+  // Changed scores and masks (scored = 1; 2-byte pools): cap and cap_in (base 2
+  // and 2 log2(e) softmax_scale / cap; cap = 0: none), a bias of slope x distance
+  // per query head, each sequence's bidirectional prefix, each query's first key
+  // (NULL: none).
+  int scored;
+  float cap, cap_in;
+  const float* slopes;
+  const int32_t* prefix;
+  const int32_t* first_key;
   // Launch order inside one call. The kernels after the planner are launched
   // as programmatic dependents of the kernel before them, so a grid can start
   // while its predecessor drains. pdl_first = 1 for the first kernel after the
