@@ -327,6 +327,17 @@ __device__ __forceinline__ void tc_softmax_tile(const AttnArgs& a, TcBars* bars,
     }
     m_use = m_new;
     const float mu = m_use == -INFINITY ? 0.f : m_use;
+    // Scores whose unit in the last place is no longer small (past 2^20): the
+    // product below, unrounded, would differ from the rounded maximum by more
+    // than an exponent can be, so it is rounded first.
+    float factor = sl2;
+    if constexpr (I4) {
+      if (__any_sync(0xffffffffu, fabsf(mu) > 0x1p20f)) {
+#pragma unroll
+        for (int e = 0; e < C::BN; ++e) xs[e] *= sl2;
+        factor = 1.f;
+      }
+    }
     // Pass 2: P = exp2(S * scale * log2(e) - m) as bf16 pairs into the first
     // 64 columns of this tile's S region (key k -> column k / 2). Chunk c
     // reads S columns [32c, 32c+32) and writes P columns [16c, 16c+16), which
@@ -349,7 +360,7 @@ __device__ __forceinline__ void tc_softmax_tile(const AttnArgs& a, TcBars* bars,
         if constexpr (SC)
           fadd2(y0, y1, xs[c * 32 + e], xs[c * 32 + e + 1], -mu, -mu);
         else
-          ffma2(y0, y1, xs[c * 32 + e], xs[c * 32 + e + 1], sl2, sl2, -mu, -mu);
+          ffma2(y0, y1, xs[c * 32 + e], xs[c * 32 + e + 1], factor, factor, -mu, -mu);
         const float p0 = fast_exp2(y0), p1 = fast_exp2(y1);
         fadd2(ls[e & 7], ls[(e + 1) & 7], ls[e & 7], ls[(e + 1) & 7], p0, p1);
         pk[e >> 1] = Elem<F16 || Kind::WIDE>::pack(p0, p1);   // P has the MMA's operand type

@@ -1,0 +1,409 @@
+// Attention over 4-bit pools for prompts: the tensor-core prefill kernel of
+// attn_tc.cu with K and V widened to f16 on the way.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+
+#include "attn_tc.cuh"
+
+namespace pa {
+
+// ---------------------------------------------------------------------------
+// Work items, softmax, products and epilogue are the prefill kernel's. What
+// differs is how K, V and Q reach the products:
+//  * Warps 0, 2 and 3 of the control warpgroup widen. A unit is 16 keys of K or
+//    V; warp w of them takes every third one, in the order K(0), V(0), K(1), ...
+//    of key tiles. It copies its units' codes, scales and minima ahead of their
+//    use into a ring of its own (a lane copies what it reads back itself, but for
+//    the scales), so no barrier stands between the pools and the registers.
+//  * A code n becomes the f16 number n exactly (n or 16 n in the low mantissa bits
+//    of 1024, then one subtraction or multiply-add), and n scale + minimum is one
+//    f16 multiply-add: the one rounding, at most half a step of the value. Rows
+//    past the sequence are zeros.
+//  * The widened tiles have the 2-byte kernel's layout (128-byte swizzle), two
+//    buffers each for K and V; the products that read a buffer free it.
+//  * Q is taken as f16 after a power-of-two row scale, in place, by the same
+//    warps, once per item; 2^-k joins the softmax scale. The sign of a negative
+//    softmax scale goes into Q, so the row maximum of the raw products serves
+//    every scale.
+// ---------------------------------------------------------------------------
+
+// A unit's piece, 32 codes (16 bytes, row r), as 64 bytes of f16: chunks c0 .. c0
+// + 3 of row r of a 128-byte swizzled tile.
+__device__ __forceinline__ void widen_int4_piece(const uint4& x, uint32_t params, uint8_t* dst,
+                                                 int r, int c0) {
+  const __half2 s = __half2half2(__ushort_as_half(static_cast<unsigned short>(params & 0xffffu)));
+  const __half2 m = __half2half2(__ushort_as_half(static_cast<unsigned short>(params >> 16)));
+  const __half2 k1024 = __half2half2(__ushort_as_half(0x6400));
+  const __half2 k16th = __half2half2(__ushort_as_half(0x2C00));
+  const __half2 k64 = __half2half2(__ushort_as_half(0xD400));   // -1024 / 16
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    uint32_t y[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t t = w[v] >> (8 * (k >> 1));
+      uint32_t h = (t & ((k & 1) ? 0x00F000F0u : 0x000F000Fu)) | 0x64006400u;
+      __half2 n = *reinterpret_cast<__half2*>(&h);
+      n = (k & 1) ? __hfma2(n, k16th, k64) : __hsub2(n, k1024);
+      n = __hfma2(n, s, m);
+      y[k] = *reinterpret_cast<uint32_t*>(&n);
+    }
+    *reinterpret_cast<uint4*>(dst + r * 128 + (((c0 + v) ^ (r & 7)) << 4)) =
+        make_uint4(y[0], y[1], y[2], y[3]);
+  }
+}
+
+// The Q tiles in place: row r of tile X times +-2^k, as f16, with 2^k bringing
+// the row's largest |q| to [2^14, 2^15); 2^-k goes to rs[X * 128 + r]. sign: of the
+// softmax scale (0: the row becomes zeros).
+template <int D, bool F16>
+__device__ __forceinline__ void q_to_f16(uint8_t* q, float* rs, int tiles, float sign, int ct,
+                                         int threads) {
+  using C = TcCfg<D>;
+  for (int row = ct; row < tiles * C::BM; row += threads) {
+    uint8_t* p = q + row / C::BM * C::Q_TILE + row % C::BM * 128;
+    const int sw = row & 7;
+    float top = 0.f;
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c) {
+      const uint4 x = *reinterpret_cast<const uint4*>(p + (c >> 3) * C::Q_HALF +
+                                                      (((c & 7) ^ sw) << 4));
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 f = Elem<F16>::unpack(w[k]);
+        top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+      }
+    }
+    const int ex = static_cast<int>(__float_as_uint(top) >> 23);
+    const int up = ex == 255 ? 0 : min(126, 141 - ex);
+    const float by = sign * __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+    rs[row] = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c) {
+      uint4* at = reinterpret_cast<uint4*>(p + (c >> 3) * C::Q_HALF + (((c & 7) ^ sw) << 4));
+      const uint4 x = *at;
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+      uint32_t y[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 f = Elem<F16>::unpack(w[k]);
+        y[k] = pack_f16(f.x * by, f.y * by);
+      }
+      *at = make_uint4(y[0], y[1], y[2], y[3]);
+    }
+  }
+}
+
+template <int D, bool F16>
+__global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
+int4_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ AttnArgs a,
+                   const __grid_constant__ Int4Pools pool) {
+  using C = TcCfg<D>;
+  using I = TcI4<D>;
+  using Kind = TcKind<D, F16, false, false, false, true>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  TcBars* bars = reinterpret_cast<TcBars*>(smem + I::OFF_BAR);
+
+  pdl_enter(a.pdl_first);
+  if (static_cast<int>(blockIdx.x) >= a.header[1] || call_aborted(a)) return;
+  const int hk = blockIdx.y;
+  const int4 it = a.items[blockIdx.x];
+  const int seg = it.x, rt = it.y, j = it.z;
+  const int4 sg = a.seg[seg];
+  const int4 sp = a.segsplit[seg];
+  const int q_start = sg.x, q_len = sg.y, kv_len = sg.z;
+  const int nsplit = sp.x, slot_base = sp.y, chunk = sp.z;
+  const int G = a.G;
+  const int TR = tc_tile_rows(G);
+  const int row0 = rt * C::TILES * TR;
+  const int R = min(C::TILES * TR, q_len * G - row0);
+  const bool two = R > TR;
+  const int kb = j * chunk;
+  int ke = min(kv_len, kb + chunk);
+  if (a.causal) ke = min(ke, kv_len - q_len + (row0 + R - 1) / G + 1);
+  const int ntiles = ke > kb ? (ke - kb + C::BN - 1) / C::BN : 0;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    mbar_init(&bars->q_full, 1);
+    mbar_init(&bars->q_conv, I::WARPS * 32);
+    for (int b = 0; b < I::BUFS; ++b) {
+      mbar_init(&bars->kw_full[b], I::UNITS);
+      mbar_init(&bars->vw_full[b], I::UNITS);
+      mbar_init(&bars->kw_free[b], 1);
+      mbar_init(&bars->vw_free[b], 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&bars->s_full[x], 1);
+      mbar_init(&bars->p_full[0][x], 128);
+      mbar_init(&bars->p_full[1][x], 128);
+      mbar_init(&bars->pv_done[x], 1);
+    }
+    mbar_init(&bars->drain, 1);
+    bars->abort = 0;
+    bars->last = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&bars->tmem_base, C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+  // The register split of the prefill kernel (384 x 168).
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;" ::: "memory");
+    if (warp == 1) {
+      // ---------------------------------------------------------- MMA issuer
+      if (lane == 0 && ntiles > 0) {
+        constexpr uint32_t fmt = Elem<true>::kTcFormat;
+        constexpr uint32_t idesc_s = mma_idesc(C::BM, C::BN, false, fmt);
+        constexpr uint32_t idesc_o = mma_idesc(C::BM, D, true, fmt);
+        constexpr int kStep = C::KV_TILE >> 4;
+        const uint64_t qdesc[2] = {smem_desc_sw128(smem_u32(smem + C::OFF_Q), 16, 1024),
+                                   smem_desc_sw128(smem_u32(smem + C::OFF_Q + C::Q_TILE), 16, 1024)};
+        const uint64_t kdesc0 = smem_desc_sw128(smem_u32(smem + I::OFF_KW), 16, 1024);
+        const uint64_t vdesc0 = smem_desc_sw128(smem_u32(smem + I::OFF_VW), C::KV_HALF, 1024);
+        auto issue_s = [&](int x, int t) {
+          tc_fence_after();
+          const uint64_t qd = qdesc[x];
+          const uint64_t kd = kdesc0 + static_cast<uint32_t>((t & 1) * kStep);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = ((kk >> 2) * C::Q_HALF + (kk & 3) * 32) >> 4;
+            const uint32_t offk = ((kk >> 2) * C::KV_HALF + (kk & 3) * 32) >> 4;
+            tc_mma(tmem + x * 128, qd + off, kd + offk, idesc_s, kk > 0);
+          }
+          tc_commit(&bars->s_full[x]);
+        };
+        auto issue_pv = [&](int x, int t, int h) {
+          tc_fence_after();
+          const uint64_t vd = vdesc0 + static_cast<uint32_t>((t & 1) * kStep);
+#pragma unroll
+          for (int k4 = 0; k4 < C::BN / 32; ++k4) {
+            const int kk = h * (C::BN / 32) + k4;
+            tc_mma_ts(tmem + C::O_COL + x * D, tmem + x * 128 + kk * 8, vd + ((kk * 16 * 128) >> 4),
+                      idesc_o, (t > 0 || kk > 0) ? 1 : 0);
+          }
+          if (h == 1) tc_commit(&bars->pv_done[x]);
+        };
+        static_assert(I::BUFS == 2, "buffer t & 1, phase t >> 1");
+        bool ok = mbar_wait(&bars->q_conv, 0) && mbar_wait(&bars->kw_full[0], 0);
+        if (ok) {
+          issue_s(0, 0);
+          if (two) issue_s(1, 0);
+          tc_commit(&bars->kw_free[0]);
+        }
+        // The order of the prefill kernel: P_A V, S_A(next), P_B V, S_B(next).
+        for (int t = 0; ok && t < ntiles; ++t) {
+          if (bars->abort) { ok = false; break; }
+          const bool more = t + 1 < ntiles;
+          if (!(ok = mbar_wait(&bars->p_full[0][0], t & 1))) break;
+          if (!(ok = mbar_wait(&bars->vw_full[t & 1], (t >> 1) & 1))) break;
+          issue_pv(0, t, 0);
+          if (!(ok = mbar_wait(&bars->p_full[1][0], t & 1))) break;
+          issue_pv(0, t, 1);
+          if (more) {
+            if (!(ok = mbar_wait(&bars->kw_full[(t + 1) & 1], ((t + 1) >> 1) & 1))) break;
+            issue_s(0, t + 1);
+          }
+          if (two) {
+            if (!(ok = mbar_wait(&bars->p_full[0][1], t & 1))) break;
+            issue_pv(1, t, 0);
+            if (!(ok = mbar_wait(&bars->p_full[1][1], t & 1))) break;
+            issue_pv(1, t, 1);
+          }
+          tc_commit(&bars->vw_free[t & 1]);
+          if (more) {
+            if (two) issue_s(1, t + 1);
+            tc_commit(&bars->kw_free[(t + 1) & 1]);
+          }
+        }
+        if (!ok) {
+          abort_call(a);
+          bars->abort = 1;
+        }
+        tc_commit(&bars->drain);
+        mbar_wait(&bars->drain, 0);
+      }
+    } else if (ntiles > 0) {
+      // ---------------------------------------------------------- widening warps
+      const int cw = warp == 0 ? 0 : warp - 1;           // 0 .. 2
+      if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&tmQ);
+        const int token0 = q_start + row0 / G;
+        mbar_arrive_expect_tx(&bars->q_full, (two ? 2 : 1) * C::HALVES * TR * 128);
+        for (int x = 0; x < (two ? 2 : 1); ++x)
+          for (int h = 0; h < C::HALVES; ++h)
+            tma_load_3d(smem + C::OFF_Q + x * C::Q_TILE + h * C::Q_HALF, &tmQ, &bars->q_full,
+                        h * 64, hk * G, token0 + x * (TR / G));
+      }
+      // Unit u of the item: tile u / (2 UNITS), K then V, 16 keys each. This
+      // warp's i-th unit is 3 i + cw. Lane i holds the page and row of the i-th
+      // unit from page0 on.
+      constexpr int PIECES = D / 32;                     // of a row, 16 bytes each
+      constexpr int PER = 16 * PIECES / 32;              // pieces per lane (2 or 1)
+      const int n_units = ntiles * 2 * I::UNITS;
+      const int mine = n_units > cw ? (n_units - cw + I::WARPS - 1) / I::WARPS : 0;
+      const int32_t* bt_row = a.bt + static_cast<int64_t>(seg) * a.bt_row_stride;
+      const int64_t rstep = static_cast<int64_t>(a.H_kv) * (D / 2);
+      const int px = lane % PIECES, pr = lane / PIECES;  // piece, first row
+      uint8_t* ring = smem + I::OFF_RING + cw * (I::SLOTS * I::SLOT);
+      const uint32_t ring_at = smem_u32(ring);
+      auto unit_key = [&](int i) {
+        const int u = I::WARPS * i + cw;
+        return kb + u / (2 * I::UNITS) * C::BN + u % I::UNITS * 16;
+      };
+      int page0 = 0, page_l = -1, row_l = 0;
+      auto load_pages = [&](int i0) {
+        page0 = i0;
+        page_l = -1;
+        row_l = 0;
+        const int key0 = unit_key(i0 + lane);
+        if (i0 + lane < mine && key0 < kv_len) {
+          const int lp = key0 / a.bs;
+          row_l = key0 - lp * a.bs;
+          page_l = __ldg(bt_row + lp);
+          if (page_l < 0 || page_l >= a.num_blocks) {
+            page_l = -1;                                 // reads as zeros
+            flag_status(a.status, PA_DEV_BAD_PAGE);
+          }
+        }
+      };
+      auto fetch = [&](int i) {
+        if (i < mine) {
+          if (i - page0 == 32) load_pages(i);
+          const int page = __shfl_sync(0xffffffffu, page_l, i - page0);
+          const int prow = __shfl_sync(0xffffffffu, row_l, i - page0);
+          const bool in = page >= 0;
+          const bool is_v = (I::WARPS * i + cw) / I::UNITS & 1;
+          const int key0 = unit_key(i);
+          const uint32_t dst = ring_at + i % I::SLOTS * I::SLOT;
+          const uint8_t* src = (is_v ? pool.vc : pool.kc) + max(page, 0) * pool.block_stride_bytes +
+                               hk * (D / 2) + (prow + pr) * rstep + px * 16;
+#pragma unroll
+          for (int x = 0; x < PER; ++x)
+            cp_async16(dst + x * 512 + lane * 16, src + x * (32 / PIECES) * rstep, in);
+          if (lane < 16)
+            cp_async4(dst + 16 * D / 2 + lane * 4,
+                      (is_v ? pool.v_params : pool.k_params) + max(page, 0) * pool.params_stride +
+                          static_cast<int64_t>(hk) * a.bs + prow + lane,
+                      in && key0 + lane < kv_len);
+        }
+        cp_async_commit();
+      };
+      load_pages(0);
+      for (int i = 0; i < I::SLOTS - 1; ++i) fetch(i);
+      bool ok = mbar_wait(&bars->q_full, 0);
+      if (ok) {
+        const float sign = a.scale_log2 > 0.f ? 1.f : a.scale_log2 < 0.f ? -1.f : 0.f;
+        q_to_f16<D, F16>(smem + C::OFF_Q, reinterpret_cast<float*>(smem + I::OFF_RS), two ? 2 : 1,
+                         sign, cw * 32 + lane, I::WARPS * 32);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        mbar_arrive(&bars->q_conv);
+      }
+      ok = __all_sync(0xffffffffu, ok);
+      for (int i = 0; ok && i < mine; ++i) {
+        fetch(i + I::SLOTS - 1);
+        const int u = I::WARPS * i + cw;
+        const int t = u / (2 * I::UNITS), buf = t & 1;
+        const bool is_v = u / I::UNITS & 1;
+        // The buffer's last reader: the products of tile t - 2.
+        if (t >= I::BUFS)
+          ok = mbar_wait(is_v ? &bars->vw_free[buf] : &bars->kw_free[buf], ((t >> 1) - 1) & 1);
+        ok = __all_sync(0xffffffffu, ok && !bars->abort);
+        if (!ok) break;
+        cp_async_wait<I::SLOTS - 1>();
+        __syncwarp();
+        const uint8_t* sl = ring + i % I::SLOTS * I::SLOT;
+        uint8_t* dst = smem + (is_v ? I::OFF_VW : I::OFF_KW) + buf * C::KV_TILE;
+        const uint32_t* par = reinterpret_cast<const uint32_t*>(sl + 16 * D / 2);
+#pragma unroll
+        for (int x = 0; x < PER; ++x) {
+          const int r = pr + x * (32 / PIECES);          // of the unit's 16
+          const uint4 w = *reinterpret_cast<const uint4*>(sl + x * 512 + lane * 16);
+          widen_int4_piece(w, par[r], dst + (px >> 1) * C::KV_HALF, u % I::UNITS * 16 + r,
+                           (px & 1) * 4);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(is_v ? &bars->vw_full[buf] : &bars->kw_full[buf]);
+      }
+      cp_async_wait<0>();
+      if (!ok) {
+        abort_call(a);
+        bars->abort = 1;
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;" ::: "memory");
+    const int X = (warp - 4) >> 2;
+    if (X == 0 || two)
+      tc_softmax_tile<Kind>(a, bars, smem, tmem, X, q_start, q_len, kv_len, kb, ke, ntiles, row0, R,
+                            hk, nsplit, slot_base, rt, j, 0);
+    if (nsplit > 1) {
+      __threadfence();
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      const int grp = slot_base + rt * nsplit;
+      int* counter = a.counters + static_cast<int64_t>(grp) * a.H_kv + hk;
+      const int tid = threadIdx.x - 128;
+      if (tid == 0) bars->last = (atomicAdd(counter, 1) == nsplit - 1) ? 1 : 0;
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (bars->last) {
+        __threadfence();
+        combine_splits<D, F16>(a, grp, nsplit, hk, R, row0, q_start, tid, 256);
+        if (tid == 0) *counter = 0;
+      }
+    }
+  }
+
+  // ---------------------------------------------------------------- teardown
+  tc_fence_before();
+  __syncthreads();
+  // After an abort: Q's copy may still be in flight.
+  if (threadIdx.x == 0 && bars->abort && ntiles > 0) mbar_wait(&bars->q_full, 0);
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+template <int D, bool F16>
+static cudaError_t launch_int4_prompt_d(const CUtensorMap& tmQ, const AttnArgs& a,
+                                        const Int4Pools& pool, int items_bound, cudaStream_t st) {
+  static std::atomic<bool> configured[kMaxDevices];
+  cudaError_t e = opt_in_smem(int4_prompt_kernel<D, F16>, TcI4<D>::SMEM_BYTES, configured);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(items_bound + 1, a.H_kv);   // (one column more: see pdl_enter)
+  cfg.blockDim = dim3(TcCfg<D>::THREADS);
+  cfg.dynamicSmemBytes = TcI4<D>::SMEM_BYTES;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, int4_prompt_kernel<D, F16>, tmQ, a, pool);
+  return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+cudaError_t launch_int4_prompt(const CUtensorMap& tmQ, const AttnArgs& a, const Int4Pools& pool,
+                               int items_bound, cudaStream_t st) {
+  if (a.D == 128)
+    return a.f16 ? launch_int4_prompt_d<128, true>(tmQ, a, pool, items_bound, st)
+                 : launch_int4_prompt_d<128, false>(tmQ, a, pool, items_bound, st);
+  return a.f16 ? launch_int4_prompt_d<64, true>(tmQ, a, pool, items_bound, st)
+               : launch_int4_prompt_d<64, false>(tmQ, a, pool, items_bound, st);
+}
+
+}  // namespace pa

@@ -1548,7 +1548,26 @@ pa_status pa_varlen_fwd_int4kv(const pa_kv_update* update, const void* q, int64_
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const long long cap = static_cast<long long>(bt_stride) * block_size;
   const int kv_cap = cap > kMaxKeys ? kMaxKeys : static_cast<int>(cap);
-  if (p.many) return PA_ERR_UNSUPPORTED;
+  if (p.many) {
+    CUtensorMap tmQ;
+    if (!encode_q_map(&tmQ, q, head_size, num_heads, total_q, q_token_stride, d.G,
+                      dtype == PA_F16))
+      return PA_ERR_CUDA;
+    PlanPasses pp{};
+    pp.p[0] = make_plan(c, ws, p.tc, 0, 0, 0, kv_cap, causal, 0);
+    if (launch_plan(pp, 1, c.st) != cudaSuccess) return PA_ERR_CUDA;
+    AttnArgs t = make_attn(c, ws, p.tc, bt_stride, 0, causal, out, lse);
+    set_class(t, ws, p.tc, 1);
+    t.pdl_first = 1;
+    const Int4Pools pools{static_cast<const uint8_t*>(key_cache),
+                          static_cast<const uint8_t*>(value_cache),
+                          cache_block_stride,
+                          kv.k_params,
+                          kv.v_params,
+                          kv.params_stride};
+    if (launch_int4_prompt(tmQ, t, pools, p.tc.items_bound[1], c.st) != cudaSuccess)
+      return PA_ERR_CUDA;
+  }
   Int4DecodeArgs a{};
   a.q = static_cast<const uint16_t*>(q);
   a.q_stride = q_token_stride;

@@ -332,6 +332,17 @@ struct Int4DecodeArgs {
   int32_t* status;
   int ranges;                     // set by the launcher
 };
+// 4-bit pools of the prompt kernel (int4_prompt.cu).
+struct Int4Pools {
+  const uint8_t* kc;
+  const uint8_t* vc;
+  int64_t block_stride_bytes;
+  const uint32_t* k_params;
+  const uint32_t* v_params;
+  int64_t params_stride;
+};
+cudaError_t launch_int4_prompt(const CUtensorMap& tmQ, const AttnArgs& a, const Int4Pools& pool,
+                               int items_bound, cudaStream_t st);
 size_t int4_decode_part_rows(int sms, int H_kv, int nr);
 cudaError_t launch_int4_decode(Int4DecodeArgs a, int D, bool f16, int nr, int sms,
                                cudaStream_t st);

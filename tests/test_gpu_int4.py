@@ -394,3 +394,110 @@ def test_update_in_the_call():
     assert torch.equal(out, out2) and torch.equal(lse, lse2)
     for x, y in zip(one, pools):
         assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
+LONG = [
+    # Prompts, chunks and mixed batches (more than 32 packed rows somewhere).
+    ([(33, 33)], 1, 1, 64, 16, "f16"),
+    ([(100, 100), (1, 1), (17, 9)], 8, 2, 128, 16, "bf16"),
+    ([(300, 300), (129, 40), (0, 20)], 6, 2, 128, 48, "f16"),               # G = 3
+    ([(700, 130), (515, 1), (64, 64), (40, 3), (90, 0)], 16, 4, 64, 32, "bf16"),
+    ([(260, 260)], 8, 8, 128, 64, "bf16"),                                  # a KV head per head
+    ([(400, 7)], 40, 1, 128, 128, "f16"),                                   # G = 40
+    ([(3000, 50), (2500, 33)], 8, 2, 128, 16, "bf16"),                      # split over the keys
+    ([(128, 128), (256, 129)], 32, 4, 64, 16, "f16"),
+]
+
+
+@pytest.mark.parametrize("seqs,H,hk,D,bs,dt", LONG)
+def test_prompts(seqs, H, hk, D, bs, dt):
+    b = Batch(seqs, H, hk, D, bs, dt, seed=len(seqs) + D + bs)
+    out, lse = b.run()
+    b.check(out, lse)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+def test_prompts_not_causal_sinks_scales(dt):
+    b = Batch([(200, 70), (20, 50)], 8, 2, 128, 16, dt, seed=23)
+    sinks = torch.randn(8)
+    for scale in (b.scale, -0.2, 0.0):
+        for causal in (True, False):
+            out, lse = b.run(causal, scale, sinks=sinks.to(DEV))
+            b.check(out, lse, causal, scale, sinks)
+
+
+def test_prompts_large_and_small_numbers():
+    b = Batch([(150, 100)], 4, 2, 128, 16, "bf16", seed=28, spread=1.0)
+    b.q[:30] *= 1e30
+    b.q[30:60] *= 1e-30
+    b.q[60] = 0
+    out, lse = b.run(scale=1e-3)
+    b.check(out, lse, scale=1e-3)
+
+
+def test_prompt_bad_pages():
+    b = Batch([(300, 60)], 4, 2, 128, 16, "f16", seed=29)
+    b.table[0, 3] = 10 ** 6
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out, lse = b.run(dev_status=status)
+    assert status.item() == pa.PA_DEV_BAD_PAGE
+    b.codes = [torch.cat([c, torch.zeros_like(c[:1])]) for c in b.codes]
+    b.params = [torch.cat([p, torch.zeros_like(p[:1])]) for p in b.params]
+    b.table[0, 3] = b.codes[0].shape[0] - 1
+    b.check(out, lse)
+
+
+def test_run_together_and_captured():
+    # A prompt and then decode steps as a program runs them, eagerly and captured:
+    # rotate and write, attend; the same bits, and the definition's values.
+    g = torch.Generator().manual_seed(77)
+    H, hk, D, bs, n = 8, 2, 128, 16, 90
+    ends = [(0, n), (n, n + 1), (n + 1, n + 2), (n + 2, n + 3)]
+    table = torch.randperm(12, generator=g)[None].int()
+    rows = pa.rope_table(200, D, device=DEV)
+    d_table = table.to(DEV)
+    qkv = torch.randn((n + 3, H + 2 * hk, D), generator=g).bfloat16()
+    d_qkv = qkv.to(DEV)
+    got = []
+    for captured in (False, True):
+        pools = pa.int4_pools(12, bs, hk, D, DEV)
+        for a, b in ends:
+            pos = torch.arange(a, b, device=DEV)
+            slots = d_table[0, pos // bs].long() * bs + pos % bs
+            x = d_qkv[a:b]
+            cu = torch.tensor([0, b - a], dtype=torch.int32, device=DEV)
+            lens = torch.tensor([b], dtype=torch.int32, device=DEV)
+            sms = torch.cuda.get_device_properties(0).multi_processor_count
+            ws = pa.alloc_workspace(pa.varlen_fwd_int4kv_workspace_size(
+                1, b - a, b - a, b, H, hk, D, bs, sms), DEV)
+            q = torch.empty((b - a, H, D), dtype=torch.bfloat16, device=DEV)
+            out, lse = torch.empty_like(q), torch.empty((H, b - a), device=DEV)
+
+            def step():
+                pa.rope_and_cache_int4(x[:, :H], x[:, H:H + hk], x[:, H + hk:], pos, rows, *pools,
+                                       slots, out=q)
+                pa.varlen_fwd_int4kv(q, *pools, cu, lens, d_table, b - a, b, D ** -0.5, True,
+                                     out=out, lse=lse, workspace=ws)
+            if captured:
+                graph = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(graph):
+                    step()
+                graph.replay()
+                graph.replay()
+            else:
+                step()
+            torch.cuda.synchronize()
+            got.append((q.clone(), out.clone(), lse.clone()))
+    for one, two in zip(got[:4], got[4:]):
+        assert all(torch.equal(x, y) for x, y in zip(one, two))
+    cos_sin = rows.cpu()
+    kq = ref.quantize_int4(turned(qkv[:, H:H + hk].float(), cos_sin[:n + 3], False))
+    vq = ref.quantize_int4(qkv[:, H + hk:].float())
+    key, value = (c.double() * p[..., :1].double() + p[..., 1:].double() for c, p in (kq, vq))
+    for (a, b), (q, out, lse) in zip(ends, got):
+        assert torch.equal(q.cpu(), turned(qkv[a:b, :H].float(), cos_sin[a:b], False).bfloat16())
+        want, wl = ref.attend(q.cpu(), key[:b], value[:b], D ** -0.5)
+        # Weights 2^-11 and V 2^-11 of values up to 4, scores 2^-12 A with A < 40.
+        tol = want.abs() * 2.0 ** -8 + 4 * (2 * 40 * 2.0 ** -12 + 3 * 2.0 ** -11)
+        assert ((out.cpu().double() - want).abs() <= tol).all()
+        assert ((lse.cpu().double() - wl).abs() <= 40 * 2.0 ** -12 + 1e-5).all()
