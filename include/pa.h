@@ -732,9 +732,10 @@ pa_status pa_gather_cache_int4(const void* key_cache, const void* value_cache,
  * f16, and apply scale and minimum to the sums; q is taken as f16 after a
  * power-of-two row scale, exact for every bf16 element of at least 2^-28 of its
  * row's largest. The weights times V's scale are rounded to f16 after a
- * power-of-two row scale. Longer sequences run on the tensor-core kernel with K
- * and V widened to f16 values (one rounding, at most 2^-11 of a value) and the
- * weights in f16.
+ * power-of-two row scale. Longer sequences run on the tensor-core kernel: q.k the
+ * same way, V widened to f16 values (one rounding, at most 2^-11 of a value) and
+ * the weights in f16; there, as in the other prefill kernels, a NaN in V also
+ * reaches queries of the call that stand less than a key tile in front of it.
  * In pages that are read, rows past a sequence's keys do not matter.
  */
 size_t pa_varlen_fwd_int4kv_workspace_size(int num_seqs, int total_q, int max_seqlen_q,

@@ -82,7 +82,13 @@ struct TcI4 {
   static constexpr int SLOTS = 8;                         // units in a warp's ring
   static constexpr int SLOT = 16 * D / 2 + 64;
   static constexpr int OFF_RS = OFF_RING + WARPS * SLOTS * SLOT;   // float[TILES * BM]
-  static constexpr int OFF_BAR = OFF_RS + C::TILES * C::BM * 4;
+  static constexpr int OFF_TAU = OFF_RS + C::TILES * C::BM * 4;    // float[TILES * BM]
+  // Per key tile: scale 2^24 and minimum of its keys as float32, (s, s, m, m) of
+  // two keys at a time. Those of tile t are written when S(t - 2) is complete, so
+  // a ring of four leaves the softmax of t - 1 its own.
+  static constexpr int PARS = 4;
+  static constexpr int OFF_PAR = OFF_TAU + C::TILES * C::BM * 4;
+  static constexpr int OFF_BAR = OFF_PAR + PARS * C::BN * 8;
   static constexpr int SMEM_BYTES = OFF_BAR + 512 + 1024;
 };
 static_assert(TcI4<128>::SMEM_BYTES <= 227 * 1024, "the 4-bit layout fits shared memory");
@@ -100,7 +106,7 @@ struct TcBars {
   // commit). Buffer b holds tiles b, b + VBUF, ... (phase t / VBUF).
   uint64_t q_conv, vw_full[2], vw_free[2];
   // 4-bit pools: likewise widened K tiles (vw for V), one arrival per unit.
-  uint64_t kw_full[2], kw_free[2];
+  uint64_t kw_full[2], kw_free[2], par_full[4];
   uint32_t tmem_base;
   volatile int abort;
   volatile int last;
@@ -155,6 +161,7 @@ struct TcKind {
   static constexpr bool WIDE = FP8 || I4;
   static constexpr int OFF_RS = I4 ? TcI4<D>::OFF_RS : TcFp8::OFF_RS;
 };
+static_assert(sizeof(TcBars) <= 512, "the barriers' place");
 
 // Bits 0 .. n - 1 (none for n <= 0, all from n = 32 on).
 __device__ __forceinline__ uint32_t below_mask(int n) {
@@ -246,6 +253,8 @@ __device__ __forceinline__ void tc_softmax_tile(const AttnArgs& a, TcBars* bars,
       sl2 *= reinterpret_cast<const float*>(smem + Kind::OFF_RS)[X * C::BM + r];
     }
   }
+  float tau = 0.f;   // I4: sum of the row's (scaled) q
+  if constexpr (I4) tau = reinterpret_cast<const float*>(smem + TcI4<D>::OFF_TAU)[X * C::BM + r];
   for (int t = 0; ok && t < ntiles; ++t) {
     if (!mbar_wait(&bars->s_full[X], t & 1)) { ok = false; break; }
     tc_fence_after();
@@ -258,6 +267,20 @@ __device__ __forceinline__ void tc_softmax_tile(const AttnArgs& a, TcBars* bars,
       tmem_ld32(tm_row + s_col + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&xs_u[c * 32]));
     tmem_wait_ld();
     float* xs = reinterpret_cast<float*>(xs_u);
+    if constexpr (I4) {
+      // The products are with the keys' codes: q.k = scale (q.n) + minimum (sum of
+      // q), in float32.
+      using I = TcI4<D>;
+      if (!mbar_wait(&bars->par_full[t % I::PARS], (t / I::PARS) & 1)) { ok = false; break; }
+      const float4* par = reinterpret_cast<const float4*>(smem + I::OFF_PAR + t % I::PARS * C::BN * 8);
+#pragma unroll
+      for (int e = 0; e < C::BN; e += 2) {
+        const float4 p = par[e / 2];
+        float u0, u1;
+        fmul2(u0, u1, p.z, p.w, tau, tau);
+        ffma2(xs[e], xs[e + 1], p.x, p.y, xs[e], xs[e + 1], u0, u1);
+      }
+    }
     if constexpr (SC) {
       score_tile<C::BN>(a, xs, sl2, slope, pos, key0);
       if (edge || key0 < low) {

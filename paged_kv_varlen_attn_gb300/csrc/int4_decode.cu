@@ -20,16 +20,21 @@ namespace pa {
 //      join after: q.k = scale (q.n) + minimum (sum of q).
 //   V  The MMA wants pairs of keys, so two keys' words are put together by
 //      halves (byte permutes) and masked the same way: 6 instructions for 8.
-//      O^T[D x 8 rows] += N^T W^T with W the weights times V's scale, and
-//      the minima enter by a sum of weights x minimum per row.
-// Two references are kept per row: m for the weights p = 2^(x - m), whose sum is
-// taken in float32, and M for w = 2^(x + log2 scale_V - M), the f16 operand; each
-// is raised only when its exponent passes it by more than 8. So neither large
-// differences between the scales of V's rows nor small ones lose weights: w is
-// within 2^-11 of its value down to 2^-14 of the row's largest product.
+//      O^T[D x 8 rows] += N^T W^T with W = weight x V's scale / ref, ref a power
+//      of two that is raised when a scale passes it (the weights stay below 2^8,
+//      so W stays inside f16 and keeps its eleven bits down to 2^-22 of that).
+//      The rest of the value enters by sums per row: of weights x (minimum + 8
+//      scale), and of W as rounded, eightfold, which is taken off: so a weight's
+//      rounding weighs with code - 8 and not with the code. That sum is one more
+//      row of the product (ones for codes), and is taken off every 128 keys
+//      already, before the sums of codes grow past what float32 keeps of the
+//      difference (f16 outputs were off by 3.4e-4 of their size otherwise, by
+//      6e-4 without the eightfold sum; the output's own rounding is 2.1e-4).
+// The weights are 2^(score - m) against a running maximum m that is raised only
+// when a score passes it by more than 8; their sum is float32.
 //
 // Nothing is planned on the device and nothing depends on the key bound: the
-// slices (16 keys) of all sequences of the class, one after another, are cut
+// slices (32 keys) of all sequences of the class, one after another, are cut
 // into equal ranges, and warp (range, KV head) streams its range through a ring
 // of its own, filled by asynchronous copies that run ahead across sequences.
 // Every warp counts the ranges for itself from the lengths. A sequence's state
@@ -39,15 +44,17 @@ namespace pa {
 // bytes are read at about the same time.
 // ---------------------------------------------------------------------------
 constexpr int kI4Warps = 4;        // of a block; they share nothing
-constexpr int kI4Slots = 4;        // slices in a warp's ring
-constexpr int kI4MinSlices = 4;    // of a range
+constexpr int kI4Slots = 3;        // slices in a warp's ring
+constexpr int kI4MinSlices = 2;    // of a range
+constexpr int kI4Keys = 32;        // of a slice: two halves of 16, each in one page
 
 template <int D, int NR>
 struct I4Cfg {
-  static constexpr int CODES = 16 * D / 2;             // bytes of a slice of K or of V
-  static constexpr int SLOT = 2 * CODES + 128;         // K, V, their params
+  static constexpr int CODES = 16 * D / 2;             // bytes of a half's K or V
+  static constexpr int PAR = 4 * CODES;                // K of both halves, V of both, params
+  static constexpr int SLOT = PAR + 2 * kI4Keys * 4;
   static constexpr int SMEM_BYTES = kI4Warps * kI4Slots * SLOT;
-  static constexpr int BLOCKS = NR == 1 ? 5 : NR == 2 ? 3 : 2;   // per SM
+  static constexpr int BLOCKS = NR == 1 ? 4 : 2;   // per SM
 };
 
 // One sequence, as the kernels of this file count it.
@@ -72,8 +79,13 @@ __device__ __forceinline__ I4Seq i4_seq(const Int4DecodeArgs& a, int s, bool rep
   q.kv = min(max(q.kv, 0), a.kv_len_cap);
   const bool mine = q.q_len > a.tokens_min && q.q_len <= a.tokens_max;
   // A sequence without keys has one slice that nobody sees.
-  q.n = mine ? max(1, (q.kv + 15) >> 4) : 0;
+  q.n = mine ? max(1, (q.kv + kI4Keys - 1) / kI4Keys) : 0;
   return q;
+}
+
+// 1 / x of a power of two.
+__device__ __forceinline__ float inverse_power(float x) {
+  return __uint_as_float((254u << 23) - __float_as_uint(x));
 }
 
 // Slices of a range, given all of them.
@@ -129,19 +141,19 @@ int4_decode_kernel(const __grid_constant__ Int4DecodeArgs a) {
     }
     before += __shfl_sync(kAll, incl, 31);
   }
+  int i = static_cast<int>(begin - before);            // slice of the sequence
 
   // ---------------------------------------------------------------- copies
   // The next slice to copy: slice f_i of f_n of the sequence in lane f_at of the
-  // 32 whose lengths the lanes hold from f_base on; lane i holds the page and
-  // the row of slice f_page0 + i.
+  // 32 whose lengths the lanes hold from f_base on. Lane x holds the page and the
+  // row of half f_half0 + x of that sequence.
   int f_base = base, f_at = first, f_kv_l = sq.kv, f_n_l = sq.n;
-  int f_i = static_cast<int>(begin - before);
-  int f_n = __shfl_sync(kAll, f_n_l, f_at), f_kv = __shfl_sync(kAll, f_kv_l, f_at);
-  int f_page0 = 0, f_left = count;
+  int f_i = i, f_n = __shfl_sync(kAll, f_n_l, f_at), f_kv = __shfl_sync(kAll, f_kv_l, f_at);
+  int f_half0 = 0, f_left = count;
   int page_l = -1, row_l = 0;
   auto load_pages = [&]() {
-    f_page0 = f_i;
-    const int key0 = (f_i + lane) * 16;
+    f_half0 = 2 * f_i;
+    const int key0 = (f_half0 + lane) * 16;
     page_l = -1;
     row_l = 0;
     if (key0 < f_kv) {
@@ -157,11 +169,25 @@ int4_decode_kernel(const __grid_constant__ Int4DecodeArgs a) {
   load_pages();
   uint8_t* ring = smem + warp * (kI4Slots * C::SLOT);
   const uint32_t ring_at = smem_u32(ring);
-  const int64_t rstep = static_cast<int64_t>(a.H_kv) * (D / 2);
-  // Row g of S^T is key (g >> 1) + 4 (g & 1) of the slice's halves: so the four
-  // keys of a lane in O^T, 2c and 2c + 1 of each half, are rows c and c + 4 of
-  // shared memory, and eight lanes that read them take different banks.
+  const int rstep = a.H_kv * (D / 2);                  // (checked to fit by the host)
+  // Row g of S^T is key (g >> 1) + 4 (g & 1) of the half's halves: so the four
+  // keys of a lane in O^T, 2c and 2c + 1 of each, are rows c and c + 4 of shared
+  // memory, and eight lanes that read them take different banks.
   const int kg = (g >> 1) + 4 * (g & 1);
+  // What this lane copies of a half. D = 128: of K its own pieces (rows kg and kg
+  // + 8), of V piece c of rows g and g + 8 to place c ^ (g & 2); D = 64: piece
+  // lane & 1 of row lane / 2 of both. And one row's scale and minimum, of K in
+  // lanes 0-15, of V in the others: those of keys x, x + 8, x + 16, x + 24 of the
+  // slice side by side.
+  const int k_row = D == 128 ? kg : lane >> 1, v_row = D == 128 ? g : lane >> 1;
+  const int piece = D == 128 ? c : lane & 1;
+  const uint8_t* k_src = a.kc + hk * (D / 2) + static_cast<int64_t>(k_row) * rstep + piece * 16;
+  const uint8_t* v_src = a.vc + hk * (D / 2) + static_cast<int64_t>(v_row) * rstep + piece * 16;
+  const int p_row = lane & 15;
+  const uint32_t* p_src = (lane < 16 ? a.k_params : a.v_params) +
+                          static_cast<int64_t>(hk) * a.bs + p_row;
+  const uint32_t v_place = D == 128 ? g * 64 + ((c ^ (g & 2)) << 4) : lane * 16;
+  const uint32_t p_place = C::PAR + (lane >> 4) * (kI4Keys * 4) + (p_row & 7) * 16 + (p_row >> 3) * 4;
   auto fetch = [&](int slot) {
     if (f_left > 0) {
       if (f_i == f_n) {                                // the next sequence that has slices
@@ -197,36 +223,36 @@ int4_decode_kernel(const __grid_constant__ Int4DecodeArgs a) {
         f_kv = __shfl_sync(kAll, f_kv_l, f_at);
         f_i = 0;
         load_pages();
-      } else if (f_i - f_page0 == 32) {
+      } else if (2 * f_i - f_half0 == 32) {
         load_pages();
       }
-      const int page = __shfl_sync(kAll, page_l, f_i - f_page0);
-      const int prow = __shfl_sync(kAll, row_l, f_i - f_page0);
-      const bool in = page >= 0;
-      const uint32_t dst = ring_at + slot * C::SLOT;
-      const int64_t at = max(page, 0) * a.block_stride_bytes + hk * (D / 2) + prow * rstep;
-      const uint8_t* kp = a.kc + at;
-      const uint8_t* vp = a.vc + at;
-      if constexpr (D == 128) {
-        // K: this lane's own pieces; V: piece x of row r at place x ^ (r & 2).
-        cp_async16(dst + lane * 16, kp + kg * rstep + c * 16, in);
-        cp_async16(dst + 512 + lane * 16, kp + (8 + kg) * rstep + c * 16, in);
+      const uint32_t dst0 = ring_at + slot * C::SLOT;
 #pragma unroll
-        for (int it = 0; it < 2; ++it) {
-          const int r = it * 8 + g;
-          cp_async16(dst + C::CODES + r * 64 + ((c ^ (r & 2)) << 4), vp + r * rstep + c * 16, in);
+      for (int h = 0; h < 2; ++h) {
+        const int page = __shfl_sync(kAll, page_l, 2 * f_i - f_half0 + h);
+        const uint32_t prow = __shfl_sync(kAll, row_l, 2 * f_i - f_half0 + h);
+        const uint32_t dst = dst0 + h * C::CODES;
+        if (page >= 0) {
+          const uint64_t at = static_cast<uint64_t>(static_cast<uint32_t>(page)) * a.page_bytes +
+                              static_cast<uint64_t>(prow) * static_cast<uint32_t>(rstep);
+          const uint8_t* kp = k_src + at;
+          const uint8_t* vp = v_src + at;
+          cp_async16(dst + lane * 16, kp);
+          cp_async16(dst + 2 * C::CODES + v_place, vp);
+          if constexpr (D == 128) {
+            cp_async16(dst + 512 + lane * 16, kp + 8 * rstep);
+            cp_async16(dst + 2 * C::CODES + 512 + v_place, vp + 8 * rstep);
+          }
+          // Scales and minima; zeros past the sequence (what is there is nobody's).
+          cp_async4(dst0 + p_place + h * 8,
+                    p_src + static_cast<uint64_t>(static_cast<uint32_t>(page)) * a.page_params + prow,
+                    32 * f_i + 16 * h + p_row < f_kv);
+        } else {
+          // No page: codes do not matter where scale and minimum are zero, but
+          // they must be some.
+          cp_async4(dst0 + p_place + h * 8, p_src, false);
         }
-      } else {
-        const int64_t from = (lane >> 1) * rstep + (lane & 1) * 16;
-        cp_async16(dst + lane * 16, kp + from, in);
-        cp_async16(dst + C::CODES + lane * 16, vp + from, in);
       }
-      // Scales and minima; zeros past the sequence (what is there is nobody's).
-      const int r = lane & 15;
-      cp_async4(dst + 2 * C::CODES + lane * 4,
-                (lane < 16 ? a.k_params : a.v_params) + max(page, 0) * a.params_stride +
-                    static_cast<int64_t>(hk) * a.bs + prow + r,
-                in && f_i * 16 + r < f_kv);
       ++f_i;
       --f_left;
     }
@@ -236,7 +262,7 @@ int4_decode_kernel(const __grid_constant__ Int4DecodeArgs a) {
   for (int u = 0; u < kI4Slots - 1; ++u) fetch(u);
 
   // ---------------------------------------------------------------- sequences
-  int at = first, i = static_cast<int>(begin - before), left = count;
+  int at = first, left = count;
   int slot = 0, to = kI4Slots - 1;
   long long flat = begin;          // slice of all slices at which this part starts
 #pragma unroll 1
@@ -254,13 +280,14 @@ int4_decode_kernel(const __grid_constant__ Int4DecodeArgs a) {
     const int q0 = __shfl_sync(kAll, sq.q0, at), q_len = __shfl_sync(kAll, sq.q_len, at);
     const int i0 = i, i1 = min(n, i + left);
     const int rows = q_len * a.G, past = kv - q_len;
+    // Keys that every row sees.
+    const int seen_by_all = min(kv, a.causal ? past + 1 : kv);
 
     // Q as B fragments, f16 after a power-of-two scale that brings the row's
     // largest element to 2^14 .. 2^15 (infinities and NaN stay what they are);
     // the operand of the codes in the upper four bits is a sixteenth.
     uint32_t qf[NR][2 * KW][2];
     float sa[NR][2], sb[NR][2];    // of rows 2c, 2c + 1: scale of q.n, and of sum(q)
-    int lim[NR][2];                // their last visible key
 #pragma unroll
     for (int nr = 0; nr < NR; ++nr) {
       const int r = min(8 * nr + g, rows - 1), t = r / a.G;
@@ -304,24 +331,40 @@ int4_decode_kernel(const __grid_constant__ Int4DecodeArgs a) {
         const int from = (2 * c + e) * 4;
         sa[nr][e] = a.scale_log2 * __shfl_sync(kAll, down, from);
         sb[nr][e] = a.scale_log2 * (__shfl_sync(kAll, sum, from) * __shfl_sync(kAll, down, from));
-        const int row = min(8 * nr + 2 * c + e, rows - 1);
-        lim[nr][e] = a.causal ? past + row / a.G : kv - 1;
       }
     }
-    float m[NR][2], mw[NR][2], l[NR][2], lv[NR][2];    // lv: sum of weights x minimum of V
-    float acc[NR][D / 16][4];
+    float m[NR][2], l[NR][2], lv[NR][2];               // lv: sum of weights x middle of V's row
+    float acc[NR][D / 16][4], accw[NR][4];             // accw: sum of W, every entry of a column
+    float ref = 0.f;                                   // power of two, at least V's scales so far
 #pragma unroll
     for (int nr = 0; nr < NR; ++nr) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        m[nr][e] = mw[nr][e] = -INFINITY;
+        m[nr][e] = -INFINITY;
         l[nr][e] = lv[nr][e] = 0.f;
       }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) accw[nr][e] = 0.f;
 #pragma unroll
       for (int t = 0; t < D / 16; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[nr][t][e] = 0.f;
     }
+    // Takes the eightfold sum of W off the sums of codes.
+    auto centre = [&]() {
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr) {
+#pragma unroll
+        for (int t = 0; t < D / 16; ++t) {
+          ffma2(acc[nr][t][0], acc[nr][t][1], accw[nr][0], accw[nr][1], -0x1p-21f, -0x1p-21f,
+                acc[nr][t][0], acc[nr][t][1]);
+          ffma2(acc[nr][t][2], acc[nr][t][3], accw[nr][0], accw[nr][1], -0x1p-17f, -0x1p-17f,
+                acc[nr][t][2], acc[nr][t][3]);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) accw[nr][e] = 0.f;
+      }
+    };
 
 #pragma unroll 1
     for (; i < i1; ++i) {
@@ -330,21 +373,24 @@ int4_decode_kernel(const __grid_constant__ Int4DecodeArgs a) {
       cp_async_wait<kI4Slots - 1>();
       __syncwarp();
       const uint8_t* sl = ring + slot * C::SLOT;
-      const int key0 = 16 * i;
+      const int key0 = kI4Keys * i;
       // ----------------------------------------------------------- S^T = N Q^T
-      float st[NR][4];
+      float st[NR][2][4];
 #pragma unroll
-      for (int nr = 0; nr < NR; ++nr) st[nr][0] = st[nr][1] = st[nr][2] = st[nr][3] = 0.f;
-      {
+      for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) st[nr][h][0] = st[nr][h][1] = st[nr][h][2] = st[nr][h][3] = 0.f;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
         uint32_t w0[KW], w1[KW];
         if constexpr (D == 128) {
-          const uint4 x0 = *reinterpret_cast<const uint4*>(sl + lane * 16);
-          const uint4 x1 = *reinterpret_cast<const uint4*>(sl + 512 + lane * 16);
+          const uint4 x0 = *reinterpret_cast<const uint4*>(sl + h * C::CODES + lane * 16);
+          const uint4 x1 = *reinterpret_cast<const uint4*>(sl + h * C::CODES + 512 + lane * 16);
           w0[0] = x0.x; w0[1] = x0.y; w0[2] = x0.z; w0[3] = x0.w;
           w1[0] = x1.x; w1[1] = x1.y; w1[2] = x1.z; w1[3] = x1.w;
         } else {
-          const uint2 x0 = *reinterpret_cast<const uint2*>(sl + kg * 32 + c * 8);
-          const uint2 x1 = *reinterpret_cast<const uint2*>(sl + (8 + kg) * 32 + c * 8);
+          const uint2 x0 = *reinterpret_cast<const uint2*>(sl + h * C::CODES + kg * 32 + c * 8);
+          const uint2 x1 = *reinterpret_cast<const uint2*>(sl + h * C::CODES + (8 + kg) * 32 + c * 8);
           w0[0] = x0.x; w0[1] = x0.y;
           w1[0] = x1.x; w1[1] = x1.y;
         }
@@ -355,119 +401,163 @@ int4_decode_kernel(const __grid_constant__ Int4DecodeArgs a) {
             const uint32_t a0 = w0[v] >> (8 * k), a1 = w1[v] >> (8 * k);
 #pragma unroll
             for (int nr = 0; nr < NR; ++nr)
-              mma_16816_f16(st[nr], a0 & 0x000F000Fu, a1 & 0x000F000Fu, a0 & 0x00F000F0u,
+              mma_16816_f16(st[nr][h], a0 & 0x000F000Fu, a1 & 0x000F000Fu, a0 & 0x00F000F0u,
                             a1 & 0x00F000F0u, qf[nr][2 * v + k][0], qf[nr][2 * v + k][1]);
           }
         }
       }
       // ----------------------------------------------------------- softmax
-      const uint32_t* par = reinterpret_cast<const uint32_t*>(sl + 2 * C::CODES);
-      float ks[2], km[2], vl[2], vm[2];                // keys kg and kg + 8
+      // Keys kg + 8 h of the slice, h = 0 .. 3: entries 2 (h & 1) of st[h >> 1].
+      const uint4 pk = *reinterpret_cast<const uint4*>(sl + C::PAR + kg * 16);
+      const uint4 pv = *reinterpret_cast<const uint4*>(sl + C::PAR + kI4Keys * 4 + kg * 16);
+      const uint32_t pkw[4] = {pk.x, pk.y, pk.z, pk.w}, pvw[4] = {pv.x, pv.y, pv.z, pv.w};
+      float ks[4], km[4], vs[4], vm[4];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float2 pk = Elem<true>::unpack(par[kg + 8 * h]);
-        const float2 pv = Elem<true>::unpack(par[16 + kg + 8 * h]);
-        ks[h] = pk.x * 0x1p24f;
-        km[h] = pk.y;
-        vl[h] = fast_log2(pv.x);
-        vm[h] = pv.y;
+      for (int h = 0; h < 4; ++h) {
+        const float2 k = Elem<true>::unpack(pkw[h]), v = Elem<true>::unpack(pvw[h]);
+        ks[h] = k.x * 0x1p24f;
+        km[h] = k.y;
+        vs[h] = v.x;
+        vm[h] = fmaf(8.f, v.x, v.y);
       }
-      uint32_t wb[NR][2];
+      const bool whole = key0 + kI4Keys <= seen_by_all;
+      const float vtop = fmaxf(fmax3(vs[0], vs[1], vs[2]), vs[3]);
+      if (__any_sync(kAll, vtop > ref)) {              // raise the reference of V's scales
+        float top = vtop;
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
+        // The power of two above it, and 4: a larger one is then seldom met.
+        const float nr_ref = __uint_as_float(((__float_as_uint(top) >> 23) + 3u) << 23);
+        const float f = ref == 0.f ? 0.f : ref * inverse_power(nr_ref);
+        ref = nr_ref;
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) accw[nr][e] *= f;
+#pragma unroll
+          for (int t = 0; t < D / 16; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[nr][t][e] *= f;
+        }
+      }
+      // W = weight x scale / ref x 2^6: at most 2^8 x 1 x 2^6 = 2^14.
+      const float wscale = ref == 0.f ? 0.f : 64.f * inverse_power(ref);
+      uint32_t wb[NR][4];
 #pragma unroll
       for (int nr = 0; nr < NR; ++nr) {
-        float x[4], y[4], vme[4];
+        float x[4][2];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int h = e >> 1, r = e & 1;
-          x[e] = st[nr][e] * ks[h] * sa[nr][r] + km[h] * sb[nr][r];
-          y[e] = x[e] + vl[h];
-          vme[e] = vm[h];
+        for (int h = 0; h < 4; ++h) {
+          float t0, t1, u0, u1;
+          fmul2(t0, t1, ks[h], ks[h], sa[nr][0], sa[nr][1]);
+          fmul2(u0, u1, km[h], km[h], sb[nr][0], sb[nr][1]);
+          ffma2(x[h][0], x[h][1], st[nr][h >> 1][2 * (h & 1)], st[nr][h >> 1][2 * (h & 1) + 1], t0,
+                t1, u0, u1);
         }
-        if (key0 + 15 > past || key0 + 15 >= kv) {     // not all 16 are seen by every row
+        if (!whole) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (key0 + kg + 8 * (e >> 1) > lim[nr][e & 1]) {
-              x[e] = y[e] = -INFINITY;
-              vme[e] = 0.f;
-            }
+          for (int e = 0; e < 2; ++e) {
+            const int row = min(8 * nr + 2 * c + e, rows - 1);
+            const int lim = a.causal ? past + row / a.G : kv - 1;   // last visible key
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+              if (key0 + kg + 8 * h > lim) x[h][e] = -INFINITY;
           }
         }
-        const float x0 = fmaxf(x[0], x[2]), x1 = fmaxf(x[1], x[3]);
-        const float y0 = fmaxf(y[0], y[2]), y1 = fmaxf(y[1], y[3]);
-        if (__any_sync(kAll, x0 > m[nr][0] + 8.f || x1 > m[nr][1] + 8.f ||
-                                 y0 > mw[nr][0] + 8.f || y1 > mw[nr][1] + 8.f)) {
-          float xm[2] = {x0, x1}, ym[2] = {y0, y1};
+        const float x0 = fmaxf(fmax3(x[0][0], x[1][0], x[2][0]), x[3][0]);
+        const float x1 = fmaxf(fmax3(x[0][1], x[1][1], x[2][1]), x[3][1]);
+        if (__any_sync(kAll, x0 > m[nr][0] + 8.f || x1 > m[nr][1] + 8.f)) {
+          float xm[2] = {x0, x1};
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
 #pragma unroll
-            for (int o = 4; o < 32; o <<= 1) {
-              xm[e] = fmaxf(xm[e], __shfl_xor_sync(kAll, xm[e], o));
-              ym[e] = fmaxf(ym[e], __shfl_xor_sync(kAll, ym[e], o));
-            }
-            const float nm = fmaxf(m[nr][e], xm[e]), nw = fmaxf(mw[nr][e], ym[e]);
+            for (int o = 4; o < 32; o <<= 1) xm[e] = fmaxf(xm[e], __shfl_xor_sync(kAll, xm[e], o));
+            const float nm = fmaxf(m[nr][e], xm[e]);
             const float f = m[nr][e] == -INFINITY ? 0.f : fast_exp2(m[nr][e] - nm);
-            const float fw = mw[nr][e] == -INFINITY ? 0.f : fast_exp2(mw[nr][e] - nw);
             l[nr][e] *= f;
             lv[nr][e] *= f;
             m[nr][e] = nm;
-            mw[nr][e] = nw;
+            accw[nr][e] *= f;
+            accw[nr][2 + e] *= f;
 #pragma unroll
             for (int t = 0; t < D / 16; ++t) {
-              acc[nr][t][e] *= fw;
-              acc[nr][t][2 + e] *= fw;
+              acc[nr][t][e] *= f;
+              acc[nr][t][2 + e] *= f;
             }
           }
         }
-        float w[4];
+        const float m0 = m[nr][0] == -INFINITY ? 0.f : m[nr][0];
+        const float m1 = m[nr][1] == -INFINITY ? 0.f : m[nr][1];
+        float w[4][2];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = e & 1;
-          const float p = fast_exp2(x[e] - (m[nr][r] == -INFINITY ? 0.f : m[nr][r]));
-          w[e] = fast_exp2(y[e] - (mw[nr][r] == -INFINITY ? 0.f : mw[nr][r]));
-          l[nr][r] += p;
-          lv[nr][r] = fmaf(p, vme[e], lv[nr][r]);
+        for (int h = 0; h < 4; ++h) {
+          float y0, y1;
+          fadd2(y0, y1, x[h][0], x[h][1], -m0, -m1);
+          const float p0 = fast_exp2(y0), p1 = fast_exp2(y1);
+          fadd2(l[nr][0], l[nr][1], l[nr][0], l[nr][1], p0, p1);
+          const float f = vs[h] * wscale;
+          if (whole) {
+            ffma2(lv[nr][0], lv[nr][1], p0, p1, vm[h], vm[h], lv[nr][0], lv[nr][1]);
+            fmul2(w[h][0], w[h][1], p0, p1, f, f);
+          } else {   // a key that a row does not see adds nothing, whatever it holds
+            const bool s0 = x[h][0] != -INFINITY, s1 = x[h][1] != -INFINITY;
+            lv[nr][0] = s0 ? fmaf(p0, vm[h], lv[nr][0]) : lv[nr][0];
+            lv[nr][1] = s1 ? fmaf(p1, vm[h], lv[nr][1]) : lv[nr][1];
+            w[h][0] = s0 ? p0 * f : 0.f;
+            w[h][1] = s1 ? p1 * f : 0.f;
+          }
         }
-        wb[nr][0] = movmatrix_trans(pack_f16(w[0], w[1]));
-        wb[nr][1] = movmatrix_trans(pack_f16(w[2], w[3]));
+#pragma unroll
+        for (int h = 0; h < 4; ++h) wb[nr][h] = movmatrix_trans(pack_f16(w[h][0], w[h][1]));
       }
       // ----------------------------------------------------------- O^T += N^T W^T
-      uint32_t wv[4][VW];          // keys c, c + 4, c + 8, c + 12; this lane's 8 VW dims
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int r = c + 4 * k;
-        if constexpr (D == 128) {
-          const uint2 x = *reinterpret_cast<const uint2*>(
-              sl + C::CODES + r * 64 + (((g >> 1) ^ (r & 2)) << 4) + (g & 1) * 8);
-          wv[k][0] = x.x;
-          wv[k][1] = x.y;
-        } else {
-          wv[k][0] = *reinterpret_cast<const uint32_t*>(sl + C::CODES + r * 32 + g * 4);
+      for (int h = 0; h < 2; ++h) {
+        uint32_t wv[4][VW];        // keys c, c + 4, c + 8, c + 12 of the half; 8 VW dims
+        const uint8_t* vt = sl + (2 + h) * C::CODES;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int r = c + 4 * k;
+          if constexpr (D == 128) {
+            const uint2 x = *reinterpret_cast<const uint2*>(
+                vt + r * 64 + (((g >> 1) ^ (r & 2)) << 4) + (g & 1) * 8);
+            wv[k][0] = x.x;
+            wv[k][1] = x.y;
+          } else {
+            wv[k][0] = *reinterpret_cast<const uint32_t*>(vt + r * 32 + g * 4);
+          }
         }
-      }
 #pragma unroll
-      for (int j = 0; j < VW; ++j) {
+        for (int nr = 0; nr < NR; ++nr)
+          mma_16816_f16(accw[nr], 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u,
+                        wb[nr][2 * h], wb[nr][2 * h + 1]);
 #pragma unroll
-        for (int odd = 0; odd < 2; ++odd) {
-          const uint32_t t0 = prmt(wv[0][j], wv[1][j], odd ? 0x7632 : 0x5410);
-          const uint32_t t1 = prmt(wv[2][j], wv[3][j], odd ? 0x7632 : 0x5410);
+        for (int j = 0; j < VW; ++j) {
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const uint32_t u0 = t0 >> (8 * k), u1 = t1 >> (8 * k);
+          for (int odd = 0; odd < 2; ++odd) {
+            const uint32_t t0 = prmt(wv[0][j], wv[1][j], odd ? 0x7632 : 0x5410);
+            const uint32_t t1 = prmt(wv[2][j], wv[3][j], odd ? 0x7632 : 0x5410);
 #pragma unroll
-            for (int nr = 0; nr < NR; ++nr)
-              mma_16816_f16(acc[nr][4 * j + 2 * odd + k], u0 & 0x000F000Fu, u0 & 0x00F000F0u,
-                            u1 & 0x000F000Fu, u1 & 0x00F000F0u, wb[nr][0], wb[nr][1]);
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t u0 = t0 >> (8 * k), u1 = t1 >> (8 * k);
+#pragma unroll
+              for (int nr = 0; nr < NR; ++nr)
+                mma_16816_f16(acc[nr][4 * j + 2 * odd + k], u0 & 0x000F000Fu, u0 & 0x00F000F0u,
+                              u1 & 0x000F000Fu, u1 & 0x00F000F0u, wb[nr][2 * h], wb[nr][2 * h + 1]);
+            }
           }
         }
       }
+      if ((i & 3) == 3) centre();
       if (++slot == kI4Slots) slot = 0;
       __syncwarp();                                    // the slot may be filled again
     }
+    centre();
 
     // ---------------------------------------------------------------- the state
     // acc[4 j + 2 odd + k] holds, of this lane's 8 j .. 8 j + 7 dims, 4 k + odd
     // (entries 0, 1: rows 2c, 2c + 1) and 4 k + 2 + odd (2, 3; sixteenfold).
-    const bool whole = i0 == 0 && i1 == n;
+    const bool all = i0 == 0 && i1 == n;
 #pragma unroll
     for (int nr = 0; nr < NR; ++nr) {
 #pragma unroll
@@ -482,9 +572,8 @@ int4_decode_kernel(const __grid_constant__ Int4DecodeArgs a) {
         if (row >= rows) continue;
         const int t = row / a.G, head = hk * a.G + row - t * a.G;
         float M = m[nr][e], of = 1.f;
-        // Of the unscaled sums: 2^(M_w - m) and the codes' 2^24.
-        const float fw = mw[nr][e] == -INFINITY ? 0.f : fast_exp2(mw[nr][e] - M) * 0x1p24f;
-        if (whole && a.sinks) of = add_sink(M, L, __ldg(a.sinks + head) * kLog2e);
+        const float fw = ref * (0x1p24f / 64.f);       // of the sums of codes
+        if (all && a.sinks) of = add_sink(M, L, __ldg(a.sinks + head) * kLog2e);
         const float inv = L == 0.f ? 0.f : of / L;
         const float lse = L == 0.f ? -INFINITY : (M + fast_log2(L)) * kLn2;
         float o[VW][8];
@@ -496,7 +585,7 @@ int4_decode_kernel(const __grid_constant__ Int4DecodeArgs a) {
             o[j][d] = fmaf(acc[nr][4 * j + x][e], fw, V) * inv;
             o[j][d + 2] = fmaf(acc[nr][4 * j + x][2 + e], fw * 0.0625f, V) * inv;
           }
-        if (whole) {
+        if (all) {
           uint4* dst = reinterpret_cast<uint4*>(
               a.out + (static_cast<int64_t>(q0 + t) * a.H + head) * D + g * (8 * VW));
 #pragma unroll
@@ -520,7 +609,7 @@ int4_decode_kernel(const __grid_constant__ Int4DecodeArgs a) {
     left -= i1 - i0;
     flat += i1 - i0;
     i = 0;
-    ++at;                                              // at 32 the search above goes on
+    ++at;
     if (at == 32 && left > 0) {
       base += 32;
       sq = I4Seq{0, 0, 0, 0};
@@ -629,8 +718,10 @@ static cudaError_t launch_int4_decode_nr(const Int4DecodeArgs& a, cudaStream_t s
 }
 
 int int4_decode_ranges(int sms, int H_kv, int nr) {
-  const int blocks = nr == 1 ? I4Cfg<128, 1>::BLOCKS
-                             : nr == 2 ? I4Cfg<128, 2>::BLOCKS : I4Cfg<128, 4>::BLOCKS;
+  const int blocks = nr == 1   ? I4Cfg<128, 1>::BLOCKS
+                     : nr == 2 ? I4Cfg<128, 2>::BLOCKS
+                     : nr == 3 ? I4Cfg<128, 3>::BLOCKS
+                               : I4Cfg<128, 4>::BLOCKS;
   const int n = sms * blocks * kI4Warps / H_kv;
   return n < 1 ? 1 : n;
 }
@@ -647,6 +738,7 @@ cudaError_t launch_int4_decode(Int4DecodeArgs a, int D, bool f16, int nr, int sm
     constexpr bool kF16 = decltype(half)::value;
     if (nr == 1) return launch_int4_decode_nr<kD, kF16, 1>(a, st);
     if (nr == 2) return launch_int4_decode_nr<kD, kF16, 2>(a, st);
+    if (nr == 3) return launch_int4_decode_nr<kD, kF16, 3>(a, st);
     return launch_int4_decode_nr<kD, kF16, 4>(a, st);
   };
   using std::integral_constant;

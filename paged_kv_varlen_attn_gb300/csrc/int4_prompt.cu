@@ -17,19 +17,36 @@ namespace pa {
 //    of key tiles. It copies its units' codes, scales and minima ahead of their
 //    use into a ring of its own (a lane copies what it reads back itself, but for
 //    the scales), so no barrier stands between the pools and the registers.
-//  * A code n becomes the f16 number n exactly (n or 16 n in the low mantissa bits
-//    of 1024, then one subtraction or multiply-add), and n scale + minimum is one
-//    f16 multiply-add: the one rounding, at most half a step of the value. Rows
-//    past the sequence are zeros.
+//  * K reaches the product as codes: n in the low four bits of an f16 is the
+//    subnormal n 2^-24, in the next four n 2^-20, so a mask makes two numbers;
+//    the query's elements that meet the latter are a sixteenth. The softmax
+//    applies scale and minimum to the sums, in float32 (one multiply and one
+//    multiply-add per two scores): with K rounded to f16 values instead, the
+//    log-sum-exp lost ten of its bits.
+//  * V becomes values: n exactly as f16 (from 1024 + n or 1024 + 16 n), and n
+//    scale + minimum by one multiply-add: one rounding, at most half a step of
+//    the value. Rows past the sequence are zeros.
 //  * The widened tiles have the 2-byte kernel's layout (128-byte swizzle), two
 //    buffers each for K and V; the products that read a buffer free it.
 //  * Q is taken as f16 after a power-of-two row scale, in place, by the same
-//    warps, once per item; 2^-k joins the softmax scale. The sign of a negative
+//    warps, once per item, which also sum it; 2^-k joins the softmax scale. The sign of a negative
 //    softmax scale goes into Q, so the row maximum of the raw products serves
 //    every scale.
 // ---------------------------------------------------------------------------
 
-// A unit's piece, 32 codes (16 bytes, row r), as 64 bytes of f16: chunks c0 .. c0
+// A unit's piece of K: 32 codes (16 bytes, row r) as 64 bytes of f16 subnormals,
+// n 2^-24 (elements 0, 1, 4, 5 of 8) or n 2^-20 (2, 3, 6, 7).
+__device__ __forceinline__ void spread_int4_piece(const uint4& x, uint8_t* dst, int r, int c0) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    const uint32_t t = w[v] >> 8;
+    *reinterpret_cast<uint4*>(dst + r * 128 + (((c0 + v) ^ (r & 7)) << 4)) =
+        make_uint4(w[v] & 0x000F000Fu, w[v] & 0x00F000F0u, t & 0x000F000Fu, t & 0x00F000F0u);
+  }
+}
+
+// A unit's piece of V: 32 codes (16 bytes, row r), as 64 bytes of f16: chunks c0 .. c0
 // + 3 of row r of a 128-byte swizzled tile.
 __device__ __forceinline__ void widen_int4_piece(const uint4& x, uint32_t params, uint8_t* dst,
                                                  int r, int c0) {
@@ -57,11 +74,12 @@ __device__ __forceinline__ void widen_int4_piece(const uint4& x, uint32_t params
 }
 
 // The Q tiles in place: row r of tile X times +-2^k, as f16, with 2^k bringing
-// the row's largest |q| to [2^14, 2^15); 2^-k goes to rs[X * 128 + r]. sign: of the
-// softmax scale (0: the row becomes zeros).
+// the row's largest |q| to [2^14, 2^15), elements 2, 3, 6, 7 of 8 a sixteenth of
+// that; 2^-k goes to rs[X * 128 + r], the sum of the scaled row to tau. sign: of
+// the softmax scale (0: the row becomes zeros).
 template <int D, bool F16>
-__device__ __forceinline__ void q_to_f16(uint8_t* q, float* rs, int tiles, float sign, int ct,
-                                         int threads) {
+__device__ __forceinline__ void q_to_f16(uint8_t* q, float* rs, float* tau, int tiles, float sign,
+                                         int ct, int threads) {
   using C = TcCfg<D>;
   for (int row = ct; row < tiles * C::BM; row += threads) {
     uint8_t* p = q + row / C::BM * C::Q_TILE + row % C::BM * 128;
@@ -82,6 +100,7 @@ __device__ __forceinline__ void q_to_f16(uint8_t* q, float* rs, int tiles, float
     const int up = ex == 255 ? 0 : min(126, 141 - ex);
     const float by = sign * __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
     rs[row] = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+    float sum = 0.f;
 #pragma unroll
     for (int c = 0; c < D / 8; ++c) {
       uint4* at = reinterpret_cast<uint4*>(p + (c >> 3) * C::Q_HALF + (((c & 7) ^ sw) << 4));
@@ -91,10 +110,13 @@ __device__ __forceinline__ void q_to_f16(uint8_t* q, float* rs, int tiles, float
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const float2 f = Elem<F16>::unpack(w[k]);
-        y[k] = pack_f16(f.x * by, f.y * by);
+        const float y0 = f.x * by, y1 = f.y * by;
+        sum += y0 + y1;
+        y[k] = (k & 1) ? pack_f16(y0 * 0.0625f, y1 * 0.0625f) : pack_f16(y0, y1);
       }
       *at = make_uint4(y[0], y[1], y[2], y[3]);
     }
+    tau[row] = sum;
   }
 }
 
@@ -139,6 +161,7 @@ int4_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       mbar_init(&bars->kw_free[b], 1);
       mbar_init(&bars->vw_free[b], 1);
     }
+    for (int b = 0; b < I::PARS; ++b) mbar_init(&bars->par_full[b], I::UNITS);
     for (int x = 0; x < 2; ++x) {
       mbar_init(&bars->s_full[x], 1);
       mbar_init(&bars->p_full[0][x], 128);
@@ -305,8 +328,9 @@ int4_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       bool ok = mbar_wait(&bars->q_full, 0);
       if (ok) {
         const float sign = a.scale_log2 > 0.f ? 1.f : a.scale_log2 < 0.f ? -1.f : 0.f;
-        q_to_f16<D, F16>(smem + C::OFF_Q, reinterpret_cast<float*>(smem + I::OFF_RS), two ? 2 : 1,
-                         sign, cw * 32 + lane, I::WARPS * 32);
+        q_to_f16<D, F16>(smem + C::OFF_Q, reinterpret_cast<float*>(smem + I::OFF_RS),
+                         reinterpret_cast<float*>(smem + I::OFF_TAU), two ? 2 : 1, sign,
+                         cw * 32 + lane, I::WARPS * 32);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         mbar_arrive(&bars->q_conv);
       }
@@ -326,16 +350,30 @@ int4_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         const uint8_t* sl = ring + i % I::SLOTS * I::SLOT;
         uint8_t* dst = smem + (is_v ? I::OFF_VW : I::OFF_KW) + buf * C::KV_TILE;
         const uint32_t* par = reinterpret_cast<const uint32_t*>(sl + 16 * D / 2);
+        const int r0 = u % I::UNITS * 16;                // of the tile
 #pragma unroll
         for (int x = 0; x < PER; ++x) {
           const int r = pr + x * (32 / PIECES);          // of the unit's 16
           const uint4 w = *reinterpret_cast<const uint4*>(sl + x * 512 + lane * 16);
-          widen_int4_piece(w, par[r], dst + (px >> 1) * C::KV_HALF, u % I::UNITS * 16 + r,
-                           (px & 1) * 4);
+          uint8_t* half = dst + (px >> 1) * C::KV_HALF;
+          if (is_v)
+            widen_int4_piece(w, par[r], half, r0 + r, (px & 1) * 4);
+          else
+            spread_int4_piece(w, half, r0 + r, (px & 1) * 4);
+        }
+        if (!is_v && lane < 16) {
+          const float2 sm = Elem<true>::unpack(par[lane]);
+          float* to = reinterpret_cast<float*>(smem + I::OFF_PAR + t % I::PARS * C::BN * 8) +
+                      (r0 + lane) / 2 * 4 + (lane & 1);
+          to[0] = sm.x * 0x1p24f;
+          to[2] = sm.y;
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) mbar_arrive(is_v ? &bars->vw_full[buf] : &bars->kw_full[buf]);
+        if (lane == 0) {
+          mbar_arrive(is_v ? &bars->vw_full[buf] : &bars->kw_full[buf]);
+          if (!is_v) mbar_arrive(&bars->par_full[t % I::PARS]);
+        }
       }
       cp_async_wait<0>();
       if (!ok) {

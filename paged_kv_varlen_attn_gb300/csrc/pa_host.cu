@@ -1445,10 +1445,10 @@ pa_status pa_gather_cache_int4(const void* key_cache, const void* value_cache,
 }
 
 // The kernels of a call over 4-bit pools, from host-known bounds only: decode of
-// at most 8 packed rows (nr = 1), short queries of more (nr = 2 or 4), prompts.
+// at most 8 packed rows (nr = 1), short queries of more (nr = 2 to 4), prompts.
 struct Int4Plan {
   bool few, some, many;
-  int nr;                // of `some`
+  int nr;                // of `some`: groups of 8 rows
   PassLayout tc;         // of `many`
   size_t parts, end;     // partial states of the decode kernels; all bytes
   size_t part_rows;
@@ -1458,8 +1458,9 @@ static Int4Plan plan_int4(const PassDims& d) {
   Int4Plan p{};
   const long long rows = static_cast<long long>(d.max_q) * d.G;
   p.few = d.G <= 8;
-  p.nr = rows <= 16 || 2 * d.G > kI4MaxRows ? 2 : 4;
-  if (d.G > 16) p.nr = 4;
+  // Its most rows: whole tokens within the bound and the class.
+  const long long most = rows < kI4MaxRows ? rows : static_cast<long long>(kI4MaxRows / d.G) * d.G;
+  p.nr = most <= 16 ? 2 : most <= 24 ? 3 : 4;
   p.some = d.max_q > 8 / d.G && kI4MaxRows / d.G > 8 / d.G;
   p.many = rows > kI4MaxRows;
   size_t off = 0;
@@ -1573,10 +1574,10 @@ pa_status pa_varlen_fwd_int4kv(const pa_kv_update* update, const void* q, int64_
   a.q_stride = q_token_stride;
   a.kc = static_cast<const uint8_t*>(key_cache);
   a.vc = static_cast<const uint8_t*>(value_cache);
-  a.block_stride_bytes = cache_block_stride;
+  a.page_bytes = static_cast<uint64_t>(cache_block_stride);
   a.k_params = kv.k_params;
   a.v_params = kv.v_params;
-  a.params_stride = kv.params_stride;
+  a.page_params = static_cast<uint64_t>(kv.params_stride);
   a.cu = cu_seqlens_q;
   a.seqused_k = seqused_k;
   a.bt = block_table;

@@ -302,18 +302,18 @@ struct Int4RowsArgs {
 cudaError_t launch_int4_rows(const Int4RowsArgs& a, int D, bool f16, cudaStream_t st, int sms);
 
 // Decode and short queries over 4-bit pools (int4_decode.cu): the sequences
-// with tokens_min < q_len <= tokens_max, at most 8 nr packed rows each (nr: 1,
-// 2 or 4).
+// with tokens_min < q_len <= tokens_max, at most 8 nr packed rows each (nr: 1 to
+// 4).
 constexpr int kI4MaxRows = 32;
 struct Int4DecodeArgs {
   const uint16_t* q;
   int64_t q_stride;
   const uint8_t* kc;
   const uint8_t* vc;
-  int64_t block_stride_bytes;
+  uint64_t page_bytes;            // between the pools' pages
   const uint32_t* k_params;       // (scale, minimum) f16 pairs: page b, head h, row r at
-  const uint32_t* v_params;       // b * params_stride + h * bs + r
-  int64_t params_stride;
+  const uint32_t* v_params;       // b * page_params + h * bs + r
+  uint64_t page_params;
   const int32_t* cu;
   const int32_t* seqused_k;
   const int32_t* bt;
