@@ -667,7 +667,8 @@ pa_status pa_evict(void* key_cache, void* value_cache, int64_t cache_block_strid
  *            32-bit little-endian word w holds element 8w + 2i in bits 4i .. 4i +
  *            3 and element 8w + 2i + 1 in bits 16 + 4i .. 19 + 4i.
  *   params : pairs of f16, (scale, minimum); row r of page b, KV head h is pair
- *            b * params_block_stride + h * block_size + r, 4-byte aligned.
+ *            b * params_block_stride + h * block_size + r; 16-byte aligned,
+ *            params_block_stride (in pairs) a multiple of 4.
  * A row x is written as follows, in float32 with every operation rounded once:
  *   elements beyond +-32752 count as +-32752;
  *   scale = f16((max x - min x) * (1 / 15)), minimum = f16(min x);

@@ -33,29 +33,43 @@ namespace pa {
 // The weights are 2^(score - m) against a running maximum m that is raised only
 // when a score passes it by more than 8; their sum is float32.
 //
-// Nothing is planned on the device and nothing depends on the key bound: the
-// slices (32 keys) of all sequences of the class, one after another, are cut
-// into equal ranges, and warp (range, KV head) streams its range through a ring
-// of its own, filled by asynchronous copies that run ahead across sequences.
-// Every warp counts the ranges for itself from the lengths. A sequence's state
-// that a range does not hold whole goes to the workspace (two slots per warp),
-// and int4_combine_kernel merges those, in order: no atomics, the same bits on
-// every run. The warps of neighbouring KV heads are neighbours, so a page's
-// bytes are read at about the same time.
+// Nothing is planned on the device and nothing depends on the key bound. A
+// block's warps are HB KV heads times KS runs of 32 keys; a slice is the 32 KS
+// keys that they take at a time. The slices of all sequences of the class, one
+// after another, are cut into equal ranges, one per block of a head group, and
+// every warp counts them for itself from the lengths. The block's warps take
+// turns at copying the slices into its ring, by TMA boxes of 16 keys x HB heads
+// that a lane issues per 16 keys; the copies run ahead across sequences. (A ring
+// per warp, filled by its own 16-byte copies, cost 158 of 604 instructions per 32
+// keys, and 64 sequences 77.4 us.)
+// A sequence's state that a warp does not hold whole goes to the workspace (two
+// slots per warp), and int4_combine_kernel merges those, in order: no atomics,
+// the same bits on every run.
 // ---------------------------------------------------------------------------
-constexpr int kI4Warps = 4;        // of a block; they share nothing
-constexpr int kI4Slots = 3;        // slices in a warp's ring
-constexpr int kI4MinSlices = 2;    // of a range
-constexpr int kI4Keys = 32;        // of a slice: two halves of 16, each in one page
+constexpr bool kI4WeightTerms = false;
+constexpr int kI4MinSlices = 1;    // of a range
+constexpr int kI4Keys = 32;        // of a warp: two halves of 16, each in one page
 
 template <int D, int NR>
 struct I4Cfg {
-  static constexpr int CODES = 16 * D / 2;             // bytes of a half's K or V
-  static constexpr int PAR = 4 * CODES;                // K of both halves, V of both, params
-  static constexpr int SLOT = PAR + 2 * kI4Keys * 4;
-  static constexpr int SMEM_BYTES = kI4Warps * kI4Slots * SLOT;
-  static constexpr int BLOCKS = NR == 1 ? 4 : 2;   // per SM
+  static constexpr int WARPS = 4;
+  static constexpr int THREADS = WARPS * 32;
+  static constexpr int BLOCKS = NR == 1 ? 4 : 2;       // per SM
+  static constexpr int STAGES = (NR == 1 ? 3 : 6) + (D == 64 ? 2 : 0);
+  // Of a stage: 16 keys of K of each warp, twice, as many of V, their params (of a
+  // half's heads at a TMA destination of its own, so on 128 bytes).
+  static constexpr int HALF = 16 * D / 2;              // 16 keys of a head
+  static constexpr int OFF_V = 2 * WARPS * HALF;
+  static constexpr int OFF_KP = 2 * OFF_V;
+  static constexpr int OFF_VP = OFF_KP + 2 * WARPS * 128;
+  static constexpr int STAGE = OFF_VP + 2 * WARPS * 128;
+  static constexpr int OFF_BAR = STAGES * STAGE;
+  static constexpr int SMEM_BYTES = OFF_BAR + 2 * STAGES * 8 + 64 + 1024;
 };
+static_assert(I4Cfg<128, 1>::STAGE % 1024 == 0 && I4Cfg<64, 1>::STAGE % 256 == 0, "swizzled tiles");
+static_assert(I4Cfg<64, 1>::BLOCKS * (I4Cfg<64, 1>::SMEM_BYTES + 1024) <= 228 * 1024, "blocks");
+static_assert(I4Cfg<128, 2>::BLOCKS * (I4Cfg<128, 2>::SMEM_BYTES + 1024) <= 228 * 1024, "blocks");
+static_assert(I4Cfg<128, 1>::BLOCKS * (I4Cfg<128, 1>::SMEM_BYTES + 1024) <= 228 * 1024, "blocks");
 
 // One sequence, as the kernels of this file count it.
 struct I4Seq {
@@ -79,191 +93,252 @@ __device__ __forceinline__ I4Seq i4_seq(const Int4DecodeArgs& a, int s, bool rep
   q.kv = min(max(q.kv, 0), a.kv_len_cap);
   const bool mine = q.q_len > a.tokens_min && q.q_len <= a.tokens_max;
   // A sequence without keys has one slice that nobody sees.
-  q.n = mine ? max(1, (q.kv + kI4Keys - 1) / kI4Keys) : 0;
+  q.n = mine ? max(1, static_cast<int>((q.kv + a.slice_keys - 1u) / a.slice_keys)) : 0;
   return q;
 }
 
+// D += A(16x16, row) * B(16x8, col), f16 operands: mma_16816_f16 left to the
+// compiler's scheduling.
+__device__ __forceinline__ void mma_codes(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                          uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7},"
+      " {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
 // 1 / x of a power of two.
 __device__ __forceinline__ float inverse_power(float x) {
   return __uint_as_float((254u << 23) - __float_as_uint(x));
 }
 
+// A quotient; numbers of this size hardly ever need 64 bits.
+__device__ __forceinline__ long long i4_div(long long a, long long b) {
+  return (a | b) >> 32 ? a / b : static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+}
 // Slices of a range, given all of them.
 __device__ __forceinline__ long long i4_per_range(const Int4DecodeArgs& a, long long total) {
-  const long long per = (total + a.ranges - 1) / a.ranges;
+  const long long per = i4_div(total + a.ranges - 1, a.ranges);
   return per < kI4MinSlices ? kI4MinSlices : per;
 }
+// Token of a packed row (below 32).
+__device__ __forceinline__ int i4_token(const Int4DecodeArgs& a, int row) {
+  return row * a.g_inv >> 16;
+}
 
-template <int D, bool F16, int NR>
-__global__ void __launch_bounds__(kI4Warps * 32, I4Cfg<D, NR>::BLOCKS)
-int4_decode_kernel(const __grid_constant__ Int4DecodeArgs a) {
-  using C = I4Cfg<D, NR>;
-  using E = Elem<F16>;
-  constexpr int KW = D / 32;       // words of a key per lane in S^T
-  constexpr int VW = D / 64;       // words of a key per lane in O^T
+// Where a range starts: the sequence base + at (base a multiple of 32), its slice
+// i, slice `begin` of all; and the range's slices (0: none).
+struct I4Start {
+  int base, at, i, count;
+  long long begin;
+};
+
+// By one warp; the last block's leaves each sequence's first slice and the
+// slices of a range to the combine kernel, in a.table.
+__device__ __forceinline__ I4Start i4_start(const Int4DecodeArgs& a, int range, bool report,
+                                            bool table) {
   constexpr unsigned kAll = 0xffffffffu;
-  extern __shared__ __align__(128) uint8_t smem[];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = lane >> 2, c = lane & 3;
-  pdl_trigger();                   // the combine kernel may be placed when these blocks have been
-  const int wid = static_cast<int>(blockIdx.x) * kI4Warps + warp;
-  const int range = wid / a.H_kv, hk = wid - range * a.H_kv;
-  if (range >= a.ranges) return;
-
-  // All slices, then this warp's range and the sequence in which it starts.
+  const int lane = threadIdx.x & 31;
+  I4Start f{};
   long long total = 0;
-  for (int s = lane; s < a.num_seqs; s += 32) total += i4_seq(a, s, wid == 0).n;
+  for (int s = lane; s < a.num_seqs; s += 32) total += i4_seq(a, s, report).n;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kAll, total, o);
   const long long per = i4_per_range(a, total);
-  const long long begin = range * per;
-  if (begin >= total) return;
-  const int count = static_cast<int>(min(per, total - begin));
-  int base = 0;                    // lane i holds sequence base + i
+  f.begin = range * per;
+  f.count = static_cast<int>(max(0ll, min(per, total - f.begin)));
+  if (f.count == 0 && !table) return f;
+  if (table && lane == 0) a.table[0] = per;
+  bool found = false;
   long long before = 0;            // slices of the sequences in front of base
-  I4Seq sq;
-  int first = 0;                   // lane of the first sequence
-  for (;; base += 32) {
-    if (base >= a.num_seqs) return;                    // (lengths changed under the call)
-    sq = I4Seq{0, 0, 0, 0};
-    if (base + lane < a.num_seqs) sq = i4_seq(a, base + lane, false);
-    long long incl = sq.n;
+  for (int base = 0; base < a.num_seqs; base += 32) {
+    const int n = base + lane < a.num_seqs ? i4_seq(a, base + lane, false).n : 0;
+    int incl = n;                  // (32 times 2^25 slices: 31 bits)
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(kAll, incl, o);
+      const int x = __shfl_up_sync(kAll, incl, o);
       if (lane >= o) incl += x;
     }
-    const unsigned past = __ballot_sync(kAll, before + incl > begin);
-    if (past) {
-      first = __ffs(past) - 1;
-      before += __shfl_sync(kAll, incl - sq.n, first);
-      break;
+    if (table && base + lane < a.num_seqs) a.table[1 + base + lane] = before + incl - n;
+    const unsigned past = __ballot_sync(kAll, before + incl > f.begin);
+    if (past && !found) {
+      found = true;
+      f.base = base;
+      f.at = __ffs(past) - 1;
+      f.i = static_cast<int>(f.begin - (before + __shfl_sync(kAll, incl - n, f.at)));
+      if (!table) break;
     }
     before += __shfl_sync(kAll, incl, 31);
   }
-  int i = static_cast<int>(begin - before);            // slice of the sequence
+  if (!found) f.count = 0;         // (or the lengths changed under the call)
+  return f;
+}
 
-  // ---------------------------------------------------------------- copies
-  // The next slice to copy: slice f_i of f_n of the sequence in lane f_at of the
-  // 32 whose lengths the lanes hold from f_base on. Lane x holds the page and the
-  // row of half f_half0 + x of that sequence.
-  int f_base = base, f_at = first, f_kv_l = sq.kv, f_n_l = sq.n;
-  int f_i = i, f_n = __shfl_sync(kAll, f_n_l, f_at), f_kv = __shfl_sync(kAll, f_kv_l, f_at);
-  int f_half0 = 0, f_left = count;
-  int page_l = -1, row_l = 0;
-  auto load_pages = [&]() {
-    f_half0 = 2 * f_i;
-    const int key0 = (f_half0 + lane) * 16;
-    page_l = -1;
-    row_l = 0;
-    if (key0 < f_kv) {
+// Bytes between the params of a stage's halves.
+__device__ __forceinline__ int i4_par_pitch(const Int4DecodeArgs& a) {
+  return (a.heads_per_block * 64 + 127) & ~127;
+}
+
+// A warp's turns at copying: every WARPS-th slice of the block's range.
+template <int D, int NR>
+struct I4Copier {
+  using C = I4Cfg<D, NR>;
+  int base, at, n_l, kv_l;       // lane x holds the lengths of sequence base + x
+  int i, n, kv;                  // the next slice, of sequence base + at
+  int turn;                      // its place in the range
+  int slot, phase;               // its slot, and the parity of the slot's last use
+  int page, row;                 // lane h: of its half h
+
+  __device__ __forceinline__ void load_pages(const Int4DecodeArgs& a) {
+    const int lane = threadIdx.x & 31, halves = 2 * a.key_runs;
+    page = a.num_blocks;                               // outside the pool: reads as zeros
+    row = 0;
+    const int key0 = (i * halves + lane) * 16;
+    if (lane < halves && key0 < kv) {
       const int lp = a.bs_shift >= 0 ? key0 >> a.bs_shift : key0 / a.bs;
-      row_l = key0 - lp * a.bs;
-      page_l = __ldg(a.bt + static_cast<int64_t>(f_base + f_at) * a.bt_stride + lp);
-      if (page_l < 0 || page_l >= a.num_blocks) {
-        page_l = -1;                                   // reads as zeros
+      row = key0 - lp * a.bs;
+      page = __ldg(a.bt + static_cast<int64_t>(base + at) * a.bt_stride + lp);
+      if (page < 0 || page >= a.num_blocks) {
+        page = a.num_blocks;
         flag_status(a.status, PA_DEV_BAD_PAGE);
       }
     }
-  };
-  load_pages();
-  uint8_t* ring = smem + warp * (kI4Slots * C::SLOT);
-  const uint32_t ring_at = smem_u32(ring);
-  const int rstep = a.H_kv * (D / 2);                  // (checked to fit by the host)
-  // Row g of S^T is key (g >> 1) + 4 (g & 1) of the half's halves: so the four
-  // keys of a lane in O^T, 2c and 2c + 1 of each, are rows c and c + 4 of shared
-  // memory, and eight lanes that read them take different banks.
-  const int kg = (g >> 1) + 4 * (g & 1);
-  // What this lane copies of a half. D = 128: of K its own pieces (rows kg and kg
-  // + 8), of V piece c of rows g and g + 8 to place c ^ (g & 2); D = 64: piece
-  // lane & 1 of row lane / 2 of both. And one row's scale and minimum, of K in
-  // lanes 0-15, of V in the others: those of keys x, x + 8, x + 16, x + 24 of the
-  // slice side by side.
-  const int k_row = D == 128 ? kg : lane >> 1, v_row = D == 128 ? g : lane >> 1;
-  const int piece = D == 128 ? c : lane & 1;
-  const uint8_t* k_src = a.kc + hk * (D / 2) + static_cast<int64_t>(k_row) * rstep + piece * 16;
-  const uint8_t* v_src = a.vc + hk * (D / 2) + static_cast<int64_t>(v_row) * rstep + piece * 16;
-  const int p_row = lane & 15;
-  const uint32_t* p_src = (lane < 16 ? a.k_params : a.v_params) +
-                          static_cast<int64_t>(hk) * a.bs + p_row;
-  const uint32_t v_place = D == 128 ? g * 64 + ((c ^ (g & 2)) << 4) : lane * 16;
-  const uint32_t p_place = C::PAR + (lane >> 4) * (kI4Keys * 4) + (p_row & 7) * 16 + (p_row >> 3) * 4;
-  auto fetch = [&](int slot) {
-    if (f_left > 0) {
-      if (f_i == f_n) {                                // the next sequence that has slices
-        for (;;) {
-          const unsigned later = __ballot_sync(kAll, f_n_l > 0) & ~((2u << f_at) - 1u);
-          if (later) {
-            f_at = __ffs(later) - 1;
-            break;
+  }
+  // On by so many slices, across sequences; there are as many.
+  __device__ __forceinline__ void advance(const Int4DecodeArgs& a, int by) {
+    i += by;
+    if (i >= n) next_sequence(a);
+    load_pages(a);
+  }
+  __device__ __forceinline__ void next_sequence(const Int4DecodeArgs& a) {
+    constexpr unsigned kAll = 0xffffffffu;
+    const int lane = threadIdx.x & 31;
+    while (i >= n) {
+      i -= n;
+      do {
+        if (++at == 32) {
+          at = 0;
+          base += 32;
+          n_l = kv_l = 0;
+          if (base + lane < a.num_seqs) {
+            const I4Seq q = i4_seq(a, base + lane, false);
+            n_l = q.n;
+            kv_l = q.kv;
           }
-          f_base += 32;
-          if (f_base >= a.num_seqs) {                  // (lengths changed under the call)
-            f_left = 0;
-            break;
-          }
-          f_n_l = 0;
-          if (f_base + lane < a.num_seqs) {
-            const I4Seq x = i4_seq(a, f_base + lane, false);
-            f_n_l = x.n;
-            f_kv_l = x.kv;
-          }
-          const unsigned any = __ballot_sync(kAll, f_n_l > 0);
-          if (any) {
-            f_at = __ffs(any) - 1;
-            break;
-          }
-          f_at = 31;
         }
-        if (f_left == 0) {
-          cp_async_commit();
-          return;
-        }
-        f_n = __shfl_sync(kAll, f_n_l, f_at);
-        f_kv = __shfl_sync(kAll, f_kv_l, f_at);
-        f_i = 0;
-        load_pages();
-      } else if (2 * f_i - f_half0 == 32) {
-        load_pages();
+        n = __shfl_sync(kAll, n_l, at);
+      } while (n == 0 && base < a.num_seqs);
+      kv = __shfl_sync(kAll, kv_l, at);
+      if (n == 0) {                                    // (lengths changed under the call)
+        i = kv = 0;
+        break;
       }
-      const uint32_t dst0 = ring_at + slot * C::SLOT;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int page = __shfl_sync(kAll, page_l, 2 * f_i - f_half0 + h);
-        const uint32_t prow = __shfl_sync(kAll, row_l, 2 * f_i - f_half0 + h);
-        const uint32_t dst = dst0 + h * C::CODES;
-        if (page >= 0) {
-          const uint64_t at = static_cast<uint64_t>(static_cast<uint32_t>(page)) * a.page_bytes +
-                              static_cast<uint64_t>(prow) * static_cast<uint32_t>(rstep);
-          const uint8_t* kp = k_src + at;
-          const uint8_t* vp = v_src + at;
-          cp_async16(dst + lane * 16, kp);
-          cp_async16(dst + 2 * C::CODES + v_place, vp);
-          if constexpr (D == 128) {
-            cp_async16(dst + 512 + lane * 16, kp + 8 * rstep);
-            cp_async16(dst + 2 * C::CODES + 512 + v_place, vp + 8 * rstep);
-          }
-          // Scales and minima; zeros past the sequence (what is there is nobody's).
-          cp_async4(dst0 + p_place + h * 8,
-                    p_src + static_cast<uint64_t>(static_cast<uint32_t>(page)) * a.page_params + prow,
-                    32 * f_i + 16 * h + p_row < f_kv);
-        } else {
-          // No page: codes do not matter where scale and minimum are zero, but
-          // they must be some.
-          cp_async4(dst0 + p_place + h * 8, p_src, false);
-        }
-      }
-      ++f_i;
-      --f_left;
     }
-    cp_async_commit();
-  };
-#pragma unroll
-  for (int u = 0; u < kI4Slots - 1; ++u) fetch(u);
+  }
+  // The slice into its slot, once the slot's last one is used; on to the next.
+  __device__ __forceinline__ bool copy(const Int4DecodeArgs& a, const CUtensorMap* tm,
+                                       uint8_t* smem, uint64_t* full, uint64_t* empty, int head0,
+                                       int count) {
+    const int lane = threadIdx.x & 31;
+    bool ok = true;
+    if (turn >= C::STAGES) ok = mbar_wait(&empty[slot], phase ^ 1);
+    if (!__all_sync(0xffffffffu, ok)) return false;
+    if (lane == 0)
+      mbar_arrive_expect_tx(&full[slot],
+                            2 * a.key_runs * a.heads_per_block * (2 * C::HALF + 128));
+    __syncwarp();
+    if (lane < 2 * a.key_runs) {
+      uint8_t* st = smem + slot * C::STAGE;
+      const int of = lane * a.heads_per_block, p_of = lane * i4_par_pitch(a);
+      tma_load_4d(st + of * C::HALF, tm, &full[slot], 0, row, head0, page);
+      tma_load_4d(st + C::OFF_V + of * C::HALF, tm + 1, &full[slot], 0, row, head0, page);
+      tma_load_3d(st + C::OFF_KP + p_of, tm + 2, &full[slot], row, head0, page);
+      tma_load_3d(st + C::OFF_VP + p_of, tm + 3, &full[slot], row, head0, page);
+    }
+    for (slot += C::WARPS; slot >= C::STAGES; slot -= C::STAGES) phase ^= 1;
+    turn += C::WARPS;
+    if (turn < count) advance(a, C::WARPS);
+    return true;
+  }
+};
 
-  // ---------------------------------------------------------------- sequences
-  int at = first, left = count;
-  int slot = 0, to = kI4Slots - 1;
+template <int D, bool F16, int NR>
+__global__ void __launch_bounds__(I4Cfg<D, NR>::THREADS, I4Cfg<D, NR>::BLOCKS)
+int4_decode_kernel(const __grid_constant__ Int4Maps maps, const __grid_constant__ Int4DecodeArgs a) {
+  using C = I4Cfg<D, NR>;
+  using E = Elem<F16>;
+  constexpr int KW = D / 32;       // words of a key per lane in S^T
+  constexpr int CH = D / 32;       // 16-byte pieces of a key
+  constexpr int WT = kI4WeightTerms && F16 ? 2 : 1;   // of W
+  constexpr unsigned kAll = 0xffffffffu;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* empty = full + C::STAGES;
+  I4Start* start = reinterpret_cast<I4Start*>(empty + C::STAGES);
+  volatile int* abort = reinterpret_cast<volatile int*>(start + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, c = lane & 3;
+  pdl_trigger();                   // the combine kernel may be placed when these blocks have been
+  const int groups = a.H_kv / a.heads_per_block;
+  const int range = static_cast<int>(blockIdx.x) / groups;
+  const int group = static_cast<int>(blockIdx.x) - range * groups;
+  const int consumers = a.heads_per_block * a.key_runs;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], consumers);
+    }
+    *abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1 && lane < 4) tma_prefetch_desc(maps.m + lane);
+  pdl_wait();                      // what the stream did before is done (see the launcher)
+  if (warp == 0) {
+    const I4Start f = i4_start(a, range, blockIdx.x == 0, blockIdx.x == gridDim.x - 1);
+    if (lane == 0) *start = f;
+  }
+  __syncthreads();
+  I4Start from = *start;
+  if (from.count == 0) return;
+  I4Seq sq{0, 0, 0, 0};            // lane x holds sequence base + x
+  if (from.base + lane < a.num_seqs) sq = i4_seq(a, from.base + lane, false);
+  const int head0 = group * a.heads_per_block;
+  I4Copier<D, NR> copier;
+  copier.base = from.base;
+  copier.at = from.at;
+  copier.n_l = sq.n;
+  copier.kv_l = sq.kv;
+  copier.i = from.i;
+  copier.n = __shfl_sync(kAll, sq.n, from.at);
+  copier.kv = __shfl_sync(kAll, sq.kv, from.at);
+  copier.turn = warp;
+  copier.slot = warp % C::STAGES;
+  copier.phase = (warp / C::STAGES) & 1;
+  bool ok = true;
+  if (warp < from.count) copier.advance(a, warp);
+  // The first slices: turns 0 .. STAGES - 2.
+  while (copier.turn < min(C::STAGES - 1, from.count))
+    copier.copy(a, maps.m, smem, full, empty, head0, from.count);
+  int base = from.base, at = from.at, i = from.i;
+  const long long begin = from.begin;
+  const int run = warp / a.heads_per_block, hl = warp - run * a.heads_per_block;
+  const int hk = head0 + hl;
+  const bool idle = warp >= consumers;                 // copies only
+
+  // This warp's first half in a stage, and from there to the second.
+  const int k_at = (2 * run * a.heads_per_block + hl) * C::HALF, k_next = a.heads_per_block * C::HALF;
+  const int p_next = i4_par_pitch(a), p_at = C::OFF_KP + 2 * run * p_next + hl * 64;
+  // Row g (g + 8) of S^T is key g (g + 8) of a half; the tiles are swizzled: 16-byte
+  // piece x of row r lies at x ^ (r / 2 % 4) of four (D = 64: x ^ (r / 4 % 2) of two).
+  const int k_piece = D == 128 ? (c ^ ((g >> 1) & 3)) * 16 : ((c >> 1) ^ ((g >> 2) & 1)) * 16 + (c & 1) * 8;
+  // This lane's row address in the transposed loads: matrices keys 0-7 | 8-15 of a
+  // piece, then of the next.
+  const uint32_t smem_at = smem_u32(smem);
+  const int v_row = (lane & 7) + ((lane >> 3) & 1) * 8, v_half = lane >> 4;
+  const int v_swizzle = D == 128 ? (v_row >> 1) & 3 : (v_row >> 2) & 1;
+  int left = from.count, t = 0, slot = 0;
+  uint32_t phase = 0;
   long long flat = begin;          // slice of all slices at which this part starts
 #pragma unroll 1
   while (left > 0) {
@@ -290,7 +365,7 @@ int4_decode_kernel(const __grid_constant__ Int4DecodeArgs a) {
     float sa[NR][2], sb[NR][2];    // of rows 2c, 2c + 1: scale of q.n, and of sum(q)
 #pragma unroll
     for (int nr = 0; nr < NR; ++nr) {
-      const int r = min(8 * nr + g, rows - 1), t = r / a.G;
+      const int r = min(8 * nr + g, rows - 1), t = i4_token(a, r);
       const uint4* qrow = reinterpret_cast<const uint4*>(
           a.q + static_cast<int64_t>(q0 + t) * a.q_stride +
           static_cast<int64_t>(hk * a.G + r - t * a.G) * D + c * (8 * KW));
@@ -367,50 +442,74 @@ int4_decode_kernel(const __grid_constant__ Int4DecodeArgs a) {
     };
 
 #pragma unroll 1
-    for (; i < i1; ++i) {
-      fetch(to);
-      if (++to == kI4Slots) to = 0;
-      cp_async_wait<kI4Slots - 1>();
-      __syncwarp();
-      const uint8_t* sl = ring + slot * C::SLOT;
-      const int key0 = kI4Keys * i;
+    for (; i < i1; ++i, ++t, ++slot) {
+      if (slot == C::STAGES) {
+        slot = 0;
+        phase ^= 1;
+      }
+      // In turn, the slice that goes where the last one was: the other warps have
+      // had this one's time to be done with that.
+      const bool mine = copier.turn == t + C::STAGES - 1 && copier.turn < from.count;
+      if (idle) {
+        if (mine) ok = copier.copy(a, maps.m, smem, full, empty, head0, from.count);
+        continue;
+      }
+      ok = __all_sync(kAll, ok && mbar_wait(&full[slot], phase));
+      if (!ok) break;
+      const uint8_t* sl = smem + slot * C::STAGE;
+      const uint32_t sl_at = smem_at + slot * C::STAGE;
+      const int key0 = (i * a.key_runs + run) * kI4Keys;
+      if (key0 >= kv) {                                // none of this warp's
+        if (mine) ok = copier.copy(a, maps.m, smem, full, empty, head0, from.count);
+        if (lane == 0) mbar_arrive(&empty[slot]);
+        continue;
+      }
       // ----------------------------------------------------------- S^T = N Q^T
       float st[NR][2][4];
 #pragma unroll
       for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
         for (int h = 0; h < 2; ++h) st[nr][h][0] = st[nr][h][1] = st[nr][h][2] = st[nr][h][3] = 0.f;
+      uint32_t w0[2][KW], w1[2][KW];                   // keys g, g + 8 of each half
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        uint32_t w0[KW], w1[KW];
+        const uint8_t* kt = sl + k_at + h * k_next + g * (D / 2) + k_piece;
         if constexpr (D == 128) {
-          const uint4 x0 = *reinterpret_cast<const uint4*>(sl + h * C::CODES + lane * 16);
-          const uint4 x1 = *reinterpret_cast<const uint4*>(sl + h * C::CODES + 512 + lane * 16);
-          w0[0] = x0.x; w0[1] = x0.y; w0[2] = x0.z; w0[3] = x0.w;
-          w1[0] = x1.x; w1[1] = x1.y; w1[2] = x1.z; w1[3] = x1.w;
+          const uint4 x0 = *reinterpret_cast<const uint4*>(kt);
+          const uint4 x1 = *reinterpret_cast<const uint4*>(kt + 8 * (D / 2));
+          w0[h][0] = x0.x; w0[h][1] = x0.y; w0[h][2] = x0.z; w0[h][3] = x0.w;
+          w1[h][0] = x1.x; w1[h][1] = x1.y; w1[h][2] = x1.z; w1[h][3] = x1.w;
         } else {
-          const uint2 x0 = *reinterpret_cast<const uint2*>(sl + h * C::CODES + kg * 32 + c * 8);
-          const uint2 x1 = *reinterpret_cast<const uint2*>(sl + h * C::CODES + (8 + kg) * 32 + c * 8);
-          w0[0] = x0.x; w0[1] = x0.y;
-          w1[0] = x1.x; w1[1] = x1.y;
+          const uint2 x0 = *reinterpret_cast<const uint2*>(kt);
+          const uint2 x1 = *reinterpret_cast<const uint2*>(kt + 8 * (D / 2));
+          w0[h][0] = x0.x; w0[h][1] = x0.y;
+          w1[h][0] = x1.x; w1[h][1] = x1.y;
         }
+      }
 #pragma unroll
-        for (int v = 0; v < KW; ++v) {
+      for (int v = 0; v < KW; ++v) {
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const uint32_t a0 = w0[v] >> (8 * k), a1 = w1[v] >> (8 * k);
+        for (int k = 0; k < 2; ++k) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t a0 = w0[h][v] >> (8 * k), a1 = w1[h][v] >> (8 * k);
 #pragma unroll
             for (int nr = 0; nr < NR; ++nr)
-              mma_16816_f16(st[nr][h], a0 & 0x000F000Fu, a1 & 0x000F000Fu, a0 & 0x00F000F0u,
-                            a1 & 0x00F000F0u, qf[nr][2 * v + k][0], qf[nr][2 * v + k][1]);
+              mma_codes(st[nr][h], a0 & 0x000F000Fu, a1 & 0x000F000Fu, a0 & 0x00F000F0u,
+                        a1 & 0x00F000F0u, qf[nr][2 * v + k][0], qf[nr][2 * v + k][1]);
           }
         }
       }
       // ----------------------------------------------------------- softmax
-      // Keys kg + 8 h of the slice, h = 0 .. 3: entries 2 (h & 1) of st[h >> 1].
-      const uint4 pk = *reinterpret_cast<const uint4*>(sl + C::PAR + kg * 16);
-      const uint4 pv = *reinterpret_cast<const uint4*>(sl + C::PAR + kI4Keys * 4 + kg * 16);
-      const uint32_t pkw[4] = {pk.x, pk.y, pk.z, pk.w}, pvw[4] = {pv.x, pv.y, pv.z, pv.w};
+      // Keys 8 h + g of the warp's, h = 0 .. 3: entries 2 (h & 1) of st[h >> 1].
+      const uint8_t* par = sl + p_at + g * 4;
+      uint32_t pkw[4], pvw[4];
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        const uint8_t* p = par + (h >> 1) * p_next + (h & 1) * 32;
+        pkw[h] = *reinterpret_cast<const uint32_t*>(p);
+        pvw[h] = *reinterpret_cast<const uint32_t*>(p + (C::OFF_VP - C::OFF_KP));
+      }
       float ks[4], km[4], vs[4], vm[4];
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
@@ -418,9 +517,14 @@ int4_decode_kernel(const __grid_constant__ Int4DecodeArgs a) {
         ks[h] = k.x * 0x1p24f;
         km[h] = k.y;
         vs[h] = v.x;
-        vm[h] = fmaf(8.f, v.x, v.y);
+        vm[h] = F16 ? fmaf(8.f, v.x, v.y) : v.y;
       }
       const bool whole = key0 + kI4Keys <= seen_by_all;
+      if (!whole) {                                    // what lies past the sequence is nobody's
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+          if (key0 + 8 * h + g >= kv) vs[h] = vm[h] = 0.f;
+      }
       const float vtop = fmaxf(fmax3(vs[0], vs[1], vs[2]), vs[3]);
       if (__any_sync(kAll, vtop > ref)) {              // raise the reference of V's scales
         float top = vtop;
@@ -442,7 +546,7 @@ int4_decode_kernel(const __grid_constant__ Int4DecodeArgs a) {
       }
       // W = weight x scale / ref x 2^6: at most 2^8 x 1 x 2^6 = 2^14.
       const float wscale = ref == 0.f ? 0.f : 64.f * inverse_power(ref);
-      uint32_t wb[NR][4];
+      uint32_t wb[NR][WT][4];
 #pragma unroll
       for (int nr = 0; nr < NR; ++nr) {
         float x[4][2];
@@ -458,10 +562,10 @@ int4_decode_kernel(const __grid_constant__ Int4DecodeArgs a) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int row = min(8 * nr + 2 * c + e, rows - 1);
-            const int lim = a.causal ? past + row / a.G : kv - 1;   // last visible key
+            const int lim = a.causal ? past + i4_token(a, row) : kv - 1;   // last visible key
 #pragma unroll
             for (int h = 0; h < 4; ++h)
-              if (key0 + kg + 8 * h > lim) x[h][e] = -INFINITY;
+              if (key0 + 8 * h + g > lim) x[h][e] = -INFINITY;
           }
         }
         const float x0 = fmaxf(fmax3(x[0][0], x[1][0], x[2][0]), x[3][0]);
@@ -508,58 +612,63 @@ int4_decode_kernel(const __grid_constant__ Int4DecodeArgs a) {
           }
         }
 #pragma unroll
-        for (int h = 0; h < 4; ++h) wb[nr][h] = movmatrix_trans(pack_f16(w[h][0], w[h][1]));
+        for (int h = 0; h < 4; ++h) {
+          const uint32_t top = pack_f16(w[h][0], w[h][1]);
+          wb[nr][0][h] = movmatrix_trans(top);
+          if constexpr (WT == 2) {
+            const float2 f = Elem<true>::unpack(top);
+            wb[nr][WT - 1][h] = movmatrix_trans(pack_f16(w[h][0] - f.x, w[h][1] - f.y));
+          }
+        }
       }
       // ----------------------------------------------------------- O^T += N^T W^T
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        uint32_t wv[4][VW];        // keys c, c + 4, c + 8, c + 12 of the half; 8 VW dims
-        const uint8_t* vt = sl + (2 + h) * C::CODES;
+        // Transposed loads: 16 bits of a key (four elements of one parity) are an
+        // element of an 8x8 matrix, so a register holds them of two keys.
+        const uint32_t vt = sl_at + C::OFF_V + k_at + h * k_next + v_row * (D / 2);
+        uint32_t wv[CH][2];        // piece x, keys 2c, 2c + 1 and 2c + 8, 2c + 9
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int r = c + 4 * k;
-          if constexpr (D == 128) {
-            const uint2 x = *reinterpret_cast<const uint2*>(
-                vt + r * 64 + (((g >> 1) ^ (r & 2)) << 4) + (g & 1) * 8);
-            wv[k][0] = x.x;
-            wv[k][1] = x.y;
-          } else {
-            wv[k][0] = *reinterpret_cast<const uint32_t*>(vt + r * 32 + g * 4);
-          }
+        for (int x = 0; x < CH; x += 2)
+          ldsm_x4_t(vt + (((x + v_half) ^ v_swizzle) << 4), wv[x][0], wv[x][1], wv[x + 1][0],
+                    wv[x + 1][1]);
+        if constexpr (F16) {
+#pragma unroll
+          for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+            for (int y = 0; y < WT; ++y)
+              mma_codes(accw[nr], 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u,
+                        wb[nr][y][2 * h], wb[nr][y][2 * h + 1]);
         }
 #pragma unroll
-        for (int nr = 0; nr < NR; ++nr)
-          mma_16816_f16(accw[nr], 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u,
-                        wb[nr][2 * h], wb[nr][2 * h + 1]);
+        for (int x = 0; x < CH; ++x) {
 #pragma unroll
-        for (int j = 0; j < VW; ++j) {
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t u0 = wv[x][0] >> (8 * k), u1 = wv[x][1] >> (8 * k);
 #pragma unroll
-          for (int odd = 0; odd < 2; ++odd) {
-            const uint32_t t0 = prmt(wv[0][j], wv[1][j], odd ? 0x7632 : 0x5410);
-            const uint32_t t1 = prmt(wv[2][j], wv[3][j], odd ? 0x7632 : 0x5410);
+            for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const uint32_t u0 = t0 >> (8 * k), u1 = t1 >> (8 * k);
-#pragma unroll
-              for (int nr = 0; nr < NR; ++nr)
-                mma_16816_f16(acc[nr][4 * j + 2 * odd + k], u0 & 0x000F000Fu, u0 & 0x00F000F0u,
-                              u1 & 0x000F000Fu, u1 & 0x00F000F0u, wb[nr][2 * h], wb[nr][2 * h + 1]);
-            }
+              for (int y = 0; y < WT; ++y)
+                mma_codes(acc[nr][2 * x + k], u0 & 0x000F000Fu, u0 & 0x00F000F0u, u1 & 0x000F000Fu,
+                          u1 & 0x00F000F0u, wb[nr][y][2 * h], wb[nr][y][2 * h + 1]);
           }
         }
       }
-      if ((i & 3) == 3) centre();
-      if (++slot == kI4Slots) slot = 0;
-      __syncwarp();                                    // the slot may be filled again
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[slot]);        // the slot may be filled again
+      if (mine) ok = copier.copy(a, maps.m, smem, full, empty, head0, from.count);
+      if (F16 && (i & 3) == 3) centre();
     }
-    centre();
+    if (!ok) break;
+    if (F16 && !idle) centre();
 
     // ---------------------------------------------------------------- the state
-    // acc[4 j + 2 odd + k] holds, of this lane's 8 j .. 8 j + 7 dims, 4 k + odd
-    // (entries 0, 1: rows 2c, 2c + 1) and 4 k + 2 + odd (2, 3; sixteenfold).
-    const bool all = i0 == 0 && i1 == n;
+    // acc[2 x + k] holds elements 32 x + 8 (g / 2) + g % 2 + 4 k (entries 0, 1: rows
+    // 2c, 2c + 1) and 2 further (2, 3; sixteenfold): with lane ^ 4, eight of a row.
+    const bool all = i0 == 0 && i1 == n && a.key_runs == 1;
 #pragma unroll
     for (int nr = 0; nr < NR; ++nr) {
+      if (idle) break;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         float L = l[nr][e], V = lv[nr][e];
@@ -569,40 +678,41 @@ int4_decode_kernel(const __grid_constant__ Int4DecodeArgs a) {
           V += __shfl_xor_sync(kAll, V, o);
         }
         const int row = 8 * nr + 2 * c + e;
-        if (row >= rows) continue;
-        const int t = row / a.G, head = hk * a.G + row - t * a.G;
+        const int t = i4_token(a, min(row, rows - 1)), head = hk * a.G + min(row, rows - 1) - t * a.G;
         float M = m[nr][e], of = 1.f;
         const float fw = ref * (0x1p24f / 64.f);       // of the sums of codes
         if (all && a.sinks) of = add_sink(M, L, __ldg(a.sinks + head) * kLog2e);
         const float inv = L == 0.f ? 0.f : of / L;
         const float lse = L == 0.f ? -INFINITY : (M + fast_log2(L)) * kLn2;
-        float o[VW][8];
+        const int64_t at_row =
+            ((static_cast<int64_t>(blockIdx.x) * C::WARPS + warp) * 2 + (flat == begin ? 0 : 1)) *
+                (8 * NR) + row;
 #pragma unroll
-        for (int j = 0; j < VW; ++j)
+        for (int x = 0; x < CH; ++x) {
+          float o[4];                                  // elements 2 j + g % 2 of eight
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {                // x = 2 odd + k
-            const int d = 4 * (x & 1) + (x >> 1);
-            o[j][d] = fmaf(acc[nr][4 * j + x][e], fw, V) * inv;
-            o[j][d + 2] = fmaf(acc[nr][4 * j + x][2 + e], fw * 0.0625f, V) * inv;
+          for (int k = 0; k < 2; ++k) {
+            o[2 * k] = fmaf(acc[nr][2 * x + k][e], fw, V) * inv;
+            o[2 * k + 1] = fmaf(acc[nr][2 * x + k][2 + e], fw * 0.0625f, V) * inv;
           }
-        if (all) {
-          uint4* dst = reinterpret_cast<uint4*>(
-              a.out + (static_cast<int64_t>(q0 + t) * a.H + head) * D + g * (8 * VW));
-#pragma unroll
-          for (int j = 0; j < VW; ++j)
-            dst[j] = make_uint4(E::pack(o[j][0], o[j][1]), E::pack(o[j][2], o[j][3]),
-                                E::pack(o[j][4], o[j][5]), E::pack(o[j][6], o[j][7]));
-          if (a.lse && g == 0) a.lse[static_cast<int64_t>(head) * a.total_q + q0 + t] = lse;
-        } else {
-          const int64_t at_row =
-              (static_cast<int64_t>(wid) * 2 + (flat == begin ? 0 : 1)) * (8 * NR) + row;
-          float4* dst = reinterpret_cast<float4*>(a.part_o + at_row * D + g * (8 * VW));
-#pragma unroll
-          for (int j = 0; j < VW; ++j) {
-            __stcg(dst + 2 * j, make_float4(o[j][0], o[j][1], o[j][2], o[j][3]));
-            __stcg(dst + 2 * j + 1, make_float4(o[j][4], o[j][5], o[j][6], o[j][7]));
-          }
-          if (g == 0) __stcg(a.part_lse + at_row, lse);
+          // An even row of lanes takes elements 0 .. 3, an odd one 4 .. 7.
+          const bool odd = g & 1;
+          const float t0 = __shfl_xor_sync(kAll, odd ? o[0] : o[2], 4);
+          const float t1 = __shfl_xor_sync(kAll, odd ? o[1] : o[3], 4);
+          const float y0 = odd ? t0 : o[0], y1 = odd ? o[2] : t0;
+          const float y2 = odd ? t1 : o[1], y3 = odd ? o[3] : t1;
+          const int col = 32 * x + 4 * g;
+          if (row >= rows) continue;
+          if (all)
+            *reinterpret_cast<uint2*>(a.out + (static_cast<int64_t>(q0 + t) * a.H + head) * D +
+                                      col) = make_uint2(E::pack(y0, y1), E::pack(y2, y3));
+          else
+            __stcg(reinterpret_cast<float4*>(a.part_o + at_row * D + col),
+                   make_float4(y0, y1, y2, y3));
+        }
+        if (g == 0 && row < rows) {
+          if (!all) __stcg(a.part_lse + at_row, lse);
+          else if (a.lse) a.lse[static_cast<int64_t>(head) * a.total_q + q0 + t] = lse;
         }
       }
     }
@@ -617,19 +727,30 @@ int4_decode_kernel(const __grid_constant__ Int4DecodeArgs a) {
       at = 0;
     }
   }
-  cp_async_wait<0>();
+  if (!ok) {
+    flag_status(a.status, PA_DEV_TIMEOUT);
+    *abort = 1;
+  }
+  __syncthreads();
+  // After a wait that gave up: the copies in flight end before the block does.
+  if (*abort && warp == 0)
+    for (int u = 0; u < from.count; ++u)
+      if (!mbar_wait(&full[u % C::STAGES], (u / C::STAGES) & 1)) break;
 }
 
 // ---------------------------------------------------------------------------
-// The sequences whose slices lie in more than one range: their states, in the
-// ranges' order. A block per (sequence, KV head).
+// The sequences whose slices lie in more than one range or key run: their
+// states, in the ranges' order. A block takes two rows of a (sequence, KV head); a
+// thread takes four dims of a row and a part of the states, joined through
+// shared memory in order.
 // ---------------------------------------------------------------------------
-constexpr int kI4CombineThreads = 128;
+constexpr int kI4CombineThreads = 256, kI4CombineRows = 2;
 
 template <int D, bool F16, int NR>
-__global__ void __launch_bounds__(kI4CombineThreads)
+__global__ void __launch_bounds__(kI4CombineThreads, 5)
 int4_combine_kernel(const __grid_constant__ Int4DecodeArgs a) {
-  __shared__ long long sums[2][kI4CombineThreads / 32];
+  __shared__ float4 part_o[kI4CombineThreads];
+  __shared__ float2 part_ml[kI4CombineThreads];
   const int s = static_cast<int>(blockIdx.x) / a.H_kv;
   const int hk = static_cast<int>(blockIdx.x) - s * a.H_kv;
   const I4Seq sq = i4_seq(a, s, false);
@@ -637,109 +758,138 @@ int4_combine_kernel(const __grid_constant__ Int4DecodeArgs a) {
     pdl_leave();                                       // (the grid ends after its predecessor)
     return;
   }
-  long long total = 0, before = 0;
-  for (int x = threadIdx.x; x < a.num_seqs; x += kI4CombineThreads) {
-    const int n = i4_seq(a, x, false).n;
-    total += n;
-    if (x < s) before += n;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    total += __shfl_xor_sync(0xffffffffu, total, o);
-    before += __shfl_xor_sync(0xffffffffu, before, o);
-  }
-  if ((threadIdx.x & 31) == 0) {
-    sums[0][threadIdx.x >> 5] = total;
-    sums[1][threadIdx.x >> 5] = before;
-  }
-  __syncthreads();
-  total = before = 0;
-#pragma unroll
-  for (int w = 0; w < kI4CombineThreads / 32; ++w) {
-    total += sums[0][w];
-    before += sums[1][w];
-  }
-  const long long per = i4_per_range(a, total);
-  const int r0 = static_cast<int>(before / per);
-  const int r1 = static_cast<int>((before + sq.n - 1) / per);
-  if (r0 == r1) {                                      // written by its warp
-    pdl_leave();
-    return;
-  }
+  const int groups = a.H_kv / a.heads_per_block, group = hk / a.heads_per_block;
+  const int hl = hk - group * a.heads_per_block;
+  constexpr int WIDTH = kI4CombineRows * (D / 4), PARTS = kI4CombineThreads / WIDTH;
+  const int rows = sq.q_len * a.G, part = threadIdx.x / WIDTH;
+  const int unit = threadIdx.x - part * WIDTH;
+  const int row = blockIdx.y * kI4CombineRows + unit / (D / 4), col = unit % (D / 4) * 4;
   pdl_wait();
-  const int rows = sq.q_len * a.G;
-  const int64_t step = static_cast<int64_t>(a.H_kv) * 2 * (8 * NR);
-  // The first part starts inside its range (slot 1) unless at its border.
-  const int64_t at0 = (static_cast<int64_t>(r0) * a.H_kv + hk) * 2 * (8 * NR);
-  const int64_t first = at0 + (before == r0 * per ? 0 : 8 * NR);
-  for (int u = threadIdx.x; u < rows * (D / 4); u += kI4CombineThreads) {
-    const int row = u / (D / 4), col = u % (D / 4) * 4;
-    float mx = -INFINITY, sw = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-    merge_states(mx, sw, o, a.part_lse, a.part_o, first + row, 0, 1, D, col);
-    merge_states(mx, sw, o, a.part_lse, a.part_o, at0 + step + row, step, r1 - r0, D, col);
-    const int t = row / a.G, head = hk * a.G + row - t * a.G;
-    if (a.sinks) {
-      const float ls[kBatch] = {__ldg(a.sinks + head)};
-      const float4 z[kBatch] = {make_float4(0.f, 0.f, 0.f, 0.f)};
-      merge_batch(mx, sw, o, ls, z, 1);
+  if (blockIdx.y * kI4CombineRows >= rows) return;
+  const long long per = __ldcg(a.table), before = __ldcg(a.table + 1 + s);
+  const int r0 = static_cast<int>(i4_div(before, per));
+  const int r1 = static_cast<int>(i4_div(before + sq.n - 1, per));
+  const int n = (r1 - r0 + 1) * a.key_runs;
+  if (n == 1) return;                                  // written by its warp
+  // State j: range r0 + j / key_runs, run j % key_runs. A range's first sequence
+  // has slot 0 of its warps, one that starts inside slot 1.
+  const bool inside = before > r0 * per;
+  const int run_shift = 31 - __clz(a.key_runs);        // 1, 2 or 4
+  const int j1 = n * (part + 1) / PARTS;
+  float mx = -INFINITY, sw = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+  if (row < rows) {
+    for (int j = n * part / PARTS; j < j1; j += kBatch) {
+      float l[kBatch];
+      float4 v[kBatch];
+#pragma unroll
+      for (int x = 0; x < kBatch; ++x) {
+        if (j + x >= j1) continue;
+        const int q = (j + x) >> run_shift, run = j + x - (q << run_shift);
+        const int64_t slot =
+            ((static_cast<int64_t>(r0 + q) * groups + group) * I4Cfg<D, NR>::WARPS +
+             run * a.heads_per_block + hl) * 2 + (q == 0 && inside ? 1 : 0);
+        const int64_t at = slot * (8 * NR) + row;
+        l[x] = __ldcg(a.part_lse + at);
+        v[x] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * D + col));
+      }
+      merge_batch(mx, sw, o, l, v, min(kBatch, j1 - j));
     }
-    const float inv = sw == 0.f ? 0.f : 1.f / sw;
-    *reinterpret_cast<uint2*>(a.out + (static_cast<int64_t>(sq.q0 + t) * a.H + head) * D + col) =
-        make_uint2(Elem<F16>::pack(o[0] * inv, o[1] * inv),
-                   Elem<F16>::pack(o[2] * inv, o[3] * inv));
-    if (a.lse && col == 0)
-      a.lse[static_cast<int64_t>(head) * a.total_q + sq.q0 + t] =
-          sw == 0.f ? -INFINITY : mx + fast_log2(sw) * kLn2;
   }
+  part_o[threadIdx.x] = make_float4(o[0], o[1], o[2], o[3]);
+  part_ml[threadIdx.x] = make_float2(mx, sw);
+  __syncthreads();
+  if (part != 0 || row >= rows) return;
+#pragma unroll
+  for (int p = 1; p < PARTS; ++p) {
+    const float2 ml = part_ml[threadIdx.x + p * WIDTH];
+    const float4 x = part_o[threadIdx.x + p * WIDTH];
+    const float nm = fmaxf(mx, ml.x);
+    const float f0 = mx == -INFINITY ? 0.f : fast_exp2((mx - nm) * kLog2e);
+    const float f1 = ml.x == -INFINITY ? 0.f : fast_exp2((ml.x - nm) * kLog2e);
+    mx = nm;
+    sw = sw * f0 + ml.y * f1;
+    o[0] = o[0] * f0 + x.x * f1;
+    o[1] = o[1] * f0 + x.y * f1;
+    o[2] = o[2] * f0 + x.z * f1;
+    o[3] = o[3] * f0 + x.w * f1;
+  }
+  const int t = i4_token(a, row), head = hk * a.G + row - t * a.G;
+  if (a.sinks) {
+    const float ls[kBatch] = {__ldg(a.sinks + head)};
+    const float4 z[kBatch] = {make_float4(0.f, 0.f, 0.f, 0.f)};
+    merge_batch(mx, sw, o, ls, z, 1);
+  }
+  const float inv = sw == 0.f ? 0.f : 1.f / sw;
+  *reinterpret_cast<uint2*>(a.out + (static_cast<int64_t>(sq.q0 + t) * a.H + head) * D + col) =
+      make_uint2(Elem<F16>::pack(o[0] * inv, o[1] * inv), Elem<F16>::pack(o[2] * inv, o[3] * inv));
+  if (a.lse && col == 0)
+    a.lse[static_cast<int64_t>(head) * a.total_q + sq.q0 + t] =
+        sw == 0.f ? -INFINITY : mx + fast_log2(sw) * kLn2;
 }
 
 template <int D, bool F16, int NR>
-static cudaError_t launch_int4_decode_nr(const Int4DecodeArgs& a, cudaStream_t st) {
+static cudaError_t launch_int4_decode_nr(const Int4Maps& maps, const Int4DecodeArgs& a,
+                                         cudaStream_t st) {
   using C = I4Cfg<D, NR>;
   static std::atomic<bool> configured[kMaxDevices];
   cudaError_t e = opt_in_smem(int4_decode_kernel<D, F16, NR>, C::SMEM_BYTES, configured);
   if (e != cudaSuccess) return e;
-  const long long warps = static_cast<long long>(a.ranges) * a.H_kv;
-  int4_decode_kernel<D, F16, NR>
-      <<<static_cast<unsigned>((warps + kI4Warps - 1) / kI4Warps), kI4Warps * 32, C::SMEM_BYTES,
-         st>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  const unsigned blocks = static_cast<unsigned>(a.ranges) * (a.H_kv / a.heads_per_block);
+  // Both kernels are programmatic dependents of what is in front of them on the
+  // stream, of whatever kind: their blocks may be placed while that ends, and wait
+  // for it (griddepcontrol.wait) before they read anything.
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.num_seqs) * static_cast<unsigned>(a.H_kv));
-  cfg.blockDim = dim3(kI4CombineThreads);
-  cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  cfg.stream = st;
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM_BYTES;
+  e = cudaLaunchKernelEx(&cfg, int4_decode_kernel<D, F16, NR>, maps, a);
+  if (e != cudaSuccess || (e = cudaGetLastError()) != cudaSuccess) return e;
+  const int most = min(a.tokens_max, a.max_q) * a.G;   // rows of a sequence
+  cfg.gridDim = dim3(static_cast<unsigned>(a.num_seqs) * static_cast<unsigned>(a.H_kv),
+                     (most + kI4CombineRows - 1) / kI4CombineRows);
+  cfg.blockDim = dim3(kI4CombineThreads);
+  cfg.dynamicSmemBytes = 0;
   e = cudaLaunchKernelEx(&cfg, int4_combine_kernel<D, F16, NR>, a);
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
-int int4_decode_ranges(int sms, int H_kv, int nr) {
-  const int blocks = nr == 1   ? I4Cfg<128, 1>::BLOCKS
-                     : nr == 2 ? I4Cfg<128, 2>::BLOCKS
-                     : nr == 3 ? I4Cfg<128, 3>::BLOCKS
-                               : I4Cfg<128, 4>::BLOCKS;
-  const int n = sms * blocks * kI4Warps / H_kv;
+int int4_decode_heads(int H_kv) {
+  for (int h = I4Cfg<128, 1>::WARPS; h > 1; --h)
+    if (H_kv % h == 0) return h;
+  return 1;
+}
+// Ranges: the blocks that are resident, shared among the head groups.
+static int i4_ranges(int sms, int H_kv, int nr) {
+  const int blocks = nr == 1 ? I4Cfg<128, 1>::BLOCKS : I4Cfg<128, 2>::BLOCKS;
+  const int n = sms * blocks / (H_kv / int4_decode_heads(H_kv));
   return n < 1 ? 1 : n;
 }
 
 size_t int4_decode_part_rows(int sms, int H_kv, int nr) {
-  return static_cast<size_t>(int4_decode_ranges(sms, H_kv, nr)) * H_kv * 2 * 8 * nr;
+  return static_cast<size_t>(i4_ranges(sms, H_kv, nr)) * (H_kv / int4_decode_heads(H_kv)) *
+         I4Cfg<128, 1>::WARPS * 2 * 8 * nr;
 }
 
-cudaError_t launch_int4_decode(Int4DecodeArgs a, int D, bool f16, int nr, int sms,
-                               cudaStream_t st) {
-  a.ranges = int4_decode_ranges(sms, a.H_kv, nr);
+cudaError_t launch_int4_decode(const Int4Maps& maps, Int4DecodeArgs a, int D, bool f16, int nr,
+                               int sms, cudaStream_t st) {
+  a.ranges = i4_ranges(sms, a.H_kv, nr);
+  a.heads_per_block = int4_decode_heads(a.H_kv);
+  a.key_runs = I4Cfg<128, 1>::WARPS / a.heads_per_block;
+  a.slice_keys = a.key_runs * kI4Keys;
+  a.g_inv = (65536 + a.G - 1) / a.G;
   auto by_rows = [&](auto d, auto half) {
     constexpr int kD = decltype(d)::value;
     constexpr bool kF16 = decltype(half)::value;
-    if (nr == 1) return launch_int4_decode_nr<kD, kF16, 1>(a, st);
-    if (nr == 2) return launch_int4_decode_nr<kD, kF16, 2>(a, st);
-    if (nr == 3) return launch_int4_decode_nr<kD, kF16, 3>(a, st);
-    return launch_int4_decode_nr<kD, kF16, 4>(a, st);
+    if (nr == 1) return launch_int4_decode_nr<kD, kF16, 1>(maps, a, st);
+    if (nr == 2) return launch_int4_decode_nr<kD, kF16, 2>(maps, a, st);
+    if (nr == 3) return launch_int4_decode_nr<kD, kF16, 3>(maps, a, st);
+    return launch_int4_decode_nr<kD, kF16, 4>(maps, a, st);
   };
   using std::integral_constant;
   if (D == 128)

@@ -217,10 +217,9 @@ pa_status check_int4(const KvFormat& kv, const void* kc, const void* vc, int64_t
   if (D != 64 && D != 128) return PA_ERR_UNSUPPORTED;
   if (!kc || !vc || !aligned16(kc) || !aligned16(vc) || !kv.k_params || !kv.v_params)
     return PA_ERR_INVALID_ARG;
-  if (((reinterpret_cast<uintptr_t>(kv.k_params) | reinterpret_cast<uintptr_t>(kv.v_params)) & 3u))
-    return PA_ERR_INVALID_ARG;
+  if (!aligned16(kv.k_params) || !aligned16(kv.v_params)) return PA_ERR_INVALID_ARG;
   if (block_stride < static_cast<int64_t>(bs) * H_kv * (D / 2) || block_stride % 16 != 0 ||
-      kv.params_stride < static_cast<int64_t>(bs) * H_kv)
+      kv.params_stride < static_cast<int64_t>(bs) * H_kv || kv.params_stride % 4 != 0)
     return PA_ERR_INVALID_ARG;
   return PA_OK;
 }
@@ -422,6 +421,37 @@ bool encode_q_map(CUtensorMap* map, const void* q, int D, int H, int total_q, in
                   box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
+}
+
+// The maps of a 4-bit cache's decode kernel (see Int4Maps).
+bool encode_int4_maps(Int4Maps* maps, const KvFormat& kv, const void* kc, const void* vc,
+                      int64_t block_stride, int H_kv, int D, int bs, int num_blocks) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t pages = num_blocks > 0 ? num_blocks : 1, row = D / 2;
+  const cuuint32_t heads = int4_decode_heads(H_kv), one[4] = {1, 1, 1, 1};
+  const cuuint64_t dims[4] = {row, static_cast<cuuint64_t>(bs), static_cast<cuuint64_t>(H_kv),
+                              pages};
+  const cuuint64_t strides[3] = {H_kv * row, row, static_cast<cuuint64_t>(block_stride)};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(row), 16, heads, 1};
+  const cuuint64_t pdims[3] = {static_cast<cuuint64_t>(bs), static_cast<cuuint64_t>(H_kv), pages};
+  const cuuint64_t pstrides[2] = {static_cast<cuuint64_t>(bs) * 4,
+                                  static_cast<cuuint64_t>(kv.params_stride) * 4};
+  const cuuint32_t pbox[3] = {16, heads, 1};
+  const void* codes[2] = {kc, vc};
+  void* params[2] = {kv.k_params, kv.v_params};
+  for (int x = 0; x < 2; ++x) {
+    if (fn(&maps->m[x], CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(codes[x]), dims,
+           strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+           D == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
+           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return false;
+    if (fn(&maps->m[2 + x], CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, params[x], pdims, pstrides, pbox,
+           one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return false;
+  }
+  return true;
 }
 
 // Point a kernel's arguments at its class's work list and partial-slot pool.
@@ -1450,7 +1480,7 @@ struct Int4Plan {
   bool few, some, many;
   int nr;                // of `some`: groups of 8 rows
   PassLayout tc;         // of `many`
-  size_t parts, end;     // partial states of the decode kernels; all bytes
+  size_t table, parts, end;   // partial states of the decode kernels; all bytes
   size_t part_rows;
 };
 
@@ -1468,7 +1498,8 @@ static Int4Plan plan_int4(const PassDims& d) {
     p.tc = layout_pass(d, 0);
     off = p.tc.end;
   }
-  p.parts = align_up(off);
+  p.table = align_up(off);
+  p.parts = align_up(p.table + (static_cast<size_t>(d.num_segs) + 1) * 8);
   if (p.few) p.part_rows = int4_decode_part_rows(d.sms, d.H_kv, 1);
   if (p.some) {
     const size_t n = int4_decode_part_rows(d.sms, d.H_kv, p.nr);
@@ -1572,12 +1603,6 @@ pa_status pa_varlen_fwd_int4kv(const pa_kv_update* update, const void* q, int64_
   Int4DecodeArgs a{};
   a.q = static_cast<const uint16_t*>(q);
   a.q_stride = q_token_stride;
-  a.kc = static_cast<const uint8_t*>(key_cache);
-  a.vc = static_cast<const uint8_t*>(value_cache);
-  a.page_bytes = static_cast<uint64_t>(cache_block_stride);
-  a.k_params = kv.k_params;
-  a.v_params = kv.v_params;
-  a.page_params = static_cast<uint64_t>(kv.params_stride);
   a.cu = cu_seqlens_q;
   a.seqused_k = seqused_k;
   a.bt = block_table;
@@ -1598,19 +1623,25 @@ pa_status pa_varlen_fwd_int4kv(const pa_kv_update* update, const void* q, int64_
   a.sinks = sinks;
   a.out = static_cast<uint16_t*>(out);
   a.lse = lse;
+  a.table = reinterpret_cast<long long*>(ws + p.table);
   a.part_lse = reinterpret_cast<float*>(ws + p.parts);
   a.part_o = reinterpret_cast<float*>(ws + align_up(p.parts + p.part_rows * 4));
   a.status = dev_status;
+  Int4Maps maps;
+  if ((p.few || p.some) &&
+      !encode_int4_maps(&maps, kv, key_cache, value_cache, cache_block_stride, num_kv_heads,
+                        head_size, block_size, num_blocks))
+    return PA_ERR_CUDA;
   if (p.few) {
     a.tokens_min = 0;
     a.tokens_max = 8 / d.G;
-    if (launch_int4_decode(a, head_size, dtype == PA_F16, 1, sms, c.st) != cudaSuccess)
+    if (launch_int4_decode(maps, a, head_size, dtype == PA_F16, 1, sms, c.st) != cudaSuccess)
       return PA_ERR_CUDA;
   }
   if (p.some) {
     a.tokens_min = 8 / d.G;
     a.tokens_max = kI4MaxRows / d.G;
-    if (launch_int4_decode(a, head_size, dtype == PA_F16, p.nr, sms, c.st) != cudaSuccess)
+    if (launch_int4_decode(maps, a, head_size, dtype == PA_F16, p.nr, sms, c.st) != cudaSuccess)
       return PA_ERR_CUDA;
   }
   return PA_OK;

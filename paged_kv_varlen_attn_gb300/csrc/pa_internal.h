@@ -305,15 +305,15 @@ cudaError_t launch_int4_rows(const Int4RowsArgs& a, int D, bool f16, cudaStream_
 // with tokens_min < q_len <= tokens_max, at most 8 nr packed rows each (nr: 1 to
 // 4).
 constexpr int kI4MaxRows = 32;
+// TMA maps: codes of K and V as (byte, row, head, page), boxes of a row's bytes x
+// 16 x int4_decode_heads x 1, swizzled by the row's bytes; their (scale, minimum)
+// pairs as (row, head, page), boxes 16 x int4_decode_heads x 1.
+struct Int4Maps {
+  CUtensorMap m[4];
+};
 struct Int4DecodeArgs {
   const uint16_t* q;
   int64_t q_stride;
-  const uint8_t* kc;
-  const uint8_t* vc;
-  uint64_t page_bytes;            // between the pools' pages
-  const uint32_t* k_params;       // (scale, minimum) f16 pairs: page b, head h, row r at
-  const uint32_t* v_params;       // b * page_params + h * bs + r
-  uint64_t page_params;
   const int32_t* cu;
   const int32_t* seqused_k;
   const int32_t* bt;
@@ -329,8 +329,13 @@ struct Int4DecodeArgs {
   float* lse;                     // [H, total_q] or NULL
   float* part_o;                  // [int4_decode_part_rows][D]
   float* part_lse;                // [int4_decode_part_rows]
+  long long* table;               // [1 + num_seqs]: slices of a range, first slices
   int32_t* status;
-  int ranges;                     // set by the launcher
+  // Set by the launcher: ranges of slices, KV heads and runs of 32 keys of a
+  // block, keys of a slice.
+  int ranges, heads_per_block, key_runs;
+  unsigned slice_keys;
+  int g_inv;                      // 2^16 / G, rounded up
 };
 // 4-bit pools of the prompt kernel (int4_prompt.cu).
 struct Int4Pools {
@@ -344,8 +349,9 @@ struct Int4Pools {
 cudaError_t launch_int4_prompt(const CUtensorMap& tmQ, const AttnArgs& a, const Int4Pools& pool,
                                int items_bound, cudaStream_t st);
 size_t int4_decode_part_rows(int sms, int H_kv, int nr);
-cudaError_t launch_int4_decode(Int4DecodeArgs a, int D, bool f16, int nr, int sms,
-                               cudaStream_t st);
+int int4_decode_heads(int H_kv);
+cudaError_t launch_int4_decode(const Int4Maps& maps, Int4DecodeArgs a, int D, bool f16, int nr,
+                               int sms, cudaStream_t st);
 
 // Eviction (evict.cu). Rows of head_size elements are row_bytes long.
 struct EvictArgs {

@@ -120,7 +120,8 @@ def test_write_misaligned(lib, mem):
     for name in ("key", "value", "kc", "vc"):
         at = dict(key=p[0], value=p[1], kc=p[2], vc=p[3])[name]
         assert write(lib, p, n=1, **{name: at + 8}) == INVALID
-    assert write(lib, p, n=1, kp=p[4] + 2) == INVALID
+    assert write(lib, p, n=1, kp=p[4] + 4) == INVALID
+    assert write(lib, p, n=1, pp=HK * BS + 2) == INVALID
     assert write(lib, p, n=1, slots=p[6] + 4) == INVALID
     assert write(lib, p) == 0                     # nothing to write
 
