@@ -12,11 +12,11 @@ namespace pa {
 // ---------------------------------------------------------------------------
 // Work items, softmax, products and epilogue are the prefill kernel's. What
 // differs is how K, V and Q reach the products:
-//  * Warps 0, 2 and 3 of the control warpgroup widen. A unit is 16 keys of K or
-//    V; warp w of them takes every third one, in the order K(0), V(0), K(1), ...
-//    of key tiles. It copies its units' codes, scales and minima ahead of their
-//    use into a ring of its own (a lane copies what it reads back itself, but for
-//    the scales), so no barrier stands between the pools and the registers.
+//  * Warp 0 of the control warpgroup widens K, warps 2 and 3 widen V, half a tile
+//    each, which costs the three about the same. A unit is 16 keys; a warp takes
+//    them by pairs, whose codes, scales and minima it copies ahead of their use
+//    into a ring of its own (a lane copies the codes that it reads back itself), so
+//    no barrier stands between the pools and the registers.
 //  * K reaches the product as codes: n in the low four bits of an f16 is the
 //    subnormal n 2^-24, in the next four n 2^-20, so a mask makes two numbers;
 //    the query's elements that meet the latter are a sixteenth. The softmax
@@ -28,28 +28,27 @@ namespace pa {
 //    the value. Rows past the sequence are zeros.
 //  * The widened tiles have the 2-byte kernel's layout (128-byte swizzle), two
 //    buffers each for K and V; the products that read a buffer free it.
-//  * Q is taken as f16 after a power-of-two row scale, in place, by the same
-//    warps, once per item, which also sum it; 2^-k joins the softmax scale. The sign of a negative
+//  * Q is taken as f16 after a power-of-two row scale, in place, by warps
+//    2 and 3, once per item, which also sum it; 2^-k joins the softmax scale. The sign of a negative
 //    softmax scale goes into Q, so the row maximum of the raw products serves
 //    every scale.
 // ---------------------------------------------------------------------------
 
-// A unit's piece of K: 32 codes (16 bytes, row r) as 64 bytes of f16 subnormals,
-// n 2^-24 (elements 0, 1, 4, 5 of 8) or n 2^-20 (2, 3, 6, 7).
-__device__ __forceinline__ void spread_int4_piece(const uint4& x, uint8_t* dst, int r, int c0) {
+// A piece of K, 32 codes (16 bytes), as 64 bytes of f16 subnormals: n 2^-24
+// (elements 0, 1, 4, 5 of 8) or n 2^-20 (2, 3, 6, 7), at to[0 .. 3].
+__device__ __forceinline__ void spread_int4_piece(const uint4& x, uint8_t* dst, const int (&to)[4]) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
   for (int v = 0; v < 4; ++v) {
     const uint32_t t = w[v] >> 8;
-    *reinterpret_cast<uint4*>(dst + r * 128 + (((c0 + v) ^ (r & 7)) << 4)) =
+    *reinterpret_cast<uint4*>(dst + to[v]) =
         make_uint4(w[v] & 0x000F000Fu, w[v] & 0x00F000F0u, t & 0x000F000Fu, t & 0x00F000F0u);
   }
 }
 
-// A unit's piece of V: 32 codes (16 bytes, row r), as 64 bytes of f16: chunks c0 .. c0
-// + 3 of row r of a 128-byte swizzled tile.
+// A piece of V as 64 bytes of f16 values.
 __device__ __forceinline__ void widen_int4_piece(const uint4& x, uint32_t params, uint8_t* dst,
-                                                 int r, int c0) {
+                                                 const int (&to)[4]) {
   const __half2 s = __half2half2(__ushort_as_half(static_cast<unsigned short>(params & 0xffffu)));
   const __half2 m = __half2half2(__ushort_as_half(static_cast<unsigned short>(params >> 16)));
   const __half2 k1024 = __half2half2(__ushort_as_half(0x6400));
@@ -68,9 +67,131 @@ __device__ __forceinline__ void widen_int4_piece(const uint4& x, uint32_t params
       n = __hfma2(n, s, m);
       y[k] = *reinterpret_cast<uint32_t*>(&n);
     }
-    *reinterpret_cast<uint4*>(dst + r * 128 + (((c0 + v) ^ (r & 7)) << 4)) =
-        make_uint4(y[0], y[1], y[2], y[3]);
+    *reinterpret_cast<uint4*>(dst + to[v]) = make_uint4(y[0], y[1], y[2], y[3]);
   }
+}
+
+// A widening warp: units u0 .. u0 + UPT - 1 of every K (or V) tile, by pairs,
+// through a ring of RING pairs at `ring`.
+template <int D, bool IS_V, int UPT, int RING>
+__device__ __forceinline__ bool widen_tiles(const AttnArgs& a, const Int4Pools& pool, TcBars* bars,
+                                            uint8_t* smem, uint8_t* ring, const int32_t* bt_row,
+                                            int hk, int kb, int kv_len, int ntiles, int u0) {
+  using C = TcCfg<D>;
+  using I = TcI4<D>;
+  constexpr int PIECES = D / 32;                         // of a row, 16 bytes each
+  constexpr int PER = 16 * PIECES / 32;                  // of a unit, per lane (2 or 1)
+  constexpr int PAIR = 2 * I::SLOT, PPT = UPT / 2;       // bytes of a pair, pairs of a tile
+  const int lane = threadIdx.x & 31;
+  const int px = lane % PIECES, pr = lane / PIECES;      // piece, first row
+  const int64_t rstep = static_cast<int64_t>(a.H_kv) * (D / 2);
+  const uint8_t* src0 = (IS_V ? pool.vc : pool.kc) + hk * (D / 2) + pr * rstep + px * 16;
+  const uint32_t* par0 = (IS_V ? pool.v_params : pool.k_params) +
+                         static_cast<int64_t>(hk) * a.bs + (lane & 15);
+  const uint32_t ring_at = smem_u32(ring);
+  const int pairs = ntiles * PPT;
+  // Lane i: page and row of unit 2 page0 + i of this warp's.
+  int page0 = 0, page_l = -1, row_l = 0;
+  auto load_pages = [&](int q) {
+    page0 = q;
+    page_l = -1;
+    row_l = 0;
+    const int n = 2 * q + lane, key0 = kb + n / UPT * C::BN + (u0 + n % UPT) * 16;
+    if (n < 2 * pairs && key0 < kv_len) {
+      const int lp = key0 / a.bs;
+      row_l = key0 - lp * a.bs;
+      page_l = __ldg(bt_row + lp);
+      if (page_l < 0 || page_l >= a.num_blocks) {
+        page_l = -1;                                     // reads as zeros
+        flag_status(a.status, PA_DEV_BAD_PAGE);
+      }
+    }
+  };
+  int f_slot = 0;
+  auto fetch = [&](int q) {
+    if (q < pairs) {
+      if (q - page0 == 16) load_pages(q);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int page = __shfl_sync(0xffffffffu, page_l, 2 * (q - page0) + x);
+        const int prow = __shfl_sync(0xffffffffu, row_l, 2 * (q - page0) + x);
+        const uint32_t dst = ring_at + f_slot * PAIR + x * I::SLOT;
+        const uint8_t* src = src0 + max(page, 0) * pool.block_stride_bytes + prow * rstep;
+#pragma unroll
+        for (int y = 0; y < PER; ++y)
+          cp_async16(dst + y * 512 + lane * 16, src + y * (32 / PIECES) * rstep, page >= 0);
+        // Scales and minima; zeros past the sequence.
+        const int n = 2 * q + x, key0 = kb + n / UPT * C::BN + (u0 + n % UPT) * 16;
+        if (lane < 16)
+          cp_async4(dst + 16 * D / 2 + lane * 4,
+                    par0 + max(page, 0) * pool.params_stride + prow,
+                    page >= 0 && key0 + lane < kv_len);
+      }
+      if (++f_slot == RING) f_slot = 0;
+    }
+    cp_async_commit();
+  };
+  load_pages(0);
+#pragma unroll
+  for (int q = 0; q < RING - 1; ++q) fetch(q);
+  // Where a piece of row pr (mod 8) goes in a 128-byte swizzled tile.
+  int to[4];
+#pragma unroll
+  for (int v = 0; v < 4; ++v)
+    to[v] = (px >> 1) * C::KV_HALF + pr * 128 + ((((px & 1) * 4 + v) ^ (pr & 7)) << 4);
+  int slot = 0, q = 0;
+  for (int t = 0; t < ntiles; ++t) {
+    const int buf = t & 1;
+    // The buffer's last reader: the products of tile t - 2.
+    bool ok = true;
+    if (t >= I::BUFS)
+      ok = mbar_wait(IS_V ? &bars->vw_free[buf] : &bars->kw_free[buf], ((t >> 1) - 1) & 1);
+    if (!__all_sync(0xffffffffu, ok && !bars->abort)) return false;
+    uint8_t* dst = smem + (IS_V ? I::OFF_VW : I::OFF_KW) + buf * C::KV_TILE + u0 * 16 * 128;
+    float* par_to = reinterpret_cast<float*>(smem + I::OFF_PAR + t % I::PARS * C::BN * 8);
+#pragma unroll 1
+    for (int p = 0; p < PPT; ++p, ++q, dst += 32 * 128) {
+      fetch(q + RING - 1);
+      cp_async_wait<RING - 1>();
+      __syncwarp();
+      const uint8_t* sl = ring + slot * PAIR;
+      uint4 w[2][PER];
+      uint32_t par[2][PER];
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int y = 0; y < PER; ++y) {
+          w[x][y] = *reinterpret_cast<const uint4*>(sl + x * I::SLOT + y * 512 + lane * 16);
+          if (IS_V)
+            par[x][y] = *reinterpret_cast<const uint32_t*>(sl + x * I::SLOT + 16 * D / 2 +
+                                                           (pr + y * (32 / PIECES)) * 4);
+        }
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int y = 0; y < PER; ++y) {
+          uint8_t* at = dst + (x * 16 + y * (32 / PIECES)) * 128;
+          if (IS_V) widen_int4_piece(w[x][y], par[x][y], at, to);
+          else spread_int4_piece(w[x][y], at, to);
+        }
+      if (!IS_V) {   // lane: key `lane` of the pair's 32
+        const float2 sm = Elem<true>::unpack(*reinterpret_cast<const uint32_t*>(
+            sl + (lane >> 4) * I::SLOT + 16 * D / 2 + (lane & 15) * 4));
+        float* at = par_to + ((u0 + 2 * p) * 16 + lane) / 2 * 4 + (lane & 1);
+        at[0] = sm.x * 0x1p24f;
+        at[2] = sm.y;
+      }
+      __syncwarp();                                      // the slot may be filled again
+      if (++slot == RING) slot = 0;
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(IS_V ? &bars->vw_full[buf] : &bars->kw_full[buf]);
+      if (!IS_V) mbar_arrive(&bars->par_full[t % I::PARS]);
+    }
+  }
+  return true;
 }
 
 // The Q tiles in place: row r of tile X times +-2^k, as f16, with 2^k bringing
@@ -154,14 +275,14 @@ int4_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
 
   if (threadIdx.x == 0) {
     mbar_init(&bars->q_full, 1);
-    mbar_init(&bars->q_conv, I::WARPS * 32);
+    mbar_init(&bars->q_conv, 64);
     for (int b = 0; b < I::BUFS; ++b) {
-      mbar_init(&bars->kw_full[b], I::UNITS);
-      mbar_init(&bars->vw_full[b], I::UNITS);
+      mbar_init(&bars->kw_full[b], 1);             // one warp widens K, two V
+      mbar_init(&bars->vw_full[b], 2);
       mbar_init(&bars->kw_free[b], 1);
       mbar_init(&bars->vw_free[b], 1);
     }
-    for (int b = 0; b < I::PARS; ++b) mbar_init(&bars->par_full[b], I::UNITS);
+    for (int b = 0; b < I::PARS; ++b) mbar_init(&bars->par_full[b], 1);
     for (int x = 0; x < 2; ++x) {
       mbar_init(&bars->s_full[x], 1);
       mbar_init(&bars->p_full[0][x], 128);
@@ -269,112 +390,26 @@ int4_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             tma_load_3d(smem + C::OFF_Q + x * C::Q_TILE + h * C::Q_HALF, &tmQ, &bars->q_full,
                         h * 64, hk * G, token0 + x * (TR / G));
       }
-      // Unit u of the item: tile u / (2 UNITS), K then V, 16 keys each. This
-      // warp's i-th unit is 3 i + cw. Lane i holds the page and row of the i-th
-      // unit from page0 on.
-      constexpr int PIECES = D / 32;                     // of a row, 16 bytes each
-      constexpr int PER = 16 * PIECES / 32;              // pieces per lane (2 or 1)
-      const int n_units = ntiles * 2 * I::UNITS;
-      const int mine = n_units > cw ? (n_units - cw + I::WARPS - 1) / I::WARPS : 0;
-      const int32_t* bt_row = a.bt + static_cast<int64_t>(seg) * a.bt_row_stride;
-      const int64_t rstep = static_cast<int64_t>(a.H_kv) * (D / 2);
-      const int px = lane % PIECES, pr = lane / PIECES;  // piece, first row
-      uint8_t* ring = smem + I::OFF_RING + cw * (I::SLOTS * I::SLOT);
-      const uint32_t ring_at = smem_u32(ring);
-      auto unit_key = [&](int i) {
-        const int u = I::WARPS * i + cw;
-        return kb + u / (2 * I::UNITS) * C::BN + u % I::UNITS * 16;
-      };
-      int page0 = 0, page_l = -1, row_l = 0;
-      auto load_pages = [&](int i0) {
-        page0 = i0;
-        page_l = -1;
-        row_l = 0;
-        const int key0 = unit_key(i0 + lane);
-        if (i0 + lane < mine && key0 < kv_len) {
-          const int lp = key0 / a.bs;
-          row_l = key0 - lp * a.bs;
-          page_l = __ldg(bt_row + lp);
-          if (page_l < 0 || page_l >= a.num_blocks) {
-            page_l = -1;                                 // reads as zeros
-            flag_status(a.status, PA_DEV_BAD_PAGE);
-          }
-        }
-      };
-      auto fetch = [&](int i) {
-        if (i < mine) {
-          if (i - page0 == 32) load_pages(i);
-          const int page = __shfl_sync(0xffffffffu, page_l, i - page0);
-          const int prow = __shfl_sync(0xffffffffu, row_l, i - page0);
-          const bool in = page >= 0;
-          const bool is_v = (I::WARPS * i + cw) / I::UNITS & 1;
-          const int key0 = unit_key(i);
-          const uint32_t dst = ring_at + i % I::SLOTS * I::SLOT;
-          const uint8_t* src = (is_v ? pool.vc : pool.kc) + max(page, 0) * pool.block_stride_bytes +
-                               hk * (D / 2) + (prow + pr) * rstep + px * 16;
-#pragma unroll
-          for (int x = 0; x < PER; ++x)
-            cp_async16(dst + x * 512 + lane * 16, src + x * (32 / PIECES) * rstep, in);
-          if (lane < 16)
-            cp_async4(dst + 16 * D / 2 + lane * 4,
-                      (is_v ? pool.v_params : pool.k_params) + max(page, 0) * pool.params_stride +
-                          static_cast<int64_t>(hk) * a.bs + prow + lane,
-                      in && key0 + lane < kv_len);
-        }
-        cp_async_commit();
-      };
-      load_pages(0);
-      for (int i = 0; i < I::SLOTS - 1; ++i) fetch(i);
-      bool ok = mbar_wait(&bars->q_full, 0);
-      if (ok) {
+      bool ok = true;
+      if (cw != 0) ok = mbar_wait(&bars->q_full, 0);
+      if (cw != 0 && ok) {
         const float sign = a.scale_log2 > 0.f ? 1.f : a.scale_log2 < 0.f ? -1.f : 0.f;
         q_to_f16<D, F16>(smem + C::OFF_Q, reinterpret_cast<float*>(smem + I::OFF_RS),
                          reinterpret_cast<float*>(smem + I::OFF_TAU), two ? 2 : 1, sign,
-                         cw * 32 + lane, I::WARPS * 32);
+                         (cw - 1) * 32 + lane, 64);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         mbar_arrive(&bars->q_conv);
       }
       ok = __all_sync(0xffffffffu, ok);
-      for (int i = 0; ok && i < mine; ++i) {
-        fetch(i + I::SLOTS - 1);
-        const int u = I::WARPS * i + cw;
-        const int t = u / (2 * I::UNITS), buf = t & 1;
-        const bool is_v = u / I::UNITS & 1;
-        // The buffer's last reader: the products of tile t - 2.
-        if (t >= I::BUFS)
-          ok = mbar_wait(is_v ? &bars->vw_free[buf] : &bars->kw_free[buf], ((t >> 1) - 1) & 1);
-        ok = __all_sync(0xffffffffu, ok && !bars->abort);
-        if (!ok) break;
-        cp_async_wait<I::SLOTS - 1>();
-        __syncwarp();
-        const uint8_t* sl = ring + i % I::SLOTS * I::SLOT;
-        uint8_t* dst = smem + (is_v ? I::OFF_VW : I::OFF_KW) + buf * C::KV_TILE;
-        const uint32_t* par = reinterpret_cast<const uint32_t*>(sl + 16 * D / 2);
-        const int r0 = u % I::UNITS * 16;                // of the tile
-#pragma unroll
-        for (int x = 0; x < PER; ++x) {
-          const int r = pr + x * (32 / PIECES);          // of the unit's 16
-          const uint4 w = *reinterpret_cast<const uint4*>(sl + x * 512 + lane * 16);
-          uint8_t* half = dst + (px >> 1) * C::KV_HALF;
-          if (is_v)
-            widen_int4_piece(w, par[r], half, r0 + r, (px & 1) * 4);
-          else
-            spread_int4_piece(w, half, r0 + r, (px & 1) * 4);
-        }
-        if (!is_v && lane < 16) {
-          const float2 sm = Elem<true>::unpack(par[lane]);
-          float* to = reinterpret_cast<float*>(smem + I::OFF_PAR + t % I::PARS * C::BN * 8) +
-                      (r0 + lane) / 2 * 4 + (lane & 1);
-          to[0] = sm.x * 0x1p24f;
-          to[2] = sm.y;
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(is_v ? &bars->vw_full[buf] : &bars->kw_full[buf]);
-          if (!is_v) mbar_arrive(&bars->par_full[t % I::PARS]);
-        }
-      }
+      const int32_t* bt_row = a.bt + static_cast<int64_t>(seg) * a.bt_row_stride;
+      uint8_t* ring = smem + I::OFF_RING;
+      constexpr int KP = I::SLOTS / 4 * 3;               // pairs: K's ring, V's halves of it
+      if (ok)
+        ok = cw == 0 ? widen_tiles<D, false, I::UNITS, KP>(a, pool, bars, smem, ring, bt_row, hk,
+                                                            kb, kv_len, ntiles, 0)
+                     : widen_tiles<D, true, I::UNITS / 2, KP / 2>(
+                           a, pool, bars, smem, ring + (cw + 1) * KP * I::SLOT, bt_row, hk, kb,
+                           kv_len, ntiles, (cw - 1) * (I::UNITS / 2));
       cp_async_wait<0>();
       if (!ok) {
         abort_call(a);
