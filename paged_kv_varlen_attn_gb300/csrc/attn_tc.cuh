@@ -81,13 +81,12 @@ struct TcI4 {
   static constexpr int WARPS = 3;
   static constexpr int SLOTS = 8;                         // units in a warp's ring
   static constexpr int SLOT = 16 * D / 2 + 64;
-  static constexpr int OFF_RS = OFF_RING + WARPS * SLOTS * SLOT;   // float[TILES * BM]
-  static constexpr int OFF_TAU = OFF_RS + C::TILES * C::BM * 4;    // float[TILES * BM]
-  // Per key tile: scale 2^24 and minimum of its keys as float32, (s, s, m, m) of
-  // two keys at a time. Those of tile t are written when S(t - 2) is complete, so
-  // a ring of four leaves the softmax of t - 1 its own.
+  // Per key tile: scale (x 2^24 where the codes are 2^-24 of theirs) and minimum of
+  // its keys as float32, (s, s, m, m) of two keys at a time. Those of tile t are
+  // written when S(t - 2) is complete, so a ring of four leaves the softmax of t -
+  // 1 its own.
   static constexpr int PARS = 4;
-  static constexpr int OFF_PAR = OFF_TAU + C::TILES * C::BM * 4;
+  static constexpr int OFF_PAR = OFF_RING + WARPS * SLOTS * SLOT;
   static constexpr int OFF_BAR = OFF_PAR + PARS * C::BN * 8;
   static constexpr int SMEM_BYTES = OFF_BAR + 512 + 1024;
 };
@@ -157,15 +156,42 @@ template <int D_, bool F16_, bool FP8_, bool WIN_, bool SC_ = false, bool I4_ = 
 struct TcKind {
   static constexpr int D = D_;
   static constexpr bool F16 = F16_, FP8 = FP8_, WIN = WIN_, SC = SC_, I4 = I4_;
-  // K and V reach the MMA widened, P in f16, and Q after a row scale.
+  // V reaches the MMA widened, P in f16.
   static constexpr bool WIDE = FP8 || I4;
-  static constexpr int OFF_RS = I4 ? TcI4<D>::OFF_RS : TcFp8::OFF_RS;
 };
 static_assert(sizeof(TcBars) <= 512, "the barriers' place");
 
 // Bits 0 .. n - 1 (none for n <= 0, all from n = 32 on).
 __device__ __forceinline__ uint32_t below_mask(int n) {
   return n >= 32 ? ~0u : (n <= 0 ? 0u : (1u << n) - 1u);
+}
+
+// A load from shared memory that stays in its place among others.
+__device__ __forceinline__ float4 lds_in_order(uint32_t at) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(at));
+  return v;
+}
+
+// Sum of row r of a Q tile (128-byte swizzled rows of 64 elements).
+template <int D, bool F16>
+__device__ __forceinline__ float q_row_sum(const uint8_t* q, int r) {
+  using C = TcCfg<D>;
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1   // (few registers: the caller has none to spare)
+  for (int c = 0; c < D / 8; ++c) {
+    const uint4 x = *reinterpret_cast<const uint4*>(q + (c >> 3) * C::Q_HALF + r * 128 +
+                                                    (((c & 7) ^ (r & 7)) << 4));
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 f = Elem<F16>::unpack(w[k]);
+      s[k] += f.x + f.y;
+    }
+  }
+  return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
 // SC: a tile's raw products as scores in base 2, capped and biased (see pa.h):
@@ -238,23 +264,27 @@ __device__ __forceinline__ void tc_softmax_tile(const AttnArgs& a, TcBars* bars,
   }
   // FP8 pools: scores use the stored codes, so k_scale joins the softmax
   // scale and v_scale the final normalisation.
-  // 4-bit pools: a negative scale's sign is Q's, a scale of zero makes Q zero.
+  // 4-bit pools: the scale's sign has joined the keys' scales and minima (zeros
+  // for a scale of zero).
   float sl2 = FP8  ? a.scale_log2 * __ldg(a.k_scale + hk)
               : I4 ? (a.scale_log2 == 0.f ? 1.f : fabsf(a.scale_log2))
                    : a.scale_log2;
   const int tid = threadIdx.x - 128 - X * 128;     // 0..127 within the warpgroup
   float m_use = -INFINITY, l = 0.f;
   bool ok = true;
-  if constexpr (Kind::WIDE) {
+  if constexpr (FP8) {
     // S holds q 2^k . k for the row's power of two 2^k (Q entered the e4m3
-    // products as two e4m3 terms, or as f16): 2^-k joins the softmax scale.
+    // products as two e4m3 terms): 2^-k joins the softmax scale.
     if (ntiles > 0) {
       ok = mbar_wait(&bars->q_conv, 0);
-      sl2 *= reinterpret_cast<const float*>(smem + Kind::OFF_RS)[X * C::BM + r];
+      sl2 *= reinterpret_cast<const float*>(smem + TcFp8::OFF_RS)[X * C::BM + r];
     }
   }
-  float tau = 0.f;   // I4: sum of the row's (scaled) q
-  if constexpr (I4) tau = reinterpret_cast<const float*>(smem + TcI4<D>::OFF_TAU)[X * C::BM + r];
+  float tau = 0.f;   // I4: sum of the row's q
+  if constexpr (I4) {
+    if (ntiles > 0 && (ok = mbar_wait(&bars->q_full, 0)))
+      tau = q_row_sum<D, F16>(smem + C::OFF_Q + X * C::Q_TILE, r);
+  }
   for (int t = 0; ok && t < ntiles; ++t) {
     if (!mbar_wait(&bars->s_full[X], t & 1)) { ok = false; break; }
     tc_fence_after();
@@ -272,13 +302,20 @@ __device__ __forceinline__ void tc_softmax_tile(const AttnArgs& a, TcBars* bars,
       // q), in float32.
       using I = TcI4<D>;
       if (!mbar_wait(&bars->par_full[t % I::PARS], (t / I::PARS) & 1)) { ok = false; break; }
-      const float4* par = reinterpret_cast<const float4*>(smem + I::OFF_PAR + t % I::PARS * C::BN * 8);
+      const uint32_t par = smem_u32(smem + I::OFF_PAR + t % I::PARS * C::BN * 8);
+      constexpr int AHEAD = 4;   // loads in flight (more of them, and registers spill)
 #pragma unroll
-      for (int e = 0; e < C::BN; e += 2) {
-        const float4 p = par[e / 2];
-        float u0, u1;
-        fmul2(u0, u1, p.z, p.w, tau, tau);
-        ffma2(xs[e], xs[e + 1], p.x, p.y, xs[e], xs[e + 1], u0, u1);
+      for (int e0 = 0; e0 < C::BN; e0 += 2 * AHEAD) {
+        float4 p[AHEAD];
+#pragma unroll
+        for (int x = 0; x < AHEAD; ++x) p[x] = lds_in_order(par + (e0 + 2 * x) * 8);
+#pragma unroll
+        for (int x = 0; x < AHEAD; ++x) {
+          const int e = e0 + 2 * x;
+          float u0, u1;
+          fmul2(u0, u1, p[x].z, p[x].w, tau, tau);
+          ffma2(xs[e], xs[e + 1], p[x].x, p[x].y, xs[e], xs[e + 1], u0, u1);
+        }
       }
     }
     if constexpr (SC) {

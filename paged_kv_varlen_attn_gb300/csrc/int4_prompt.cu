@@ -17,32 +17,39 @@ namespace pa {
 //    them by pairs, whose codes, scales and minima it copies ahead of their use
 //    into a ring of its own (a lane copies the codes that it reads back itself), so
 //    no barrier stands between the pools and the registers.
-//  * K reaches the product as codes: n in the low four bits of an f16 is the
-//    subnormal n 2^-24, in the next four n 2^-20, so a mask makes two numbers;
-//    the query's elements that meet the latter are a sixteenth. The softmax
-//    applies scale and minimum to the sums, in float32 (one multiply and one
-//    multiply-add per two scores): with K rounded to f16 values instead, the
-//    log-sum-exp lost ten of its bits.
+//  * K reaches the product as codes, exact in Q's type, and Q as it is: for f16 a
+//    mask makes two subnormals n 2^-24, for bf16 128 + n by a mask and 128 taken
+//    off. The softmax applies scale and minimum to the sums, in float32 (one
+//    multiply and one multiply-add per two scores; each row sums its Q once): with
+//    K rounded to f16 values instead, the log-sum-exp lost ten of its bits. The
+//    sign of a negative softmax scale joins scale and minimum, so the row maximum
+//    of what the softmax sees serves every scale.
 //  * V becomes values: n exactly as f16 (from 1024 + n or 1024 + 16 n), and n
 //    scale + minimum by one multiply-add: one rounding, at most half a step of
 //    the value. Rows past the sequence are zeros.
 //  * The widened tiles have the 2-byte kernel's layout (128-byte swizzle), two
 //    buffers each for K and V; the products that read a buffer free it.
-//  * Q is taken as f16 after a power-of-two row scale, in place, by warps
-//    2 and 3, once per item, which also sum it; 2^-k joins the softmax scale. The sign of a negative
-//    softmax scale goes into Q, so the row maximum of the raw products serves
-//    every scale.
 // ---------------------------------------------------------------------------
 
-// A piece of K, 32 codes (16 bytes), as 64 bytes of f16 subnormals: n 2^-24
-// (elements 0, 1, 4, 5 of 8) or n 2^-20 (2, 3, 6, 7), at to[0 .. 3].
+// A piece of K, 32 codes (16 bytes), as 64 bytes of bf16 numbers or f16 2^-24 of
+// them, at to[0 .. 3].
+template <bool F16>
 __device__ __forceinline__ void spread_int4_piece(const uint4& x, uint8_t* dst, const int (&to)[4]) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
   for (int v = 0; v < 4; ++v) {
-    const uint32_t t = w[v] >> 8;
-    *reinterpret_cast<uint4*>(dst + to[v]) =
-        make_uint4(w[v] & 0x000F000Fu, w[v] & 0x00F000F0u, t & 0x000F000Fu, t & 0x00F000F0u);
+    uint32_t y[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      y[k] = w[v] >> (4 * k) & 0x000F000Fu;
+      if constexpr (!F16) {
+        y[k] |= 0x43004300u;                             // 128 + n
+        const __nv_bfloat162 n = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&y[k]),
+                                         __float2bfloat162_rn(128.f));
+        y[k] = *reinterpret_cast<const uint32_t*>(&n);
+      }
+    }
+    *reinterpret_cast<uint4*>(dst + to[v]) = make_uint4(y[0], y[1], y[2], y[3]);
   }
 }
 
@@ -73,7 +80,7 @@ __device__ __forceinline__ void widen_int4_piece(const uint4& x, uint32_t params
 
 // A widening warp: units u0 .. u0 + UPT - 1 of every K (or V) tile, by pairs,
 // through a ring of RING pairs at `ring`.
-template <int D, bool IS_V, int UPT, int RING>
+template <int D, bool F16, bool IS_V, int UPT, int RING>
 __device__ __forceinline__ bool widen_tiles(const AttnArgs& a, const Int4Pools& pool, TcBars* bars,
                                             uint8_t* smem, uint8_t* ring, const int32_t* bt_row,
                                             int hk, int kb, int kv_len, int ntiles, int u0) {
@@ -139,6 +146,7 @@ __device__ __forceinline__ bool widen_tiles(const AttnArgs& a, const Int4Pools& 
 #pragma unroll
   for (int v = 0; v < 4; ++v)
     to[v] = (px >> 1) * C::KV_HALF + pr * 128 + ((((px & 1) * 4 + v) ^ (pr & 7)) << 4);
+  const float sign = a.scale_log2 > 0.f ? 1.f : a.scale_log2 < 0.f ? -1.f : 0.f;
   int slot = 0, q = 0;
   for (int t = 0; t < ntiles; ++t) {
     const int buf = t & 1;
@@ -172,14 +180,14 @@ __device__ __forceinline__ bool widen_tiles(const AttnArgs& a, const Int4Pools& 
         for (int y = 0; y < PER; ++y) {
           uint8_t* at = dst + (x * 16 + y * (32 / PIECES)) * 128;
           if (IS_V) widen_int4_piece(w[x][y], par[x][y], at, to);
-          else spread_int4_piece(w[x][y], at, to);
+          else spread_int4_piece<F16>(w[x][y], at, to);
         }
       if (!IS_V) {   // lane: key `lane` of the pair's 32
         const float2 sm = Elem<true>::unpack(*reinterpret_cast<const uint32_t*>(
             sl + (lane >> 4) * I::SLOT + 16 * D / 2 + (lane & 15) * 4));
         float* at = par_to + ((u0 + 2 * p) * 16 + lane) / 2 * 4 + (lane & 1);
-        at[0] = sm.x * 0x1p24f;
-        at[2] = sm.y;
+        at[0] = sm.x * (F16 ? sign * 0x1p24f : sign);
+        at[2] = sm.y * sign;
       }
       __syncwarp();                                      // the slot may be filled again
       if (++slot == RING) slot = 0;
@@ -192,53 +200,6 @@ __device__ __forceinline__ bool widen_tiles(const AttnArgs& a, const Int4Pools& 
     }
   }
   return true;
-}
-
-// The Q tiles in place: row r of tile X times +-2^k, as f16, with 2^k bringing
-// the row's largest |q| to [2^14, 2^15), elements 2, 3, 6, 7 of 8 a sixteenth of
-// that; 2^-k goes to rs[X * 128 + r], the sum of the scaled row to tau. sign: of
-// the softmax scale (0: the row becomes zeros).
-template <int D, bool F16>
-__device__ __forceinline__ void q_to_f16(uint8_t* q, float* rs, float* tau, int tiles, float sign,
-                                         int ct, int threads) {
-  using C = TcCfg<D>;
-  for (int row = ct; row < tiles * C::BM; row += threads) {
-    uint8_t* p = q + row / C::BM * C::Q_TILE + row % C::BM * 128;
-    const int sw = row & 7;
-    float top = 0.f;
-#pragma unroll
-    for (int c = 0; c < D / 8; ++c) {
-      const uint4 x = *reinterpret_cast<const uint4*>(p + (c >> 3) * C::Q_HALF +
-                                                      (((c & 7) ^ sw) << 4));
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 f = Elem<F16>::unpack(w[k]);
-        top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
-      }
-    }
-    const int ex = static_cast<int>(__float_as_uint(top) >> 23);
-    const int up = ex == 255 ? 0 : min(126, 141 - ex);
-    const float by = sign * __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
-    rs[row] = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
-    float sum = 0.f;
-#pragma unroll
-    for (int c = 0; c < D / 8; ++c) {
-      uint4* at = reinterpret_cast<uint4*>(p + (c >> 3) * C::Q_HALF + (((c & 7) ^ sw) << 4));
-      const uint4 x = *at;
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-      uint32_t y[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 f = Elem<F16>::unpack(w[k]);
-        const float y0 = f.x * by, y1 = f.y * by;
-        sum += y0 + y1;
-        y[k] = (k & 1) ? pack_f16(y0 * 0.0625f, y1 * 0.0625f) : pack_f16(y0, y1);
-      }
-      *at = make_uint4(y[0], y[1], y[2], y[3]);
-    }
-    tau[row] = sum;
-  }
 }
 
 template <int D, bool F16>
@@ -275,7 +236,6 @@ int4_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
 
   if (threadIdx.x == 0) {
     mbar_init(&bars->q_full, 1);
-    mbar_init(&bars->q_conv, 64);
     for (int b = 0; b < I::BUFS; ++b) {
       mbar_init(&bars->kw_full[b], 1);             // one warp widens K, two V
       mbar_init(&bars->vw_full[b], 2);
@@ -308,9 +268,8 @@ int4_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     if (warp == 1) {
       // ---------------------------------------------------------- MMA issuer
       if (lane == 0 && ntiles > 0) {
-        constexpr uint32_t fmt = Elem<true>::kTcFormat;
-        constexpr uint32_t idesc_s = mma_idesc(C::BM, C::BN, false, fmt);
-        constexpr uint32_t idesc_o = mma_idesc(C::BM, D, true, fmt);
+        constexpr uint32_t idesc_s = mma_idesc(C::BM, C::BN, false, Elem<F16>::kTcFormat);
+        constexpr uint32_t idesc_o = mma_idesc(C::BM, D, true, Elem<true>::kTcFormat);
         constexpr int kStep = C::KV_TILE >> 4;
         const uint64_t qdesc[2] = {smem_desc_sw128(smem_u32(smem + C::OFF_Q), 16, 1024),
                                    smem_desc_sw128(smem_u32(smem + C::OFF_Q + C::Q_TILE), 16, 1024)};
@@ -340,7 +299,7 @@ int4_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           if (h == 1) tc_commit(&bars->pv_done[x]);
         };
         static_assert(I::BUFS == 2, "buffer t & 1, phase t >> 1");
-        bool ok = mbar_wait(&bars->q_conv, 0) && mbar_wait(&bars->kw_full[0], 0);
+        bool ok = mbar_wait(&bars->q_full, 0) && mbar_wait(&bars->kw_full[0], 0);
         if (ok) {
           issue_s(0, 0);
           if (two) issue_s(1, 0);
@@ -390,26 +349,15 @@ int4_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             tma_load_3d(smem + C::OFF_Q + x * C::Q_TILE + h * C::Q_HALF, &tmQ, &bars->q_full,
                         h * 64, hk * G, token0 + x * (TR / G));
       }
-      bool ok = true;
-      if (cw != 0) ok = mbar_wait(&bars->q_full, 0);
-      if (cw != 0 && ok) {
-        const float sign = a.scale_log2 > 0.f ? 1.f : a.scale_log2 < 0.f ? -1.f : 0.f;
-        q_to_f16<D, F16>(smem + C::OFF_Q, reinterpret_cast<float*>(smem + I::OFF_RS),
-                         reinterpret_cast<float*>(smem + I::OFF_TAU), two ? 2 : 1, sign,
-                         (cw - 1) * 32 + lane, 64);
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        mbar_arrive(&bars->q_conv);
-      }
-      ok = __all_sync(0xffffffffu, ok);
       const int32_t* bt_row = a.bt + static_cast<int64_t>(seg) * a.bt_row_stride;
       uint8_t* ring = smem + I::OFF_RING;
       constexpr int KP = I::SLOTS / 4 * 3;               // pairs: K's ring, V's halves of it
-      if (ok)
-        ok = cw == 0 ? widen_tiles<D, false, I::UNITS, KP>(a, pool, bars, smem, ring, bt_row, hk,
-                                                            kb, kv_len, ntiles, 0)
-                     : widen_tiles<D, true, I::UNITS / 2, KP / 2>(
-                           a, pool, bars, smem, ring + (cw + 1) * KP * I::SLOT, bt_row, hk, kb,
-                           kv_len, ntiles, (cw - 1) * (I::UNITS / 2));
+      const bool ok =
+          cw == 0 ? widen_tiles<D, F16, false, I::UNITS, KP>(a, pool, bars, smem, ring, bt_row, hk,
+                                                              kb, kv_len, ntiles, 0)
+                  : widen_tiles<D, F16, true, I::UNITS / 2, KP / 2>(
+                        a, pool, bars, smem, ring + (cw + 1) * KP * I::SLOT, bt_row, hk, kb, kv_len,
+                        ntiles, (cw - 1) * (I::UNITS / 2));
       cp_async_wait<0>();
       if (!ok) {
         abort_call(a);
