@@ -149,12 +149,14 @@ struct AttnArgs {
   // Sliding window: a query at position p sees key j <= p if j > p - window or
   // j < first. window = 0: none (the kernels' plain instantiations).
   int window, first;
-  // Changed scores and masks (scored = 1; 2-byte pools): cap and cap_in (base 2
-  // and 2 log2(e) softmax_scale / cap; cap = 0: none), a bias of slope x distance
-  // per query head, each sequence's bidirectional prefix, each query's first key
-  // (NULL: none).
+  // Changed scores and masks (scored = 1; 2-byte pools): cap, cap_in and cap_u (base
+  // 2, 2 log2(e) softmax_scale / cap and softmax_scale / cap; cap = 0: none), a bias
+  // of slope x distance per query head, each sequence's bidirectional prefix, each
+  // query's first key (NULL: none). tanh(cap_u x) of products up to cap_x4 (-1: of
+  // none) is x P(x^2), cap_c4 P's coefficients.
   int scored;
-  float cap, cap_in;
+  float cap, cap_in, cap_u, cap_x4;
+  float cap_c4[4];
   const float* slopes;
   const int32_t* prefix;
   const int32_t* first_key;
