@@ -29,6 +29,13 @@ namespace pa {
 //    the value. Rows past the sequence are zeros.
 //  * The widened tiles have the 2-byte kernel's layout (128-byte swizzle), two
 //    buffers each for K and V; the products that read a buffer free it.
+//  * What bounds it: four prompts of 2500 to 4096 tokens, 32 heads of 128
+//    over 8, take 700 us (0.5 of 1.9 PFLOP/s), 443 with neither the widening nor the
+//    scales and minima in the softmax. Widening K and V costs 135 of the difference,
+//    the softmax's loads of scales and minima and their arithmetic 70, the two
+//    together the rest: shared memory and issue slots are shared. (Seven widening
+//    warps in four more warps of 56 registers: 960 us, they spill. Loading scales
+//    before the products are there: 1250, likewise.)
 // ---------------------------------------------------------------------------
 
 // A piece of K, 32 codes (16 bytes), as 64 bytes of bf16 numbers or f16 2^-24 of
@@ -262,9 +269,11 @@ int4_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
-  // The register split of the prefill kernel (384 x 168).
+  // The register split: 384 x 168 = 128 x 88 + 256 x 208. (200 a softmax thread, the
+  // prefill kernel's split, spills three times as much: 714 us where this takes 700;
+  // 216 leaves the widening warps too few: 735.)
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;" ::: "memory");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;" ::: "memory");
     if (warp == 1) {
       // ---------------------------------------------------------- MMA issuer
       if (lane == 0 && ntiles > 0) {
@@ -365,7 +374,7 @@ int4_prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;" ::: "memory");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;" ::: "memory");
     const int X = (warp - 4) >> 2;
     if (X == 0 || two)
       tc_softmax_tile<Kind>(a, bars, smem, tmem, X, q_start, q_len, kv_len, kb, ke, ntiles, row0, R,
