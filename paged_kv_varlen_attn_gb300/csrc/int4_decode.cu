@@ -28,8 +28,9 @@ namespace pa {
 //      rounding weighs with code - 8 and not with the code. That sum is one more
 //      row of the product (ones for codes), and is taken off every 128 keys
 //      already, before the sums of codes grow past what float32 keeps of the
-//      difference (f16 outputs were off by 3.4e-4 of their size otherwise, by
-//      6e-4 without the eightfold sum; the output's own rounding is 2.1e-4).
+//      difference. (Off by, of their size, f16 outputs: 3.3e-4; without the
+//      eightfold sum 6e-4; with W in two f16 terms 2.5e-4, but five tokens of 16
+//      sequences take 128 us then for 108. The output's own rounding is 2.1e-4.)
 // The weights are 2^(score - m) against a running maximum m that is raised only
 // when a score passes it by more than 8; their sum is float32.
 //
@@ -46,7 +47,6 @@ namespace pa {
 // slots per warp), and int4_combine_kernel merges those, in order: no atomics,
 // the same bits on every run.
 // ---------------------------------------------------------------------------
-constexpr bool kI4WeightTerms = false;
 constexpr int kI4MinSlices = 1;    // of a range
 constexpr int kI4Keys = 32;        // of a warp: two halves of 16, each in one page
 
@@ -268,7 +268,6 @@ int4_decode_kernel(const __grid_constant__ Int4Maps maps, const __grid_constant_
   using E = Elem<F16>;
   constexpr int KW = D / 32;       // words of a key per lane in S^T
   constexpr int CH = D / 32;       // 16-byte pieces of a key
-  constexpr int WT = kI4WeightTerms && F16 ? 2 : 1;   // of W
   constexpr unsigned kAll = 0xffffffffu;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -546,7 +545,7 @@ int4_decode_kernel(const __grid_constant__ Int4Maps maps, const __grid_constant_
       }
       // W = weight x scale / ref x 2^6: at most 2^8 x 1 x 2^6 = 2^14.
       const float wscale = ref == 0.f ? 0.f : 64.f * inverse_power(ref);
-      uint32_t wb[NR][WT][4];
+      uint32_t wb[NR][4];
 #pragma unroll
       for (int nr = 0; nr < NR; ++nr) {
         float x[4][2];
@@ -613,12 +612,7 @@ int4_decode_kernel(const __grid_constant__ Int4Maps maps, const __grid_constant_
         }
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
-          const uint32_t top = pack_f16(w[h][0], w[h][1]);
-          wb[nr][0][h] = movmatrix_trans(top);
-          if constexpr (WT == 2) {
-            const float2 f = Elem<true>::unpack(top);
-            wb[nr][WT - 1][h] = movmatrix_trans(pack_f16(w[h][0] - f.x, w[h][1] - f.y));
-          }
+          wb[nr][h] = movmatrix_trans(pack_f16(w[h][0], w[h][1]));
         }
       }
       // ----------------------------------------------------------- O^T += N^T W^T
@@ -635,10 +629,8 @@ int4_decode_kernel(const __grid_constant__ Int4Maps maps, const __grid_constant_
         if constexpr (F16) {
 #pragma unroll
           for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-            for (int y = 0; y < WT; ++y)
-              mma_codes(accw[nr], 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u,
-                        wb[nr][y][2 * h], wb[nr][y][2 * h + 1]);
+            mma_codes(accw[nr], 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, wb[nr][2 * h],
+                      wb[nr][2 * h + 1]);
         }
 #pragma unroll
         for (int x = 0; x < CH; ++x) {
@@ -647,10 +639,8 @@ int4_decode_kernel(const __grid_constant__ Int4Maps maps, const __grid_constant_
             const uint32_t u0 = wv[x][0] >> (8 * k), u1 = wv[x][1] >> (8 * k);
 #pragma unroll
             for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-              for (int y = 0; y < WT; ++y)
-                mma_codes(acc[nr][2 * x + k], u0 & 0x000F000Fu, u0 & 0x00F000F0u, u1 & 0x000F000Fu,
-                          u1 & 0x00F000F0u, wb[nr][y][2 * h], wb[nr][y][2 * h + 1]);
+              mma_codes(acc[nr][2 * x + k], u0 & 0x000F000Fu, u0 & 0x00F000F0u, u1 & 0x000F000Fu,
+                        u1 & 0x00F000F0u, wb[nr][2 * h], wb[nr][2 * h + 1]);
           }
         }
       }
@@ -741,16 +731,23 @@ int4_decode_kernel(const __grid_constant__ Int4Maps maps, const __grid_constant_
 // ---------------------------------------------------------------------------
 // The sequences whose slices lie in more than one range or key run: their
 // states, in the ranges' order. A block takes two rows of a (sequence, KV head); a
-// thread takes four dims of a row and a part of the states, joined through
-// shared memory in order.
+// thread takes four dims of a row and a quarter (head size 64: an eighth) of the
+// states, joined through shared memory in order. With rows for at most two blocks an
+// SM (WIDE) a block takes one row and sixteen parts: few sequences have many states
+// each. Four sequences of 60000 to 131072 keys, 64 heads: 80.6 us where two rows a
+// block take 89.0; 64 sequences 86.8 and 75.9.
 // ---------------------------------------------------------------------------
-constexpr int kI4CombineThreads = 256, kI4CombineRows = 2;
+template <int D, bool WIDE>
+struct I4Combine {
+  static constexpr int THREADS = WIDE ? 4 * D : 256, ROWS = WIDE ? 1 : 2;
+};
 
-template <int D, bool F16, int NR>
-__global__ void __launch_bounds__(kI4CombineThreads, 5)
+template <int D, bool F16, int NR, bool WIDE>
+__global__ void __launch_bounds__(I4Combine<D, WIDE>::THREADS, 1280 / I4Combine<D, WIDE>::THREADS)
 int4_combine_kernel(const __grid_constant__ Int4DecodeArgs a) {
-  __shared__ float4 part_o[kI4CombineThreads];
-  __shared__ float2 part_ml[kI4CombineThreads];
+  constexpr int THREADS = I4Combine<D, WIDE>::THREADS, ROWS = I4Combine<D, WIDE>::ROWS;
+  __shared__ float4 part_o[THREADS];
+  __shared__ float2 part_ml[THREADS];
   const int s = static_cast<int>(blockIdx.x) / a.H_kv;
   const int hk = static_cast<int>(blockIdx.x) - s * a.H_kv;
   const I4Seq sq = i4_seq(a, s, false);
@@ -760,12 +757,12 @@ int4_combine_kernel(const __grid_constant__ Int4DecodeArgs a) {
   }
   const int groups = a.H_kv / a.heads_per_block, group = hk / a.heads_per_block;
   const int hl = hk - group * a.heads_per_block;
-  constexpr int WIDTH = kI4CombineRows * (D / 4), PARTS = kI4CombineThreads / WIDTH;
+  constexpr int WIDTH = ROWS * (D / 4), PARTS = THREADS / WIDTH;
   const int rows = sq.q_len * a.G, part = threadIdx.x / WIDTH;
   const int unit = threadIdx.x - part * WIDTH;
-  const int row = blockIdx.y * kI4CombineRows + unit / (D / 4), col = unit % (D / 4) * 4;
+  const int row = blockIdx.y * ROWS + unit / (D / 4), col = unit % (D / 4) * 4;
   pdl_wait();
-  if (blockIdx.y * kI4CombineRows >= rows) return;
+  if (blockIdx.y * ROWS >= rows) return;
   const long long per = __ldcg(a.table), before = __ldcg(a.table + 1 + s);
   const int r0 = static_cast<int>(i4_div(before, per));
   const int r1 = static_cast<int>(i4_div(before + sq.n - 1, per));
@@ -828,7 +825,7 @@ int4_combine_kernel(const __grid_constant__ Int4DecodeArgs a) {
 }
 
 template <int D, bool F16, int NR>
-static cudaError_t launch_int4_decode_nr(const Int4Maps& maps, const Int4DecodeArgs& a,
+static cudaError_t launch_int4_decode_nr(const Int4Maps& maps, const Int4DecodeArgs& a, int sms,
                                          cudaStream_t st) {
   using C = I4Cfg<D, NR>;
   static std::atomic<bool> configured[kMaxDevices];
@@ -851,11 +848,17 @@ static cudaError_t launch_int4_decode_nr(const Int4Maps& maps, const Int4DecodeA
   e = cudaLaunchKernelEx(&cfg, int4_decode_kernel<D, F16, NR>, maps, a);
   if (e != cudaSuccess || (e = cudaGetLastError()) != cudaSuccess) return e;
   const int most = min(a.tokens_max, a.max_q) * a.G;   // rows of a sequence
-  cfg.gridDim = dim3(static_cast<unsigned>(a.num_seqs) * static_cast<unsigned>(a.H_kv),
-                     (most + kI4CombineRows - 1) / kI4CombineRows);
-  cfg.blockDim = dim3(kI4CombineThreads);
+  const unsigned units = static_cast<unsigned>(a.num_seqs) * static_cast<unsigned>(a.H_kv);
   cfg.dynamicSmemBytes = 0;
-  e = cudaLaunchKernelEx(&cfg, int4_combine_kernel<D, F16, NR>, a);
+  if (static_cast<int64_t>(units) * most <= 2 * sms) {
+    cfg.gridDim = dim3(units, most);
+    cfg.blockDim = dim3(I4Combine<D, true>::THREADS);
+    e = cudaLaunchKernelEx(&cfg, int4_combine_kernel<D, F16, NR, true>, a);
+  } else {
+    cfg.gridDim = dim3(units, (most + 1) / 2);
+    cfg.blockDim = dim3(I4Combine<D, false>::THREADS);
+    e = cudaLaunchKernelEx(&cfg, int4_combine_kernel<D, F16, NR, false>, a);
+  }
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
@@ -886,10 +889,10 @@ cudaError_t launch_int4_decode(const Int4Maps& maps, Int4DecodeArgs a, int D, bo
   auto by_rows = [&](auto d, auto half) {
     constexpr int kD = decltype(d)::value;
     constexpr bool kF16 = decltype(half)::value;
-    if (nr == 1) return launch_int4_decode_nr<kD, kF16, 1>(maps, a, st);
-    if (nr == 2) return launch_int4_decode_nr<kD, kF16, 2>(maps, a, st);
-    if (nr == 3) return launch_int4_decode_nr<kD, kF16, 3>(maps, a, st);
-    return launch_int4_decode_nr<kD, kF16, 4>(maps, a, st);
+    if (nr == 1) return launch_int4_decode_nr<kD, kF16, 1>(maps, a, sms, st);
+    if (nr == 2) return launch_int4_decode_nr<kD, kF16, 2>(maps, a, sms, st);
+    if (nr == 3) return launch_int4_decode_nr<kD, kF16, 3>(maps, a, sms, st);
+    return launch_int4_decode_nr<kD, kF16, 4>(maps, a, sms, st);
   };
   using std::integral_constant;
   if (D == 128)
