@@ -728,15 +728,16 @@ pa_status pa_gather_cache_int4(const void* key_cache, const void* value_cache,
  * scale + minimum. sinks as in pa_attn_opts (NULL for none). Groups of at most
  * 128 query heads per KV head (PA_ERR_UNSUPPORTED otherwise); max_seqlen_k at
  * most 2^30 (PA_ERR_INVALID_ARG).
+ * q.k is formed from the codes themselves, which the products take exactly, and
+ * scale and minimum are applied to the sums in float32.
  * Sequences of at most 32 packed query rows (tokens x heads of the group; decode
- * and short queries) form q.k from the codes themselves, which are exact in
- * f16, and apply scale and minimum to the sums; q is taken as f16 after a
- * power-of-two row scale, exact for every bf16 element of at least 2^-28 of its
- * row's largest. The weights times V's scale are rounded to f16 after a
- * power-of-two row scale. Longer sequences run on the tensor-core kernel: q.k the
- * same way, V widened to f16 values (one rounding, at most 2^-11 of a value) and
- * the weights in f16; there, as in the other prefill kernels, a NaN in V also
- * reaches queries of the call that stand less than a key tile in front of it.
+ * and short queries): q is taken as f16 after a power-of-two row scale, exact for
+ * every bf16 element of at least 2^-28 of its row's largest. The weights times V's
+ * scale are rounded to f16 after a power of two. Longer sequences run on the
+ * tensor-core kernel: q as it is, V widened to f16 values (one rounding, at most
+ * 2^-11 of a value) and the weights in f16; there, as in the other prefill kernels,
+ * a NaN in V also reaches queries of the call that stand less than a key tile in
+ * front of it.
  * In pages that are read, rows past a sequence's keys do not matter.
  */
 size_t pa_varlen_fwd_int4kv_workspace_size(int num_seqs, int total_q, int max_seqlen_q,

@@ -213,8 +213,10 @@ struct TileScore {
 // cap's tanh(u) = 1 - 2 / (1 + e^2u) takes two exponential-unit operations an element
 // where the softmax itself takes one, so tiles whose |u| all stay below 1/2 (scores up
 // to half the cap), or below 1, take a polynomial on the FMA pipe: four prompts of 2500
-// to 4096 tokens, 32 heads of 128, 409 us where the exponential takes 487 and no cap
-// 330. (A shorter polynomial for |u| below 1/4 gave nothing back: the code grew.)
+// to 4096 tokens, 32 heads of 128, 421 us where the exponential takes 487 and no cap
+// 330. (A shorter polynomial for |u| below 1/4 gave nothing back: the code grew.) A
+// tile with keys that a row does not see takes the exponentials, so that what those
+// keys hold does not choose the form, and rows outside the item have no say.
 // The bias is slope (key - row): each value takes its distance to the group's last key
 // with its factor, in one two-lane FMA, and the group's own is left to the maximum and
 // the exponent, once a group. (Last, so that the nearest key's score is not rounded at
@@ -224,7 +226,7 @@ struct TileScore {
 // none.
 template <int BN>
 __device__ __forceinline__ TileScore score_tile(const AttnArgs& a, float* xs, float sl2, float slope,
-                                                int pos, int key0) {
+                                                int pos, int key0, bool rvalid, bool hides) {
   float factor = sl2;
   if (a.cap > 0.f) {
     factor = a.cap;
@@ -233,7 +235,9 @@ __device__ __forceinline__ TileScore score_tile(const AttnArgs& a, float* xs, fl
     for (int e = 0; e < BN; e += 8)
 #pragma unroll
       for (int j = 0; j < 4; ++j) m[j] = fmax3(m[j], fabsf(xs[e + 2 * j]), fabsf(xs[e + 2 * j + 1]));
-    const float x = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+    float x = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+    if (!rvalid) x = 0.f;
+    else if (hides) x = INFINITY;
     if (__builtin_expect(__all_sync(0xffffffffu, x <= a.cap_x4), 1)) {
 #pragma unroll
       for (int e = 0; e < BN; e += 2) odd_poly2(xs[e], xs[e + 1], a.cap_c4);
@@ -249,7 +253,7 @@ __device__ __forceinline__ TileScore score_tile(const AttnArgs& a, float* xs, fl
 #pragma unroll
       for (int e = 0; e < BN; ++e) xs[e] = capped_score(xs[e], a.cap_in, 1.f);
     }
-  } else if (sl2 < 0.f) {   // (the maximum is taken before the factor)
+  } else if (sl2 < 0.f) {   // (the maximum comes before the factor)
     factor = -sl2;
 #pragma unroll
     for (int e = 0; e < BN; ++e) xs[e] = -xs[e];
@@ -371,7 +375,7 @@ __device__ __forceinline__ void tc_softmax_tile(const AttnArgs& a, TcBars* bars,
     }
     TileScore ts = {sl2, 0.f, 0.f};
     if constexpr (SC) {
-      ts = score_tile<C::BN>(a, xs, sl2, slope, pos, key0);
+      ts = score_tile<C::BN>(a, xs, sl2, slope, pos, key0, rvalid, edge || key0 < low);
       if (edge || key0 < low) {
 #pragma unroll
         for (int c = 0; c < C::BN / 32; ++c) {

@@ -713,7 +713,8 @@ static pa_status varlen_impl(const pa_kv_update* upd, const void* q, int64_t q_t
              num_kv_heads, head_size, sms};
   d.max_kv = max_seqlen_k;
   d.kv_fp8 = kv.fp8;
-  d.tc_allowed = softmax_scale > 0.f;
+  // (With changed scores the prefill kernel takes negative scales too.)
+  d.tc_allowed = softmax_scale > 0.f || (score && softmax_scale < 0.f);
   if (window > 0) {
     // A window of at least every sequence is no window; else a row tile reads
     // at most the first tokens, the window and its own tokens, in whole TMA

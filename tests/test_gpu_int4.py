@@ -7,10 +7,10 @@ Tolerances, from arithmetic:
     largest element, so a code may move by one where the quotient lies that near
     to a border, and the f16 params by one step.
   * scores: with A = scale * sum |q_i| max_i |k_i| over a row, float32 sums of
-    at most 256 terms in at most 64 roundings are off by 2^-18 A; the
-    tensor-core kernel's K values are rounded to f16, half a step each:
-    2^-12 A more (scale sum |q_i| |k_i| <= A). LSE: that, and 2^-20 (1 + |lse|)
-    for the logarithm and the exponentials.
+    at most 256 terms in at most 64 roundings are off by 2^-18 A for sums of
+    values. The kernels sum codes and q apart, scale (q.n) + minimum sum q, whose
+    parts are up to 3 A (a row's range is at most twice its largest): 3 2^-18 A.
+    LSE: that, and 2^-20 (1 + |lse|) for the logarithm and the exponentials.
   * outputs: e = 2 (score error + 2^-20) times the largest |v| of the head from
     the weights; 2^-11 (f16, half a step) of the largest weight x code sum, at
     most the largest row range of V, and of |v| (minimum and range: 3 |v|max);
@@ -276,8 +276,7 @@ class Batch:
             big_v = value.abs().amax((0, 2)) if kv else torch.zeros(self.hk)
             group = self.H // self.hk
             A = abs(scale) * q.abs().sum(-1) * big_k.repeat_interleave(group)      # [ql, H]
-            wide = ql * group > 32
-            err = A * (2.0 ** -18 + (2.0 ** -12 if wide else 0.0))
+            err = A * 3 * 2.0 ** -18
             fin = torch.isfinite(wl)
             assert torch.equal(fin, torch.isfinite(lse[:, rows]))
             lt = err.T + 2.0 ** -20 * (1 + wl.abs())

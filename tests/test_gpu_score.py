@@ -4,7 +4,8 @@ Tolerances, from arithmetic:
   * scores: float32 sums of at most 256 terms in at most 64 roundings are off by
     2^-18 A, A = scale sum |q_i| max_i |k_i| over a row. A cap has slope at most
     one, and its exponential (2 units of 2^-23), reciprocal (1) and final sum add
-    at most 2^-20 cap. The bias is rounded twice: 2^-22 of its size.
+    at most 2^-20 cap; a polynomial, 6e-7 of scores up to half the cap or 2e-7 of
+    scores up to the cap, less. The bias is rounded twice: 2^-22 of its size.
     LSE: that, and 2^-20 (1 + |lse|) for the logarithm and the exponentials.
   * outputs: 2 (score error + 2^-20) of the largest |v| from the weights, half a
     step of the type for the weights' rounding, of |v|; half a step of the output.
@@ -264,3 +265,83 @@ def test_capture():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("D,dt", [(64, "f16"), (128, "bf16"), (256, "bf16")])
+@pytest.mark.parametrize("cap", [2.0, 5.0, 12.0, 60.0, 3e6])
+def test_caps_of_every_size(D, dt, cap):
+    # Scores far past the cap, up to it, up to half of it, a few per cent of it.
+    b = Batch([(700, 300), (260, 129)], 6, 2, D, 16, dt, seed=21)
+    out, lse = b.run(softcap=cap)
+    b.check(out, lse, softcap=cap)
+    kw = dict(softcap=cap, alibi_slopes=b.slopes())
+    out, lse = b.run(**kw)
+    b.check(out, lse, **kw)
+    if D < 256:                      # (head size 256 takes positive scales)
+        out, lse = b.run(-b.scale, **kw)
+        b.check(out, lse, -b.scale, **kw)
+
+
+def test_hidden_keys_choose_nothing():
+    # What the rows past a sequence's end and in front of its documents hold, and the
+    # neighbours in the batch, do not change a bit of a capped prompt.
+    b = Batch([(300, 140), (200, 64)], 4, 2, 128, 16, "bf16", seed=22)
+    first = torch.cat([torch.full((140,), 100), torch.zeros(64)]).int()
+    kw = dict(first_key=first, softcap=40.0, alibi_slopes=b.slopes())
+    out0, lse0 = b.run(**kw)
+    for x in (0.0, 300.0, math.inf):
+        b.kc[b.kc.isnan()] = x
+        b.vc[b.vc.isnan()] = x
+        j = torch.arange(100)
+        page = b.table[0].long()[j // 16]
+        b.kc[page, j % 16] = x
+        b.vc[page, j % 16] = x
+        b.q[140:] *= 30
+        out, lse = b.run(**kw)
+        assert torch.equal(out[:140], out0[:140]) and torch.equal(lse[:, :140], lse0[:, :140])
+        used = b.kc == x
+        b.kc[used], b.vc[used] = math.nan, math.nan
+
+
+@pytest.mark.parametrize("ql", [1, 150])
+def test_scale_zero_and_negative_without_a_cap(ql):
+    b = Batch([(300, ql)], 8, 2, 128, 16, "bf16", seed=23, qscale=2.0)
+    first = torch.full((b.T,), 40, dtype=torch.int32)
+    for scale in (0.0, -0.2):
+        for kw in (dict(first_key=first), dict(alibi_slopes=b.slopes())):
+            out, lse = b.run(scale, **kw)
+            b.check(out, lse, scale, **kw)
+
+
+@pytest.mark.parametrize("slope", [8.0, -0.5, 1000.0])
+def test_slopes_of_every_size(slope):
+    b = Batch([(700, 200), (90, 90)], 4, 4, 64, 16, "f16", seed=24, qscale=3.0)
+    kw = dict(alibi_slopes=torch.full((4,), slope))
+    out, lse = b.run(**kw)
+    b.check(out, lse, **kw)
+
+
+def test_two_graphs_take_turns_with_one_workspace():
+    # Both capture the same workspace; replayed in turn on one stream, each gives what it
+    # gave alone.
+    b = Batch([(100, 1), (300, 90)], 8, 2, 128, 16, "bf16", seed=25)
+    d = [t.to(DEV) for t in (b.q, b.kc, b.vc, b.cu, b.lens, b.table)]
+    ws = pa.alloc_workspace(pa.varlen_fwd_workspace_size(
+        2, b.T, b.max_q, b.max_k, 8, 2, 128, 16,
+        torch.cuda.get_device_properties(0).multi_processor_count), DEV)
+    kws = [dict(softcap=9.0), dict(alibi_slopes=b.slopes().to(DEV))]
+    graphs, outs, wants = [], [], []
+    for kw in kws:
+        wants.append(pa.score_fwd(*d, b.max_q, b.max_k, b.scale, **kw))
+        outs.append((torch.empty_like(wants[-1][0]), torch.empty_like(wants[-1][1])))
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            pa.score_fwd(*d, b.max_q, b.max_k, b.scale, out=outs[-1][0], lse=outs[-1][1],
+                         workspace=ws, **kw)
+    for _ in range(3):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    for o, w in zip(outs, wants):
+        assert torch.equal(o[0], w[0]) and torch.equal(o[1], w[1])
+    b.check(*outs[0], softcap=9.0)
