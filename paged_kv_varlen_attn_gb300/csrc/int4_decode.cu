@@ -26,11 +26,12 @@ namespace pa {
 //      The rest of the value enters by sums per row: of weights x (minimum + 8
 //      scale), and of W as rounded, eightfold, which is taken off: so a weight's
 //      rounding weighs with code - 8 and not with the code. That sum is one more
-//      row of the product (ones for codes), and is taken off every 128 keys
-//      already, before the sums of codes grow past what float32 keeps of the
-//      difference. (Off by, of their size, f16 outputs: 3.3e-4; without the
-//      eightfold sum 6e-4; with W in two f16 terms 2.5e-4, but five tokens of 16
-//      sequences take 128 us then for 108. The output's own rounding is 2.1e-4.)
+//      row of the product (ones for codes), and is taken off after every 32 keys,
+//      before the sums of codes grow past what float32 keeps of the difference.
+//      (Off by, of their size, f16 outputs: 3.2e-4; without the eightfold sum
+//      6e-4; with W in two f16 terms 2.5e-4, but five tokens of 16 sequences take
+//      20 us more than 103. The output's own rounding is 2.1e-4. bf16 outputs, whose
+//      rounding is 1.7e-3, go without the sum.)
 // The weights are 2^(score - m) against a running maximum m that is raised only
 // when a score passes it by more than 8; their sum is float32.
 //
@@ -536,8 +537,6 @@ int4_decode_kernel(const __grid_constant__ Int4Maps maps, const __grid_constant_
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) accw[nr][e] *= f;
-#pragma unroll
           for (int t = 0; t < D / 16; ++t)
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[nr][t][e] *= f;
@@ -580,8 +579,6 @@ int4_decode_kernel(const __grid_constant__ Int4Maps maps, const __grid_constant_
             l[nr][e] *= f;
             lv[nr][e] *= f;
             m[nr][e] = nm;
-            accw[nr][e] *= f;
-            accw[nr][2 + e] *= f;
 #pragma unroll
             for (int t = 0; t < D / 16; ++t) {
               acc[nr][t][e] *= f;
@@ -647,10 +644,9 @@ int4_decode_kernel(const __grid_constant__ Int4Maps maps, const __grid_constant_
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[slot]);        // the slot may be filled again
       if (mine) ok = copier.copy(a, maps.m, smem, full, empty, head0, from.count);
-      if (F16 && (i & 3) == 3) centre();
+      if (F16) centre();
     }
     if (!ok) break;
-    if (F16 && !idle) centre();
 
     // ---------------------------------------------------------------- the state
     // acc[2 x + k] holds elements 32 x + 8 (g / 2) + g % 2 + 4 k (entries 0, 1: rows
