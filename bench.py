@@ -52,7 +52,8 @@ _CSRC = os.path.join(ROOT, "paged_kv_varlen_attn_gb300", "csrc")
 SPLIT_KERNEL_SRCS = [os.path.join(_CSRC, f) for f in
                      ("attn_split.cu", "device_common.cuh", "epilogue.cuh", "pa_internal.h")]
 TC_KERNEL_SRCS = [os.path.join(_CSRC, f) for f in
-                  ("attn_tc.cu", "device_common.cuh", "epilogue.cuh", "pa_internal.h")]
+                  ("attn_tc.cu", "attn_tc.cuh", "device_common.cuh", "epilogue.cuh",
+                   "pa_internal.h")]
 KERNEL_SRCS = {"attn_split_kernel<128>": SPLIT_KERNEL_SRCS,
                "attn_split_kernel<128, fp8>": SPLIT_KERNEL_SRCS,
                "attn_tc_kernel<128>": TC_KERNEL_SRCS,
