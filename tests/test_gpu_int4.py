@@ -496,7 +496,91 @@ def test_run_together_and_captured():
     for (a, b), (q, out, lse) in zip(ends, got):
         assert torch.equal(q.cpu(), turned(qkv[a:b, :H].float(), cos_sin[a:b], False).bfloat16())
         want, wl = ref.attend(q.cpu(), key[:b], value[:b], D ** -0.5)
-        # Weights 2^-11 and V 2^-11 of values up to 4, scores 2^-12 A with A < 40.
-        tol = want.abs() * 2.0 ** -8 + 4 * (2 * 40 * 2.0 ** -12 + 3 * 2.0 ** -11)
+        # Weights 2^-11 and V 2^-11 of values up to 4, scores 3 2^-18 A with A < 40.
+        err = 3 * 40 * 2.0 ** -18
+        tol = want.abs() * 2.0 ** -8 + 4 * (2 * err + 3 * 2.0 ** -11)
         assert ((out.cpu().double() - want).abs() <= tol).all()
-        assert ((lse.cpu().double() - wl).abs() <= 40 * 2.0 ** -12 + 1e-5).all()
+        assert ((lse.cpu().double() - wl).abs() <= err + 1e-5).all()
+
+
+@pytest.mark.parametrize("seqs,dt", [([(300, 1), (77, 1), (900, 3)], "f16"),
+                                     ([(200, 90), (50, 1), (700, 40)], "bf16")])
+def test_strided_pools_and_queries_past_32_bits(seqs, dt):
+    # Pages of K and V in one tensor, their params in another, pages 2^21 bytes apart over
+    # 5 GB; queries that are a slice of a wider row; tokens behind the last sequence.
+    H, hk, D, bs = 8, 2, 128, 16
+    b = Batch(seqs, H, hk, D, bs, dt, seed=31)
+    nb, page = b.codes[0].shape[0], bs * hk * D // 2
+    far = 5 * 2 ** 30 // 2 ** 21 - nb                 # the batch's pages are the last ones
+    store = torch.empty(((far + nb) * 2 ** 21,), dtype=torch.uint8, device=DEV)
+    shape, stride = (far + nb, bs, hk, D // 2), (2 ** 21, hk * D // 2, D // 2, 1)
+    codes = [store.as_strided(shape, stride, x * page) for x in (0, 1)]
+    params = torch.zeros((far + nb, 2, hk, bs, 2), dtype=torch.float16, device=DEV)
+    for x in (0, 1):
+        codes[x][far:].copy_(b.codes[x])
+        params[far:, x].copy_(b.params[x])
+    table = torch.where(b.table < nb, b.table + far, b.table).to(DEV)
+    wide = torch.randn((b.T + 5, H + 3, D), device=DEV).to(b.dtype)
+    wide[:b.T, 2:2 + H] = b.q.to(DEV)
+    out = torch.full((b.T + 5, H, D), 7.0, dtype=b.dtype, device=DEV)
+    lse = torch.full((H, b.T + 5), 7.0, device=DEV)
+    pa.varlen_fwd_int4kv(wide[:, 2:2 + H], *codes, params[:, 0], params[:, 1], b.cu.to(DEV),
+                         b.lens.to(DEV), table, b.max_q, b.max_k, b.scale, True, out=out, lse=lse)
+    assert (out[b.T:] == 7.0).all() and (lse[:, b.T:] == 7.0).all()
+    b.check(out[:b.T], lse[:, :b.T])
+    # The write and the way back at the same far pages; one row asked for twice.
+    slots = torch.tensor([(far + nb - 1) * bs + 3, (far + nb - 2) * bs, (far + nb - 1) * bs + 9])
+    x = torch.randn((2, 3, hk, D)).to(b.dtype)
+    pools = (*codes, params[:, 0], params[:, 1])
+    pa.reshape_and_cache_int4(x[0].to(DEV), x[1].to(DEV), *pools, slots.to(DEV))
+    again = slots[[0, 1, 2, 0]]
+    rows = pa.gather_cache_int4(*pools, again.to(DEV), torch.float16)
+    for got, new in zip(rows, x):
+        n, p = ref.quantize_int4(new.float())
+        want = (n.float() * p[..., :1].float() + p[..., 1:].float()).half()[[0, 1, 2, 0]]
+        assert torch.equal(got.cpu(), want)
+
+
+def test_two_streams_and_two_graphs():
+    # Two batches at once on streams of their own; then two graphs that share a
+    # workspace, replayed in turn.
+    batches = [Batch([(1500, 1), (40, 5), (300, 60)], 8, 2, 128, 16, "f16", seed=41),
+               Batch([(700, 1)] * 9 + [(129, 40)], 4, 4, 64, 32, "bf16", seed=42)]
+    alone = [b.run() for b in batches]
+    args = [[t.to(DEV) for t in (b.q, *b.codes, *b.params, b.cu, b.lens, b.table)] for b in batches]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(DEV) for _ in batches]
+    got = []
+    for _ in range(5):
+        for b, d, s in zip(batches, args, streams):
+            with torch.cuda.stream(s):
+                got.append(pa.varlen_fwd_int4kv(*d, b.max_q, b.max_k, b.scale, True))
+    torch.cuda.synchronize()
+    for i, (out, lse) in enumerate(got):
+        assert torch.equal(out, alone[i % 2][0]) and torch.equal(lse, alone[i % 2][1])
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    ws = pa.alloc_workspace(max(pa.varlen_fwd_int4kv_workspace_size(
+        len(b.seqs), b.T, b.max_q, b.max_k, b.H, b.hk, b.D, b.bs, sms) for b in batches), DEV)
+    graphs, outs = [], []
+    for b, d in zip(batches, args):
+        outs.append((torch.empty_like(d[0]), torch.empty((b.H, b.T), device=DEV)))
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            pa.varlen_fwd_int4kv(*d, b.max_q, b.max_k, b.scale, True, out=outs[-1][0],
+                                 lse=outs[-1][1], workspace=ws)
+    for _ in range(4):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    for o, w in zip(outs, alone):
+        assert torch.equal(o[0], w[0]) and torch.equal(o[1], w[1])
+
+
+@pytest.mark.parametrize("hk", [1, 3, 4, 7])
+@pytest.mark.parametrize("ql", [1, 20])
+def test_lengths_around_every_border(hk, ql):
+    # Keys around the pages, the steps of 32 keys, the runs of a block and a key tile.
+    lens = [1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 255, 256, 257, 511, 513]
+    b = Batch([(n, min(n, ql)) for n in lens], 2 * hk, hk, 64, 48, "bf16", seed=hk)
+    out, lse = b.run()
+    b.check(out, lse)
