@@ -26,12 +26,13 @@ namespace pa {
 //      The rest of the value enters by sums per row: of weights x (minimum + 8
 //      scale), and of W as rounded, eightfold, which is taken off: so a weight's
 //      rounding weighs with code - 8 and not with the code. That sum is one more
-//      row of the product (ones for codes), and is taken off after every 32 keys,
-//      before the sums of codes grow past what float32 keeps of the difference.
-//      (Off by, of their size, f16 outputs: 3.2e-4; without the eightfold sum
-//      6e-4; with W in two f16 terms 2.5e-4, but five tokens of 16 sequences take
-//      20 us more than 103. The output's own rounding is 2.1e-4. bf16 outputs, whose
-//      rounding is 1.7e-3, go without the sum.)
+//      row of the product (with the code 8, of either size, so that it loses what
+//      the MMA loses of products of subnormals), and is taken off after every 32
+//      keys, before the sums of codes grow past what float32 keeps of the
+//      difference. (Off by, of their size, f16 outputs: 3.0e-4; 3.2e-4 with a row
+//      of ones; 6e-4 without that sum; 2.5e-4 with W in two f16 terms and ones,
+//      but five tokens of 16 sequences take 20 us more than 99. The output's own
+//      rounding is 2.1e-4. bf16 outputs, whose rounding is 1.7e-3, go without.)
 // The weights are 2^(score - m) against a running maximum m that is raised only
 // when a score passes it by more than 8; their sum is float32.
 //
@@ -409,7 +410,7 @@ int4_decode_kernel(const __grid_constant__ Int4Maps maps, const __grid_constant_
       }
     }
     float m[NR][2], l[NR][2], lv[NR][2];               // lv: sum of weights x middle of V's row
-    float acc[NR][D / 16][4], accw[NR][4];             // accw: sum of W, every entry of a column
+    float acc[NR][D / 16][4], accw[NR][4];             // accw: of 8 W, in a column's units
     float ref = 0.f;                                   // power of two, at least V's scales so far
 #pragma unroll
     for (int nr = 0; nr < NR; ++nr) {
@@ -431,10 +432,10 @@ int4_decode_kernel(const __grid_constant__ Int4Maps maps, const __grid_constant_
       for (int nr = 0; nr < NR; ++nr) {
 #pragma unroll
         for (int t = 0; t < D / 16; ++t) {
-          ffma2(acc[nr][t][0], acc[nr][t][1], accw[nr][0], accw[nr][1], -0x1p-21f, -0x1p-21f,
-                acc[nr][t][0], acc[nr][t][1]);
-          ffma2(acc[nr][t][2], acc[nr][t][3], accw[nr][0], accw[nr][1], -0x1p-17f, -0x1p-17f,
-                acc[nr][t][2], acc[nr][t][3]);
+          fadd2(acc[nr][t][0], acc[nr][t][1], acc[nr][t][0], acc[nr][t][1], -accw[nr][0],
+                -accw[nr][1]);
+          fadd2(acc[nr][t][2], acc[nr][t][3], acc[nr][t][2], acc[nr][t][3], -accw[nr][2],
+                -accw[nr][3]);
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) accw[nr][e] = 0.f;
@@ -626,7 +627,7 @@ int4_decode_kernel(const __grid_constant__ Int4Maps maps, const __grid_constant_
         if constexpr (F16) {
 #pragma unroll
           for (int nr = 0; nr < NR; ++nr)
-            mma_codes(accw[nr], 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, wb[nr][2 * h],
+            mma_codes(accw[nr], 0x00080008u, 0x00800080u, 0x00080008u, 0x00800080u, wb[nr][2 * h],
                       wb[nr][2 * h + 1]);
         }
 #pragma unroll
