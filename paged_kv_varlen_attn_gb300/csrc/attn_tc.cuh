@@ -66,10 +66,11 @@ static_assert(kTcTileRows == TcCfg<128>::BM, "a Q tile spans the 128 TMEM lanes"
 static_assert(TcCfg<256>::SMEM_BYTES <= 227 * 1024, "head size 256 fits shared memory");
 static_assert(TcCfg<256>::O_COL + 256 <= TcCfg<256>::TMEM_COLS, "head size 256 fits TMEM");
 
-// Over 4-bit pools (head sizes 64 and 128): K and V are widened to f16 tiles
-// laid out as the 2-byte kernel's, two buffers of each, by warps 0, 2 and 3,
-// which read the codes through rings of asynchronous copies of their own. A unit
-// is 16 keys of K or of V: its codes and its 16 (scale, minimum) pairs.
+// Over 4-bit pools (head sizes 64 and 128): K is widened to codes in Q's type and V
+// to f16 values, in tiles laid out as the 2-byte kernel's, two buffers of each, by
+// warps 0 (K), 2 and 3 (V), which read the codes through rings of asynchronous
+// copies of their own. A unit is 16 keys of K or of V: its codes and its 16 (scale,
+// minimum) pairs.
 template <int D>
 struct TcI4 {
   using C = TcCfg<D>;
@@ -104,7 +105,8 @@ struct TcBars {
   // widened V tile ready (64 arrivals), widened V buffer free again (MMA
   // commit). Buffer b holds tiles b, b + VBUF, ... (phase t / VBUF).
   uint64_t q_conv, vw_full[2], vw_free[2];
-  // 4-bit pools: likewise widened K tiles (vw for V), one arrival per unit.
+  // 4-bit pools: likewise widened K tiles (vw for V), one arrival per widening warp,
+  // and the keys' scales and minima.
   uint64_t kw_full[2], kw_free[2], par_full[4];
   uint32_t tmem_base;
   volatile int abort;

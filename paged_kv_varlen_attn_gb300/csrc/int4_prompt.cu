@@ -1,5 +1,5 @@
 // Attention over 4-bit pools for prompts: the tensor-core prefill kernel of
-// attn_tc.cu with K and V widened to f16 on the way.
+// attn_tc.cu with K widened to codes and V to values on the way.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
