@@ -739,6 +739,10 @@ pa_status pa_gather_cache_int4(const void* key_cache, const void* value_cache,
  * a NaN in V also reaches queries of the call that stand less than a key tile in
  * front of it.
  * In pages that are read, rows past a sequence's keys do not matter.
+ * The workspace has a place for what any warp of the device may leave: for up to 8
+ * (32) packed rows 20 MB (40 MB) at head size 128 and 152 multiprocessors, however few
+ * the sequences; where neither 3 nor 4 divides num_kv_heads, half of that and 17 kB (66
+ * kB) per sequence and pair of KV heads (per KV head, if their number is odd).
  */
 size_t pa_varlen_fwd_int4kv_workspace_size(int num_seqs, int total_q, int max_seqlen_q,
                                            int max_seqlen_k, int num_heads, int num_kv_heads,

@@ -45,9 +45,9 @@ namespace pa {
 // that a lane issues per 16 keys; the copies run ahead across sequences. (A ring
 // per warp, filled by its own 16-byte copies, cost 158 of 604 instructions per 32
 // keys, and 64 sequences 77.4 us.)
-// A sequence's state that a warp does not hold whole goes to the workspace (two
-// slots per warp), and int4_combine_kernel merges those, in order: no atomics,
-// the same bits on every run.
+// A sequence's state that a warp does not hold whole goes to the workspace (see
+// i4_piece), and int4_combine_kernel merges those, in order: no atomics, the same
+// bits on every run.
 // ---------------------------------------------------------------------------
 constexpr int kI4MinSlices = 1;    // of a range
 constexpr int kI4Keys = 32;        // of a warp: two halves of 16, each in one page
@@ -125,6 +125,19 @@ __device__ __forceinline__ long long i4_per_range(const Int4DecodeArgs& a, long 
 // Token of a packed row (below 32).
 __device__ __forceinline__ int i4_token(const Int4DecodeArgs& a, int row) {
   return row * a.g_inv >> 16;
+}
+
+// Where the states of sequence s's slices in a range go, in units of a head group's
+// warps. With one key run a warp holds a sequence whole that lies in one range, and
+// writes its output itself: two places a range, for a sequence that began in front of
+// it or with it (0) and for one that starts inside and goes on (1). With several runs
+// every sequence of a range leaves its states, however many there are: range + s, which
+// grows from each piece to the next, since that is of the next range or of a later
+// sequence.
+__device__ __forceinline__ int64_t i4_piece(const Int4DecodeArgs& a, int range, int s,
+                                            bool inside) {
+  return a.key_runs == 1 ? 2 * static_cast<int64_t>(range) + inside
+                         : static_cast<int64_t>(range) + s;
 }
 
 // Where a range starts: the sequence base + at (base a multiple of 32), its slice
@@ -672,7 +685,7 @@ int4_decode_kernel(const __grid_constant__ Int4Maps maps, const __grid_constant_
         const float inv = L == 0.f ? 0.f : of / L;
         const float lse = L == 0.f ? -INFINITY : (M + fast_log2(L)) * kLn2;
         const int64_t at_row =
-            ((static_cast<int64_t>(blockIdx.x) * C::WARPS + warp) * 2 + (flat == begin ? 0 : 1)) *
+            ((i4_piece(a, range, base + at, flat != begin) * groups + group) * C::WARPS + warp) *
                 (8 * NR) + row;
 #pragma unroll
         for (int x = 0; x < CH; ++x) {
@@ -765,8 +778,7 @@ int4_combine_kernel(const __grid_constant__ Int4DecodeArgs a) {
   const int r1 = static_cast<int>(i4_div(before + sq.n - 1, per));
   const int n = (r1 - r0 + 1) * a.key_runs;
   if (n == 1) return;                                  // written by its warp
-  // State j: range r0 + j / key_runs, run j % key_runs. A range's first sequence
-  // has slot 0 of its warps, one that starts inside slot 1.
+  // State j: range r0 + j / key_runs, run j % key_runs.
   const bool inside = before > r0 * per;
   const int run_shift = 31 - __clz(a.key_runs);        // 1, 2 or 4
   const int j1 = n * (part + 1) / PARTS;
@@ -780,8 +792,8 @@ int4_combine_kernel(const __grid_constant__ Int4DecodeArgs a) {
         if (j + x >= j1) continue;
         const int q = (j + x) >> run_shift, run = j + x - (q << run_shift);
         const int64_t slot =
-            ((static_cast<int64_t>(r0 + q) * groups + group) * I4Cfg<D, NR>::WARPS +
-             run * a.heads_per_block + hl) * 2 + (q == 0 && inside ? 1 : 0);
+            (i4_piece(a, r0 + q, s, q == 0 && inside) * groups + group) * I4Cfg<D, NR>::WARPS +
+            run * a.heads_per_block + hl;
         const int64_t at = slot * (8 * NR) + row;
         l[x] = __ldcg(a.part_lse + at);
         v[x] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * D + col));
@@ -871,9 +883,12 @@ static int i4_ranges(int sms, int H_kv, int nr) {
   return n < 1 ? 1 : n;
 }
 
-size_t int4_decode_part_rows(int sms, int H_kv, int nr) {
-  return static_cast<size_t>(i4_ranges(sms, H_kv, nr)) * (H_kv / int4_decode_heads(H_kv)) *
-         I4Cfg<128, 1>::WARPS * 2 * 8 * nr;
+// (Pieces: see i4_piece.)
+size_t int4_decode_part_rows(int sms, int H_kv, int nr, int num_seqs) {
+  const int heads = int4_decode_heads(H_kv);
+  const size_t ranges = i4_ranges(sms, H_kv, nr);
+  const size_t pieces = I4Cfg<128, 1>::WARPS / heads == 1 ? 2 * ranges : ranges + num_seqs;
+  return pieces * (H_kv / heads) * I4Cfg<128, 1>::WARPS * 8 * nr;
 }
 
 cudaError_t launch_int4_decode(const Int4Maps& maps, Int4DecodeArgs a, int D, bool f16, int nr,

@@ -1516,9 +1516,9 @@ static Int4Plan plan_int4(const PassDims& d) {
   }
   p.table = align_up(off);
   p.parts = align_up(p.table + (static_cast<size_t>(d.num_segs) + 1) * 8);
-  if (p.few) p.part_rows = int4_decode_part_rows(d.sms, d.H_kv, 1);
+  if (p.few) p.part_rows = int4_decode_part_rows(d.sms, d.H_kv, 1, d.num_segs);
   if (p.some) {
-    const size_t n = int4_decode_part_rows(d.sms, d.H_kv, p.nr);
+    const size_t n = int4_decode_part_rows(d.sms, d.H_kv, p.nr, d.num_segs);
     if (n > p.part_rows) p.part_rows = n;
   }
   p.end = align_up(p.parts + p.part_rows * 4) + p.part_rows * d.D * 4;

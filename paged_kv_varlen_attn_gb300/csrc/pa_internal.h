@@ -350,7 +350,7 @@ struct Int4Pools {
 };
 cudaError_t launch_int4_prompt(const CUtensorMap& tmQ, const AttnArgs& a, const Int4Pools& pool,
                                int items_bound, cudaStream_t st);
-size_t int4_decode_part_rows(int sms, int H_kv, int nr);
+size_t int4_decode_part_rows(int sms, int H_kv, int nr, int num_seqs);
 int int4_decode_heads(int H_kv);
 cudaError_t launch_int4_decode(const Int4Maps& maps, Int4DecodeArgs a, int D, bool f16, int nr,
                                int sms, cudaStream_t st);
