@@ -42,9 +42,14 @@ namespace pa {
 // after another, are cut into equal ranges, one per block of a head group, and
 // every warp counts them for itself from the lengths. The block's warps take
 // turns at copying the slices into its ring, by TMA boxes of 16 keys x HB heads
-// that a lane issues per 16 keys; the copies run ahead across sequences. (A ring
-// per warp, filled by its own 16-byte copies, cost 158 of 604 instructions per 32
-// keys, and 64 sequences 77.4 us.)
+// that a lane issues per 16 keys; the copies run ahead across sequences. Every warp
+// waits for each slice and gives its slot back, one without a head of its own (3, 6, 9,
+// ... KV heads: three heads a block) too: a warp that copies turn T has then seen turn T
+// - STAGES, the slot's last, in its slot, so the uses before that one are over, and the
+// parity that it waits for means the use in question. (Waiting at its own turns only, it
+// would know no more than that turn T - WARPS - STAGES is over, which is not enough with
+// three stages.) A ring per warp, filled by its own 16-byte copies, cost 158 of 604
+// instructions per 32 keys, and 64 sequences 77.4 us.
 // A sequence's state that a warp does not hold whole goes to the workspace (see
 // i4_piece), and int4_combine_kernel merges those, in order: no atomics, the same
 // bits on every run.
@@ -301,7 +306,7 @@ int4_decode_kernel(const __grid_constant__ Int4Maps maps, const __grid_constant_
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], consumers);
+      mbar_init(&empty[s], C::WARPS);
     }
     *abort = 0;
     fence_mbar_init();
@@ -338,7 +343,7 @@ int4_decode_kernel(const __grid_constant__ Int4Maps maps, const __grid_constant_
   const long long begin = from.begin;
   const int run = warp / a.heads_per_block, hl = warp - run * a.heads_per_block;
   const int hk = head0 + hl;
-  const bool idle = warp >= consumers;                 // copies only
+  const bool idle = warp >= consumers;                 // has no head
 
   // This warp's first half in a stage, and from there to the second.
   const int k_at = (2 * run * a.heads_per_block + hl) * C::HALF, k_next = a.heads_per_block * C::HALF;
@@ -464,16 +469,12 @@ int4_decode_kernel(const __grid_constant__ Int4Maps maps, const __grid_constant_
       // In turn, the slice that goes where the last one was: the other warps have
       // had this one's time to be done with that.
       const bool mine = copier.turn == t + C::STAGES - 1 && copier.turn < from.count;
-      if (idle) {
-        if (mine) ok = copier.copy(a, maps.m, smem, full, empty, head0, from.count);
-        continue;
-      }
       ok = __all_sync(kAll, ok && mbar_wait(&full[slot], phase));
       if (!ok) break;
       const uint8_t* sl = smem + slot * C::STAGE;
       const uint32_t sl_at = smem_at + slot * C::STAGE;
       const int key0 = (i * a.key_runs + run) * kI4Keys;
-      if (key0 >= kv) {                                // none of this warp's
+      if (idle || key0 >= kv) {                        // none of this warp's
         if (mine) ok = copier.copy(a, maps.m, smem, full, empty, head0, from.count);
         if (lane == 0) mbar_arrive(&empty[slot]);
         continue;
