@@ -761,18 +761,17 @@ int4_combine_kernel(const __grid_constant__ Int4DecodeArgs a) {
   __shared__ float2 part_ml[THREADS];
   const int s = static_cast<int>(blockIdx.x) / a.H_kv;
   const int hk = static_cast<int>(blockIdx.x) - s * a.H_kv;
+  // The lengths too: the decode kernel lets this one start before its own wait, so what
+  // the stream did in front of the call may still be under way.
+  pdl_wait();
   const I4Seq sq = i4_seq(a, s, false);
-  if (sq.n == 0) {
-    pdl_leave();                                       // (the grid ends after its predecessor)
-    return;
-  }
+  if (sq.n == 0) return;
   const int groups = a.H_kv / a.heads_per_block, group = hk / a.heads_per_block;
   const int hl = hk - group * a.heads_per_block;
   constexpr int WIDTH = ROWS * (D / 4), PARTS = THREADS / WIDTH;
   const int rows = sq.q_len * a.G, part = threadIdx.x / WIDTH;
   const int unit = threadIdx.x - part * WIDTH;
   const int row = blockIdx.y * ROWS + unit / (D / 4), col = unit % (D / 4) * 4;
-  pdl_wait();
   if (blockIdx.y * ROWS >= rows) return;
   const long long per = __ldcg(a.table), before = __ldcg(a.table + 1 + s);
   const int r0 = static_cast<int>(i4_div(before, per));
