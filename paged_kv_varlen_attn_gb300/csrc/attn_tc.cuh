@@ -315,7 +315,7 @@ __device__ __forceinline__ void tc_softmax_tile(const AttnArgs& a, TcBars* bars,
   if constexpr (SC) {
     if (rvalid) {
       lim = max(lim, prefix - 1);
-      if (a.first_key) low = __ldg(a.first_key + tok);
+      if (a.first_key) low = max(__ldg(a.first_key + tok), 0);
       if (a.slopes) slope = __ldg(a.slopes + head) * kLog2e;
     }
   }
