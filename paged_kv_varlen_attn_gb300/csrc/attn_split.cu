@@ -314,12 +314,14 @@ __device__ __forceinline__ void split_consumer(const AttnArgs& a, uint8_t* ring,
       // Mask, scale into the log2 domain, running max. A chunk inside every
       // valid row's visible range needs no mask.
       float mx[2] = {-INFINITY, -INFINITY};
-      // The score of a product, in base 2.
+      // The score of a product (of a capped one: as it is), in base 2.
       auto score = [&](float x, int r, int key) {
         if constexpr (!SC) {
           return x * sl2;
         } else {
-          const float y = a.cap > 0.f ? capped_score(x, a.cap_in, a.cap) : x * sl2;
+          const float y = a.cap > kWideCap ? wide_capped_score(x, a.cap_in, a.cap_u, a.cap)
+                          : a.cap > 0.f    ? capped_score(x, a.cap_in, a.cap)
+                                           : x * sl2;
           return a.slopes ? fmaf(-slope[r], fabsf(static_cast<float>(key - pos[r])), y) : y;
         }
       };

@@ -610,7 +610,11 @@ static cudaError_t launch_tc_d(const CUtensorMap& tmK, const CUtensorMap& tmV,
                                cudaStream_t st) {
   if constexpr (!FP8)   // changed scores: 2-byte pools
     if (a.scored)
-      return launch_tc_kind<TcKind<D, F16, false, false, true>>(tmK, tmV, tmQ, a, items_bound, st);
+      return a.cap > kWideCap
+                 ? launch_tc_kind<TcKind<D, F16, false, false, true, false, true>>(
+                       tmK, tmV, tmQ, a, items_bound, st)
+                 : launch_tc_kind<TcKind<D, F16, false, false, true>>(tmK, tmV, tmQ, a, items_bound,
+                                                                      st);
   return a.window > 0
              ? launch_tc_kind<TcKind<D, F16, FP8, true>>(tmK, tmV, tmQ, a, items_bound, st)
              : launch_tc_kind<TcKind<D, F16, FP8, false>>(tmK, tmV, tmQ, a, items_bound, st);

@@ -153,11 +153,14 @@ __device__ __forceinline__ bool zero_v_tail(TcBars* bars, uint8_t* smem, int t, 
 }
 
 // The kinds of the prefill kernels. FP8, I4: what the pools hold (else elements of
-// the activations' type). WIN: sliding window. SC: changed scores and masks.
-template <int D_, bool F16_, bool FP8_, bool WIN_, bool SC_ = false, bool I4_ = false>
+// the activations' type). WIN: sliding window. SC: changed scores and masks. WCAP: the
+// cap is above kWideCap (a kernel of its own, since the code for it, unused, cost chunks
+// with a bias at head size 64 132 -> 135 us).
+template <int D_, bool F16_, bool FP8_, bool WIN_, bool SC_ = false, bool I4_ = false,
+          bool WCAP_ = false>
 struct TcKind {
   static constexpr int D = D_;
-  static constexpr bool F16 = F16_, FP8 = FP8_, WIN = WIN_, SC = SC_, I4 = I4_;
+  static constexpr bool F16 = F16_, FP8 = FP8_, WIN = WIN_, SC = SC_, I4 = I4_, WCAP = WCAP_;
   // V reaches the MMA widened, P in f16.
   static constexpr bool WIDE = FP8 || I4;
 };
@@ -218,7 +221,8 @@ struct TileScore {
 // to 4096 tokens, 32 heads of 128, 421 us where the exponential takes 487 and no cap
 // 330. (A shorter polynomial for |u| below 1/4 gave nothing back: the code grew.) A
 // tile with keys that a row does not see takes the exponentials, so that what those
-// keys hold does not choose the form, and rows outside the item have no say.
+// keys hold does not choose the form, and rows outside the item have no say; for a cap
+// above kWideCap (WCAP) its elements choose by themselves.
 // The bias is slope (key - row): each value takes its distance to the group's last key
 // with its factor, in one two-lane FMA, and the group's own is left to the maximum and
 // the exponent, once a group. (Last, so that the nearest key's score is not rounded at
@@ -226,7 +230,7 @@ struct TileScore {
 // magnitude, an element at a time; the warp decides together, or both forms run. Six
 // chunks of 701 tokens, 16 heads of 64: 131 us, 156 with a bias an element, 116 with
 // none.
-template <int BN>
+template <int BN, bool WCAP>
 __device__ __forceinline__ TileScore score_tile(const AttnArgs& a, float* xs, float sl2, float slope,
                                                 int pos, int key0, bool rvalid, bool hides) {
   float factor = sl2;
@@ -253,7 +257,9 @@ __device__ __forceinline__ TileScore score_tile(const AttnArgs& a, float* xs, fl
       }
     } else {
 #pragma unroll
-      for (int e = 0; e < BN; ++e) xs[e] = capped_score(xs[e], a.cap_in, 1.f);
+      for (int e = 0; e < BN; ++e)
+        xs[e] = WCAP ? wide_capped_score(xs[e], a.cap_in, a.cap_u, 1.f)
+                     : capped_score(xs[e], a.cap_in, 1.f);
     }
   } else if (sl2 < 0.f) {   // (the maximum comes before the factor)
     factor = -sl2;
@@ -377,7 +383,7 @@ __device__ __forceinline__ void tc_softmax_tile(const AttnArgs& a, TcBars* bars,
     }
     TileScore ts = {sl2, 0.f, 0.f};
     if constexpr (SC) {
-      ts = score_tile<C::BN>(a, xs, sl2, slope, pos, key0, rvalid, edge || key0 < low);
+      ts = score_tile<C::BN, Kind::WCAP>(a, xs, sl2, slope, pos, key0, rvalid, edge || key0 < low);
       if (edge || key0 < low) {
 #pragma unroll
         for (int c = 0; c < C::BN / 32; ++c) {

@@ -251,15 +251,29 @@ __device__ __forceinline__ float fast_log2(float x) {
   return y;
 }
 
+constexpr float kLog2e = 1.442695040888963407f;
 __device__ __forceinline__ float fast_rcp(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 // cap tanh(s / cap) of a raw product x, as cap - 2 cap / (1 + 2^(x cap_in)) with
-// cap_in = 2 log2(e) softmax_scale / cap; in the base of cap.
+// cap_in = 2 log2(e) softmax_scale / cap; in the base of cap. Off by up to 2^-20 of cap,
+// whatever the score.
 __device__ __forceinline__ float capped_score(float x, float cap_in, float cap) {
   return fmaf(-2.f * cap, fast_rcp(1.f + fast_exp2(x * cap_in)), cap);
+}
+// The same for caps so large that this error matters (kWideCap: 128, in base 2; 2^-20 of
+// it is what float32 sums of products may be off by): scores up to 0.46 of the cap take
+// a polynomial, the others the quotient, either off by at most 2^-20 of the score. By
+// element, so that no other element's size, seen or hidden, has a say. cap_u =
+// softmax_scale / cap.
+constexpr float kWideCap = 128.f * kLog2e;
+__device__ __forceinline__ float wide_capped_score(float x, float cap_in, float cap_u, float cap) {
+  const float u = x * cap_u, t = u * u;
+  constexpr float c0 = kTanhHalf0, c1 = kTanhHalf1, c2 = kTanhHalf2, c3 = kTanhHalf3;
+  const float y = fmaf(fmaf(fmaf(c3, t, c2), t, c1), t, c0) * u;
+  return fabsf(u) <= 0.5f ? y * cap : capped_score(x, cap_in, cap);
 }
 
 // Element type of Q, the bf16/f16 K/V pools and the outputs: bfloat16
@@ -363,7 +377,6 @@ __device__ __forceinline__ WinGeo win_geo(int kv_len, int q_len, int i0, int i1,
 }
 
 constexpr float kLn2 = 0.693147180559945309f;
-constexpr float kLog2e = 1.442695040888963407f;
 
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 

@@ -654,9 +654,8 @@ static float score_cap_in(float scale, float cap) {
   return static_cast<float>(2.0 * kLog2e64 * scale / cap);
 }
 
-// tanh(u) / u for |u| <= 1/2 as the polynomial in u^2 of the smallest largest relative
-// error (5e-7; found by reweighted least squares), in terms of the product x, u = cap_u
-// x. The seventh power of cap_u has to stay a normal number.
+// The polynomial of tanh for |u| <= 1/2 in terms of the product x, u = cap_u x. The
+// seventh power of cap_u has to stay a normal number.
 static void set_cap(AttnArgs& a, float scale, float cap) {
   a.cap = static_cast<float>(cap * kLog2e64);
   a.cap_in = score_cap_in(scale, cap);
@@ -664,7 +663,7 @@ static void set_cap(AttnArgs& a, float scale, float cap) {
   a.cap_u = static_cast<float>(u);
   a.cap_x4 = -1.f;
   if (!(std::fabs(u) >= 6e-6 && std::fabs(u) <= 1e4)) return;
-  constexpr double c4[4] = {0.999999456, -0.33326318, 0.131902967, -0.0444022262};
+  constexpr double c4[4] = {kTanhHalf0, kTanhHalf1, kTanhHalf2, kTanhHalf3};
   double p = u;
   for (int k = 0; k < 4; ++k, p *= u * u) a.cap_c4[k] = static_cast<float>(c4[k] * p);
   a.cap_x4 = static_cast<float>(0.5 / std::fabs(u));
