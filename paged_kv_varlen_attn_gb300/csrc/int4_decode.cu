@@ -429,7 +429,7 @@ int4_decode_kernel(const __grid_constant__ Int4Maps maps, const __grid_constant_
     }
     float m[NR][2], l[NR][2], lv[NR][2];               // lv: sum of weights x middle of V's row
     float acc[NR][D / 16][4], accw[NR][4];             // accw: of 8 W, in a column's units
-    float ref = 0.f;                                   // power of two, at least V's scales so far
+    float ref = 0.f;                                   // power of two, at least |V's scales| so far
 #pragma unroll
     for (int nr = 0; nr < NR; ++nr) {
 #pragma unroll
@@ -540,7 +540,7 @@ int4_decode_kernel(const __grid_constant__ Int4Maps maps, const __grid_constant_
         for (int h = 0; h < 4; ++h)
           if (key0 + 8 * h + g >= kv) vs[h] = vm[h] = 0.f;
       }
-      const float vtop = fmaxf(fmax3(vs[0], vs[1], vs[2]), vs[3]);
+      const float vtop = fmaxf(fmax3(fabsf(vs[0]), fabsf(vs[1]), fabsf(vs[2])), fabsf(vs[3]));
       if (__any_sync(kAll, vtop > ref)) {              // raise the reference of V's scales
         float top = vtop;
 #pragma unroll
