@@ -543,10 +543,17 @@ int4_decode_kernel(const __grid_constant__ Int4Maps maps, const __grid_constant_
       const float vtop = fmaxf(fmax3(fabsf(vs[0]), fabsf(vs[1]), fabsf(vs[2])), fabsf(vs[3]));
       if (__any_sync(kAll, vtop > ref)) {              // raise the reference of V's scales
         float top = vtop;
+        if (top == INFINITY) {   // (without these: rows that do not see them have no part in it)
+          top = 0.f;
+#pragma unroll
+          for (int h = 0; h < 4; ++h)
+            top = fmaxf(top, fabsf(vs[h]) == INFINITY ? 0.f : fabsf(vs[h]));
+        }
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
         // The power of two above it, and 4: a larger one is then seldom met.
-        const float nr_ref = __uint_as_float(((__float_as_uint(top) >> 23) + 3u) << 23);
+        const float nr_ref =
+            top > ref ? __uint_as_float(((__float_as_uint(top) >> 23) + 3u) << 23) : ref;
         const float f = ref == 0.f ? 0.f : ref * inverse_power(nr_ref);
         ref = nr_ref;
 #pragma unroll

@@ -33,3 +33,18 @@ def test_negative_scales(kv, ql, H, hk, D, dt, share):
         p[..., 0] = torch.where(flip, -p[..., 0], p[..., 0])
     out, lse = b.run()
     b.check(out, lse)
+
+
+@pytest.mark.parametrize("D,dt,G", [(128, "bf16", 2), (64, "f16", 2), (128, "f16", 8)])
+def test_infinite_scale_of_a_hidden_key(D, dt, G):
+    # The last token's scale of V is infinite: the tokens in front of it do not see it.
+    b = Pools([90, 40, 1000], [3, 3, 3], 2 * G, 2, D, 16, dt, 42)
+    rows = [(b.table[s, (n - 1) // 16].item(), (n - 1) % 16) for s, n in enumerate(b.kv)]
+    for page, row in rows:
+        b.params[1][page, :, row] = 0.0
+    want, want_lse = b.run()
+    for page, row in rows:
+        b.params[1][page, :, row, 0] = float("inf")
+    out, lse = b.run()
+    blind = [i for i in range(9) if i % 3 != 2]
+    assert torch.equal(out[blind], want[blind]) and torch.equal(lse[:, blind], want_lse[:, blind])
