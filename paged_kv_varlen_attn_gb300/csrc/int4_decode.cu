@@ -210,7 +210,7 @@ struct I4Copier {
 
   __device__ __forceinline__ void load_pages(const Int4DecodeArgs& a) {
     const int lane = threadIdx.x & 31, halves = 2 * a.key_runs;
-    page = a.num_blocks;                               // outside the pool: reads as zeros
+    page = a.no_page;                                  // outside the pool: reads as zeros
     row = 0;
     const int key0 = (i * halves + lane) * 16;
     if (lane < halves && key0 < kv) {
@@ -218,7 +218,7 @@ struct I4Copier {
       row = key0 - lp * a.bs;
       page = __ldg(a.bt + static_cast<int64_t>(base + at) * a.bt_stride + lp);
       if (page < 0 || page >= a.num_blocks) {
-        page = a.num_blocks;
+        page = a.no_page;
         flag_status(a.status, PA_DEV_BAD_PAGE);
       }
     }

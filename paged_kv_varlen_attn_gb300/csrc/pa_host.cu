@@ -1629,6 +1629,7 @@ pa_status pa_varlen_fwd_int4kv(const pa_kv_update* update, const void* q, int64_
   a.bs = block_size;
   a.bs_shift = log2_or_none(block_size);
   a.num_blocks = num_blocks;
+  a.no_page = num_blocks > 0 ? num_blocks : 1;
   a.total_q = total_q;
   a.max_q = max_seqlen_q;
   a.max_k = max_seqlen_k;

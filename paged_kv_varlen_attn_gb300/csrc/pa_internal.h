@@ -325,6 +325,7 @@ struct Int4DecodeArgs {
   const int32_t* bt;
   int bt_stride;
   int num_seqs, H, H_kv, G, bs, num_blocks, total_q;
+  int no_page;                    // a page outside the maps, which have one at least
   int bs_shift;                   // log2(bs), or -1 where bs is no power of two
   int max_q, max_k, kv_len_cap;
   int tokens_min, tokens_max;

@@ -1,4 +1,6 @@
-"""4-bit pools whose rows hold what the cache writes do not write."""
+"""4-bit pools whose rows hold what the cache writes do not write, and pools of no pages."""
+import ctypes
+
 import pytest
 import torch
 
@@ -48,3 +50,29 @@ def test_infinite_scale_of_a_hidden_key(D, dt, G):
     out, lse = b.run()
     blind = [i for i in range(9) if i % 3 != 2]
     assert torch.equal(out[blind], want[blind]) and torch.equal(lse[:, blind], want_lse[:, blind])
+
+
+def test_pool_of_no_pages():
+    # num_blocks = 0: every page is outside the pool and reads as zeros, whatever lies at
+    # the pool's address.
+    b = Pools([16, 0, 40], [1, 1, 1], 4, 2, 128, 16, "bf16", 43)
+    lib = pa.load_library()
+    out = torch.full((3, 4, 128), 9.0, dtype=b.dtype, device=DEV)
+    lse = torch.zeros((4, 3), device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    table = torch.zeros((3, 3), dtype=torch.int32, device=DEV)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    ws = pa.alloc_workspace(pa.varlen_fwd_int4kv_workspace_size(3, 3, 1, 40, 4, 2, 128, 16, sms),
+                            DEV)
+    desc = pa.KvInt4(b.params[0].data_ptr(), b.params[1].data_ptr(), 2 * 16)
+    code = lib.pa_varlen_fwd_int4kv(
+        None, b.q.data_ptr(), 4 * 128, b.codes[0].data_ptr(), b.codes[1].data_ptr(), 16 * 2 * 64,
+        b.cu.data_ptr(), b.lens.data_ptr(), table.data_ptr(), 3, 3, 3, 1, 40, 4, 2, 128, 16, 0,
+        b.scale, 1, ctypes.byref(desc), None, out.data_ptr(), lse.data_ptr(), ws.data_ptr(),
+        ws.numel(), pa.PA_BF16, status.data_ptr(), torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert code == pa.PA_OK and status.item() == pa.PA_DEV_BAD_PAGE
+    assert (out == 0).all()
+    want = torch.tensor([16.0, 0.0, 40.0]).log().expand(4, 3)
+    assert torch.equal(lse.cpu()[:, 1], want[:, 1])
+    assert ((lse.cpu() - want).abs()[:, ::2] <= 2.0 ** -20 * 5).all()
