@@ -382,7 +382,9 @@ AttnArgs make_attn(const CommonAttn& c, uint8_t* ws, const PassLayout& L, int bt
   a.G = c.H / c.H_kv;
   a.D = c.D;
   a.bs = c.bs;
-  a.num_blocks = c.num_blocks;
+  // (The coordinate of pages outside the pool, too; a map has one page at least, so a
+  // pool of none takes one in front of it.)
+  a.num_blocks = c.num_blocks > 0 ? c.num_blocks : -1;
   a.scale_log2 = c.scale * 1.4426950408889634f;
   a.causal = causal;
   a.out = static_cast<uint16_t*>(out);
