@@ -684,7 +684,8 @@ typedef struct pa_kv_int4 {
 } pa_kv_int4;
 
 /*
- * pa_reshape_and_cache_int4 -- pa_reshape_and_cache into 4-bit pools.
+ * pa_reshape_and_cache_int4 -- pa_reshape_and_cache into 4-bit pools. (Of a slot that
+ * occurs twice, codes and (scale, minimum) may be those of different tokens.)
  */
 pa_status pa_reshape_and_cache_int4(const void* key, const void* value, int64_t key_token_stride,
                                     int64_t value_token_stride, void* key_cache, void* value_cache,
@@ -732,12 +733,12 @@ pa_status pa_gather_cache_int4(const void* key_cache, const void* value_cache,
  * scale and minimum are applied to the sums in float32.
  * Sequences of at most 32 packed query rows (tokens x heads of the group; decode
  * and short queries): q is taken as f16 after a power-of-two row scale, exact for
- * every bf16 element of at least 2^-28 of its row's largest. The weights times V's
+ * every bf16 element of at least 2^-27 of its row's largest. The weights times V's
  * scale are rounded to f16 after a power of two. Longer sequences run on the
  * tensor-core kernel: q as it is, V widened to f16 values (one rounding, at most
- * 2^-11 of a value) and the weights in f16; there, as in the other prefill kernels,
- * a NaN in V also reaches queries of the call that stand less than a key tile in
- * front of it.
+ * 2^-11 of a value, 2^-25 of one below 2^-14) and the weights in f16; there, as in
+ * the other prefill kernels, a NaN in V also reaches queries of the call that stand
+ * less than a key tile in front of it.
  * In pages that are read, rows past a sequence's keys do not matter.
  * The workspace has a place for what any warp of the device may leave: for up to 8
  * (32) packed rows 20 MB (40 MB) at head size 128 and 152 multiprocessors, however few
@@ -770,6 +771,7 @@ pa_status pa_varlen_fwd_int4kv(const pa_kv_update* update, const void* q, int64_
  *                                               into one sequence), and
  *   j <= p, or j < prefix_lens[its sequence]   (prefix_lens given: a prefix that
  *                                               sees itself whole).
+ * (A window of w tokens beside a cap or a bias: first_key = position - w + 1.)
  * score may be NULL, its pointers too; without any, this is pa_varlen_fwd_ex. A
  * row that sees no key gets out = 0 and lse = -inf (with a sink: lse = the sink).
  * A cap moves a score by at most 2^-20 of the score from its exact value, one up to 128

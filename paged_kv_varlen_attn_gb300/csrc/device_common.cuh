@@ -608,7 +608,7 @@ __device__ __forceinline__ void abort_call(const AttnArgs& a) {
 // block-table reads stay off the issue path; the boxes of a tile are issued
 // by parallel lanes. A page id outside the pool, or
 // a box past the sequence end, becomes the out-of-range coordinate
-// num_blocks, which TMA fills with zeros. The unit's first tile is tile t0 of
+// a.num_blocks, which TMA fills with zeros. The unit's first tile is tile t0 of
 // the ring's running sequence (stages and phases continue across units).
 // SEP = false: one full/empty barrier pair per stage covers K and V, and
 // issued[0] counts issued tiles. SEP = true: K and V of a stage have their own

@@ -21,8 +21,8 @@ namespace pa {
 //   V  The MMA wants pairs of keys, so two keys' words are put together by
 //      halves (byte permutes) and masked the same way: 6 instructions for 8.
 //      O^T[D x 8 rows] += N^T W^T with W = weight x V's scale / ref, ref a power
-//      of two that is raised when a scale passes it (the weights stay below 2^8,
-//      so W stays inside f16 and keeps its eleven bits down to 2^-22 of that).
+//      of two that is raised when a scale's magnitude passes it (the weights stay
+//      below 2^8, so W stays inside f16 and keeps its eleven bits down to 2^-22 of that).
 //      The rest of the value enters by sums per row: of weights x (minimum + 8
 //      scale), and of W as rounded, eightfold, which is taken off: so a weight's
 //      rounding weighs with code - 8 and not with the code. That sum is one more
@@ -61,7 +61,9 @@ template <int D, int NR>
 struct I4Cfg {
   static constexpr int WARPS = 4;
   static constexpr int THREADS = WARPS * 32;
-  static constexpr int BLOCKS = NR == 1 ? 4 : 2;       // per SM
+  // Per SM. (Beyond 16 rows 255 registers a thread do not do at head size 128: 24 rows
+  // spill 0.2 kB, 32 rows 0.9.)
+  static constexpr int BLOCKS = NR == 1 ? 4 : 2;
   static constexpr int STAGES = (NR == 1 ? 3 : 6) + (D == 64 ? 2 : 0);
   // Of a stage: 16 keys of K of each warp, twice, as many of V, their params (of a
   // half's heads at a TMA destination of its own, so on 128 bytes).

@@ -97,6 +97,10 @@ cudaError_t launch_rope_table(float* table, RopeTableArgs& a, cudaStream_t st, i
 // (profiler: DRAM 36%, issue slots 63%, resident warps 38%): a warp waits for the
 // shuffles of its items one after another, four of the norm's sum and four of
 // the partners each. A decode step's 64 tokens take 3.0 us.
+// Into 4-bit pools, prompts of 15,900 tokens in f16, 32/8 heads, take 76 us for 51 us
+// of bytes (the keys and values alone 37, with norms 90): 72% of the issue slots
+// beside 49% of DRAM, and of the time that a warp does not issue it waits as long for
+// its own last instruction (the quantizer's chain) as for its loads.
 // ---------------------------------------------------------------------------
 constexpr int kRopeItems = 8;
 

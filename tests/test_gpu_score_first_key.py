@@ -42,3 +42,14 @@ def test_first_keys_at_the_ends_of_the_range(seqs, H, hk, D, dt, cap):
     assert torch.equal(out, want) and torch.equal(lse, want_lse)
     out, lse = b.run(softcap=cap, first_key=zero + (2 ** 31 - 1))
     assert (out == 0).all() and (lse == -float("inf")).all()
+
+
+@pytest.mark.parametrize("seqs,H,hk,D,dt", SHAPES)
+def test_window_beside_a_cap_and_a_bias(seqs, H, hk, D, dt):
+    # A window of w tokens as first keys, position - w + 1.
+    b = Batch(seqs, H, hk, D, 16, dt, seed=34)
+    pos = torch.cat([torch.arange(kv - ql, kv) for kv, ql in seqs])
+    for w in (1, 50, 129):
+        kw = dict(softcap=20.0, alibi_slopes=b.slopes(), first_key=(pos - w + 1).int())
+        out, lse = b.run(**kw)
+        b.check(out, lse, **kw)
