@@ -774,8 +774,9 @@ pa_status pa_varlen_fwd_int4kv(const pa_kv_update* update, const void* q, int64_
  * (A window of w tokens beside a cap or a bias: first_key = position - w + 1.)
  * score may be NULL, its pointers too; without any, this is pa_varlen_fwd_ex. A
  * row that sees no key gets out = 0 and lse = -inf (with a sink: lse = the sink).
- * A cap moves a score by at most 2^-20 of the score from its exact value, one up to 128
- * by at most 2^-20 of the cap.
+ * A cap moves a score by at most 2^-20 of the score from its exact value (while
+ * softmax_scale / softcap is a normal float32), one up to 128 by at most 2^-20 of the
+ * cap.
  * Pools in dtype only: opts->fp8 must be NULL (PA_ERR_UNSUPPORTED). Workspace as
  * for pa_varlen_fwd.
  * Key tiles in front of the first key of all of a tile's queries are not read.

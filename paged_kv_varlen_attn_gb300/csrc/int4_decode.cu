@@ -737,12 +737,11 @@ int4_decode_kernel(const __grid_constant__ Int4Maps maps, const __grid_constant_
       at = 0;
     }
   }
-  if (!ok) {
-    flag_status(a.status, PA_DEV_TIMEOUT);
-    *abort = 1;
-  }
+  if (!ok) flag_status(a.status, PA_DEV_TIMEOUT);
+  if (!ok || left > 0) *abort = 1;
   __syncthreads();
-  // After a wait that gave up: the copies in flight end before the block does.
+  // After a wait that gave up, and where lengths shrank under the call: the copies in
+  // flight end before the block does.
   if (*abort && warp == 0)
     for (int u = 0; u < from.count; ++u)
       if (!mbar_wait(&full[u % C::STAGES], (u / C::STAGES) & 1)) break;
